@@ -32,6 +32,9 @@ QMM_BF16 = 1
 QMM_DEV_WAIT_TIMEOUT = 1
 QMM_DEV_BAD_EXPERT = 2
 QMM_DEV_EXPERT_OVERLOAD = 4
+QMM_DEV_BAD_BLOCK = 8
+QMM_DEV_KV_SHORT = 16
+QMM_DEV_BAD_POSITION = 32
 
 EXPORTED = ("qmm_quantize_groupwise", "qmm_linear", "moe_route_workspace_bytes", "moe_route_topk",
             "moe_ffn_workspace_bytes", "moe_ffn_forward", "qmm_last_error", "qmm_launch_count",
@@ -39,7 +42,9 @@ EXPORTED = ("qmm_quantize_groupwise", "qmm_linear", "moe_route_workspace_bytes",
             "qmm_diag_wait_timeout", "qmm_linear_batched_workspace_bytes",
             "qmm_linear_batched", "qmm_rope_table", "qmm_attn_decode_workspace_bytes",
             "qmm_attn_decode", "moe_decode_workspace_bytes", "moe_decode_forward",
-            "qmm_tc_timing", "qmm_tc_timing_ms")
+            "qmm_tc_timing", "qmm_tc_timing_ms", "qmm_kv_plan", "qmm_rope_append",
+            "qmm_attn_prompt_workspace_bytes", "qmm_attn_prompt",
+            "qmm_attn_paged_workspace_bytes", "qmm_attn_paged")
 QMM_NOALLOC_MAX_LOGITS = 262144
 
 
@@ -69,6 +74,12 @@ class _AttnLayer(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("max_seq", ctypes.c_int64),
                 ("wq", _Weight), ("wk", _Weight), ("wv", _Weight), ("wo", _Weight),
                 ("rope_cos", ctypes.c_void_p), ("rope_sin", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_stride", ctypes.c_int64)]
 
 
 class _Experts(ctypes.Structure):
@@ -141,6 +152,23 @@ def lib() -> ctypes.CDLL:
             L.qmm_attn_decode.argtypes = [vp, i32, i64, ctypes.POINTER(_AttnLayer), vp, vp, i32,
                                           vp, sz, vp]
             L.qmm_attn_decode.restype = ctypes.c_int
+            f32, kvp = ctypes.c_float, ctypes.POINTER(_KvCache)
+            L.qmm_kv_plan.argtypes = [vp, vp, i32, i32, vp, i64, i32, vp, i64, i64, vp, vp, vp, vp,
+                                      vp, vp]
+            L.qmm_kv_plan.restype = ctypes.c_int
+            L.qmm_rope_append.argtypes = [vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, i64, kvp,
+                                          vp, vp, vp, i32, vp]
+            L.qmm_rope_append.restype = ctypes.c_int
+            L.qmm_attn_prompt_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32]
+            L.qmm_attn_prompt_workspace_bytes.restype = sz
+            L.qmm_attn_prompt.argtypes = [vp, vp, vp, i32, i64, i64, i64, i64, i32, i32, i32, vp, i32,
+                                          f32, vp, i32, vp, sz, vp]
+            L.qmm_attn_prompt.restype = ctypes.c_int
+            L.qmm_attn_paged_workspace_bytes.argtypes = [kvp, i64, i32, i32]
+            L.qmm_attn_paged_workspace_bytes.restype = sz
+            L.qmm_attn_paged.argtypes = [vp, i64, i64, i32, kvp, vp, i64, i32, vp, vp, i32, f32, vp,
+                                         i32, vp, sz, vp]
+            L.qmm_attn_paged.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -728,4 +756,287 @@ def attn_decode(x: torch.Tensor, pos: int, layer: AttnLayer, kv_cache: torch.Ten
     _check(lib().qmm_attn_decode(_ptr(x), _dtype_code(x), pos, ctypes.byref(desc), _ptr(kv_cache),
                                  _ptr(y), _dtype_code(y), _ptr(workspace), _nbytes(workspace),
                                  _stream(stream)))
+    return y
+
+
+# ------------------------------------------------------- paged cache, batches
+
+def _on_stream(stream, *ts) -> None:
+    """Outputs and workspaces allocated here belong to torch's current stream;
+    when the work runs on another one, their memory must not be reused before
+    that stream is done with it."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    for t in ts:
+        if t is not None and t.numel():
+            t.record_stream(s)
+
+
+def _lengths(t: torch.Tensor, numel: int, name: str) -> None:
+    if t.dtype != torch.int32 or t.numel() != numel:
+        _need(t, numel, (torch.int32,), name)
+
+
+def _table(t: torch.Tensor, rows: int) -> None:
+    """A block table: int32 [rows, columns], columns contiguous."""
+    if t.dtype != torch.int32 or t.dim() != 2:
+        raise TypeError("block_table must be a 2-D int32 tensor")
+    if t.shape[0] != rows:
+        raise ValueError(f"block_table has {t.shape[0]} rows, expected {rows}")
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("block_table's columns must be contiguous and its rows apart")
+
+
+def _on_device(*ts) -> None:
+    """_require_cuda for tensors whose strides have been checked."""
+    for t in ts:
+        if not t.is_cuda and t.numel():
+            raise ValueError("tensors must live on a CUDA device")
+
+
+def _heads(t: torch.Tensor, name: str) -> int:
+    """[T, heads, head_dim] with contiguous heads; returns the row stride."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    T, h, d = t.shape
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return t.stride(0) if T > 1 else h * d
+
+
+@dataclass
+class PagedKV:
+    """One layer's paged cache: k, v [num_blocks, n_kv, block_size, head_dim],
+    fp32 or bf16 (see include/qmm.h).  The blocks of one tensor may lie apart
+    (views of one allocation that interleaves keys, values or layers); k and v
+    share their strides."""
+    k: torch.Tensor
+    v: torch.Tensor
+
+    def _desc(self) -> _KvCache:
+        k, v = self.k, self.v
+        c = self.__dict__.get("_desc_for")
+        if (c is not None and c[0] is k and c[1] is v and c[2] == k.data_ptr()
+                and c[3] == v.data_ptr() and c[4] == k.shape and c[5] == v.shape
+                and c[6] == k.stride() and c[7] == v.stride()):
+            return c[8]
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must both be [num_blocks, n_kv, block_size, head_dim]")
+        if k.dtype != v.dtype or not (k.is_cuda and v.is_cuda):
+            raise ValueError("k and v must share a dtype and live on a CUDA device")
+        nb, nkv, bs, hd = k.shape
+        block = nkv * bs * hd
+        for t in (k, v):
+            if nb and block and t.stride()[1:] != (bs * hd, hd, 1):
+                raise ValueError("the rows of a block must be contiguous")
+        if nb > 1 and k.stride(0) != v.stride(0):
+            raise ValueError("k and v must have the same block stride")
+        desc = _KvCache(_dtype_code(k), nkv, hd, bs, nb, k.data_ptr(), v.data_ptr(),
+                        k.stride(0) if nb > 1 else block)
+        self.__dict__["_desc_for"] = (k, v, k.data_ptr(), v.data_ptr(), k.shape, v.shape, k.stride(),
+                                      v.stride(), desc)
+        return desc
+
+
+def paged_kv(num_blocks: int, n_kv: int, block_size: int, head_dim: int,
+             dtype: torch.dtype = torch.bfloat16, device="cuda") -> PagedKV:
+    """An uninitialised paged cache of one layer."""
+    shape = (num_blocks, n_kv, block_size, head_dim)
+    return PagedKV(torch.empty(shape, dtype=dtype, device=device),
+                   torch.empty(shape, dtype=dtype, device=device))
+
+
+@dataclass
+class KVPlan:
+    """What kv_plan computes: cu_new int32 [R + 1], kv_lens int32 [R],
+    positions int32 [T], slots int64 [T], blocks_used int32 [1]."""
+    cu_new: torch.Tensor
+    kv_lens: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    blocks_used: torch.Tensor
+
+
+def alloc_kv_plan(R: int, T: int, device="cuda") -> KVPlan:
+    """Uninitialised outputs for kv_plan (one allocation)."""
+    words = 2 * T + (R + 1) + R + T + 1
+    buf = torch.empty((words,), dtype=torch.int32, device=device)
+    o = 2 * T
+    return KVPlan(buf[o:o + R + 1], buf[o + R + 1:o + 2 * R + 1],
+                  buf[o + 2 * R + 1:o + 2 * R + 1 + T], buf[:2 * T].view(torch.int64),
+                  buf[words - 1:])
+
+
+def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+            free_blocks: torch.Tensor, block_size: int, num_tokens: int, out: KVPlan | None = None,
+            stream=None) -> KVPlan:
+    """Block tables and slot maps from the requests' lengths (int32 [R]; see
+    include/qmm.h): fills the new entries of block_table (int32 [R, columns])
+    from free_blocks (int32) and returns the plan of num_tokens rows (as many
+    as the new tokens, or more: padding rows get -1)."""
+    R, T = ctx_lens.numel(), num_tokens
+    _lengths(ctx_lens, R, "ctx_lens")
+    _lengths(new_lens, R, "new_lens")
+    _table(block_table, R)
+    _lengths(free_blocks, free_blocks.numel(), "free_blocks")
+    _on_device(block_table)
+    _require_cuda(ctx_lens, new_lens, free_blocks)
+    if out is None:
+        out = alloc_kv_plan(R, T, ctx_lens.device)
+        _on_stream(stream, out.cu_new)
+    else:
+        _lengths(out.cu_new, R + 1, "cu_new")
+        _lengths(out.kv_lens, R, "kv_lens")
+        _lengths(out.positions, T, "positions")
+        _need(out.slots, T, (torch.int64,), "slots")
+        _lengths(out.blocks_used, 1, "blocks_used")
+        _require_cuda(out.cu_new, out.kv_lens, out.positions, out.slots, out.blocks_used)
+    _check(lib().qmm_kv_plan(_ptr(ctx_lens), _ptr(new_lens), R, block_size, _ptr(block_table),
+                             block_table.stride(0) if R > 1 else block_table.shape[1],
+                             block_table.shape[1], _ptr(free_blocks), free_blocks.numel(), T,
+                             _ptr(out.cu_new), _ptr(out.kv_lens), _ptr(out.positions),
+                             _ptr(out.slots), _ptr(out.blocks_used), _stream(stream)))
+    return out
+
+
+def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: torch.Tensor | None,
+                rope_cos: torch.Tensor, rope_sin: torch.Tensor, cache: PagedKV | None,
+                keep_kv: bool = False, n_kv: int | None = None, y_dtype: torch.dtype | None = None,
+                q: torch.Tensor | None = None, k: torch.Tensor | None = None,
+                v: torch.Tensor | None = None, stream=None):
+    """Rotates the queries and keys of qkv [T, (n_head + 2 n_kv) head_dim] and
+    stores keys and values into their rows of the cache (see include/qmm.h).
+    Returns (q, k, v): q [T, n_head, head_dim]; k, v [T, n_kv, head_dim] when
+    keep_kv (or given), else None.  Without a cache, n_kv and y_dtype say the
+    key/value heads and the output type."""
+    hd = 2 * rope_cos.shape[-1]
+    _need(rope_cos, rope_cos.shape[0] * rope_cos.shape[-1], (torch.float32,), "rope_cos")
+    _need(rope_sin, rope_cos.numel(), (torch.float32,), "rope_sin")
+    if cache is not None:
+        desc = cache._desc()
+        if desc.head_dim != hd or (n_kv is not None and n_kv != desc.n_kv):
+            raise ValueError(f"the cache has {desc.n_kv} heads of {desc.head_dim}, the call "
+                             f"{n_kv} of {hd}")
+        n_kv, ref, y_dtype = desc.n_kv, ctypes.byref(desc), cache.k.dtype
+        if slots is None:
+            raise ValueError("a cache needs slots")
+    else:
+        ref = None
+        if n_kv is None:
+            raise ValueError("without a cache, n_kv must be given")
+        y_dtype = qkv.dtype if y_dtype is None else y_dtype
+    width = (n_head + 2 * n_kv) * hd
+    if qkv.dim() != 2 or qkv.shape[1] != width:
+        raise ValueError(f"qkv has shape {tuple(qkv.shape)}, expected [T, {width}]")
+    if qkv.numel() and qkv.stride(1) != 1:
+        raise ValueError("the rows of qkv must be contiguous")
+    T = qkv.shape[0]
+    _lengths(positions, T, "positions")
+    _need(slots, T, (torch.int64,), "slots")
+    _need(q, T * n_head * hd, (y_dtype,), "q")
+    _need(k, T * n_kv * hd, (y_dtype,), "k")
+    _need(v, T * n_kv * hd, (y_dtype,), "v")
+    _on_device(qkv)
+    _require_cuda(positions, slots, rope_cos, rope_sin, q, k, v)
+    new = []
+    if q is None:
+        q = torch.empty((T, n_head, hd), dtype=y_dtype, device=qkv.device)
+        new.append(q)
+    if keep_kv and k is None:
+        k = torch.empty((T, n_kv, hd), dtype=y_dtype, device=qkv.device)
+        new.append(k)
+    if keep_kv and v is None:
+        v = torch.empty((T, n_kv, hd), dtype=y_dtype, device=qkv.device)
+        new.append(v)
+    _on_stream(stream, *new)
+    _check(lib().qmm_rope_append(_ptr(qkv), _dtype_code(qkv), T,
+                                 qkv.stride(0) if T > 1 else width, n_head, n_kv, hd,
+                                 _ptr(positions), _ptr(slots), _ptr(rope_cos), _ptr(rope_sin),
+                                 rope_cos.shape[0], ref, _ptr(q), _ptr(k), _ptr(v), _dtype_code(q),
+                                 _stream(stream)))
+    return q, k, v
+
+
+def _attn_out(q, y, y_dtype, workspace, nbytes, stream):
+    T, nh, hd = q.shape
+    _need(y, T * nh * hd, (torch.float32, torch.bfloat16), "y")
+    _require_cuda(y, workspace)
+    new = []
+    if y is None:
+        y = torch.empty((T, nh, hd), dtype=y_dtype, device=q.device)
+        new.append(y)
+    if workspace is None:  # a caller's workspace is size-checked by the library
+        workspace = torch.empty((nbytes(),), dtype=torch.uint8, device=q.device)
+        new.append(workspace)
+    _on_stream(stream, *new)
+    return y, workspace
+
+
+def qmm_attn_prompt_workspace_bytes(q: torch.Tensor, k: torch.Tensor, n_seqs: int) -> int:
+    return int(lib().qmm_attn_prompt_workspace_bytes(_dtype_code(q), q.shape[0], q.shape[1],
+                                                     k.shape[1], q.shape[2], n_seqs))
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                scale: float | None = None, y: torch.Tensor | None = None,
+                y_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts (see include/qmm.h): q [T, n_head,
+    head_dim], k, v [T, n_kv, head_dim] (rows may lie apart, as slices of a
+    stacked projection do), cu_seqlens int32 [sequences + 1]."""
+    sq, sk, sv = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    T, nh, hd = q.shape
+    nkv = k.shape[1]
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != hd:
+        raise ValueError(f"k and v must be [{T}, n_kv, {hd}]")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must share a dtype")
+    B = cu_seqlens.numel() - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must hold at least one element")
+    _lengths(cu_seqlens, B + 1, "cu_seqlens")
+    _on_device(q, k, v)
+    _require_cuda(cu_seqlens)
+    y, workspace = _attn_out(q, y, y_dtype, workspace,
+                             lambda: qmm_attn_prompt_workspace_bytes(q, k, B), stream)
+    _check(lib().qmm_attn_prompt(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), T, sq, sk, sv, nh, nkv,
+                                 hd, _ptr(cu_seqlens), B, 0.0 if scale is None else scale, _ptr(y),
+                                 _dtype_code(y), _ptr(workspace), _nbytes(workspace),
+                                 _stream(stream)))
+    return y
+
+
+def qmm_attn_paged_workspace_bytes(q: torch.Tensor, cache: PagedKV, n_requests: int) -> int:
+    return int(lib().qmm_attn_paged_workspace_bytes(ctypes.byref(cache._desc()), q.shape[0],
+                                                    q.shape[1], n_requests))
+
+
+def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q: torch.Tensor,
+               kv_lens: torch.Tensor, scale: float | None = None, y: torch.Tensor | None = None,
+               y_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Attention of each request's new tokens (one or many) over its blocks of
+    the cache (see include/qmm.h): q [T, n_head, head_dim] of the cache's
+    dtype, block_table int32 [R, columns], cu_q int32 [R + 1], kv_lens int32
+    [R] (cache rows with the new tokens)."""
+    sq = _heads(q, "q")
+    T, nh, hd = q.shape
+    desc = cache._desc()
+    if hd != desc.head_dim or q.dtype != cache.k.dtype:
+        raise ValueError(f"q is {q.dtype} with head_dim {hd}, the cache {cache.k.dtype} with "
+                         f"{desc.head_dim}")
+    R = kv_lens.numel()
+    _lengths(kv_lens, R, "kv_lens")
+    _lengths(cu_q, R + 1, "cu_q")
+    _table(block_table, R)
+    _on_device(q, block_table)
+    _require_cuda(cu_q, kv_lens)
+    y, workspace = _attn_out(q, y, y_dtype, workspace,
+                             lambda: qmm_attn_paged_workspace_bytes(q, cache, R), stream)
+    _check(lib().qmm_attn_paged(_ptr(q), T, sq, nh, ctypes.byref(desc), _ptr(block_table),
+                                block_table.stride(0) if R > 1 else block_table.shape[1],
+                                block_table.shape[1], _ptr(cu_q), _ptr(kv_lens), R,
+                                0.0 if scale is None else scale, _ptr(y), _dtype_code(y),
+                                _ptr(workspace), _nbytes(workspace), _stream(stream)))
     return y

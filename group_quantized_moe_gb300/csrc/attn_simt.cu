@@ -1,0 +1,365 @@
+// attn_simt.cu -- batched causal attention (packed prompts, or new tokens over
+// a paged cache) in fp32 on the CUDA cores, for every type and head size the
+// library takes, and the merge of divided units.
+//
+//   s_j = scale q . k_j,  m = max_j s_j,  l = sum_j 2^((s_j - m) log2 e),
+//   o = sum_j 2^((s_j - m) log2 e) v_j / l
+// over the keys j that the token sees, in one pass over KT-key tiles with the
+// running maximum and sum (o and l are rescaled when the maximum moves).
+//
+// A unit's query rows are the tokens of a block times the query heads that
+// share the key/value head (up to TR rows), so that a key or value is read
+// once for all of them.  256 threads as 16 x 16: thread (ty, tx) forms the
+// scores of rows ty RP .. + RP - 1 and keys tx, tx + 16, ... and accumulates
+// those rows' output columns 4 tx + 64 j.
+#include <cstdint>
+
+#include "attn_batch.h"
+#include "attn_sched.cuh"
+#include "qmm_device.cuh"
+#include "qmm_internal.h"
+#include "attn_internal.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// NC: 64-column groups of the head size; TR: query rows of a unit.
+template <int NC, int TR>
+struct Simt {
+  static constexpr int KT = NC <= 2 ? 64 : (NC == 4 ? 32 : 16);
+  static constexpr int LD = NC * 64 + 4;  // floats a row: rows 4 banks apart
+  static constexpr int PLD = KT + 4;
+  static constexpr int RP = TR / 16;
+  static constexpr int smem = (TR * LD + KT * LD + KT * NC * 64 + TR * PLD) * 4 + KT * 8;
+};
+
+template <bool BF16, int NC, int TR>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSched sc, int gsub,
+                                                             int nsub, AttnParts parts,
+                                                             uint32_t *status) {
+  using C = Simt<NC, TR>;
+  constexpr int KT = C::KT, LD = C::LD, PLD = C::PLD, RP = C::RP, KP = KT / 16;
+  extern __shared__ __align__(16) float sm[];
+  float *Qs = sm, *Ks = Qs + TR * LD, *Vs = Ks + KT * LD, *Ps = Vs + KT * NC * 64;
+  int64_t *krow = reinterpret_cast<int64_t *>(Ps + TR * PLD);  // element offset of a key row, -1: none
+  __shared__ int64_t scratch[kThreads / 32 + 8];
+  pdl_enter();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int hd = a.head_dim, d4 = hd / 4;
+  const int grp = a.n_head / a.n_kv;
+  zero_loose_rows(a, sc, blockIdx.x, gridDim.x);
+  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, gridDim.x, scratch);
+  if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
+  const float sl2 = a.scale * 1.4426950408889634f;
+  int64_t x = run.first;
+  int r = run.r, i = run.i, vh = run.h, tile = run.tile;
+  while (x < run.last) {
+    AttnReq q = sched_req(sc, r);
+    while (i >= sched_blocks(sc, q)) {
+      i = 0;
+      q = sched_req(sc, ++r);
+    }
+    const int ntile = sched_tiles(sc, q, i);
+    const int stop = static_cast<int>(min64(ntile, tile + (run.last - x)));
+    const int h = vh / nsub, sub = vh - h * nsub;
+    const int g = min(gsub, grp - sub * gsub);  // query heads of this unit
+    const int t0 = i * sc.U, nt = min(sc.U, q.n - t0);
+    const int rows = nt * g, head0 = h * grp + sub * gsub;
+    const int end = sched_end(sc, q, i);        // keys the last token sees
+    const int all = q.L - q.n + t0 + 1;         // keys the first token sees
+    __syncthreads();                            // the previous unit is done with Qs
+    for (int e = tid; e < TR * NC * 16; e += kThreads) {
+      const int row = e / (NC * 16), c = e - row * (NC * 16);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < rows && c < d4) {
+        const int t = row / g, hq = row - t * g;
+        v = load_x4<BF16>(a.q, static_cast<int64_t>(q.q0 + t0 + t) * a.q_stride +
+                                   static_cast<int64_t>(head0 + hq) * hd + 4 * c);
+      }
+      *reinterpret_cast<float4 *>(Qs + row * LD + 4 * c) = v;
+    }
+    float m[RP], l[RP];
+    float4 o[RP][NC];
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+      m[p] = -INFINITY;
+      l[p] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[p][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int kt = tile; kt < stop; ++kt) {
+      const int k0 = kt * KT, nk = min(KT, end - k0);  // keys of the tile any row sees
+      bool bad = false;
+      for (int k = tid; k < KT; k += kThreads) {
+        int64_t off = -1;
+        if (k < nk) {
+          if (a.block_table) {
+            const int j = k0 + k, b = j / a.block_size;
+            const int32_t id = a.block_table[r * a.table_stride + b];
+            if (id >= 0 && id < a.num_blocks)
+              off = id * a.block_stride +
+                    static_cast<int64_t>(h * a.block_size + j - b * a.block_size) * hd;
+            else
+              bad = true;
+          } else {
+            off = k0 + k;
+          }
+        }
+        krow[k] = off;
+      }
+      // keys without a block, or that some row does not see: the guarded form
+      const bool guard = __syncthreads_or(bad) || k0 + KT > all;
+      if (bad) atomicOr(status, kDevBadBlock);
+      for (int e = tid; e < KT * NC * 16; e += kThreads) {
+        const int k = e / (NC * 16), c = e - k * (NC * 16);
+        const int64_t off = krow[k];
+        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+        if (off >= 0 && c < d4) {
+          if (a.block_table) {
+            kv = load_x4<BF16>(a.k, off + 4 * c);
+            vv = load_x4<BF16>(a.v, off + 4 * c);
+          } else {
+            const int64_t row = q.q0 + off;
+            kv = load_x4<BF16>(a.k, row * a.k_stride + static_cast<int64_t>(h) * hd + 4 * c);
+            vv = load_x4<BF16>(a.v, row * a.v_stride + static_cast<int64_t>(h) * hd + 4 * c);
+          }
+        }
+        *reinterpret_cast<float4 *>(Ks + k * LD + 4 * c) = kv;
+        *reinterpret_cast<float4 *>(Vs + k * NC * 64 + 4 * c) = vv;
+      }
+      __syncthreads();
+      float s[RP][KP];
+#pragma unroll
+      for (int p = 0; p < RP; ++p)
+#pragma unroll
+        for (int k = 0; k < KP; ++k) s[p][k] = 0.0f;
+#pragma unroll 2
+      for (int c = 0; c < d4; ++c) {
+        float4 kk[KP];
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+          kk[k] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * k) * LD + 4 * c);
+#pragma unroll
+        for (int p = 0; p < RP; ++p) {
+          const float4 qq = *reinterpret_cast<const float4 *>(Qs + (ty * RP + p) * LD + 4 * c);
+#pragma unroll
+          for (int k = 0; k < KP; ++k) {
+            s[p][k] = fmaf(qq.x, kk[k].x, s[p][k]);
+            s[p][k] = fmaf(qq.y, kk[k].y, s[p][k]);
+            s[p][k] = fmaf(qq.z, kk[k].z, s[p][k]);
+            s[p][k] = fmaf(qq.w, kk[k].w, s[p][k]);
+          }
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < RP; ++p) {
+        const int row = ty * RP + p;
+        const int vis = all + row / g;  // keys this row sees
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+          const int j = tx + 16 * k;
+          s[p][k] *= sl2;
+          if (guard && (k0 + j >= vis || krow[j] < 0)) s[p][k] = -INFINITY;
+          mx = fmaxf(mx, s[p][k]);
+        }
+#pragma unroll
+        for (int w = 8; w >= 1; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
+        const float mn = fmaxf(m[p], mx);
+        const float ref = mn == -INFINITY ? 0.0f : mn;  // no key so far: every term is 0
+        const float f = ex2(m[p] - ref);
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+          const float e = ex2(s[p][k] - ref);
+          sum += e;
+          Ps[row * PLD + tx + 16 * k] = e;
+        }
+#pragma unroll
+        for (int w = 8; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
+        l[p] = fmaf(l[p], f, sum);
+        m[p] = mn;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          o[p][c].x *= f;
+          o[p][c].y *= f;
+          o[p][c].z *= f;
+          o[p][c].w *= f;
+        }
+      }
+      __syncthreads();
+      const int steps = guard ? nk : KT;
+      for (int k = 0; k < steps; ++k) {
+        float pr[RP];
+#pragma unroll
+        for (int p = 0; p < RP; ++p) pr[p] = Ps[(ty * RP + p) * PLD + k];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float4 vv = *reinterpret_cast<const float4 *>(Vs + k * NC * 64 + 64 * c + 4 * tx);
+#pragma unroll
+          for (int p = 0; p < RP; ++p) {
+            // a key the row does not see must not enter even as 0 * NaN
+            if (guard && pr[p] == 0.0f) continue;
+            o[p][c].x = fmaf(pr[p], vv.x, o[p][c].x);
+            o[p][c].y = fmaf(pr[p], vv.y, o[p][c].y);
+            o[p][c].z = fmaf(pr[p], vv.z, o[p][c].z);
+            o[p][c].w = fmaf(pr[p], vv.w, o[p][c].w);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    const bool whole = tile == 0 && stop == ntile;
+    const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+      const int row = ty * RP + p;
+      if (row >= rows) continue;
+      if (whole) {
+        const float inv = l[p] > 0.0f || l[p] != l[p] ? 1.0f / l[p] : 0.0f;
+        const int t = row / g, hq = row - t * g;
+        const int64_t y0 = (static_cast<int64_t>(q.q0 + t0 + t) * a.n_head + head0 + hq) * hd;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = 64 * c + 4 * tx;
+          if (d < hd) store_y4(a.y, y0 + d, make_float4(o[p][c].x * inv, o[p][c].y * inv,
+                                                        o[p][c].z * inv, o[p][c].w * inv), a.y_bf16);
+        }
+      } else {
+        const int64_t base = static_cast<int64_t>(slot) * parts.rows + row;
+        if (tx == 0) parts.ml[base] = make_float2(m[p], l[p]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = 64 * c + 4 * tx;
+          if (d < hd) *reinterpret_cast<float4 *>(parts.o + base * hd + d) = o[p][c];
+        }
+      }
+    }
+    if (tid == 0 && tile == 0 && !whole) {
+      const int64_t e = x + ntile - 1;  // the unit's last tile
+      parts.open[blockIdx.x] =
+          AttnOpen{q.q0 + t0, nt, vh, sched_owner(e, run.W, run.G)};
+    }
+    x += stop - tile;
+    tile = 0;
+    if (++vh == sc.nvh) {
+      vh = 0;
+      ++i;
+    }
+  }
+}
+
+// Units divided between workers: worker w (blockIdx.x) started one and left
+// its part in slot 2 w + 1; the workers after it, up to `last`, left theirs
+// in slots 2 w'.  out = sum_w 2^(m_w - M) o_w / sum_w 2^(m_w - M) l_w with
+// M = max_w m_w, in worker order.
+__global__ void __launch_bounds__(128) attn_join_kernel(AttnBatch a, int gsub, int nsub,
+                                                        AttnParts parts) {
+  pdl_enter();
+  const AttnOpen u = parts.open[blockIdx.x];
+  if (u.rows_tok == 0) return;
+  const int grp = a.n_head / a.n_kv, hd = a.head_dim;
+  const int h = u.vh / nsub, sub = u.vh - h * nsub, g = min(gsub, grp - sub * gsub);
+  const int rows = u.rows_tok * g, d4 = hd / 4;
+  const int w0 = blockIdx.x;
+  const int lanes = blockDim.x / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int row = blockIdx.y * lanes + warp; row < rows; row += gridDim.y * lanes) {
+    auto at = [&](int w) {
+      return static_cast<int64_t>(w == w0 ? 2 * w + 1 : 2 * w) * parts.rows + row;
+    };
+    float M = -INFINITY;
+    for (int w = w0 + lane; w <= u.last; w += 32) M = fmaxf(M, parts.ml[at(w)].x);
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
+    const float ref = M == -INFINITY ? 0.0f : M;
+    const int t = row / g, hq = row - t * g;
+    const int64_t y0 =
+        (static_cast<int64_t>(u.q0 + t) * a.n_head + h * grp + sub * gsub + hq) * hd;
+    for (int c = lane; c < d4; c += 32) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.0f;
+#pragma unroll 4
+      for (int w = w0; w <= u.last; ++w) {
+        const float2 ml = parts.ml[at(w)];
+        const float4 v = *reinterpret_cast<const float4 *>(parts.o + at(w) * hd + 4 * c);
+        const float f = ex2(ml.x - ref);
+        L = fmaf(f, ml.y, L);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+      store_y4(a.y, y0 + 4 * c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv),
+               a.y_bf16);
+    }
+  }
+}
+
+template <bool BF16, int NC, int TR>
+cudaError_t launch_simt(const AttnBatch &a, const AttnSched &sc, int gsub, int nsub,
+                        const AttnParts &parts, int workers, cudaStream_t s) {
+  auto kern = attn_simt_kernel<BF16, NC, TR>;
+  constexpr int smem = Simt<NC, TR>::smem;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
+  if (e != cudaSuccess) return e;
+  uint32_t *status = device_status();
+  if (!status) return cudaErrorInvalidDevice;
+  return launch_pdl(kern, dim3(workers), dim3(kThreads), smem, s, a, sc, gsub, nsub, parts, status);
+}
+
+template <bool BF16, int TR>
+cudaError_t launch_simt_nc(int nc, const AttnBatch &a, const AttnSched &sc, int gsub, int nsub,
+                           const AttnParts &parts, int workers, cudaStream_t s) {
+  if (nc == 1) return launch_simt<BF16, 1, TR>(a, sc, gsub, nsub, parts, workers, s);
+  if (nc == 2) return launch_simt<BF16, 2, TR>(a, sc, gsub, nsub, parts, workers, s);
+  if (nc == 4) return launch_simt<BF16, 4, TR>(a, sc, gsub, nsub, parts, workers, s);
+  return launch_simt<BF16, 8, TR>(a, sc, gsub, nsub, parts, workers, s);
+}
+
+int simt_nc(int head_dim) { return head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : head_dim <= 256 ? 4 : 8; }
+
+}  // namespace
+
+AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R) {
+  (void)bf16;
+  const int grp = n_head / n_kv;
+  AttnPlan p;
+  p.rows = T * grp <= static_cast<int64_t>(16) * R ? 16 : 64;
+  p.gsub = grp < p.rows ? grp : p.rows;
+  p.nsub = (grp + p.gsub - 1) / p.gsub;
+  p.U = p.rows / p.gsub;
+  const int nc = simt_nc(head_dim);
+  p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
+  p.min_tiles = 2;
+  p.workers = sm_count() * 2;
+  return p;
+}
+
+cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
+                             const AttnParts &parts, cudaStream_t s) {
+  const int nc = simt_nc(a.head_dim);
+  if (a.bf16)
+    return p.rows == 16 ? launch_simt_nc<true, 16>(nc, a, sc, p.gsub, p.nsub, parts, p.workers, s)
+                        : launch_simt_nc<true, 64>(nc, a, sc, p.gsub, p.nsub, parts, p.workers, s);
+  return p.rows == 16 ? launch_simt_nc<false, 16>(nc, a, sc, p.gsub, p.nsub, parts, p.workers, s)
+                      : launch_simt_nc<false, 64>(nc, a, sc, p.gsub, p.nsub, parts, p.workers, s);
+}
+
+cudaError_t launch_attn_join(const AttnBatch &a, const AttnPlan &p, const AttnParts &parts,
+                             cudaStream_t s) {
+  const int ny = p.rows <= 16 ? 4 : 8;
+  return launch_pdl(attn_join_kernel, dim3(p.workers, ny), dim3(128), 0, s, a, p.gsub, p.nsub,
+                    parts);
+}
+
+}  // namespace qmm

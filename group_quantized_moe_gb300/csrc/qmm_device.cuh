@@ -14,6 +14,9 @@ namespace qmm {
 constexpr uint32_t kDevWaitTimeout = 1u;
 constexpr uint32_t kDevBadExpert = 2u;
 constexpr uint32_t kDevExpertOverload = 4u;
+constexpr uint32_t kDevBadBlock = 8u;
+constexpr uint32_t kDevKvShort = 16u;
+constexpr uint32_t kDevBadPosition = 32u;
 
 // Upper bound of any single wait inside a kernel (ns of %globaltimer).
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

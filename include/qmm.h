@@ -72,8 +72,17 @@ enum {
                                 output is incomplete                        */
   QMM_DEV_BAD_EXPERT = 2u,   /* topk_idx held an index outside [0, E); that
                                 assignment contributed nothing              */
-  QMM_DEV_EXPERT_OVERLOAD = 4u /* moe_route_load_stats found an expert chosen
+  QMM_DEV_EXPERT_OVERLOAD = 4u, /* moe_route_load_stats found an expert chosen
                                 more often than its threshold             */
+  QMM_DEV_BAD_BLOCK = 8u,   /* a block table entry that was needed, or a slot,
+                               lay outside the cache: those keys were left out
+                               (qmm_attn_paged), that row was not written
+                               (qmm_rope_append)                           */
+  QMM_DEV_KV_SHORT = 16u,   /* qmm_kv_plan ran out of free blocks, table
+                               columns or token rows: tokens without a block
+                               have slot -1                                */
+  QMM_DEV_BAD_POSITION = 32u /* qmm_rope_append met a position beyond its
+                               table: that token's row is zeros            */
 };
 
 typedef void *qmm_stream_t; /* a cudaStream_t */
@@ -289,6 +298,124 @@ size_t qmm_attn_decode_workspace_bytes(const qmm_attn_layer *L);
 int qmm_attn_decode(const void *x, int32_t x_dtype, int64_t pos, const qmm_attn_layer *L,
                     float *kv_cache, void *y, int32_t y_dtype, void *workspace,
                     size_t workspace_bytes, qmm_stream_t stream);
+
+/*
+ * Serving many requests from a paged cache.  The decode step above holds one
+ * sequence in one contiguous cache; a server holds many, of lengths that it
+ * cannot foresee, so keys and values live in blocks of block_size rows that
+ * requests take from a common pool, and a table per request says which
+ * [P1 section 3.4 defines the attention itself; the cache is its
+ * [heads, rows, head_dim] slice cut into blocks].  One step of such a server:
+ * qmm_kv_plan (tables and slots from the lengths), the projections
+ * (qmm_linear), qmm_rope_append (rotation and cache write), qmm_attn_paged or,
+ * for prompts without earlier context, qmm_attn_prompt.  Lengths are read on
+ * the device only, so a captured step can be replayed with others.
+ *
+ * A layer's cache: k and v of [num_blocks][n_kv][block_size][head_dim], fp32
+ * or bf16, consecutive blocks block_stride elements apart (at least one
+ * block; more where one allocation interleaves keys and values or layers).
+ * block_size 16, 32, 64, 128 or 256; pointers and block_stride multiples of
+ * 16 bytes. */
+typedef struct qmm_kv_cache {
+  int32_t dtype;           /* QMM_F32 or QMM_BF16                            */
+  int32_t n_kv, head_dim;  /* head_dim a multiple of 4 in [4, 512]           */
+  int32_t block_size;
+  int64_t num_blocks;
+  void *k, *v;
+  int64_t block_stride;    /* elements between blocks                        */
+} qmm_kv_cache;
+
+/*
+ * Block tables and slot maps of R requests from their lengths: request r
+ * holds ctx_lens[r] rows and adds new_lens[r] tokens.  With S = block_size:
+ *   cu_new[r]     = sum_{i<r} new_lens[i]                       [R + 1]
+ *   kv_lens[r]    = ctx_lens[r] + new_lens[r]                   [R]
+ *   block_table[r, b] for ceil(ctx_lens[r] / S) <= b < ceil(kv_lens[r] / S)
+ *                 = the next blocks of free_blocks, requests in order
+ *   *blocks_used  = blocks asked for (take that many off the free list)
+ *   positions[t]  = ctx_lens[r] + t - cu_new[r], slots[t] =
+ *                   block_table[r, positions[t] / S] * S + positions[t] % S
+ *                   for token t of request r; -1 for t >= cu_new[R]
+ * block_table [R, max_blocks] int32, rows table_stride elements apart; its
+ * earlier entries are read, those behind the new ones left alone.  T: rows of
+ * positions and slots (may exceed the tokens).  Lengths below 0 count as 0.
+ * When the free list, the table's columns or T are too short, entries become
+ * -1, the tokens concerned get slot -1 and QMM_DEV_KV_SHORT is set.
+ * R <= 16384.  One kernel launch.
+ */
+int qmm_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int32_t R, int32_t block_size,
+                int32_t *block_table, int64_t table_stride, int32_t max_blocks,
+                const int32_t *free_blocks, int64_t n_free, int64_t T, int32_t *cu_new,
+                int32_t *kv_lens, int32_t *positions, int64_t *slots, int32_t *blocks_used,
+                qmm_stream_t stream);
+
+/*
+ * Rotary positions and the cache write of T tokens.  qkv: rows row_stride
+ * elements apart, each [(n_head + 2 n_kv) head_dim]: the query heads, the key
+ * heads, the value heads (the stacked projection's output), fp32 or bf16.
+ * Pairs (2i, 2i + 1) of every query and key head turn by the angles of row
+ * positions[t] of the qmm_rope_table tables, in fp32, as in qmm_attn_decode.
+ *   q [T, n_head, head_dim]           <- rotated queries
+ *   k, v [T, n_kv, head_dim]          <- rotated keys and values (NULL: skip)
+ *   cache row slots[t]                <- the same (cache NULL: skip; slot < 0:
+ *                                        that token is not stored)
+ * q, k, v of y_dtype, which a cache must share.  A token with a position
+ * below 0 is padding: zeros in q, k and v, nothing stored; a position >=
+ * max_seq does the same and sets QMM_DEV_BAD_POSITION; a slot beyond the
+ * cache is not stored and sets QMM_DEV_BAD_BLOCK.  Two tokens must not share
+ * a slot.  row_stride a multiple of 4; pointers 16-byte aligned.
+ */
+int qmm_rope_append(const void *qkv, int32_t x_dtype, int64_t T, int64_t row_stride, int32_t n_head,
+                    int32_t n_kv, int32_t head_dim, const int32_t *positions, const int64_t *slots,
+                    const float *rope_cos, const float *rope_sin, int64_t max_seq,
+                    const qmm_kv_cache *cache, void *q, void *k, void *v, int32_t y_dtype,
+                    qmm_stream_t stream);
+
+/*
+ * Causal attention over packed prompts, grouped heads.  Sequence b holds rows
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of q [T, n_head, head_dim] and of
+ * k, v [T, n_kv, head_dim] (rows q_stride, k_stride, v_stride elements apart,
+ * heads contiguous); query head h reads key/value head h / (n_head / n_kv):
+ *   s_j = scale q_i . k_j,  p = softmax(s) over j <= i of the sequence,
+ *   y_i = sum_j p_j v_j
+ * y [T, n_head, head_dim] fp32 or bf16 (y_dtype), contiguous; rows that
+ * belong to no sequence become zeros.  scale 0: 1 / sqrt(head_dim).  dtype:
+ * of q, k and v.  A key that a row does not see never touches it, whatever it
+ * holds (NaN included).  Strides are multiples of 4 elements, pointers
+ * 16-byte aligned; workspace: qmm_attn_prompt_workspace_bytes bytes, 256-byte
+ * aligned, contents on entry do not matter.  Two kernel launches; results are
+ * reproducible bit for bit.
+ */
+size_t qmm_attn_prompt_workspace_bytes(int32_t dtype, int64_t T, int32_t n_head, int32_t n_kv,
+                                       int32_t head_dim, int32_t n_seqs);
+
+int qmm_attn_prompt(const void *q, const void *k, const void *v, int32_t dtype, int64_t T,
+                    int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_head,
+                    int32_t n_kv, int32_t head_dim, const int32_t *cu_seqlens, int32_t n_seqs,
+                    float scale, void *y, int32_t y_dtype, void *workspace, size_t workspace_bytes,
+                    qmm_stream_t stream);
+
+/*
+ * Attention of new tokens over the paged cache: one token per request
+ * (decode), chunks of a prompt, or both in one call.  Request r's queries are
+ * rows cu_q[r] .. cu_q[r + 1] - 1 of q [T, n_head, head_dim] (the cache's
+ * type), n of them; its cache holds L = kv_lens[r] rows, the new tokens' own
+ * keys and values last (qmm_rope_append has written them), key j in row
+ * j % block_size of block block_table[r, j / block_size].  Query i sees the
+ * keys j <= L - n + i; a query that sees none (L < n) gives a row of zeros.
+ * y, scale, workspace and the rest as for qmm_attn_prompt.  Rows of a block
+ * beyond L are not used, whatever they hold.  A block index outside the cache
+ * leaves its keys out and sets QMM_DEV_BAD_BLOCK; L is held to max_blocks *
+ * block_size.
+ */
+size_t qmm_attn_paged_workspace_bytes(const qmm_kv_cache *cache, int64_t T, int32_t n_head,
+                                      int32_t R);
+
+int qmm_attn_paged(const void *q, int64_t T, int64_t q_stride, int32_t n_head,
+                   const qmm_kv_cache *cache, const int32_t *block_table, int64_t table_stride,
+                   int32_t max_blocks, const int32_t *cu_q, const int32_t *kv_lens, int32_t R,
+                   float scale, void *y, int32_t y_dtype, void *workspace, size_t workspace_bytes,
+                   qmm_stream_t stream);
 
 /*
  * The routed MoE layer of a decode batch in one launch [P1 section 3.5: the
