@@ -29,6 +29,11 @@ struct AttnPlan {
 AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R);
 cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                              const AttnParts &parts, cudaStream_t s);
+// The tensor-core form: whether it takes a call, its plan, its launch.
+bool attn_tc_takes(const AttnBatch &a);
+AttnPlan attn_tc_plan(int n_head, int n_kv);
+cudaError_t launch_attn_tc(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
+                           const AttnParts &parts, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnBatch &a, const AttnPlan &p, const AttnParts &parts,
                              cudaStream_t s);
 

@@ -1,0 +1,765 @@
+// attn_tc.cu -- batched causal attention for bf16 on the 5th-generation tensor
+// cores (tcgen05): packed prompts, chunks and single tokens over a paged cache.
+//
+//   S = Q K^T (fp32 in tensor memory), P = 2^(scale log2e (S - m)) rounded to
+//   bf16, O += P V (fp32 in tensor memory), l += row sums of the unrounded P
+// over 128-key tiles, with m the row maximum so far.  O and l are rescaled
+// only when the maximum has grown by more than 2^8: until then P is at most
+// 2^8, far inside bf16 and fp32, and the ratio O / l does not depend on m.
+//
+// Query rows: a tile holds 128 / gsub tokens times the gsub query heads that
+// share a key/value head, so that a key or value tile is read once for all of
+// them.  CTA = 12 warps, one per SM, persistent over its run of the call's
+// tiles (attn_sched.cuh).  A unit has two query tiles (A, B):
+//   pair    more tokens than one tile holds: warpgroup 0 owns A, warpgroup 1
+//           owns B, and every key tile serves both;
+//   single  one tile (decoding, short prompts): the warpgroups take the key
+//           tiles in turn and their results meet in shared memory.
+// Either way the tensor core works for one warpgroup while the other one
+// computes its exponentials.
+//   warps 0-3, 4-7  warpgroups: thread = query row.  S from tensor memory,
+//             maximum, exponentials, P back over S's columns; the epilogue.
+//   warp 8    TMA producer of key and value tiles, one box per (block, 64
+//             columns), each lane its own boxes
+//   warp 9    MMA issuer (one lane): P V of a tile, then Q K^T of the same
+//             warpgroup's next tile, which may overwrite S and P because the
+//             tensor core runs its work in order
+//   warp 10   value tiles that hold keys some row does not see: rows beyond
+//             the unit's last key become zeros (0 * NaN would reach the sums),
+//             non-finite values are taken out and the unit marked, so that
+//             its epilogue adds them to the rows that do see them
+//   warp 11   TMA producer of the query tiles
+// Every wait is bounded; on a timeout the CTA raises QMM_DEV_WAIT_TIMEOUT,
+// all roles leave their loops, wait (bounded) for what they have in flight,
+// and the tensor memory is freed.
+#include <cstdint>
+
+#include "attn_batch.h"
+#include "attn_internal.h"
+#include "attn_sched.cuh"
+#include "qmm_device.cuh"
+#include "qmm_internal.h"
+#include "tc_device.cuh"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kKT = 128;              // keys per tile
+constexpr int kWarpKv = 8, kWarpMma = 9, kWarpClean = 10, kWarpQ = 11;
+constexpr uint32_t kChunk = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
+constexpr float kRescale = 8.0f;      // log2 of the growth of the maximum that is let pass
+
+template <int NCH>  // 64-column chunks of the head size
+struct Tc {
+  static constexpr uint32_t tile = NCH * kChunk;            // one Q, K or V tile
+  static constexpr int stages = NCH == 1 ? 10 : 5;          // K and V tiles in turn
+  static constexpr uint32_t q_off = 0, kv_off = 2 * tile, bar_off = kv_off + stages * tile;
+  // q_full, q_free, x_full, drain, s_full[2], p_full[2], o_full[2], then
+  // full[stages], free[stages], clean[stages]
+  static constexpr int nbar = 10 + 3 * stages;
+  static constexpr uint32_t misc_off = bar_off + nbar * 8;
+  static constexpr uint32_t bytes = misc_off + 16 + 64 + 2 * 128 * 4 + 1024;
+  static constexpr uint32_t o_col = 256, o_step = NCH * 64;  // tensor memory columns of O
+};
+
+struct TcAttn {
+  AttnBatch a;
+  AttnSched sc;
+  AttnParts parts;
+  int gsub, nsub, tpt;  // query heads and tokens of a tile
+  int box_rows;         // rows per key box
+  float sl2;            // scale log2(e)
+  uint32_t *status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ bool nonfinite_bf16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+
+// Value tiles are [key][column] in shared memory, columns contiguous: for the
+// product P V the operand's N axis (columns) is the contiguous one.  128B
+// swizzle: 64-column chunks kChunk apart, groups of eight keys 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_values(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(kChunk >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+// bf16 x bf16 -> fp32, M = 128; values: B with N contiguous.
+__device__ __forceinline__ uint32_t idesc_bf16(int n, bool values) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (values ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// A unit of this worker's run, walked by every role on its own.
+struct Unit {
+  AttnReq q;
+  int r, i, vh;            // request, token block, (virtual) head
+  int tile, stop, ntile;   // this worker's tiles [tile, stop) of ntile
+  int t0, nt;              // first token of the block, tokens
+  bool pair;
+  int ntile_a;             // tiles that query tile A reaches
+  int end, all;            // keys the last / first token sees
+  int64_t x;               // global tile index of `tile`
+};
+
+__device__ __forceinline__ bool unit_set(const TcAttn &p, const AttnRun &run, Unit &u) {
+  if (u.x >= run.last) return false;
+  u.q = sched_req(p.sc, u.r);
+  while (u.i >= sched_blocks(p.sc, u.q)) {
+    u.i = 0;
+    u.q = sched_req(p.sc, ++u.r);
+  }
+  u.ntile = sched_tiles(p.sc, u.q, u.i);
+  u.stop = static_cast<int>(min64(u.ntile, u.tile + (run.last - u.x)));
+  u.t0 = u.i * p.sc.U;
+  u.nt = min(p.sc.U, u.q.n - u.t0);
+  u.pair = u.nt > p.tpt;
+  u.end = u.q.L - u.q.n + u.t0 + u.nt;
+  u.all = u.q.L - u.q.n + u.t0 + 1;
+  const int end_a = u.q.L - u.q.n + u.t0 + min(u.nt, p.tpt);
+  u.ntile_a = end_a > kKT ? (end_a + kKT - 1) / kKT : 1;
+  return true;
+}
+
+__device__ __forceinline__ bool unit_first(const TcAttn &p, const AttnRun &run, Unit &u) {
+  u.x = run.first;
+  u.r = run.r;
+  u.i = run.i;
+  u.vh = run.h;
+  u.tile = run.tile;
+  return unit_set(p, run, u);
+}
+
+__device__ __forceinline__ bool unit_next(const TcAttn &p, const AttnRun &run, Unit &u) {
+  u.x += u.stop - u.tile;
+  u.tile = 0;
+  if (++u.vh == p.sc.nvh) {
+    u.vh = 0;
+    ++u.i;
+  }
+  return unit_set(p, run, u);
+}
+
+// The key tiles first, first + step, ... < last of warpgroup w.
+__device__ __forceinline__ void wg_tiles(const Unit &u, int w, int &first, int &last, int &step) {
+  first = u.pair ? u.tile : u.tile + w;
+  last = u.pair && w == 0 ? min(u.stop, u.ntile_a) : u.stop;
+  step = u.pair ? 1 : 2;
+}
+
+template <int NCH, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const TcAttn p) {
+  using C = Tc<NCH>;
+  constexpr int NS = C::stages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + C::bar_off;
+  const uint32_t q_full = bars, q_free = bars + 8, x_full = bars + 16, drain = bars + 24;
+  auto s_full = [&](int w) { return bars + 32 + 8 * w; };
+  auto p_full = [&](int w) { return bars + 48 + 8 * w; };
+  auto o_full = [&](int w) { return bars + 64 + 8 * w; };
+  auto full = [&](int s) { return bars + 80 + 8 * s; };
+  auto freed = [&](int s) { return bars + 80 + 8 * (NS + s); };
+  auto clean = [&](int s) { return bars + 80 + 8 * (2 * NS + s); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + C::misc_off);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + C::misc_off + 4);
+  volatile int *bad_seen = reinterpret_cast<volatile int *>(gbase + C::misc_off + 8);
+  volatile int *marked = reinterpret_cast<volatile int *>(gbase + C::misc_off + 16);  // [16]
+  float *xm = reinterpret_cast<float *>(gbase + C::misc_off + 80), *xl = xm + 128;
+  __shared__ int64_t scratch[kThreads / 32 + 8];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 8);
+    mbar_init(x_full, 4);
+    mbar_init(drain, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(s_full(w), 1);
+      mbar_init(p_full(w), 4);
+      mbar_init(o_full(w), 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(freed(s), 2);  // the tensor core's and warp 10's
+      mbar_init(clean(s), 1);
+    }
+    mbar_fence_init();
+    *abort_flag = 0;
+    *bad_seen = 0;
+    for (int k = 0; k < 16; ++k) marked[k] = 0;
+  }
+  if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_slot), 512);
+  pdl_enter();
+  zero_loose_rows(p.a, p.sc, blockIdx.x, gridDim.x);
+  if (threadIdx.x == 0) p.parts.open[blockIdx.x].rows_tok = 0;
+  const AttnRun run = sched_run<kThreads>(p.sc, blockIdx.x, gridDim.x, scratch);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int hd = p.a.head_dim, grp = p.a.n_head / p.a.n_kv;
+  const int nch = (hd + 63) / 64;  // chunks that hold columns
+  Unit u;
+
+  // 384 threads launched with 168 registers: 2 x 208 + 88 = 3 x 168
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kWarpKv) {
+      // ------------------------------------------------ key and value tiles
+      uint32_t n = 0;  // tiles loaded so far; stage n % NS
+      bool ok = true;
+      for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u)) {
+        const int h = u.vh / p.nsub;
+        const int32_t *table = PAGED ? p.a.block_table + u.r * p.a.table_stride : nullptr;
+        // box `lane` of a tile: block lane / nch, columns of chunk lane % nch
+        const int c = lane % nch, b = lane / nch, row0 = b * p.box_rows;
+        auto block_of = [&](int kt) {
+          const int k0 = kt * kKT + row0;
+          if (!PAGED || row0 >= kKT || k0 >= u.end) return 0;
+          return table[k0 / p.a.block_size];
+        };
+        int id = block_of(u.tile);
+        for (int kt = u.tile; kt < u.stop && ok; ++kt) {
+          const int k0 = kt * kKT;
+          const int keys = max(0, min(kKT, u.end - k0));
+          const int boxes = PAGED ? (keys + p.box_rows - 1) / p.box_rows : 1;
+          const int mine = id;
+          if (kt + 1 < u.stop) id = block_of(kt + 1);
+          const bool issue = b < boxes;
+          const bool bad = PAGED && issue && (mine < 0 || mine >= p.a.num_blocks);
+          if (bad) {
+            *bad_seen = 1;
+            atomicOr(p.status, kDevBadBlock);
+          }
+          __syncwarp();
+          for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
+            const int s = n % NS;
+            ok = __all_sync(0xFFFFFFFFu,
+                            wait_ok(freed(s), ((n / NS) & 1u) ^ 1u, p.status, abort_flag));
+            if (!ok) break;
+            if (lane == 0)
+              mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(boxes * p.box_rows * 128 * nch));
+            __syncwarp();
+            if (issue) {
+              const uint32_t dst = base + C::kv_off + s * C::tile + c * kChunk + row0 * 128;
+              const CUtensorMap *tm = kv ? &tm_v : &tm_k;
+              if (PAGED)  // a bad index: block num_blocks, outside the map, reads as zeros
+                tma_load_4d(dst, tm, c * 64, (k0 + row0) & (p.a.block_size - 1), h,
+                            bad ? static_cast<int>(p.a.num_blocks) : mine, full(s));
+              else
+                tma_load_3d(dst, tm, c * 64, h, u.q.q0 + k0, full(s));
+            }
+          }
+        }
+      }
+      // copies still landing (after an abort; otherwise all have been consumed)
+      const uint32_t from = n > NS ? n - NS : 0;
+      for (uint32_t k = from; k < n; ++k) mbar_wait_bounded(full(k % NS), (k / NS) & 1u, p.status);
+    } else if (warp == kWarpQ) {
+      // -------------------------------------------------------- query tiles
+      uint32_t n = 0;
+      for (bool go = unit_first(p, run, u); go; go = unit_next(p, run, u), ++n) {
+        if (!__all_sync(0xFFFFFFFFu, wait_ok(q_free, (n & 1u) ^ 1u, p.status, abort_flag))) break;
+        const int h = u.vh / p.nsub, sub = u.vh - h * p.nsub;
+        const int tiles = u.pair ? 2 : 1;
+        if (lane == 0)
+          mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * nch * p.tpt * p.gsub * 128));
+        __syncwarp();
+        if (lane < tiles * nch) {
+          const int c = lane % nch, w = lane / nch;
+          tma_load_3d(base + C::q_off + w * C::tile + c * kChunk, &tm_q, c * 64,
+                      h * grp + sub * p.gsub, u.q.q0 + u.t0 + w * p.tpt, q_full);
+        }
+      }
+      if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1u, p.status);
+    } else if (warp == kWarpClean) {
+      // --------------------------- value tiles with keys that some row misses
+      uint32_t n = 0;
+      int unit = 0;
+      bool ok = true;
+      for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u), ++unit) {
+        for (int kt = u.tile; kt < u.stop && ok; ++kt) {
+          for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
+            const int s = n % NS;
+            ok = __all_sync(0xFFFFFFFFu, wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag));
+            if (!ok) break;
+            const int k0 = kt * kKT;
+            if (kv && k0 + kKT > u.all) {
+              const int lo = max(0, u.all - k0), hi = max(0, min(kKT, u.end - k0));
+              uint8_t *v = gbase + C::kv_off + s * C::tile;
+              bool found = false;
+              for (int e = lane; e < nch * (kKT - lo) * 8; e += 32) {
+                const int row = lo + (e >> 3) % (kKT - lo), c = (e >> 3) / (kKT - lo);
+                uint4 *d = reinterpret_cast<uint4 *>(v + c * kChunk + row * 128 + (e & 7) * 16);
+                if (row >= hi) {
+                  *d = make_uint4(0u, 0u, 0u, 0u);
+                  continue;
+                }
+                uint4 t = *d;
+                uint32_t w[4] = {t.x, t.y, t.z, t.w};
+                bool hit = false;
+  #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (nonfinite_bf16(w[k])) {
+                    w[k] &= 0xFFFF0000u;
+                    hit = true;
+                  }
+                  if (nonfinite_bf16(w[k] >> 16)) {
+                    w[k] &= 0xFFFFu;
+                    hit = true;
+                  }
+                }
+                if (hit) {
+                  *d = make_uint4(w[0], w[1], w[2], w[3]);
+                  found = true;
+                }
+              }
+              if (found) marked[unit & 15] = unit + 1;
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) {
+              mbar_arrive(clean(s));
+              mbar_arrive(freed(s));
+            }
+          }
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ MMA issue
+      if (lane == 0) {
+        const int ksteps = (hd + 15) / 16;
+        const uint32_t id_s = idesc_bf16(kKT, false), id_o = idesc_bf16(ksteps * 16, true);
+        uint32_t n0 = 0, nq = 0, np[2] = {0, 0};
+        bool ok = true;
+        for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u), ++nq) {
+          if (!(ok = wait_ok(q_full, nq & 1u, p.status, abort_flag))) break;
+          int first[2], last[2], step, cur[2];
+          wg_tiles(u, 0, first[0], last[0], step);
+          wg_tiles(u, 1, first[1], last[1], step);
+          // tile kt's keys are load n0 + 2 (kt - tile), its values the next one;
+          // warpgroup 1 is the last user of every tile of a pair
+          auto qk = [&](int w, int kt) {
+            const uint32_t n = n0 + 2 * (kt - u.tile);
+            const int s = n % NS;
+            if (!wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag)) return false;
+            tc_fence_after();
+            const uint64_t qd = smem_desc_sw128(base + C::q_off + (u.pair ? w : 0) * C::tile);
+            const uint64_t kd = smem_desc_sw128(base + C::kv_off + s * C::tile);
+            for (int k = 0; k < ksteps; ++k) {
+              const uint64_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
+              tc_mma_ss(tmem + w * 128, qd + off, kd + off, id_s, k > 0);
+            }
+            tc_commit(s_full(w));
+            if (!u.pair || w == 1) tc_commit(freed(s));
+            return true;
+          };
+          auto pv = [&](int w, int kt) {
+            const uint32_t n = n0 + 2 * (kt - u.tile) + 1;
+            const int s = n % NS;
+            if (!wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag)) return false;
+            if (!wait_ok(clean(s), (n / NS) & 1u, p.status, abort_flag)) return false;
+            if (!wait_ok(p_full(w), np[w]++ & 1u, p.status, abort_flag)) return false;
+            tc_fence_after();
+            const uint64_t vd = desc_values(base + C::kv_off + s * C::tile);
+            const uint32_t o = tmem + C::o_col + w * C::o_step;
+  #pragma unroll
+            for (int k = 0; k < kKT / 16; ++k)
+              tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o,
+                        kt != first[w] || k > 0);
+            if (!u.pair || w == 1) tc_commit(freed(s));
+            return true;
+          };
+          for (int w = 0; w < 2 && ok; ++w) {
+            cur[w] = first[w];
+            if (cur[w] < last[w]) ok = qk(w, cur[w]);
+          }
+          while (ok && (cur[0] < last[0] || cur[1] < last[1])) {
+            for (int w = 0; w < 2 && ok; ++w) {
+              if (cur[w] >= last[w]) continue;
+              ok = pv(w, cur[w]);
+              cur[w] += step;
+              if (!ok) break;
+              if (cur[w] < last[w])
+                ok = qk(w, cur[w]);
+              else if (u.pair)
+                tc_commit(o_full(w));
+            }
+          }
+          // single: both results at once, when nothing reads the query tile any
+          // more (its shared memory carries warpgroup 1's result to warpgroup 0)
+          if (ok && !u.pair) {
+            tc_commit(o_full(0));
+            if (first[1] < last[1]) tc_commit(o_full(1));
+          }
+          n0 += 2 * (u.stop - u.tile);
+        }
+        tc_commit(drain);
+        mbar_wait_bounded(drain, 0u, p.status);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------------------------------------------------- warpgroups
+    const int w = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp % 4)
+    const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + C::o_col + w * C::o_step;
+    const int ochunks = (hd + 31) / 32;
+    uint32_t nt = 0, no = 0, nx = 0;
+    int unit = 0;
+    bool ok = true;
+    for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u), ++unit) {
+      int first, last, step;
+      wg_tiles(u, w, first, last, step);
+      const int h = u.vh / p.nsub, sub = u.vh - h * p.nsub;
+      const int g = min(p.gsub, grp - sub * p.gsub);
+      // rows of a tile are (token, head) with gsub heads a token, of which g count
+      const int tok = row / p.gsub, hq = row - tok * p.gsub;
+      const int tw = u.pair ? w * p.tpt : 0;  // first token of this warpgroup's query tile
+      const bool live = tok < min(p.tpt, u.nt - tw) && hq < g;
+      const bool busy = __any_sync(0xFFFFFFFFu, live);
+      const int vis = u.all + tw + tok;       // keys this row sees
+      const int all = u.all + tw;             // keys every row of the tile sees
+      float m = -INFINITY, l = 0.0f;
+      for (int kt = first; kt < last; kt += step, ++nt) {
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(s_full(w), nt & 1u, p.status, abort_flag)))) break;
+        tc_fence_after();
+        if (u.pair && kt + step >= last) {  // the last read of this query tile is done
+          if (lane == 0) mbar_arrive(q_free);
+        }
+        if (busy) {
+          uint32_t s[128];
+          tmem_ld128(ts, s);
+          const int k0 = kt * kKT;
+          if (k0 + kKT > all) {
+            const int lim = vis - k0;
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (j >= lim) s[j] = 0xFF800000u;
+          }
+          if (PAGED && *bad_seen) {  // leave out the keys of blocks outside the cache
+            const int j = k0 + lane * 16;
+            bool bad = false;
+            if (lane < 8 && j < u.end) {
+              const int32_t id = p.a.block_table[u.r * p.a.table_stride + j / p.a.block_size];
+              bad = id < 0 || id >= p.a.num_blocks;
+            }
+            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, bad);
+#pragma unroll
+            for (int q = 0; q < 128; ++q)
+              if (bits >> (q / 16) & 1u) s[q] = 0xFF800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 128; j += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(s[j + k]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool grow = (top - m) * p.sl2 > kRescale;  // -inf - -inf: NaN, no
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float mn = grow ? top : m;
+            const float f = mn == m ? 1.0f : ex2((m - mn) * p.sl2);
+            l *= f;
+            m = mn;
+            if (kt != first) {
+              for (int c = 0; c < ochunks; ++c) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * c, o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st32(to + 32 * c, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.0f : m * p.sl2;
+          const f32x2 a2 = pack2(p.sl2, p.sl2), b2 = pack2(-ref, -ref);
+          f32x2 sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int k = 32 * c + 2 * j;
+              float x0, x1;
+              unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), a2, b2), x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              sum[j & 1] = add2(sum[j & 1], pack2(x0, x1));
+              pk[j] = bf16x2(x0, x1);
+            }
+            tmem_st16(ts + 16 * c, pk);
+          }
+          float s0, s1;
+          unpack2(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(w));
+      }
+      if (!ok) break;
+      const bool have = first < last;
+      if (have) {
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(o_full(w), no++ & 1u, p.status, abort_flag)))) break;
+        tc_fence_after();
+      } else {
+        // no tile here: still one arrival per unit and warp, not before the
+        // unit's queries are in (so none counts for an earlier unit)
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(q_full, unit & 1u, p.status, abort_flag)))) break;
+        if (u.pair && lane == 0) mbar_arrive(q_free);
+      }
+      // single: warpgroup 1's result to warpgroup 0 through the query tiles' memory
+      const bool join = !u.pair && u.stop - u.tile > 1;
+      float *xo = reinterpret_cast<float *>(gbase + C::q_off);
+      auto xat = [&](int c4) { return xo + row * (NCH * 64) + ((c4 ^ (row & 7)) << 2); };
+      float f0 = 1.0f, f1 = 0.0f;
+      if (!u.pair) {
+        if (w == 1) {
+          if (join) {
+            if (busy) {
+              for (int c = 0; c < ochunks; ++c) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * c, o);
+                if (live)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4 *>(xat(8 * c + j)) =
+                        make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              }
+              if (live) {
+                xm[row] = m;
+                xl[row] = l;
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_full);
+          }
+          if (lane == 0) mbar_arrive(q_free);
+          continue;
+        }
+        if (join) {
+          if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(x_full, nx++ & 1u, p.status, abort_flag)))) break;
+          if (live) {
+            const float m1 = xm[row], mn = fmaxf(m, m1);
+            const float r = mn == -INFINITY ? 0.0f : mn;
+            f0 = ex2((m - r) * p.sl2);
+            f1 = ex2((m1 - r) * p.sl2);
+            l = l * f0 + xl[row] * f1;
+            m = mn;
+          }
+        }
+      }
+      if (busy) {
+        const bool whole = u.tile == 0 && u.stop == u.ntile;
+        const float inv = whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+        const int64_t y0 = (static_cast<int64_t>(u.q.q0 + u.t0 + tw + tok) * p.a.n_head + h * grp +
+                            sub * p.gsub + hq) * hd;
+        const int64_t slot = (2 * blockIdx.x + (u.tile == 0 ? 1 : 0)) *
+                                 static_cast<int64_t>(p.parts.rows) + (tw + tok) * g + hq;
+        if (!whole && live)
+          p.parts.ml[slot] = make_float2(m == -INFINITY ? m : m * p.sl2, l);
+        const bool mark = marked[unit & 15] == unit + 1;
+        for (int c = 0; c < ochunks; ++c) {
+          uint32_t o[32];
+          if (have)
+            tmem_ld32(to + 32 * c, o);
+          else
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
+          if (!live) continue;
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]);
+          if (join) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 t = *reinterpret_cast<const float4 *>(xat(8 * c + j));
+              v[4 * j] = v[4 * j] * f0 + t.x * f1;
+              v[4 * j + 1] = v[4 * j + 1] * f0 + t.y * f1;
+              v[4 * j + 2] = v[4 * j + 2] * f0 + t.z * f1;
+              v[4 * j + 3] = v[4 * j + 3] * f0 + t.w * f1;
+            }
+          }
+          if (mark) {  // non-finite values that were taken out: into the rows that see them
+            const int j0 = max(u.tile * kKT, (u.all > 0 ? u.all : 0) / kKT * kKT);
+            const int j1 = min(min(vis, u.end), u.stop * kKT);
+            for (int j = max(j0, u.all > 0 ? u.all : 0); j < j1; ++j) {
+              const uint16_t *src = static_cast<const uint16_t *>(p.a.v);
+              if (PAGED) {
+                const int32_t id = p.a.block_table[u.r * p.a.table_stride + j / p.a.block_size];
+                if (id < 0 || id >= p.a.num_blocks) continue;
+                src += id * p.a.block_stride +
+                       static_cast<int64_t>(h * p.a.block_size + (j & (p.a.block_size - 1))) * hd;
+              } else {
+                src += static_cast<int64_t>(u.q.q0 + j) * p.a.v_stride + static_cast<int64_t>(h) * hd;
+              }
+              for (int k = 0; k < 32; ++k) {
+                if (32 * c + k >= hd) break;
+                const uint32_t b = src[32 * c + k];
+                if (nonfinite_bf16(b)) {
+#pragma unroll
+                  for (int t = 0; t < 32; ++t)
+                    if (t == k) v[t] += __uint_as_float(b << 16);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            const int d = 32 * c + j;
+            if (d >= hd) break;
+            const float4 lo = make_float4(v[j] * inv, v[j + 1] * inv, v[j + 2] * inv, v[j + 3] * inv);
+            const float4 hi =
+                make_float4(v[j + 4] * inv, v[j + 5] * inv, v[j + 6] * inv, v[j + 7] * inv);
+            if (!whole) {
+              float4 *o4 = reinterpret_cast<float4 *>(p.parts.o + slot * hd + d);
+              o4[0] = lo;
+              o4[1] = hi;
+            } else if (p.a.y_bf16) {
+              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.y) + y0 + d) =
+                  make_uint4(bf16x2(lo.x, lo.y), bf16x2(lo.z, lo.w), bf16x2(hi.x, hi.y),
+                             bf16x2(hi.z, hi.w));
+            } else {
+              float4 *y4 = reinterpret_cast<float4 *>(static_cast<float *>(p.a.y) + y0 + d);
+              y4[0] = lo;
+              y4[1] = hi;
+            }
+          }
+        }
+      }
+      if (!u.pair) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_free);
+      }
+      if (threadIdx.x == 0 && u.tile == 0 && u.stop < u.ntile)
+        p.parts.open[blockIdx.x] = AttnOpen{u.q.q0 + u.t0, u.nt, u.vh,
+                                            sched_owner(u.x + u.ntile - 1, run.W, run.G)};
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// bf16 [rows][heads][head_dim] as a 3-D map, box [64 columns, heads, rows].
+bool map_rows(CUtensorMap *m, const void *p, int64_t rows, int64_t stride, int heads, int hd,
+              int box_heads, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 [block][n_kv][block_size][head_dim] as a 4-D map, box [64 columns,
+// box_rows, 1, 1].
+bool map_blocks(CUtensorMap *m, const void *p, const AttnBatch &a, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t hd = a.head_dim;
+  cuuint64_t dims[4] = {hd, static_cast<cuuint64_t>(a.block_size), static_cast<cuuint64_t>(a.n_kv),
+                        static_cast<cuuint64_t>(a.num_blocks)};
+  cuuint64_t strides[3] = {hd * 2, hd * 2 * a.block_size, static_cast<cuuint64_t>(a.block_stride) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NCH, bool PAGED>
+cudaError_t run_tc(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const TcAttn &p,
+                   int workers, cudaStream_t s) {
+  auto kern = attn_tc_kernel<NCH, PAGED>;
+  static_assert(Tc<NCH>::bytes <= 227 * 1024, "shared memory");
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), Tc<NCH>::bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(workers), dim3(kThreads), Tc<NCH>::bytes, s, q, k, v, p);
+}
+
+}  // namespace
+
+// Head sizes a multiple of 8 up to 128 (TMA rows of whole 16-byte units;
+// tensor memory holds two 128-column results), rows and blocks 16 bytes apart.
+bool attn_tc_takes(const AttnBatch &a) {
+  if (!a.bf16 || a.head_dim % 8 != 0 || a.head_dim > 128 || a.q_stride % 8 != 0) return false;
+  const int64_t most = int64_t(1) << 38;  // strides below 2^40 bytes
+  if (a.q_stride > most) return false;
+  if (a.block_table) return a.num_blocks > 0 && a.block_stride % 8 == 0 && a.block_stride < most;
+  return a.k_stride % 8 == 0 && a.v_stride % 8 == 0 && a.k_stride < most && a.v_stride < most;
+}
+
+AttnPlan attn_tc_plan(int n_head, int n_kv) {
+  const int grp = n_head / n_kv;
+  AttnPlan p;
+  p.rows = 256;
+  p.gsub = grp < 128 ? grp : 128;
+  p.nsub = (grp + p.gsub - 1) / p.gsub;
+  p.U = 2 * (128 / p.gsub);
+  p.KT = kKT;
+  p.min_tiles = 2;
+  p.workers = sm_count();
+  return p;
+}
+
+cudaError_t launch_attn_tc(const AttnBatch &a, const AttnPlan &pl, const AttnSched &sc,
+                           const AttnParts &parts, cudaStream_t s) {
+  TcAttn p{};
+  p.a = a;
+  p.sc = sc;
+  p.parts = parts;
+  p.gsub = pl.gsub;
+  p.nsub = pl.nsub;
+  p.tpt = pl.U / 2;
+  p.box_rows = a.block_table ? (a.block_size < kKT ? a.block_size : kKT) : kKT;
+  p.sl2 = a.scale * 1.4426950408889634f;
+  p.status = device_status();
+  if (!p.status) return cudaErrorInvalidDevice;
+  CUtensorMap q, k, v;
+  bool ok = map_rows(&q, a.q, a.T, a.q_stride, a.n_head, a.head_dim, p.gsub, p.tpt);
+  if (a.block_table)
+    ok = ok && map_blocks(&k, a.k, a, p.box_rows) && map_blocks(&v, a.v, a, p.box_rows);
+  else
+    ok = ok && map_rows(&k, a.k, a.T, a.k_stride, a.n_kv, a.head_dim, 1, kKT) &&
+         map_rows(&v, a.v, a.T, a.v_stride, a.n_kv, a.head_dim, 1, kKT);
+  if (!ok) return cudaErrorInvalidValue;
+  if (a.head_dim <= 64)
+    return a.block_table ? run_tc<1, true>(q, k, v, p, pl.workers, s)
+                         : run_tc<1, false>(q, k, v, p, pl.workers, s);
+  return a.block_table ? run_tc<2, true>(q, k, v, p, pl.workers, s)
+                       : run_tc<2, false>(q, k, v, p, pl.workers, s);
+}
+
+}  // namespace qmm
