@@ -4,13 +4,14 @@
 // rows, and token t of it sees the keys 0 .. L - n + t.  A unit of work is
 // (request, block of U consecutive tokens, key/value head); its cost is the
 // number of KT-key tiles its last token reaches (at least one, so that a
-// token that sees no key still gets its row of zeros).  The units are laid
-// end to end in the order (request, token block, head) and the W tiles of
-// the whole call are cut into G equal runs, one per worker: every worker
-// gets the same work whatever the lengths are, and a long context is split
-// over as many workers as its share of the work asks for.  A unit that a cut
-// divides leaves one partial result per worker, merged afterwards in worker
-// order, so results are reproducible bit for bit.
+// token that sees no key still gets its row of zeros), and `fixed` tiles more
+// for what a unit costs besides its tiles (loading its queries, writing its
+// results).  The units are laid end to end in the order (request, token
+// block, head) and the cost W of the whole call is cut into G equal runs, one
+// per worker: every worker gets the same work whatever the lengths are, and a
+// long context is split over as many workers as its share of the work asks
+// for.  A unit that a cut divides leaves one partial result per worker,
+// merged afterwards in worker order, so results are reproducible bit for bit.
 //
 // Everything here is computed on the device from the lengths (a call can be
 // captured in a graph and replayed with other lengths in the same buffers).
@@ -27,7 +28,8 @@ struct AttnSched {
   int nvh;             // key/value heads (times the splits of a large query group)
   int U;               // tokens per unit
   int KT;              // keys per tile
-  int min_tiles;       // a worker gets at least this many tiles
+  int fixed;           // cost of a unit besides its tiles
+  int min_run;         // a worker's run costs at least this much
   int64_t T;           // query rows in the buffers
   int64_t cap;         // largest cache length the block table can hold
 };
@@ -52,6 +54,13 @@ __device__ __forceinline__ AttnReq sched_req(const AttnSched &s, int r) {
   return q;
 }
 
+// a / b for a >= 0, b > 0: the 64-bit division is several times the 32-bit
+// one, and nearly every call fits the latter.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // sum_{i < n} floor((a i + b) / m) for n, a, b >= 0, m > 0: the whole parts of
 // a / m and b / m are taken out, and what is left counts the lattice points
 // under a line, which is the same sum with the axes exchanged (the steps of
@@ -59,12 +68,13 @@ __device__ __forceinline__ AttnReq sched_req(const AttnSched &s, int r) {
 __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t total = 0;
   while (n > 0) {
-    total += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
+    const int64_t qa = div_pos(a, m), qb = div_pos(b, m);
+    total += n * (n - 1) / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
     const int64_t y = a * n + b;
-    n = y / m;
-    b = y % m;
+    n = div_pos(y, m);
+    b = y - n * m;
     const int64_t t = m;
     m = a;
     a = t;
@@ -88,35 +98,48 @@ __device__ __forceinline__ int sched_tiles(const AttnSched &s, const AttnReq &q,
   return e > s.KT ? (e + s.KT - 1) / s.KT : 1;
 }
 
-// Tiles of one head in the token blocks before block i.
+// Cost of one head's units in the token blocks before block i.
 __device__ inline int64_t sched_before(const AttnSched &s, const AttnReq &q, int i) {
   // block j < i is full: its last token sees c + (j + 1) U keys, c = L - n
   const int64_t c = static_cast<int64_t>(q.L) - q.n;
   int64_t j0 = 0;  // blocks whose last token sees no key: one tile each
   if (c < 0) {
-    j0 = -c / s.U;
+    j0 = div_pos(-c, s.U);
     if (j0 > i) j0 = i;
   }
-  return j0 + floor_sum(i - j0, s.KT, s.U, c + (j0 + 1) * s.U + s.KT - 1);
+  return j0 + floor_sum(i - j0, s.KT, s.U, c + (j0 + 1) * s.U + s.KT - 1) +
+         static_cast<int64_t>(i) * s.fixed;
 }
 
 __device__ __forceinline__ int64_t sched_cost(const AttnSched &s, const AttnReq &q) {
   const int m = sched_blocks(s, q);
   if (m == 0) return 0;
   const int64_t before = m > 1 ? sched_before(s, q, m - 1) : 0;
-  return (before + sched_tiles(s, q, m - 1)) * s.nvh;
+  return (before + sched_tiles(s, q, m - 1) + s.fixed) * s.nvh;
 }
 
-// One worker's run: where it starts and how many tiles it has.  W and G
-// describe the cut (worker w starts at tile floor(w W / G)).
+// One worker's run [first, last) of the call's cost W, cut into G runs, and
+// the unit that holds its start: request r, token block i, head h, beginning
+// at cost `unit`.
 struct AttnRun {
-  int64_t W, first, last;  // tiles of the call; this worker's [first, last)
+  int64_t W, first, last, unit;
   int G;
-  int r, i, h, tile;       // request, token block, head, tile where it starts
+  int r, i, h;
 };
 
+// Runs are W / G long, the first W mod G of them one longer.
+__device__ __forceinline__ int64_t sched_first(int64_t w, int64_t base, int64_t more) {
+  return w * base + (w < more ? w : more);
+}
+
+// Worker whose run holds cost x.
+__device__ __forceinline__ int sched_owner(int64_t x, int64_t W, int G) {
+  const int64_t base = div_pos(W, G), more = W - base * G, edge = more * (base + 1);
+  return static_cast<int>(x < edge ? div_pos(x, base + 1) : more + div_pos(x - edge, base));
+}
+
 // The run of worker w of at most `workers`, by all NT threads of a block.
-// scratch: 8 (NT / 32 + 8) bytes of shared memory.  A worker without work
+// scratch: 8 (NT / 32 + 4) bytes of shared memory.  A worker without work
 // gets first == last.
 template <int NT>
 __device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *scratch) {
@@ -133,48 +156,58 @@ __device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *sc
   }
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
-  int64_t base = 0, W = 0;
+  int64_t lo = inc - mine, W = 0;  // lo: cost before this thread's requests
 #pragma unroll
   for (int k = 0; k < NT / 32; ++k) {
     const int64_t v = scratch[k];
-    if (k < warp) base += v;
+    if (k < warp) lo += v;
     W += v;
   }
   AttnRun run;
   run.W = W;
-  const int64_t g = W / s.min_tiles;
+  const int64_t g = div_pos(W, s.min_run);
   run.G = g < 1 ? 1 : (g < workers ? static_cast<int>(g) : workers);
-  run.first = w < run.G ? w * W / run.G : W;
-  run.last = w < run.G ? (w + 1) * W / run.G : W;
-  int *found = reinterpret_cast<int *>(scratch + NT / 32);
-  const int64_t lo = base + inc - mine;
+  const int64_t base = div_pos(W, run.G), more = W - base * run.G;
+  run.first = w < run.G ? sched_first(w, base, more) : W;
+  run.last = w < run.G ? sched_first(w + 1, base, more) : W;
+  int64_t *found = scratch + NT / 32;
   if (run.first < run.last && run.first >= lo && run.first < lo + mine) {
-    int64_t o = run.first - lo;
     int r = r0;
     AttnReq q = sched_req(s, r);
-    for (int64_t c = sched_cost(s, q); o >= c; c = sched_cost(s, q)) {
-      o -= c;
+    for (int64_t c = sched_cost(s, q); run.first >= lo + c && r + 1 < r1; c = sched_cost(s, q)) {
+      lo += c;
       q = sched_req(s, ++r);
     }
-    int a = 0, b = sched_blocks(s, q);  // the block holding tile o of the request
+    int a = 0, b = sched_blocks(s, q);  // the block whose units hold the start
     while (b - a > 1) {
       const int mid = (a + b) >> 1;
-      if (sched_before(s, q, mid) * s.nvh <= o) a = mid;
+      if (lo + sched_before(s, q, mid) * s.nvh <= run.first) a = mid;
       else b = mid;
     }
-    o -= sched_before(s, q, a) * s.nvh;
-    const int t = sched_tiles(s, q, a);
+    if (a > 0) lo += sched_before(s, q, a) * s.nvh;
+    const int cost = sched_tiles(s, q, a) + s.fixed;
+    const int64_t h = div_pos(run.first - lo, cost);
     found[0] = r;
     found[1] = a;
-    found[2] = static_cast<int>(o / t);
-    found[3] = static_cast<int>(o % t);
+    found[2] = h;
+    found[3] = lo + h * cost;
   }
   __syncthreads();
-  run.r = found[0];
-  run.i = found[1];
-  run.h = found[2];
-  run.tile = found[3];
+  const bool work = run.first < run.last;  // else nothing was found
+  run.r = work ? static_cast<int>(found[0]) : 0;
+  run.i = work ? static_cast<int>(found[1]) : 0;
+  run.h = work ? static_cast<int>(found[2]) : 0;
+  run.unit = work ? found[3] : W;
   return run;
+}
+
+// The tiles [tile, stop) of a unit of ntile tiles that begins at cost x which
+// a run holds (a cut inside the fixed cost leaves all tiles to the later run).
+__device__ __forceinline__ void sched_part(const AttnSched &s, const AttnRun &run, int64_t x,
+                                           int ntile, int &tile, int &stop) {
+  const int64_t a = run.first - x - s.fixed, b = run.last - x - s.fixed;
+  tile = a <= 0 ? 0 : static_cast<int>(a);
+  stop = b <= 0 ? 0 : (b < ntile ? static_cast<int>(b) : ntile);
 }
 
 // What a worker leaves for the merge: the unit that is still open when its
@@ -184,13 +217,5 @@ struct AttnOpen {
   int vh;            // (virtual) head
   int last;          // the worker whose run ends it
 };
-
-// Worker that processes tile x of a call cut into G runs of W tiles.
-__device__ __forceinline__ int sched_owner(int64_t x, int64_t W, int G) {
-  int w = static_cast<int>(x * G / W);
-  while (w + 1 < G && (w + 1) * W / G <= x) ++w;
-  while (w > 0 && w * W / G > x) --w;
-  return w;
-}
 
 }  // namespace qmm

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm, *Ks = Qs + TR * LD, *Vs = Ks + KT * LD, *Ps = Vs + KT * NC * 64;
   int64_t *krow = reinterpret_cast<int64_t *>(Ps + TR * PLD);  // element offset of a key row, -1: none
-  __shared__ int64_t scratch[kThreads / 32 + 8];
+  __shared__ int64_t scratch[kThreads / 32 + 4];
   pdl_enter();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int hd = a.head_dim, d4 = hd / 4;
@@ -59,16 +59,20 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
   const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, gridDim.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
-  int64_t x = run.first;
-  int r = run.r, i = run.i, vh = run.h, tile = run.tile;
-  while (x < run.last) {
-    AttnReq q = sched_req(sc, r);
+  int64_t x = run.unit;
+  int r = run.r, i = run.i, vh = run.h;
+  AttnReq q;
+  for (int ntile = 0; x < run.last; x += sc.fixed + ntile, vh = vh + 1 == sc.nvh ? 0 : vh + 1, i += vh == 0) {
+    q = sched_req(sc, r);
     while (i >= sched_blocks(sc, q)) {
+      if (++r >= sc.R) return;  // lengths that changed during the call
       i = 0;
-      q = sched_req(sc, ++r);
+      q = sched_req(sc, r);
     }
-    const int ntile = sched_tiles(sc, q, i);
-    const int stop = static_cast<int>(min64(ntile, tile + (run.last - x)));
+    ntile = sched_tiles(sc, q, i);
+    int tile, stop;
+    sched_part(sc, run, x, ntile, tile, stop);
+    if (tile >= stop) continue;
     const int h = vh / nsub, sub = vh - h * nsub;
     const int g = min(gsub, grp - sub * gsub);  // query heads of this unit
     const int t0 = i * sc.U, nt = min(sc.U, q.n - t0);
@@ -244,15 +248,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
       }
     }
     if (tid == 0 && tile == 0 && !whole) {
-      const int64_t e = x + ntile - 1;  // the unit's last tile
-      parts.open[blockIdx.x] =
-          AttnOpen{q.q0 + t0, nt, vh, sched_owner(e, run.W, run.G)};
-    }
-    x += stop - tile;
-    tile = 0;
-    if (++vh == sc.nvh) {
-      vh = 0;
-      ++i;
+      const int64_t e = x + sc.fixed + ntile - 1;  // the unit's last tile
+      parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_owner(e, run.W, run.G)};
     }
   }
 }
@@ -341,7 +338,8 @@ AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim
   p.U = p.rows / p.gsub;
   const int nc = simt_nc(head_dim);
   p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
-  p.min_tiles = 2;
+  p.fixed = 1;
+  p.min_run = 2;
   p.workers = sm_count() * 2;
   return p;
 }

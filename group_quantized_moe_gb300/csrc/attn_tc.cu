@@ -90,6 +90,21 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
+// Zeroes the non-finite bf16 values of eight; whether there were any.
+__device__ __forceinline__ bool drop_nonfinite(uint4 &t) {
+  uint32_t w[4] = {t.x, t.y, t.z, t.w};
+  uint32_t hit = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t m = (nonfinite_bf16(w[k]) ? 0xFFFFu : 0u) |
+                       (nonfinite_bf16(w[k] >> 16) ? 0xFFFF0000u : 0u);
+    w[k] &= ~m;
+    hit |= m;
+  }
+  t = make_uint4(w[0], w[1], w[2], w[3]);
+  return hit != 0;
+}
+
 // Value tiles are [key][column] in shared memory, columns contiguous: for the
 // product P V the operand's N axis (columns) is the contiguous one.  128B
 // swizzle: 64-column chunks kChunk apart, groups of eight keys 1024 bytes apart.
@@ -115,40 +130,49 @@ struct Unit {
   bool pair;
   int ntile_a;             // tiles that query tile A reaches
   int end, all;            // keys the last / first token sees
-  int64_t x;               // global tile index of `tile`
+  int64_t x;               // cost before the unit
 };
 
+// The unit at cost u.x (or the next one of the run that has tiles here).
 __device__ __forceinline__ bool unit_set(const TcAttn &p, const AttnRun &run, Unit &u) {
-  if (u.x >= run.last) return false;
-  u.q = sched_req(p.sc, u.r);
-  while (u.i >= sched_blocks(p.sc, u.q)) {
-    u.i = 0;
-    u.q = sched_req(p.sc, ++u.r);
+  while (u.x < run.last) {
+    u.q = sched_req(p.sc, u.r);
+    while (u.i >= sched_blocks(p.sc, u.q)) {
+      if (++u.r >= p.sc.R) return false;  // lengths that changed during the call
+      u.i = 0;
+      u.q = sched_req(p.sc, u.r);
+    }
+    u.ntile = sched_tiles(p.sc, u.q, u.i);
+    sched_part(p.sc, run, u.x, u.ntile, u.tile, u.stop);
+    if (u.tile < u.stop) {
+      u.t0 = u.i * p.sc.U;
+      u.nt = min(p.sc.U, u.q.n - u.t0);
+      u.pair = u.nt > p.tpt;
+      u.end = u.q.L - u.q.n + u.t0 + u.nt;
+      u.all = u.q.L - u.q.n + u.t0 + 1;
+      const int end_a = u.q.L - u.q.n + u.t0 + min(u.nt, p.tpt);
+      u.ntile_a = end_a > kKT ? (end_a + kKT - 1) / kKT : 1;
+      return true;
+    }
+    u.x += p.sc.fixed + u.ntile;
+    if (++u.vh == p.sc.nvh) {
+      u.vh = 0;
+      ++u.i;
+    }
   }
-  u.ntile = sched_tiles(p.sc, u.q, u.i);
-  u.stop = static_cast<int>(min64(u.ntile, u.tile + (run.last - u.x)));
-  u.t0 = u.i * p.sc.U;
-  u.nt = min(p.sc.U, u.q.n - u.t0);
-  u.pair = u.nt > p.tpt;
-  u.end = u.q.L - u.q.n + u.t0 + u.nt;
-  u.all = u.q.L - u.q.n + u.t0 + 1;
-  const int end_a = u.q.L - u.q.n + u.t0 + min(u.nt, p.tpt);
-  u.ntile_a = end_a > kKT ? (end_a + kKT - 1) / kKT : 1;
-  return true;
+  return false;
 }
 
 __device__ __forceinline__ bool unit_first(const TcAttn &p, const AttnRun &run, Unit &u) {
-  u.x = run.first;
+  u.x = run.unit;
   u.r = run.r;
   u.i = run.i;
   u.vh = run.h;
-  u.tile = run.tile;
   return unit_set(p, run, u);
 }
 
 __device__ __forceinline__ bool unit_next(const TcAttn &p, const AttnRun &run, Unit &u) {
-  u.x += u.stop - u.tile;
-  u.tile = 0;
+  u.x += p.sc.fixed + u.ntile;
   if (++u.vh == p.sc.nvh) {
     u.vh = 0;
     ++u.i;
@@ -187,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *bad_seen = reinterpret_cast<volatile int *>(gbase + C::misc_off + 8);
   volatile int *marked = reinterpret_cast<volatile int *>(gbase + C::misc_off + 16);  // [16]
   float *xm = reinterpret_cast<float *>(gbase + C::misc_off + 80), *xl = xm + 128;
-  __shared__ int64_t scratch[kThreads / 32 + 8];
+  __shared__ int64_t scratch[kThreads / 32 + 4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -307,34 +331,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const int k0 = kt * kKT;
             if (kv && k0 + kKT > u.all) {
-              const int lo = max(0, u.all - k0), hi = max(0, min(kKT, u.end - k0));
-              uint8_t *v = gbase + C::kv_off + s * C::tile;
+              const int lo = max(0, u.all - k0), hi = max(lo, min(kKT, u.end - k0));
+              uint8_t *v = gbase + C::kv_off + s * C::tile + (lane & 7) * 16;
               bool found = false;
-              for (int e = lane; e < nch * (kKT - lo) * 8; e += 32) {
-                const int row = lo + (e >> 3) % (kKT - lo), c = (e >> 3) / (kKT - lo);
-                uint4 *d = reinterpret_cast<uint4 *>(v + c * kChunk + row * 128 + (e & 7) * 16);
-                if (row >= hi) {
-                  *d = make_uint4(0u, 0u, 0u, 0u);
-                  continue;
-                }
-                uint4 t = *d;
-                uint32_t w[4] = {t.x, t.y, t.z, t.w};
-                bool hit = false;
-  #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (nonfinite_bf16(w[k])) {
-                    w[k] &= 0xFFFF0000u;
-                    hit = true;
-                  }
-                  if (nonfinite_bf16(w[k] >> 16)) {
-                    w[k] &= 0xFFFFu;
-                    hit = true;
+              // eight lanes a row of a chunk, four rows a step, four steps at once
+              for (int c = 0; c < nch; ++c) {
+                uint8_t *vc = v + c * kChunk;
+                for (int r0 = lo + (lane >> 3); r0 < hi; r0 += 16) {
+                  uint4 t[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    t[k] = r0 + 4 * k < hi ? *reinterpret_cast<const uint4 *>(vc + (r0 + 4 * k) * 128)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if (drop_nonfinite(t[k])) {
+                      *reinterpret_cast<uint4 *>(vc + (r0 + 4 * k) * 128) = t[k];
+                      found = true;
+                    }
                   }
                 }
-                if (hit) {
-                  *d = make_uint4(w[0], w[1], w[2], w[3]);
-                  found = true;
-                }
+                for (int r = hi + (lane >> 3); r < kKT; r += 4)
+                  *reinterpret_cast<uint4 *>(vc + r * 128) = make_uint4(0u, 0u, 0u, 0u);
               }
               if (found) marked[unit & 15] = unit + 1;
               fence_proxy_async_smem();
@@ -659,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (threadIdx.x == 0 && u.tile == 0 && u.stop < u.ntile)
         p.parts.open[blockIdx.x] = AttnOpen{u.q.q0 + u.t0, u.nt, u.vh,
-                                            sched_owner(u.x + u.ntile - 1, run.W, run.G)};
+                                            sched_owner(u.x + p.sc.fixed + u.ntile - 1, run.W, run.G)};
     }
   }
   tc_fence_before();
@@ -729,7 +747,8 @@ AttnPlan attn_tc_plan(int n_head, int n_kv) {
   p.nsub = (grp + p.gsub - 1) / p.gsub;
   p.U = 2 * (128 / p.gsub);
   p.KT = kKT;
-  p.min_tiles = 2;
+  p.fixed = 2;
+  p.min_run = 2;
   p.workers = sm_count();
   return p;
 }
