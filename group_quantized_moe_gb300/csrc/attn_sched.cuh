@@ -3,15 +3,20 @@
 // A call has R requests; request r has n new tokens (query rows) and L cache
 // rows, and token t of it sees the keys 0 .. L - n + t.  A unit of work is
 // (request, block of U consecutive tokens, key/value head); its cost is the
-// number of KT-key tiles its last token reaches (at least one, so that a
-// token that sees no key still gets its row of zeros), and `fixed` tiles more
-// for what a unit costs besides its tiles (loading its queries, writing its
-// results).  The units are laid end to end in the order (request, token
-// block, head) and the cost W of the whole call is cut into G equal runs, one
-// per worker: every worker gets the same work whatever the lengths are, and a
-// long context is split over as many workers as its share of the work asks
-// for.  A unit that a cut divides leaves one partial result per worker,
-// merged afterwards in worker order, so results are reproducible bit for bit.
+// number of keys its last token sees, and `fixed` keys more for what a unit
+// costs besides them (loading its queries, writing its results).  The units
+// are laid end to end in the order (request, token block, head) and the cost
+// W of the whole call is cut into G equal runs, one per worker: every worker
+// gets the same work whatever the lengths are, and a long context is split
+// over as many workers as its share of the work asks for.  A tile of KT keys
+// belongs to the run that holds its first key.  A unit that a cut divides
+// leaves one partial result per worker, merged afterwards in worker order,
+// so results are reproducible bit for bit.
+//
+// Costs are counted in keys, not in tiles, because the cost of a request's
+// token blocks then grows by U from block to block and a prefix of them is
+// a quadratic; with tiles it is a sum of rounded quotients, whose closed form
+// (Euclid's steps) took a thread 12 us on a call of nine prompts.
 //
 // Everything here is computed on the device from the lengths (a call can be
 // captured in a graph and replayed with other lengths in the same buffers).
@@ -27,9 +32,10 @@ struct AttnSched {
   int R;
   int nvh;             // key/value heads (times the splits of a large query group)
   int U;               // tokens per unit
-  int KT;              // keys per tile
-  int fixed;           // cost of a unit besides its tiles
-  int min_run;         // a worker's run costs at least this much
+  int kt_shift;        // log2 of the keys per tile
+  int fixed;           // cost of a unit besides its keys
+  int min_run;         // a worker's run costs at least this much (one tile or more, so
+                       // that no run inside a unit is without a tile of it)
   int64_t T;           // query rows in the buffers
   int64_t cap;         // largest cache length the block table can hold
 };
@@ -61,28 +67,6 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
   return a / b;
 }
 
-// sum_{i < n} floor((a i + b) / m) for n, a, b >= 0, m > 0: the whole parts of
-// a / m and b / m are taken out, and what is left counts the lattice points
-// under a line, which is the same sum with the axes exchanged (the steps of
-// Euclid's algorithm on a and m).
-__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t total = 0;
-  while (n > 0) {
-    const int64_t qa = div_pos(a, m), qb = div_pos(b, m);
-    total += n * (n - 1) / 2 * qa + n * qb;
-    a -= qa * m;
-    b -= qb * m;
-    const int64_t y = a * n + b;
-    n = div_pos(y, m);
-    b = y - n * m;
-    const int64_t t = m;
-    m = a;
-    a = t;
-    if (m == 0) break;
-  }
-  return total;
-}
-
 __device__ __forceinline__ int sched_blocks(const AttnSched &s, const AttnReq &q) {
   return (q.n + s.U - 1) / s.U;
 }
@@ -94,28 +78,24 @@ __device__ __forceinline__ int sched_end(const AttnSched &s, const AttnReq &q, i
 }
 
 __device__ __forceinline__ int sched_tiles(const AttnSched &s, const AttnReq &q, int i) {
-  const int e = sched_end(s, q, i);
-  return e > s.KT ? (e + s.KT - 1) / s.KT : 1;
+  const int e = sched_end(s, q, i), kt = 1 << s.kt_shift;
+  return e > kt ? (e + kt - 1) >> s.kt_shift : 1;
 }
 
-// Cost of one head's units in the token blocks before block i.
-__device__ inline int64_t sched_before(const AttnSched &s, const AttnReq &q, int i) {
-  // block j < i is full: its last token sees c + (j + 1) U keys, c = L - n
-  const int64_t c = static_cast<int64_t>(q.L) - q.n;
-  int64_t j0 = 0;  // blocks whose last token sees no key: one tile each
-  if (c < 0) {
-    j0 = div_pos(-c, s.U);
-    if (j0 > i) j0 = i;
-  }
-  return j0 + floor_sum(i - j0, s.KT, s.U, c + (j0 + 1) * s.U + s.KT - 1) +
-         static_cast<int64_t>(i) * s.fixed;
+// Cost of one unit of block i, and of one head's units in the blocks before
+// it (all of them full).  Rows that see no key (L < n) cost as if L = n.
+__device__ __forceinline__ int64_t sched_unit(const AttnSched &s, const AttnReq &q, int i) {
+  return static_cast<int64_t>(max(q.L - q.n, 0)) + min(q.n, (i + 1) * s.U) + s.fixed;
+}
+
+__device__ __forceinline__ int64_t sched_before(const AttnSched &s, const AttnReq &q, int i) {
+  const int64_t n = i;
+  return n * (static_cast<int64_t>(max(q.L - q.n, 0)) + s.fixed) + n * (n + 1) / 2 * s.U;
 }
 
 __device__ __forceinline__ int64_t sched_cost(const AttnSched &s, const AttnReq &q) {
   const int m = sched_blocks(s, q);
-  if (m == 0) return 0;
-  const int64_t before = m > 1 ? sched_before(s, q, m - 1) : 0;
-  return (before + sched_tiles(s, q, m - 1) + s.fixed) * s.nvh;
+  return m == 0 ? 0 : (sched_before(s, q, m - 1) + sched_unit(s, q, m - 1)) * s.nvh;
 }
 
 // One worker's run [first, last) of the call's cost W, cut into G runs, and
@@ -184,8 +164,8 @@ __device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *sc
       if (lo + sched_before(s, q, mid) * s.nvh <= run.first) a = mid;
       else b = mid;
     }
-    if (a > 0) lo += sched_before(s, q, a) * s.nvh;
-    const int cost = sched_tiles(s, q, a) + s.fixed;
+    lo += sched_before(s, q, a) * s.nvh;
+    const int64_t cost = sched_unit(s, q, a);
     const int64_t h = div_pos(run.first - lo, cost);
     found[0] = r;
     found[1] = a;
@@ -201,13 +181,21 @@ __device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *sc
   return run;
 }
 
-// The tiles [tile, stop) of a unit of ntile tiles that begins at cost x which
-// a run holds (a cut inside the fixed cost leaves all tiles to the later run).
+// The tiles [tile, stop) of a unit of ntile tiles at cost x whose first keys
+// the run holds (a cut inside the fixed cost leaves all tiles to the later run).
 __device__ __forceinline__ void sched_part(const AttnSched &s, const AttnRun &run, int64_t x,
                                            int ntile, int &tile, int &stop) {
+  const int64_t up = (1 << s.kt_shift) - 1;
   const int64_t a = run.first - x - s.fixed, b = run.last - x - s.fixed;
-  tile = a <= 0 ? 0 : static_cast<int>(a);
-  stop = b <= 0 ? 0 : (b < ntile ? static_cast<int>(b) : ntile);
+  tile = a <= 0 ? 0 : static_cast<int>((a + up) >> s.kt_shift);
+  stop = b <= 0 ? 0 : static_cast<int>((b + up) >> s.kt_shift);
+  if (stop > ntile) stop = ntile;
+}
+
+// The worker that has a unit's last tile.
+__device__ __forceinline__ int sched_last(const AttnSched &s, const AttnRun &run, int64_t x,
+                                          int ntile) {
+  return sched_owner(x + s.fixed + (static_cast<int64_t>(ntile - 1) << s.kt_shift), run.W, run.G);
 }
 
 // What a worker leaves for the merge: the unit that is still open when its

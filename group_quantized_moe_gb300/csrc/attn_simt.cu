@@ -62,14 +62,15 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
   int64_t x = run.unit;
   int r = run.r, i = run.i, vh = run.h;
   AttnReq q;
-  for (int ntile = 0; x < run.last; x += sc.fixed + ntile, vh = vh + 1 == sc.nvh ? 0 : vh + 1, i += vh == 0) {
+  for (int64_t next = 0; x < run.last; x = next, vh = vh + 1 == sc.nvh ? 0 : vh + 1, i += vh == 0) {
     q = sched_req(sc, r);
     while (i >= sched_blocks(sc, q)) {
       if (++r >= sc.R) return;  // lengths that changed during the call
       i = 0;
       q = sched_req(sc, r);
     }
-    ntile = sched_tiles(sc, q, i);
+    const int ntile = sched_tiles(sc, q, i);
+    next = x + sched_unit(sc, q, i);
     int tile, stop;
     sched_part(sc, run, x, ntile, tile, stop);
     if (tile >= stop) continue;
@@ -248,8 +249,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
       }
     }
     if (tid == 0 && tile == 0 && !whole) {
-      const int64_t e = x + sc.fixed + ntile - 1;  // the unit's last tile
-      parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_owner(e, run.W, run.G)};
+      parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, ntile)};
     }
   }
 }
@@ -338,8 +338,8 @@ AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim
   p.U = p.rows / p.gsub;
   const int nc = simt_nc(head_dim);
   p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
-  p.fixed = 1;
-  p.min_run = 2;
+  p.fixed = p.KT;
+  p.min_run = 2 * p.KT;
   p.workers = sm_count() * 2;
   return p;
 }

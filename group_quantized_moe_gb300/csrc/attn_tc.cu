@@ -28,7 +28,8 @@
 //             the unit's last key become zeros (0 * NaN would reach the sums),
 //             non-finite values are taken out and the unit marked, so that
 //             its epilogue adds them to the rows that do see them
-//   warp 11   TMA producer of the query tiles
+//   warp 11   walks the run and hands its units to the other roles through a
+//             ring in shared memory; TMA producer of the query tiles
 // Every wait is bounded; on a timeout the CTA raises QMM_DEV_WAIT_TIMEOUT,
 // all roles leave their loops, wait (bounded) for what they have in flight,
 // and the tensor memory is freed.
@@ -48,6 +49,7 @@ constexpr int kThreads = 384;
 constexpr int kKT = 128;              // keys per tile
 constexpr int kWarpKv = 8, kWarpMma = 9, kWarpClean = 10, kWarpQ = 11;
 constexpr uint32_t kChunk = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
+constexpr int kUnits = 4;             // units in the ring between warp 11 and the others
 constexpr float kRescale = 8.0f;      // log2 of the growth of the maximum that is let pass
 
 template <int NCH>  // 64-column chunks of the head size
@@ -55,11 +57,12 @@ struct Tc {
   static constexpr uint32_t tile = NCH * kChunk;            // one Q, K or V tile
   static constexpr int stages = NCH == 1 ? 10 : 5;          // K and V tiles in turn
   static constexpr uint32_t q_off = 0, kv_off = 2 * tile, bar_off = kv_off + stages * tile;
-  // q_full, q_free, x_full, drain, s_full[2], p_full[2], o_full[2], then
-  // full[stages], free[stages], clean[stages]
-  static constexpr int nbar = 10 + 3 * stages;
-  static constexpr uint32_t misc_off = bar_off + nbar * 8;
-  static constexpr uint32_t bytes = misc_off + 16 + 64 + 2 * 128 * 4 + 1024;
+  // q_full, q_free, x_full, drain, s_full[2], p_full[2], o_full[2],
+  // u_full[kUnits], u_free[kUnits], then full, freed, clean [stages]
+  static constexpr int nbar = 10 + 2 * kUnits + 3 * stages;
+  static constexpr uint32_t unit_off = (bar_off + nbar * 8 + 15) & ~15u;
+  static constexpr uint32_t misc_off = unit_off + kUnits * 64;  // tmem, abort, bad, -, marked[16]
+  static constexpr uint32_t bytes = misc_off + 80 + 2 * 128 * 4 + 1024;
   static constexpr uint32_t o_col = 256, o_step = NCH * 64;  // tensor memory columns of O
 };
 
@@ -69,6 +72,7 @@ struct TcAttn {
   AttnParts parts;
   int gsub, nsub, tpt;  // query heads and tokens of a tile
   int box_rows;         // rows per key box
+  int block_shift;      // log2 of the cache's block size
   float sl2;            // scale log2(e)
   uint32_t *status;
 };
@@ -81,6 +85,11 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -121,64 +130,13 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n, bool values) {
          (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
-// A unit of this worker's run, walked by every role on its own.
-struct Unit {
-  AttnReq q;
-  int r, i, vh;            // request, token block, (virtual) head
-  int tile, stop, ntile;   // this worker's tiles [tile, stop) of ntile
-  int t0, nt;              // first token of the block, tokens
-  bool pair;
-  int ntile_a;             // tiles that query tile A reaches
-  int end, all;            // keys the last / first token sees
-  int64_t x;               // cost before the unit
+// One unit of this worker's run, as the roles see it.
+struct __align__(16) Unit {
+  int valid, pair, q_row, nt;      // 0: no unit any more; first query row, tokens
+  int h, head0, g, r;              // key/value head, first query head, heads, request
+  int tile, stop, ntile, ntile_a;  // this worker's tiles [tile, stop); tiles that query tile A reaches
+  int all, end, k_row, pad;        // keys the first / last token sees; first key row (packed keys)
 };
-
-// The unit at cost u.x (or the next one of the run that has tiles here).
-__device__ __forceinline__ bool unit_set(const TcAttn &p, const AttnRun &run, Unit &u) {
-  while (u.x < run.last) {
-    u.q = sched_req(p.sc, u.r);
-    while (u.i >= sched_blocks(p.sc, u.q)) {
-      if (++u.r >= p.sc.R) return false;  // lengths that changed during the call
-      u.i = 0;
-      u.q = sched_req(p.sc, u.r);
-    }
-    u.ntile = sched_tiles(p.sc, u.q, u.i);
-    sched_part(p.sc, run, u.x, u.ntile, u.tile, u.stop);
-    if (u.tile < u.stop) {
-      u.t0 = u.i * p.sc.U;
-      u.nt = min(p.sc.U, u.q.n - u.t0);
-      u.pair = u.nt > p.tpt;
-      u.end = u.q.L - u.q.n + u.t0 + u.nt;
-      u.all = u.q.L - u.q.n + u.t0 + 1;
-      const int end_a = u.q.L - u.q.n + u.t0 + min(u.nt, p.tpt);
-      u.ntile_a = end_a > kKT ? (end_a + kKT - 1) / kKT : 1;
-      return true;
-    }
-    u.x += p.sc.fixed + u.ntile;
-    if (++u.vh == p.sc.nvh) {
-      u.vh = 0;
-      ++u.i;
-    }
-  }
-  return false;
-}
-
-__device__ __forceinline__ bool unit_first(const TcAttn &p, const AttnRun &run, Unit &u) {
-  u.x = run.unit;
-  u.r = run.r;
-  u.i = run.i;
-  u.vh = run.h;
-  return unit_set(p, run, u);
-}
-
-__device__ __forceinline__ bool unit_next(const TcAttn &p, const AttnRun &run, Unit &u) {
-  u.x += p.sc.fixed + u.ntile;
-  if (++u.vh == p.sc.nvh) {
-    u.vh = 0;
-    ++u.i;
-  }
-  return unit_set(p, run, u);
-}
 
 // The key tiles first, first + step, ... < last of warpgroup w.
 __device__ __forceinline__ void wg_tiles(const Unit &u, int w, int &first, int &last, int &step) {
@@ -187,11 +145,42 @@ __device__ __forceinline__ void wg_tiles(const Unit &u, int w, int &first, int &
   step = u.pair ? 1 : 2;
 }
 
+// Adds the non-finite values that warp 10 took out of the unit's value tiles
+// to a row that sees their keys (p v of a non-finite v is v, whatever p > 0).
+template <bool PAGED>
+__device__ __noinline__ void add_marked(const TcAttn &p, const Unit &u, int vis, void *out, bool bf16) {
+  const int hd = p.a.head_dim;
+  const int last = min(min(vis, u.end), u.stop * kKT);
+#pragma unroll 1
+  for (int j = max(u.tile * kKT, max(u.all, 0)); j < last; ++j) {
+    const uint16_t *src = static_cast<const uint16_t *>(p.a.v);
+    if (PAGED) {
+      const int32_t id = p.a.block_table[u.r * p.a.table_stride + j / p.a.block_size];
+      if (id < 0 || id >= p.a.num_blocks) continue;
+      src += id * p.a.block_stride +
+             static_cast<int64_t>(u.h * p.a.block_size + (j & (p.a.block_size - 1))) * hd;
+    } else {
+      src += (static_cast<int64_t>(u.k_row) + j) * p.a.v_stride + static_cast<int64_t>(u.h) * hd;
+    }
+#pragma unroll 1
+    for (int d = 0; d < hd; ++d) {
+      if (!nonfinite_bf16(src[d])) continue;
+      const float v = __uint_as_float(static_cast<uint32_t>(src[d]) << 16);
+      if (bf16) {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(out) + d;
+        *y = __float2bfloat16_rn(__bfloat162float(*y) + v);
+      } else {
+        static_cast<float *>(out)[d] += v;
+      }
+    }
+  }
+}
+
 template <int NCH, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const TcAttn p) {
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcAttn p) {
   using C = Tc<NCH>;
   constexpr int NS = C::stages;
   extern __shared__ uint8_t smem_raw[];
@@ -203,9 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_full = [&](int w) { return bars + 32 + 8 * w; };
   auto p_full = [&](int w) { return bars + 48 + 8 * w; };
   auto o_full = [&](int w) { return bars + 64 + 8 * w; };
-  auto full = [&](int s) { return bars + 80 + 8 * s; };
-  auto freed = [&](int s) { return bars + 80 + 8 * (NS + s); };
-  auto clean = [&](int s) { return bars + 80 + 8 * (2 * NS + s); };
+  auto u_full = [&](uint32_t n) { return bars + 80 + 8 * (n % kUnits); };
+  auto u_free = [&](uint32_t n) { return bars + 80 + 8 * (kUnits + n % kUnits); };
+  constexpr int kStageBars = 80 + 16 * kUnits;
+  auto full = [&](int s) { return bars + kStageBars + 8 * s; };
+  auto freed = [&](int s) { return bars + kStageBars + 8 * (NS + s); };
+  auto clean = [&](int s) { return bars + kStageBars + 8 * (2 * NS + s); };
+  Unit *units = reinterpret_cast<Unit *>(gbase + C::unit_off);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + C::misc_off);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + C::misc_off + 4);
   volatile int *bad_seen = reinterpret_cast<volatile int *>(gbase + C::misc_off + 8);
@@ -223,6 +216,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full(w), 1);
       mbar_init(p_full(w), 4);
       mbar_init(o_full(w), 1);
+    }
+    for (int k = 0; k < kUnits; ++k) {
+      mbar_init(u_full(k), 1);
+      mbar_init(u_free(k), 11);  // warps 0-7, 8, 9, 10
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
@@ -243,118 +240,194 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int hd = p.a.head_dim, grp = p.a.n_head / p.a.n_kv;
-  const int nch = (hd + 63) / 64;  // chunks that hold columns
-  Unit u;
+  const int hd = p.a.head_dim;
+  const int nch = NCH == 1 ? 1 : (hd + 63) / 64;  // chunks that hold columns
+  // the whole warp, or (`one`) this thread alone, waits for a barrier
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, wait_ok(bar, parity, p.status, abort_flag)) != 0;
+  };
 
   // 384 threads launched with 168 registers: 2 x 208 + 88 = 3 x 168
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == kWarpKv) {
-      // ------------------------------------------------ key and value tiles
-      uint32_t n = 0;  // tiles loaded so far; stage n % NS
-      bool ok = true;
-      for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u)) {
-        const int h = u.vh / p.nsub;
-        const int32_t *table = PAGED ? p.a.block_table + u.r * p.a.table_stride : nullptr;
-        // box `lane` of a tile: block lane / nch, columns of chunk lane % nch
-        const int c = lane % nch, b = lane / nch, row0 = b * p.box_rows;
-        auto block_of = [&](int kt) {
-          const int k0 = kt * kKT + row0;
-          if (!PAGED || row0 >= kKT || k0 >= u.end) return 0;
-          return table[k0 / p.a.block_size];
-        };
-        int id = block_of(u.tile);
-        for (int kt = u.tile; kt < u.stop && ok; ++kt) {
-          const int k0 = kt * kKT;
-          const int keys = max(0, min(kKT, u.end - k0));
-          const int boxes = PAGED ? (keys + p.box_rows - 1) / p.box_rows : 1;
-          const int mine = id;
-          if (kt + 1 < u.stop) id = block_of(kt + 1);
-          const bool issue = b < boxes;
-          const bool bad = PAGED && issue && (mine < 0 || mine >= p.a.num_blocks);
-          if (bad) {
-            *bad_seen = 1;
-            atomicOr(p.status, kDevBadBlock);
+    if (warp == kWarpQ) {
+      // ------------------------------------------- units, and query tiles
+      const int grp = p.a.n_head / p.a.n_kv;
+      int64_t x = run.unit;
+      int r = run.r, i = run.i, vh = run.h;
+      AttnReq q{};
+      bool fresh = true;
+      // the next unit of the run with tiles of it, into ring slot n
+      auto publish = [&](uint32_t n) {
+        Unit u{};
+        while (x < run.last) {
+          if (fresh) q = sched_req(p.sc, r);
+          fresh = false;
+          if (i >= sched_blocks(p.sc, q)) {
+            if (++r >= p.sc.R) break;  // lengths that changed during the call
+            i = 0;
+            fresh = true;
+            continue;
           }
-          __syncwarp();
-          for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
-            const int s = n % NS;
-            ok = __all_sync(0xFFFFFFFFu,
-                            wait_ok(freed(s), ((n / NS) & 1u) ^ 1u, p.status, abort_flag));
-            if (!ok) break;
-            if (lane == 0)
-              mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(boxes * p.box_rows * 128 * nch));
-            __syncwarp();
-            if (issue) {
-              const uint32_t dst = base + C::kv_off + s * C::tile + c * kChunk + row0 * 128;
-              const CUtensorMap *tm = kv ? &tm_v : &tm_k;
-              if (PAGED)  // a bad index: block num_blocks, outside the map, reads as zeros
-                tma_load_4d(dst, tm, c * 64, (k0 + row0) & (p.a.block_size - 1), h,
-                            bad ? static_cast<int>(p.a.num_blocks) : mine, full(s));
-              else
-                tma_load_3d(dst, tm, c * 64, h, u.q.q0 + k0, full(s));
-            }
+          u.ntile = sched_tiles(p.sc, q, i);
+          sched_part(p.sc, run, x, u.ntile, u.tile, u.stop);
+          if (u.tile < u.stop) {
+            const int t0 = i * p.sc.U, ctx = q.L - q.n;
+            u.valid = 1;
+            u.nt = min(p.sc.U, q.n - t0);
+            u.pair = u.nt > p.tpt;
+            u.q_row = q.q0 + t0;
+            u.h = vh / p.nsub;
+            const int sub = vh - u.h * p.nsub;
+            u.head0 = u.h * grp + sub * p.gsub;
+            u.g = min(p.gsub, grp - sub * p.gsub);
+            u.r = r;
+            const int end_a = ctx + t0 + min(u.nt, p.tpt);
+            u.ntile_a = end_a > kKT ? (end_a + kKT - 1) / kKT : 1;
+            u.all = ctx + t0 + 1;
+            u.end = ctx + t0 + u.nt;
+            u.k_row = q.q0;
+            if (lane == 0 && u.tile == 0 && u.stop < u.ntile)
+              p.parts.open[blockIdx.x] =
+                  AttnOpen{u.q_row, u.nt, vh, sched_last(p.sc, run, x, u.ntile)};
           }
+          x += sched_unit(p.sc, q, i);
+          if (++vh == p.sc.nvh) {
+            vh = 0;
+            ++i;
+          }
+          if (u.valid) break;
         }
-      }
-      // copies still landing (after an abort; otherwise all have been consumed)
-      const uint32_t from = n > NS ? n - NS : 0;
-      for (uint32_t k = from; k < n; ++k) mbar_wait_bounded(full(k % NS), (k / NS) & 1u, p.status);
-    } else if (warp == kWarpQ) {
-      // -------------------------------------------------------- query tiles
-      uint32_t n = 0;
-      for (bool go = unit_first(p, run, u); go; go = unit_next(p, run, u), ++n) {
-        if (!__all_sync(0xFFFFFFFFu, wait_ok(q_free, (n & 1u) ^ 1u, p.status, abort_flag))) break;
-        const int h = u.vh / p.nsub, sub = u.vh - h * p.nsub;
+        if (lane == 0) {
+          units[n % kUnits] = u;
+          mbar_arrive(u_full(n));
+        }
+        __syncwarp();
+        return u.valid != 0;
+      };
+      uint32_t pub = 0, n = 0;  // units handed out, query tiles loaded
+      bool more = true, ok = true;
+      while (ok) {
+        for (; ok && more && pub < n + 3; ++pub) {
+          ok = wait_warp(u_free(pub), ((pub / kUnits) & 1u) ^ 1u);
+          if (ok) more = publish(pub);
+        }
+        if (!ok || (!more && n + 1 == pub)) break;
+        if (!wait_warp(q_free, (n & 1u) ^ 1u)) break;
+        const Unit &u = units[n % kUnits];
         const int tiles = u.pair ? 2 : 1;
         if (lane == 0)
           mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * nch * p.tpt * p.gsub * 128));
         __syncwarp();
         if (lane < tiles * nch) {
           const int c = lane % nch, w = lane / nch;
-          tma_load_3d(base + C::q_off + w * C::tile + c * kChunk, &tm_q, c * 64,
-                      h * grp + sub * p.gsub, u.q.q0 + u.t0 + w * p.tpt, q_full);
+          tma_load_3d(base + C::q_off + w * C::tile + c * kChunk, &tm_q, c * 64, u.head0,
+                      u.q_row + w * p.tpt, q_full);
         }
+        ++n;
       }
       if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1u, p.status);
-    } else if (warp == kWarpClean) {
-      // --------------------------- value tiles with keys that some row misses
-      uint32_t n = 0;
-      int unit = 0;
+    } else if (warp == kWarpKv) {
+      // ------------------------------------------------ key and value tiles
+      uint32_t n = 0;  // tiles loaded so far; stage n % NS
+      int s = 0;
+      uint32_t phase = 1;
       bool ok = true;
-      for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u), ++unit) {
+      // box `lane` of a tile: block lane / nch, columns of chunk lane % nch
+      const int c = lane % nch, row0 = lane / nch * p.box_rows;
+      for (uint32_t un = 0; ok; ++un) {
+        if (!wait_warp(u_full(un), (un / kUnits) & 1u)) break;
+        const Unit u = units[un % kUnits];
+        if (!u.valid) break;
+        const int32_t *table = PAGED ? p.a.block_table + u.r * p.a.table_stride : nullptr;
+        auto block_of = [&](int kt) {
+          const int k0 = kt * kKT + row0;
+          if (!PAGED || row0 >= kKT || k0 >= u.end) return 0;
+          return table[k0 >> p.block_shift];
+        };
+        int id = block_of(u.tile);
         for (int kt = u.tile; kt < u.stop && ok; ++kt) {
-          for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
-            const int s = n % NS;
-            ok = __all_sync(0xFFFFFFFFu, wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag));
+          const int k0 = kt * kKT;
+          const int keys = max(0, min(kKT, u.end - k0));
+          const int rows = PAGED ? (keys + p.box_rows - 1) & ~(p.box_rows - 1) : kKT;
+          const int mine = id;
+          if (kt + 1 < u.stop) id = block_of(kt + 1);
+          const bool issue = row0 < rows;
+          const bool bad = PAGED && issue && (mine < 0 || mine >= p.a.num_blocks);
+          if (bad) {
+            *bad_seen = 1;
+            atomicOr(p.status, kDevBadBlock);
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = wait_warp(freed(s), phase);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(rows * 128 * nch));
+            __syncwarp();
+            if (issue) {
+              const uint32_t dst = base + C::kv_off + s * C::tile + c * kChunk + row0 * 128;
+              const CUtensorMap *tm = kv ? &tm_v : &tm_k;
+              if (PAGED)  // a bad index: block num_blocks, outside the map, reads as zeros
+                tma_load_4d(dst, tm, c * 64, (k0 + row0) & (p.a.block_size - 1), u.h,
+                            bad ? static_cast<int>(p.a.num_blocks) : mine, full(s));
+              else
+                tma_load_3d(dst, tm, c * 64, u.h, u.k_row + k0, full(s));
+            }
+            ++n;
+            if (++s == NS) {
+              s = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        if (lane == 0) mbar_arrive(u_free(un));
+      }
+      // copies still landing (after an abort; otherwise all have been consumed)
+      for (uint32_t k = n > NS ? n - NS : 0; k < n; ++k)
+        mbar_wait_bounded(full(k % NS), (k / NS) & 1u, p.status);
+    } else if (warp == kWarpClean) {
+      // ------------------------- value tiles with keys that some row misses
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (uint32_t un = 0; ok; ++un) {
+        if (!wait_warp(u_full(un), (un / kUnits) & 1u)) break;
+        const Unit &ur = units[un % kUnits];
+        if (!ur.valid) break;
+        const int tile = ur.tile, stop = ur.stop, all = ur.all, end = ur.end;
+        for (int kt = tile; kt < stop && ok; ++kt) {
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = wait_warp(full(s), phase);
             if (!ok) break;
             const int k0 = kt * kKT;
-            if (kv && k0 + kKT > u.all) {
-              const int lo = max(0, u.all - k0), hi = max(lo, min(kKT, u.end - k0));
+            if (kv && k0 + kKT > all) {
+              const int lo = max(0, all - k0), hi = max(lo, min(kKT, end - k0));
               uint8_t *v = gbase + C::kv_off + s * C::tile + (lane & 7) * 16;
               bool found = false;
               // eight lanes a row of a chunk, four rows a step, four steps at once
-              for (int c = 0; c < nch; ++c) {
-                uint8_t *vc = v + c * kChunk;
+#pragma unroll 1
+              for (int c = 0; c < nch; ++c, v += kChunk) {
+#pragma unroll 1
                 for (int r0 = lo + (lane >> 3); r0 < hi; r0 += 16) {
                   uint4 t[4];
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
-                    t[k] = r0 + 4 * k < hi ? *reinterpret_cast<const uint4 *>(vc + (r0 + 4 * k) * 128)
+                    t[k] = r0 + 4 * k < hi ? *reinterpret_cast<const uint4 *>(v + (r0 + 4 * k) * 128)
                                            : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
                     if (drop_nonfinite(t[k])) {
-                      *reinterpret_cast<uint4 *>(vc + (r0 + 4 * k) * 128) = t[k];
+                      *reinterpret_cast<uint4 *>(v + (r0 + 4 * k) * 128) = t[k];
                       found = true;
                     }
                   }
                 }
                 for (int r = hi + (lane >> 3); r < kKT; r += 4)
-                  *reinterpret_cast<uint4 *>(vc + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+                  *reinterpret_cast<uint4 *>(v + r * 128) = make_uint4(0u, 0u, 0u, 0u);
               }
-              if (found) marked[unit & 15] = unit + 1;
+              if (found) marked[un & 15u] = static_cast<int>(un + 1);
               fence_proxy_async_smem();
               __syncwarp();
             }
@@ -362,83 +435,103 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(clean(s));
               mbar_arrive(freed(s));
             }
+            if (++s == NS) {
+              s = 0;
+              phase ^= 1u;
+            }
           }
         }
+        if (lane == 0) mbar_arrive(u_free(un));
       }
-    } else {
+    } else if (lane == 0) {
       // ------------------------------------------------------------ MMA issue
-      if (lane == 0) {
-        const int ksteps = (hd + 15) / 16;
-        const uint32_t id_s = idesc_bf16(kKT, false), id_o = idesc_bf16(ksteps * 16, true);
-        uint32_t n0 = 0, nq = 0, np[2] = {0, 0};
-        bool ok = true;
-        for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u), ++nq) {
-          if (!(ok = wait_ok(q_full, nq & 1u, p.status, abort_flag))) break;
-          int first[2], last[2], step, cur[2];
-          wg_tiles(u, 0, first[0], last[0], step);
-          wg_tiles(u, 1, first[1], last[1], step);
-          // tile kt's keys are load n0 + 2 (kt - tile), its values the next one;
-          // warpgroup 1 is the last user of every tile of a pair
-          auto qk = [&](int w, int kt) {
-            const uint32_t n = n0 + 2 * (kt - u.tile);
+      const int ksteps = (hd + 15) / 16;
+      const uint32_t id_s = idesc_bf16(kKT, false), id_o = idesc_bf16(ksteps * 16, true);
+      const uint64_t kd0 = smem_desc_sw128(base + C::kv_off), vd0 = desc_values(base + C::kv_off);
+      const uint64_t qd0 = smem_desc_sw128(base + C::q_off);
+      uint32_t n0 = 0;                    // loads before the unit
+      uint32_t np = 0, np_other = 0;      // P tiles taken from this / the other warpgroup
+      bool ok = true;
+      for (uint32_t un = 0; ok; ++un) {
+        if (!wait_ok(u_full(un), (un / kUnits) & 1u, p.status, abort_flag)) break;
+        const Unit &u = units[un % kUnits];
+        if (!u.valid) break;
+        const int tile = u.tile, stop = u.stop;
+        const bool pair = u.pair != 0;
+        int cur, last, step, cur_other, last_other;
+        wg_tiles(u, 0, cur, last, step);
+        wg_tiles(u, 1, cur_other, last_other, step);
+        if (!(ok = wait_ok(q_full, un & 1u, p.status, abort_flag))) break;
+        // tile kt's keys are load n0 + 2 (kt - tile), its values the next one;
+        // warpgroup 1 is the last user of every tile of a pair
+        auto qk = [&](int w, int kt) {
+          const uint32_t n = n0 + 2 * (kt - tile);
+          const int s = n % NS;
+          if (!wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
+          const uint64_t kd = kd0 + s * (C::tile >> 4);
+#pragma unroll
+          for (int k = 0; k < NCH * 4; ++k) {
+            constexpr int kC = kChunk >> 4;
+            if (k < ksteps)
+              tc_mma_ss(tmem + w * 128, qd + (k / 4) * kC + (k % 4) * 2, kd + (k / 4) * kC + (k % 4) * 2,
+                        id_s, k > 0);
+          }
+          tc_commit(s_full(w));
+          if (!pair || w) tc_commit(freed(s));
+          return true;
+        };
+        if (cur < last) ok = qk(0, cur);
+        if (ok && cur_other < last_other) ok = qk(1, cur_other);
+        bool first = true, first_other = true;
+        int w = 0;  // the warpgroup whose state cur, last, np, first hold; it changes every turn
+        for (; ok && (cur < last || cur_other < last_other); w ^= 1) {
+          if (cur < last) {
+            const uint32_t n = n0 + 2 * (cur - tile) + 1;
             const int s = n % NS;
-            if (!wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag)) return false;
+            if (!(ok = wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag))) break;
+            if (!(ok = wait_ok(clean(s), (n / NS) & 1u, p.status, abort_flag))) break;
+            if (!(ok = wait_ok(p_full(w), np++ & 1u, p.status, abort_flag))) break;
             tc_fence_after();
-            const uint64_t qd = smem_desc_sw128(base + C::q_off + (u.pair ? w : 0) * C::tile);
-            const uint64_t kd = smem_desc_sw128(base + C::kv_off + s * C::tile);
-            for (int k = 0; k < ksteps; ++k) {
-              const uint64_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
-              tc_mma_ss(tmem + w * 128, qd + off, kd + off, id_s, k > 0);
-            }
-            tc_commit(s_full(w));
-            if (!u.pair || w == 1) tc_commit(freed(s));
-            return true;
-          };
-          auto pv = [&](int w, int kt) {
-            const uint32_t n = n0 + 2 * (kt - u.tile) + 1;
-            const int s = n % NS;
-            if (!wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag)) return false;
-            if (!wait_ok(clean(s), (n / NS) & 1u, p.status, abort_flag)) return false;
-            if (!wait_ok(p_full(w), np[w]++ & 1u, p.status, abort_flag)) return false;
-            tc_fence_after();
-            const uint64_t vd = desc_values(base + C::kv_off + s * C::tile);
+            const uint64_t vd = vd0 + s * (C::tile >> 4);
             const uint32_t o = tmem + C::o_col + w * C::o_step;
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < kKT / 16; ++k)
-              tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o,
-                        kt != first[w] || k > 0);
-            if (!u.pair || w == 1) tc_commit(freed(s));
-            return true;
-          };
-          for (int w = 0; w < 2 && ok; ++w) {
-            cur[w] = first[w];
-            if (cur[w] < last[w]) ok = qk(w, cur[w]);
+              tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
+            if (!pair || w) tc_commit(freed(s));
+            first = false;
+            cur += step;
+            if (cur < last)
+              ok = qk(w, cur);
+            else if (pair)
+              tc_commit(o_full(w));
           }
-          while (ok && (cur[0] < last[0] || cur[1] < last[1])) {
-            for (int w = 0; w < 2 && ok; ++w) {
-              if (cur[w] >= last[w]) continue;
-              ok = pv(w, cur[w]);
-              cur[w] += step;
-              if (!ok) break;
-              if (cur[w] < last[w])
-                ok = qk(w, cur[w]);
-              else if (u.pair)
-                tc_commit(o_full(w));
-            }
-          }
-          // single: both results at once, when nothing reads the query tile any
-          // more (its shared memory carries warpgroup 1's result to warpgroup 0)
-          if (ok && !u.pair) {
-            tc_commit(o_full(0));
-            if (first[1] < last[1]) tc_commit(o_full(1));
-          }
-          n0 += 2 * (u.stop - u.tile);
+          const int c = cur, l = last;
+          const uint32_t m = np;
+          const bool f = first;
+          cur = cur_other, last = last_other, np = np_other, first = first_other;
+          cur_other = c, last_other = l, np_other = m, first_other = f;
         }
-        tc_commit(drain);
-        mbar_wait_bounded(drain, 0u, p.status);
+        if (!ok) break;
+        if (w == 1) {
+          const uint32_t m = np;
+          np = np_other;
+          np_other = m;
+        }
+        // single: both results at once, when nothing reads the query tile any
+        // more (its shared memory carries warpgroup 1's result to warpgroup 0)
+        if (!pair) {
+          tc_commit(o_full(0));
+          if (stop - tile > 1) tc_commit(o_full(1));
+        }
+        n0 += 2 * (stop - tile);
+        mbar_arrive(u_free(un));
       }
-      __syncwarp();
+      tc_commit(drain);
+      mbar_wait_bounded(drain, 0u, p.status);
     }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------- warpgroups
@@ -446,55 +539,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp % 4)
     const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + C::o_col + w * C::o_step;
     const int ochunks = (hd + 31) / 32;
+    // rows of a tile are (token, head) with gsub heads a token, of which g count
+    const int tok = row / p.gsub, hq = row - tok * p.gsub;
     uint32_t nt = 0, no = 0, nx = 0;
-    int unit = 0;
     bool ok = true;
-    for (bool go = unit_first(p, run, u); go && ok; go = unit_next(p, run, u), ++unit) {
+    for (uint32_t un = 0; ok; ++un) {
+      if (!(ok = wait_warp(u_full(un), (un / kUnits) & 1u))) break;
+      const Unit &u = units[un % kUnits];
+      if (!u.valid) break;
       int first, last, step;
       wg_tiles(u, w, first, last, step);
-      const int h = u.vh / p.nsub, sub = u.vh - h * p.nsub;
-      const int g = min(p.gsub, grp - sub * p.gsub);
-      // rows of a tile are (token, head) with gsub heads a token, of which g count
-      const int tok = row / p.gsub, hq = row - tok * p.gsub;
-      const int tw = u.pair ? w * p.tpt : 0;  // first token of this warpgroup's query tile
-      const bool live = tok < min(p.tpt, u.nt - tw) && hq < g;
+      const bool pair = u.pair != 0;
+      const int tw = pair ? w * p.tpt : 0;    // first token of this warpgroup's query tile
+      const bool live = tok < min(p.tpt, u.nt - tw) && hq < u.g;
       const bool busy = __any_sync(0xFFFFFFFFu, live);
-      const int vis = u.all + tw + tok;       // keys this row sees
       const int all = u.all + tw;             // keys every row of the tile sees
+      const int vis = all + tok;              // keys this row sees
       float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
       for (int kt = first; kt < last; kt += step, ++nt) {
-        if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(s_full(w), nt & 1u, p.status, abort_flag)))) break;
+        if (!(ok = wait_warp(s_full(w), nt & 1u))) break;
         tc_fence_after();
-        if (u.pair && kt + step >= last) {  // the last read of this query tile is done
-          if (lane == 0) mbar_arrive(q_free);
-        }
+        // the last read of this query tile is done
+        if (pair && kt + step >= last && lane == 0) mbar_arrive(q_free);
         if (busy) {
           uint32_t s[128];
           tmem_ld128(ts, s);
           const int k0 = kt * kKT;
-          if (k0 + kKT > all) {
-            const int lim = vis - k0;
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (j >= lim) s[j] = 0xFF800000u;
-          }
-          if (PAGED && *bad_seen) {  // leave out the keys of blocks outside the cache
+          uint32_t gone = 0;  // 16-key pieces in blocks outside the cache
+          if (PAGED && *bad_seen) {
             const int j = k0 + lane * 16;
             bool bad = false;
             if (lane < 8 && j < u.end) {
-              const int32_t id = p.a.block_table[u.r * p.a.table_stride + j / p.a.block_size];
+              const int32_t id = p.a.block_table[u.r * p.a.table_stride + (j >> p.block_shift)];
               bad = id < 0 || id >= p.a.num_blocks;
             }
-            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, bad);
-#pragma unroll
-            for (int q = 0; q < 128; ++q)
-              if (bits >> (q / 16) & 1u) s[q] = 0xFF800000u;
+            gone = __ballot_sync(0xFFFFFFFFu, bad);
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (k0 + kKT > all || gone) {
+            const int lim = vis - k0;
 #pragma unroll
-          for (int j = 0; j < 128; j += 4)
+            for (int b = 0; b < 4; ++b) {
+              const int left = lim - 32 * b;
+              uint32_t keep = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+              if (gone >> (2 * b) & 1u) keep &= 0xFFFF0000u;
+              if (gone >> (2 * b + 1) & 1u) keep &= 0x0000FFFFu;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(s[j + k]));
+              for (int j = 0; j < 32; ++j)
+                if (!(keep >> j & 1u)) s[32 * b + j] = 0xFF800000u;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+#pragma unroll
+          for (int j = 8; j < 128; j += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool grow = (top - m) * p.sl2 > kRescale;  // -inf - -inf: NaN, no
           if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -503,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= f;
             m = mn;
             if (kt != first) {
+#pragma unroll 1
               for (int c = 0; c < ochunks; ++c) {
                 uint32_t o[32];
                 tmem_ld32(to + 32 * c, o);
@@ -542,46 +645,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const bool have = first < last;
       if (have) {
-        if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(o_full(w), no++ & 1u, p.status, abort_flag)))) break;
+        if (!(ok = wait_warp(o_full(w), no++ & 1u))) break;
         tc_fence_after();
       } else {
         // no tile here: still one arrival per unit and warp, not before the
         // unit's queries are in (so none counts for an earlier unit)
-        if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(q_full, unit & 1u, p.status, abort_flag)))) break;
-        if (u.pair && lane == 0) mbar_arrive(q_free);
+        if (!(ok = wait_warp(q_full, un & 1u))) break;
+        if (pair && lane == 0) mbar_arrive(q_free);
       }
       // single: warpgroup 1's result to warpgroup 0 through the query tiles' memory
-      const bool join = !u.pair && u.stop - u.tile > 1;
+      const bool join = !pair && u.stop - u.tile > 1;
       float *xo = reinterpret_cast<float *>(gbase + C::q_off);
       auto xat = [&](int c4) { return xo + row * (NCH * 64) + ((c4 ^ (row & 7)) << 2); };
       float f0 = 1.0f, f1 = 0.0f;
-      if (!u.pair) {
-        if (w == 1) {
-          if (join) {
-            if (busy) {
-              for (int c = 0; c < ochunks; ++c) {
-                uint32_t o[32];
-                tmem_ld32(to + 32 * c, o);
-                if (live)
-#pragma unroll
-                  for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4 *>(xat(8 * c + j)) =
-                        make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-              }
-              if (live) {
-                xm[row] = m;
-                xl[row] = l;
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(x_full);
-          }
-          if (lane == 0) mbar_arrive(q_free);
-          continue;
-        }
+      if (!pair && w == 1) {
         if (join) {
-          if (!(ok = __all_sync(0xFFFFFFFFu, wait_ok(x_full, nx++ & 1u, p.status, abort_flag)))) break;
+          if (busy) {
+#pragma unroll 1
+            for (int c = 0; c < ochunks; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * c, o);
+              if (live)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  *reinterpret_cast<uint4 *>(xat(8 * c + j)) =
+                      make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+            if (live) {
+              xm[row] = m;
+              xl[row] = l;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(x_full);
+        }
+      } else {
+        if (join) {
+          if (!(ok = wait_warp(x_full, nx++ & 1u))) break;
           if (live) {
             const float m1 = xm[row], mn = fmaxf(m, m1);
             const float r = mn == -INFINITY ? 0.0f : mn;
@@ -591,93 +692,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = mn;
           }
         }
-      }
-      if (busy) {
-        const bool whole = u.tile == 0 && u.stop == u.ntile;
-        const float inv = whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
-        const int64_t y0 = (static_cast<int64_t>(u.q.q0 + u.t0 + tw + tok) * p.a.n_head + h * grp +
-                            sub * p.gsub + hq) * hd;
-        const int64_t slot = (2 * blockIdx.x + (u.tile == 0 ? 1 : 0)) *
-                                 static_cast<int64_t>(p.parts.rows) + (tw + tok) * g + hq;
-        if (!whole && live)
-          p.parts.ml[slot] = make_float2(m == -INFINITY ? m : m * p.sl2, l);
-        const bool mark = marked[unit & 15] == unit + 1;
-        for (int c = 0; c < ochunks; ++c) {
-          uint32_t o[32];
-          if (have)
-            tmem_ld32(to + 32 * c, o);
-          else
+        if (busy) {
+          const bool whole = u.tile == 0 && u.stop == u.ntile;
+          const float inv = whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+          const int64_t slot = (2 * blockIdx.x + (u.tile == 0 ? 1 : 0)) *
+                                   static_cast<int64_t>(p.parts.rows) + (tw + tok) * u.g + hq;
+          const int64_t y0 = (static_cast<int64_t>(u.q_row + tw + tok) * p.a.n_head + u.head0 + hq) * hd;
+          const bool bf16 = whole && p.a.y_bf16;
+          uint8_t *out = !whole ? reinterpret_cast<uint8_t *>(p.parts.o + slot * hd)
+                                : static_cast<uint8_t *>(p.a.y) + y0 * (bf16 ? 2 : 4);
+          if (!whole && live) p.parts.ml[slot] = make_float2(m == -INFINITY ? m : m * p.sl2, l);
+#pragma unroll 1
+          for (int c = 0; c < ochunks; ++c) {
+            uint32_t o[32];
+            if (have)
+              tmem_ld32(to + 32 * c, o);
+            else
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0u;
-          if (!live) continue;
-          float v[32];
+              for (int j = 0; j < 32; ++j) o[j] = 0u;
+            if (!live) continue;
+            float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]);
-          if (join) {
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (f0 * inv);
+            if (join) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 t = *reinterpret_cast<const float4 *>(xat(8 * c + j));
-              v[4 * j] = v[4 * j] * f0 + t.x * f1;
-              v[4 * j + 1] = v[4 * j + 1] * f0 + t.y * f1;
-              v[4 * j + 2] = v[4 * j + 2] * f0 + t.z * f1;
-              v[4 * j + 3] = v[4 * j + 3] * f0 + t.w * f1;
-            }
-          }
-          if (mark) {  // non-finite values that were taken out: into the rows that see them
-            const int j0 = max(u.tile * kKT, (u.all > 0 ? u.all : 0) / kKT * kKT);
-            const int j1 = min(min(vis, u.end), u.stop * kKT);
-            for (int j = max(j0, u.all > 0 ? u.all : 0); j < j1; ++j) {
-              const uint16_t *src = static_cast<const uint16_t *>(p.a.v);
-              if (PAGED) {
-                const int32_t id = p.a.block_table[u.r * p.a.table_stride + j / p.a.block_size];
-                if (id < 0 || id >= p.a.num_blocks) continue;
-                src += id * p.a.block_stride +
-                       static_cast<int64_t>(h * p.a.block_size + (j & (p.a.block_size - 1))) * hd;
-              } else {
-                src += static_cast<int64_t>(u.q.q0 + j) * p.a.v_stride + static_cast<int64_t>(h) * hd;
+              for (int j = 0; j < 8; ++j) {
+                const float4 t = *reinterpret_cast<const float4 *>(xat(8 * c + j));
+                v[4 * j] = fmaf(t.x, f1 * inv, v[4 * j]);
+                v[4 * j + 1] = fmaf(t.y, f1 * inv, v[4 * j + 1]);
+                v[4 * j + 2] = fmaf(t.z, f1 * inv, v[4 * j + 2]);
+                v[4 * j + 3] = fmaf(t.w, f1 * inv, v[4 * j + 3]);
               }
-              for (int k = 0; k < 32; ++k) {
-                if (32 * c + k >= hd) break;
-                const uint32_t b = src[32 * c + k];
-                if (nonfinite_bf16(b)) {
+            }
 #pragma unroll
-                  for (int t = 0; t < 32; ++t)
-                    if (t == k) v[t] += __uint_as_float(b << 16);
+            for (int j = 0; j < 32; j += 8) {
+              const int d = 32 * c + j;
+              if (d < hd) {
+                if (bf16) {
+                  *reinterpret_cast<uint4 *>(out + d * 2) =
+                      make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
+                                 bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
+                } else {
+                  float4 *y4 = reinterpret_cast<float4 *>(out + d * 4);
+                  y4[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                  y4[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
                 }
               }
             }
           }
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            const int d = 32 * c + j;
-            if (d >= hd) break;
-            const float4 lo = make_float4(v[j] * inv, v[j + 1] * inv, v[j + 2] * inv, v[j + 3] * inv);
-            const float4 hi =
-                make_float4(v[j + 4] * inv, v[j + 5] * inv, v[j + 6] * inv, v[j + 7] * inv);
-            if (!whole) {
-              float4 *o4 = reinterpret_cast<float4 *>(p.parts.o + slot * hd + d);
-              o4[0] = lo;
-              o4[1] = hi;
-            } else if (p.a.y_bf16) {
-              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.y) + y0 + d) =
-                  make_uint4(bf16x2(lo.x, lo.y), bf16x2(lo.z, lo.w), bf16x2(hi.x, hi.y),
-                             bf16x2(hi.z, hi.w));
-            } else {
-              float4 *y4 = reinterpret_cast<float4 *>(static_cast<float *>(p.a.y) + y0 + d);
-              y4[0] = lo;
-              y4[1] = hi;
-            }
-          }
+          if (live && marked[un & 15u] == static_cast<int>(un + 1))
+            add_marked<PAGED>(p, u, vis, out, bf16);
         }
+        if (!pair) fence_proxy_async_smem();
       }
-      if (!u.pair) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_free);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (!pair) mbar_arrive(q_free);
+        mbar_arrive(u_free(un));
       }
-      if (threadIdx.x == 0 && u.tile == 0 && u.stop < u.ntile)
-        p.parts.open[blockIdx.x] = AttnOpen{u.q.q0 + u.t0, u.nt, u.vh,
-                                            sched_owner(u.x + p.sc.fixed + u.ntile - 1, run.W, run.G)};
     }
   }
   tc_fence_before();
@@ -747,8 +820,8 @@ AttnPlan attn_tc_plan(int n_head, int n_kv) {
   p.nsub = (grp + p.gsub - 1) / p.gsub;
   p.U = 2 * (128 / p.gsub);
   p.KT = kKT;
-  p.fixed = 2;
-  p.min_run = 2;
+  p.fixed = 2 * kKT;
+  p.min_run = 2 * kKT;
   p.workers = sm_count();
   return p;
 }
@@ -763,6 +836,7 @@ cudaError_t launch_attn_tc(const AttnBatch &a, const AttnPlan &pl, const AttnSch
   p.nsub = pl.nsub;
   p.tpt = pl.U / 2;
   p.box_rows = a.block_table ? (a.block_size < kKT ? a.block_size : kKT) : kKT;
+  while (a.block_table && (1 << p.block_shift) < a.block_size) ++p.block_shift;
   p.sl2 = a.scale * 1.4426950408889634f;
   p.status = device_status();
   if (!p.status) return cudaErrorInvalidDevice;
