@@ -87,6 +87,13 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -443,8 +450,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) mbar_arrive(u_free(un));
       }
-    } else if (lane == 0) {
+    } else {
       // ------------------------------------------------------------ MMA issue
+      // The whole warp walks the units on warp-uniform values (so that the
+      // descriptors live in uniform registers); one elected lane issues.
+      const bool lead = elect_one();
       const int ksteps = (hd + 15) / 16;
       const uint32_t id_s = idesc_bf16(kKT, false), id_o = idesc_bf16(ksteps * 16, true);
       const uint64_t kd0 = smem_desc_sw128(base + C::kv_off), vd0 = desc_values(base + C::kv_off);
@@ -453,33 +463,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t np = 0, np_other = 0;      // P tiles taken from this / the other warpgroup
       bool ok = true;
       for (uint32_t un = 0; ok; ++un) {
-        if (!wait_ok(u_full(un), (un / kUnits) & 1u, p.status, abort_flag)) break;
+        if (!wait_warp(u_full(un), (un / kUnits) & 1u)) break;
         const Unit &u = units[un % kUnits];
-        if (!u.valid) break;
-        const int tile = u.tile, stop = u.stop;
-        const bool pair = u.pair != 0;
-        int cur, last, step, cur_other, last_other;
-        wg_tiles(u, 0, cur, last, step);
-        wg_tiles(u, 1, cur_other, last_other, step);
-        if (!(ok = wait_ok(q_full, un & 1u, p.status, abort_flag))) break;
+        auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+        if (!same(u.valid)) break;
+        const int tile = same(u.tile), stop = same(u.stop), ntile_a = same(u.ntile_a);
+        const bool pair = same(u.pair) != 0;
+        const int step = pair ? 1 : 2;
+        int cur = tile, last = pair ? min(stop, ntile_a) : stop;
+        int cur_other = pair ? tile : tile + 1, last_other = stop;
+        if (!(ok = wait_warp(q_full, un & 1u))) break;
         // tile kt's keys are load n0 + 2 (kt - tile), its values the next one;
         // warpgroup 1 is the last user of every tile of a pair
         auto qk = [&](int w, int kt) {
           const uint32_t n = n0 + 2 * (kt - tile);
           const int s = n % NS;
-          if (!wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag)) return false;
+          if (!wait_warp(full(s), (n / NS) & 1u)) return false;
           tc_fence_after();
           const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
           const uint64_t kd = kd0 + s * (C::tile >> 4);
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < NCH * 4; ++k) {
-            constexpr int kC = kChunk >> 4;
-            if (k < ksteps)
-              tc_mma_ss(tmem + w * 128, qd + (k / 4) * kC + (k % 4) * 2, kd + (k / 4) * kC + (k % 4) * 2,
-                        id_s, k > 0);
+            for (int k = 0; k < NCH * 4; ++k) {
+              constexpr int kC = kChunk >> 4;
+              if (k < ksteps)
+                tc_mma_ss(tmem + w * 128, qd + (k / 4) * kC + (k % 4) * 2,
+                          kd + (k / 4) * kC + (k % 4) * 2, id_s, k > 0);
+            }
+            tc_commit(s_full(w));
+            if (!pair || w) tc_commit(freed(s));
           }
-          tc_commit(s_full(w));
-          if (!pair || w) tc_commit(freed(s));
+          __syncwarp();
           return true;
         };
         if (cur < last) ok = qk(0, cur);
@@ -490,22 +504,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cur < last) {
             const uint32_t n = n0 + 2 * (cur - tile) + 1;
             const int s = n % NS;
-            if (!(ok = wait_ok(full(s), (n / NS) & 1u, p.status, abort_flag))) break;
-            if (!(ok = wait_ok(clean(s), (n / NS) & 1u, p.status, abort_flag))) break;
-            if (!(ok = wait_ok(p_full(w), np++ & 1u, p.status, abort_flag))) break;
+            if (!(ok = wait_warp(full(s), (n / NS) & 1u))) break;
+            if (!(ok = wait_warp(clean(s), (n / NS) & 1u))) break;
+            if (!(ok = wait_warp(p_full(w), np++ & 1u))) break;
             tc_fence_after();
             const uint64_t vd = vd0 + s * (C::tile >> 4);
             const uint32_t o = tmem + C::o_col + w * C::o_step;
+            const bool more = cur + step < last;
+            if (lead) {
 #pragma unroll
-            for (int k = 0; k < kKT / 16; ++k)
-              tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
-            if (!pair || w) tc_commit(freed(s));
+              for (int k = 0; k < kKT / 16; ++k)
+                tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
+              if (!pair || w) tc_commit(freed(s));
+              if (pair && !more) tc_commit(o_full(w));
+            }
+            __syncwarp();
             first = false;
             cur += step;
-            if (cur < last)
-              ok = qk(w, cur);
-            else if (pair)
-              tc_commit(o_full(w));
+            if (more) ok = qk(w, cur);
           }
           const int c = cur, l = last;
           const uint32_t m = np;
@@ -521,15 +537,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // single: both results at once, when nothing reads the query tile any
         // more (its shared memory carries warpgroup 1's result to warpgroup 0)
-        if (!pair) {
-          tc_commit(o_full(0));
-          if (stop - tile > 1) tc_commit(o_full(1));
+        if (lead) {
+          if (!pair) {
+            tc_commit(o_full(0));
+            if (stop - tile > 1) tc_commit(o_full(1));
+          }
+          mbar_arrive(u_free(un));
         }
         n0 += 2 * (stop - tile);
-        mbar_arrive(u_free(un));
+        __syncwarp();
       }
-      tc_commit(drain);
-      mbar_wait_bounded(drain, 0u, p.status);
+      if (lead) {
+        tc_commit(drain);
+        mbar_wait_bounded(drain, 0u, p.status);
+      }
     }
     __syncwarp();
   } else {
