@@ -49,16 +49,18 @@ __device__ __forceinline__ void store_y4(void *y, int64_t i, float4 v, bool bf16
 }
 
 // Output rows that belong to no request (padding before the first or behind
-// the last) become zeros; worker w of n takes its share.
-__device__ __forceinline__ void zero_loose_rows(const AttnBatch &a, const AttnSched &s, int w,
-                                                int n) {
+// the last) become zeros; worker w of n, with its first `threads` threads,
+// takes its share.
+__device__ __forceinline__ void zero_loose_rows(const AttnBatch &a, const AttnSched &s, int w, int n,
+                                                int threads) {
   int64_t lo = s.R > 0 ? s.cu[0] : 0, hi = s.R > 0 ? s.cu[s.R] : 0;
   lo = lo < 0 ? 0 : (lo > a.T ? a.T : lo);
   hi = hi < lo ? lo : (hi > a.T ? a.T : hi);
   const int64_t per = static_cast<int64_t>(a.n_head) * a.head_dim / 4;
   const int64_t total = (lo + a.T - hi) * per;
-  for (int64_t e = static_cast<int64_t>(w) * blockDim.x + threadIdx.x; e < total;
-       e += static_cast<int64_t>(n) * blockDim.x) {
+#pragma unroll 1
+  for (int64_t e = static_cast<int64_t>(w) * threads + threadIdx.x; e < total;
+       e += static_cast<int64_t>(n) * threads) {
     const int64_t u = e < lo * per ? e : e - lo * per + hi * per;
     store_y4(a.y, 4 * u, make_float4(0.f, 0.f, 0.f, 0.f), a.y_bf16);
   }

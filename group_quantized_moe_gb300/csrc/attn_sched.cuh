@@ -6,9 +6,10 @@
 // number of keys its last token sees, and `fixed` keys more for what a unit
 // costs besides them (loading its queries, writing its results).  The units
 // are laid end to end in the order (request, token block, head) and the cost
-// W of the whole call is cut into G equal runs, one per worker: every worker
-// gets the same work whatever the lengths are, and a long context is split
-// over as many workers as its share of the work asks for.  A tile of KT keys
+// W of the whole call is cut into equal runs of `step`, worker w's being
+// [w step, (w + 1) step): every worker gets the same work whatever the lengths
+// are, and a long context is split over as many workers as its share of the
+// work asks for.  A tile of KT keys
 // belongs to the run that holds its first key.  A unit that a cut divides
 // leaves one partial result per worker, merged afterwards in worker order,
 // so results are reproducible bit for bit.
@@ -24,6 +25,8 @@
 
 #include <cstdint>
 
+#include "qmm_device.cuh"
+
 namespace qmm {
 
 struct AttnSched {
@@ -36,6 +39,7 @@ struct AttnSched {
   int fixed;           // cost of a unit besides its keys
   int min_run;         // a worker's run costs at least this much (one tile or more, so
                        // that no run inside a unit is without a tile of it)
+  uint64_t per_worker; // 2^64 / workers, rounded up
   int64_t T;           // query rows in the buffers
   int64_t cap;         // largest cache length the block table can hold
 };
@@ -58,13 +62,6 @@ __device__ __forceinline__ AttnReq sched_req(const AttnSched &s, int r) {
   if (L > s.cap) L = s.cap;
   q.L = static_cast<int>(L);
   return q;
-}
-
-// a / b for a >= 0, b > 0: the 64-bit division is several times the 32-bit
-// one, and nearly every call fits the latter.
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
 }
 
 __device__ __forceinline__ int sched_blocks(const AttnSched &s, const AttnReq &q) {
@@ -98,38 +95,34 @@ __device__ __forceinline__ int64_t sched_cost(const AttnSched &s, const AttnReq 
   return m == 0 ? 0 : (sched_before(s, q, m - 1) + sched_unit(s, q, m - 1)) * s.nvh;
 }
 
-// One worker's run [first, last) of the call's cost W, cut into G runs, and
-// the unit that holds its start: request r, token block i, head h, beginning
-// at cost `unit`.
+// One worker's run [first, last) of the call's cost, and the unit that holds
+// its start: request r, token block i, head h, beginning at cost `unit`.
 struct AttnRun {
-  int64_t W, first, last, unit;
-  int G;
+  int64_t first, last, unit, step;
   int r, i, h;
 };
 
-// Runs are W / G long, the first W mod G of them one longer.
-__device__ __forceinline__ int64_t sched_first(int64_t w, int64_t base, int64_t more) {
-  return w * base + (w < more ? w : more);
+// floor(a / b) for a >= 0, b > 0 and a quotient that fits an int (a worker, a
+// head): the quotient in fp32, put right; far shorter than a 64-bit division.
+__device__ __forceinline__ int small_quotient(int64_t a, int64_t b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  while (static_cast<int64_t>(q) * b > a) --q;
+  while ((static_cast<int64_t>(q) + 1) * b <= a) ++q;
+  return q;
 }
 
-// Worker whose run holds cost x.
-__device__ __forceinline__ int sched_owner(int64_t x, int64_t W, int G) {
-  const int64_t base = div_pos(W, G), more = W - base * G, edge = more * (base + 1);
-  return static_cast<int>(x < edge ? div_pos(x, base + 1) : more + div_pos(x - edge, base));
-}
-
-// The run of worker w of at most `workers`, by all NT threads of a block.
-// scratch: 8 (NT / 32 + 4) bytes of shared memory.  A worker without work
-// gets first == last.
+// The run of worker w, by all NT threads of a block.  scratch: 8 (NT / 32 + 4)
+// bytes of shared memory.  A worker without work gets first >= last.
 template <int NT>
-__device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *scratch) {
+__device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t *scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (s.R + NT - 1) / NT;
   const int r0 = min(s.R, tid * per), r1 = min(s.R, r0 + per);
   int64_t mine = 0;
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) mine += sched_cost(s, sched_req(s, r));
   int64_t inc = mine;  // inclusive over the warp
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += v;
@@ -137,28 +130,28 @@ __device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *sc
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
   int64_t lo = inc - mine, W = 0;  // lo: cost before this thread's requests
-#pragma unroll
+#pragma unroll 4
   for (int k = 0; k < NT / 32; ++k) {
     const int64_t v = scratch[k];
     if (k < warp) lo += v;
     W += v;
   }
   AttnRun run;
-  run.W = W;
-  const int64_t g = div_pos(W, s.min_run);
-  run.G = g < 1 ? 1 : (g < workers ? static_cast<int>(g) : workers);
-  const int64_t base = div_pos(W, run.G), more = W - base * run.G;
-  run.first = w < run.G ? sched_first(w, base, more) : W;
-  run.last = w < run.G ? sched_first(w + 1, base, more) : W;
+  const int64_t even = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(W), s.per_worker)) + 1;
+  run.step = even > s.min_run ? even : s.min_run;
+  run.first = w * run.step;
+  run.last = min64(run.first + run.step, W);
   int64_t *found = scratch + NT / 32;
   if (run.first < run.last && run.first >= lo && run.first < lo + mine) {
     int r = r0;
     AttnReq q = sched_req(s, r);
+#pragma unroll 1
     for (int64_t c = sched_cost(s, q); run.first >= lo + c && r + 1 < r1; c = sched_cost(s, q)) {
       lo += c;
       q = sched_req(s, ++r);
     }
     int a = 0, b = sched_blocks(s, q);  // the block whose units hold the start
+#pragma unroll 1
     while (b - a > 1) {
       const int mid = (a + b) >> 1;
       if (lo + sched_before(s, q, mid) * s.nvh <= run.first) a = mid;
@@ -166,7 +159,7 @@ __device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *sc
     }
     lo += sched_before(s, q, a) * s.nvh;
     const int64_t cost = sched_unit(s, q, a);
-    const int64_t h = div_pos(run.first - lo, cost);
+    const int h = small_quotient(run.first - lo, cost);
     found[0] = r;
     found[1] = a;
     found[2] = h;
@@ -177,7 +170,7 @@ __device__ AttnRun sched_run(const AttnSched &s, int w, int workers, int64_t *sc
   run.r = work ? static_cast<int>(found[0]) : 0;
   run.i = work ? static_cast<int>(found[1]) : 0;
   run.h = work ? static_cast<int>(found[2]) : 0;
-  run.unit = work ? found[3] : W;
+  run.unit = work ? found[3] : run.last;
   return run;
 }
 
@@ -195,7 +188,7 @@ __device__ __forceinline__ void sched_part(const AttnSched &s, const AttnRun &ru
 // The worker that has a unit's last tile.
 __device__ __forceinline__ int sched_last(const AttnSched &s, const AttnRun &run, int64_t x,
                                           int ntile) {
-  return sched_owner(x + s.fixed + (static_cast<int64_t>(ntile - 1) << s.kt_shift), run.W, run.G);
+  return small_quotient(x + s.fixed + (static_cast<int64_t>(ntile - 1) << s.kt_shift), run.step);
 }
 
 // What a worker leaves for the merge: the unit that is still open when its

@@ -50,6 +50,7 @@ constexpr int kKT = 128;              // keys per tile
 constexpr int kWarpKv = 8, kWarpMma = 9, kWarpClean = 10, kWarpQ = 11;
 constexpr uint32_t kChunk = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
 constexpr int kUnits = 4;             // units in the ring between warp 11 and the others
+constexpr int kCols = 64;             // scores per step of the two passes
 constexpr float kRescale = 8.0f;      // log2 of the growth of the maximum that is let pass
 
 template <int NCH>  // 64-column chunks of the head size
@@ -104,6 +105,10 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[32]) { tmem_ld32(a, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[64]) { tmem_ld64(a, r); }
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[16]) { tmem_st16(a, r); }
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[32]) { tmem_st32(a, r); }
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
 // Zeroes the non-finite bf16 values of eight; whether there were any.
@@ -240,16 +245,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_slot), 512);
   pdl_enter();
-  zero_loose_rows(p.a, p.sc, blockIdx.x, gridDim.x);
   if (threadIdx.x == 0) p.parts.open[blockIdx.x].rows_tok = 0;
-  const AttnRun run = sched_run<kThreads>(p.sc, blockIdx.x, gridDim.x, scratch);
+  const AttnRun run = sched_run<kThreads>(p.sc, blockIdx.x, scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int hd = p.a.head_dim;
   const int nch = NCH == 1 ? 1 : (hd + 63) / 64;  // chunks that hold columns
-  // the whole warp, or (`one`) this thread alone, waits for a barrier
+  // the whole warp waits for a barrier
   auto wait_warp = [&](uint32_t bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, wait_ok(bar, parity, p.status, abort_flag)) != 0;
   };
@@ -475,59 +479,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(q_full, un & 1u))) break;
         // tile kt's keys are load n0 + 2 (kt - tile), its values the next one;
         // warpgroup 1 is the last user of every tile of a pair
-        auto qk = [&](int w, int kt) {
-          const uint32_t n = n0 + 2 * (kt - tile);
-          const int s = n % NS;
-          if (!wait_warp(full(s), (n / NS) & 1u)) return false;
+        // A turn of warpgroup w: P V of the tile whose scores it has had, then
+        // Q K^T of its next tile; for a pair all waits come first, while the
+        // tensor core works on the turn before.  The two take turns; cur
+        // (the next tile), last, np, held (scores out), first belong to w and
+        // change hands after every turn.
+        bool held = false, held_other = false, first = true, first_other = true;
+        int w = 0;
+        for (; ok && (held || held_other || cur < last || cur_other < last_other); w ^= 1) {
+          const bool more = cur < last;
+          const uint32_t nv = n0 + 2 * (cur - step - tile) + 1, nk = n0 + 2 * (cur - tile);
+          const int sv = nv % NS, sk = nk % NS;
+          if (held && !(ok = wait_warp(clean(sv), (nv / NS) & 1u))) break;
+          // single: the stage of these keys may be that of values still in use
+          if (more && pair && !(ok = wait_warp(full(sk), (nk / NS) & 1u))) break;
+          if (held && !(ok = wait_warp(p_full(w), np++ & 1u))) break;
           tc_fence_after();
-          const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
-          const uint64_t kd = kd0 + s * (C::tile >> 4);
-          if (lead) {
-#pragma unroll
-            for (int k = 0; k < NCH * 4; ++k) {
-              constexpr int kC = kChunk >> 4;
-              if (k < ksteps)
-                tc_mma_ss(tmem + w * 128, qd + (k / 4) * kC + (k % 4) * 2,
-                          kd + (k / 4) * kC + (k % 4) * 2, id_s, k > 0);
-            }
-            tc_commit(s_full(w));
-            if (!pair || w) tc_commit(freed(s));
-          }
-          __syncwarp();
-          return true;
-        };
-        if (cur < last) ok = qk(0, cur);
-        if (ok && cur_other < last_other) ok = qk(1, cur_other);
-        bool first = true, first_other = true;
-        int w = 0;  // the warpgroup whose state cur, last, np, first hold; it changes every turn
-        for (; ok && (cur < last || cur_other < last_other); w ^= 1) {
-          if (cur < last) {
-            const uint32_t n = n0 + 2 * (cur - tile) + 1;
-            const int s = n % NS;
-            if (!(ok = wait_warp(full(s), (n / NS) & 1u))) break;
-            if (!(ok = wait_warp(clean(s), (n / NS) & 1u))) break;
-            if (!(ok = wait_warp(p_full(w), np++ & 1u))) break;
-            tc_fence_after();
-            const uint64_t vd = vd0 + s * (C::tile >> 4);
-            const uint32_t o = tmem + C::o_col + w * C::o_step;
-            const bool more = cur + step < last;
+          if (held) {
             if (lead) {
+              const uint64_t vd = vd0 + sv * (C::tile >> 4);
+              const uint32_t o = tmem + C::o_col + w * C::o_step;
 #pragma unroll
               for (int k = 0; k < kKT / 16; ++k)
                 tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
-              if (!pair || w) tc_commit(freed(s));
+              if (!pair || w) tc_commit(freed(sv));
               if (pair && !more) tc_commit(o_full(w));
             }
             __syncwarp();
-            first = false;
-            cur += step;
-            if (more) ok = qk(w, cur);
           }
+          if (more) {
+            if (!pair && !(ok = wait_warp(full(sk), (nk / NS) & 1u))) break;
+            if (lead) {
+              const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
+              const uint64_t kd = kd0 + sk * (C::tile >> 4);
+#pragma unroll
+              for (int k = 0; k < NCH * 4; ++k) {
+                constexpr int kC = kChunk >> 4;
+                if (k < ksteps)
+                  tc_mma_ss(tmem + w * 128, qd + (k / 4) * kC + (k % 4) * 2,
+                            kd + (k / 4) * kC + (k % 4) * 2, id_s, k > 0);
+              }
+              tc_commit(s_full(w));
+              if (!pair || w) tc_commit(freed(sk));
+            }
+            __syncwarp();
+          }
+          if (held) first = false;
+          held = more;
+          cur += step;
           const int c = cur, l = last;
           const uint32_t m = np;
-          const bool f = first;
-          cur = cur_other, last = last_other, np = np_other, first = first_other;
-          cur_other = c, last_other = l, np_other = m, first_other = f;
+          const bool f = first, hl = held;
+          cur = cur_other, last = last_other, np = np_other, first = first_other, held = held_other;
+          cur_other = c, last_other = l, np_other = m, first_other = f, held_other = hl;
         }
         if (!ok) break;
         if (w == 1) {
@@ -584,8 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the last read of this query tile is done
         if (pair && kt + step >= last && lane == 0) mbar_arrive(q_free);
         if (busy) {
-          uint32_t s[128];
-          tmem_ld128(ts, s);
           const int k0 = kt * kKT;
           uint32_t gone = 0;  // 16-key pieces in blocks outside the cache
           if (PAGED && *bad_seen) {
@@ -599,25 +601,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (k0 + kKT > all || gone) {
             const int lim = vis - k0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int left = lim - 32 * b;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int left = lim - 32 * c;
               uint32_t keep = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
-              if (gone >> (2 * b) & 1u) keep &= 0xFFFF0000u;
-              if (gone >> (2 * b + 1) & 1u) keep &= 0x0000FFFFu;
+              if (gone >> (2 * c) & 1u) keep &= 0xFFFF0000u;
+              if (gone >> (2 * c + 1) & 1u) keep &= 0x0000FFFFu;
+              uint32_t s[32];
+              tmem_ld32(ts + 32 * c, s);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (!(keep >> j & 1u)) s[32 * b + j] = 0xFF800000u;
+                if (!(keep >> j & 1u)) s[j] = 0xFF800000u;
+              tmem_st32(ts + 32 * c, s);
             }
+            tmem_wait_st();
           }
-          float mx[4];
+          // Two passes over the scores in tensor memory, in rolled loops: with
+          // all 128 in registers and one pass unrolled, the instructions of
+          // the eight warps did not fit the SM's instruction caches.
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < 128; c += kCols) {
+            uint32_t s[kCols];
+            tmem_ld(ts + c, s);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+            for (int j = 0; j < kCols; j += 8)
 #pragma unroll
-          for (int j = 8; j < 128; j += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
+              for (int k = 0; k < 4; ++k)
+                mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
+          }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool grow = (top - m) * p.sl2 > kRescale;  // -inf - -inf: NaN, no
           if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -639,20 +651,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float ref = m == -INFINITY ? 0.0f : m * p.sl2;
           const f32x2 a2 = pack2(p.sl2, p.sl2), b2 = pack2(-ref, -ref);
           f32x2 sum[2] = {0ull, 0ull};
+          // P's columns never pass the scores that have been read
+#pragma unroll 1
+          for (int c = 0; c < 128; c += kCols) {
+            uint32_t s[kCols], pk[kCols / 2];
+            tmem_ld(ts + c, s);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int k = 32 * c + 2 * j;
+            for (int j = 0; j < kCols / 2; ++j) {
               float x0, x1;
-              unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), a2, b2), x0, x1);
+              unpack2(fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), a2, b2),
+                      x0, x1);
               x0 = ex2(x0);
               x1 = ex2(x1);
               sum[j & 1] = add2(sum[j & 1], pack2(x0, x1));
               pk[j] = bf16x2(x0, x1);
             }
-            tmem_st16(ts + 16 * c, pk);
+            tmem_st(ts + c / 2, pk);
           }
           float s0, s1;
           unpack2(add2(sum[0], sum[1]), s0, s1);
@@ -773,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(u_free(un));
       }
     }
+    zero_loose_rows(p.a, p.sc, blockIdx.x, gridDim.x, 256);
   }
   tc_fence_before();
   __syncthreads();
