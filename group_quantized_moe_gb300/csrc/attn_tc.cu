@@ -454,77 +454,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) mbar_arrive(u_free(un));
       }
-    } else {
+    } else if (elect_one()) {
       // ------------------------------------------------------------ MMA issue
-      // The whole warp walks the units on warp-uniform values (so that the
-      // descriptors live in uniform registers); one elected lane issues.
-      const bool lead = elect_one();
+      // Everything between two turns of the tensor core is latency of this one
+      // thread, so a turn waits as little as it can: warp 10 passes the loads
+      // in order, so that one look at the latest of them covers the others.
       const int ksteps = (hd + 15) / 16;
       const uint32_t id_s = idesc_bf16(kKT, false), id_o = idesc_bf16(ksteps * 16, true);
       const uint64_t kd0 = smem_desc_sw128(base + C::kv_off), vd0 = desc_values(base + C::kv_off);
       const uint64_t qd0 = smem_desc_sw128(base + C::q_off);
       uint32_t n0 = 0;                    // loads before the unit
+      uint32_t ready = 0;                 // loads known to have passed warp 10
       uint32_t np = 0, np_other = 0;      // P tiles taken from this / the other warpgroup
       bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return wait_ok(bar, parity, p.status, abort_flag);
+      };
       for (uint32_t un = 0; ok; ++un) {
-        if (!wait_warp(u_full(un), (un / kUnits) & 1u)) break;
+        if (!wait(u_full(un), (un / kUnits) & 1u)) break;
         const Unit &u = units[un % kUnits];
-        auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-        if (!same(u.valid)) break;
-        const int tile = same(u.tile), stop = same(u.stop), ntile_a = same(u.ntile_a);
-        const bool pair = same(u.pair) != 0;
+        if (!u.valid) break;
+        const int tile = u.tile, tiles = u.stop - tile;
+        const bool pair = u.pair != 0;
         const int step = pair ? 1 : 2;
-        int cur = tile, last = pair ? min(stop, ntile_a) : stop;
-        int cur_other = pair ? tile : tile + 1, last_other = stop;
-        if (!(ok = wait_warp(q_full, un & 1u))) break;
-        // tile kt's keys are load n0 + 2 (kt - tile), its values the next one;
-        // warpgroup 1 is the last user of every tile of a pair
+        // tile index from u.tile on: the next one and the end of this and the
+        // other warpgroup; tile i's keys are load n0 + 2 i, its values the next
+        int cur = 0, last = pair ? min(tiles, u.ntile_a - tile) : tiles;
+        int cur_other = pair ? 0 : 1, last_other = tiles;
+        if (!(ok = wait(q_full, un & 1u))) break;
         // A turn of warpgroup w: P V of the tile whose scores it has had, then
-        // Q K^T of its next tile; for a pair all waits come first, while the
-        // tensor core works on the turn before.  The two take turns; cur
-        // (the next tile), last, np, held (scores out), first belong to w and
-        // change hands after every turn.
+        // Q K^T of its next tile.  The two take turns; cur, last, np, held
+        // (scores out), first belong to w and change hands after every turn.
+        // Warpgroup 1 is the last user of every tile of a pair.
         bool held = false, held_other = false, first = true, first_other = true;
         int w = 0;
-        for (; ok && (held || held_other || cur < last || cur_other < last_other); w ^= 1) {
-          const bool more = cur < last;
-          const uint32_t nv = n0 + 2 * (cur - step - tile) + 1, nk = n0 + 2 * (cur - tile);
-          const int sv = nv % NS, sk = nk % NS;
-          if (held && !(ok = wait_warp(clean(sv), (nv / NS) & 1u))) break;
-          // single: the stage of these keys may be that of values still in use
-          if (more && pair && !(ok = wait_warp(full(sk), (nk / NS) & 1u))) break;
-          if (held && !(ok = wait_warp(p_full(w), np++ & 1u))) break;
-          tc_fence_after();
+        for (; held || held_other || cur < last || cur_other < last_other; w ^= 1) {
+          const bool more = cur < last, frees = !pair || w;
+          const uint32_t nk = n0 + 2 * cur, nv = n0 + 2 * (cur - step) + 1;
+          // single: those keys' stage may be that of values still in use, so
+          // they are waited for after P V
+          const uint32_t need = more && (pair || !held) ? nk : nv;
+          if ((held || more) && static_cast<int>(need - ready) >= 0) {
+            if (!(ok = wait(clean(need % NS), (need / NS) & 1u))) break;
+            ready = need + 1;
+          }
           if (held) {
-            if (lead) {
-              const uint64_t vd = vd0 + sv * (C::tile >> 4);
-              const uint32_t o = tmem + C::o_col + w * C::o_step;
+            if (!(ok = wait(p_full(w), np++ & 1u))) break;
+            tc_fence_after();
+            const int s = nv % NS;
+            const uint64_t vd = vd0 + s * (C::tile >> 4);
+            const uint32_t o = tmem + C::o_col + w * C::o_step;
 #pragma unroll
-              for (int k = 0; k < kKT / 16; ++k)
-                tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
-              if (!pair || w) tc_commit(freed(sv));
-              if (pair && !more) tc_commit(o_full(w));
-            }
-            __syncwarp();
+            for (int k = 0; k < kKT / 16; ++k)
+              tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
+            if (frees) tc_commit(freed(s));
+            if (pair && !more) tc_commit(o_full(w));
+            first = false;
           }
           if (more) {
-            if (!pair && !(ok = wait_warp(full(sk), (nk / NS) & 1u))) break;
-            if (lead) {
-              const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
-              const uint64_t kd = kd0 + sk * (C::tile >> 4);
-#pragma unroll
-              for (int k = 0; k < NCH * 4; ++k) {
-                constexpr int kC = kChunk >> 4;
-                if (k < ksteps)
-                  tc_mma_ss(tmem + w * 128, qd + (k / 4) * kC + (k % 4) * 2,
-                            kd + (k / 4) * kC + (k % 4) * 2, id_s, k > 0);
-              }
-              tc_commit(s_full(w));
-              if (!pair || w) tc_commit(freed(sk));
+            if (static_cast<int>(nk - ready) >= 0) {
+              if (!(ok = wait(clean(nk % NS), (nk / NS) & 1u))) break;
+              ready = nk + 1;
             }
-            __syncwarp();
+            const int s = nk % NS;
+            const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
+            const uint64_t kd = kd0 + s * (C::tile >> 4);
+#pragma unroll
+            for (int k = 0; k < NCH * 4; ++k) {
+              constexpr int kC = kChunk >> 4;
+              if (k < ksteps)
+                tc_mma_ss(tmem + w * 128, qd + (k / 4) * kC + (k % 4) * 2,
+                          kd + (k / 4) * kC + (k % 4) * 2, id_s, k > 0);
+            }
+            tc_commit(s_full(w));
+            if (frees) tc_commit(freed(s));
           }
-          if (held) first = false;
           held = more;
           cur += step;
           const int c = cur, l = last;
@@ -541,20 +545,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // single: both results at once, when nothing reads the query tile any
         // more (its shared memory carries warpgroup 1's result to warpgroup 0)
-        if (lead) {
-          if (!pair) {
-            tc_commit(o_full(0));
-            if (stop - tile > 1) tc_commit(o_full(1));
-          }
-          mbar_arrive(u_free(un));
+        if (!pair) {
+          tc_commit(o_full(0));
+          if (tiles > 1) tc_commit(o_full(1));
         }
-        n0 += 2 * (stop - tile);
-        __syncwarp();
+        mbar_arrive(u_free(un));
+        n0 += 2 * tiles;
       }
-      if (lead) {
-        tc_commit(drain);
-        mbar_wait_bounded(drain, 0u, p.status);
-      }
+      tc_commit(drain);
+      mbar_wait_bounded(drain, 0u, p.status);
     }
     __syncwarp();
   } else {
