@@ -50,7 +50,6 @@ constexpr int kKT = 128;              // keys per tile
 constexpr int kWarpKv = 8, kWarpMma = 9, kWarpClean = 10, kWarpQ = 11;
 constexpr uint32_t kChunk = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
 constexpr int kUnits = 4;             // units in the ring between warp 11 and the others
-constexpr int kCols = 64;             // scores per step of the two passes
 constexpr float kRescale = 8.0f;      // log2 of the growth of the maximum that is let pass
 
 template <int NCH>  // 64-column chunks of the head size
@@ -58,9 +57,9 @@ struct Tc {
   static constexpr uint32_t tile = NCH * kChunk;            // one Q, K or V tile
   static constexpr int stages = NCH == 1 ? 10 : 5;          // K and V tiles in turn
   static constexpr uint32_t q_off = 0, kv_off = 2 * tile, bar_off = kv_off + stages * tile;
-  // q_full, q_free, x_full, drain, s_full[2], p_full[2], o_full[2],
+  // q_full, q_free, x_full, drain, s_full[2], p_full[2][2], o_full[2],
   // u_full[kUnits], u_free[kUnits], then full, freed, clean [stages]
-  static constexpr int nbar = 10 + 2 * kUnits + 3 * stages;
+  static constexpr int nbar = 12 + 2 * kUnits + 3 * stages;
   static constexpr uint32_t unit_off = (bar_off + nbar * 8 + 15) & ~15u;
   static constexpr uint32_t misc_off = unit_off + kUnits * 64;  // tmem, abort, bad, -, marked[16]
   static constexpr uint32_t bytes = misc_off + 80 + 2 * 128 * 4 + 1024;
@@ -105,10 +104,6 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[32]) { tmem_ld32(a, r); }
-__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[64]) { tmem_ld64(a, r); }
-__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[16]) { tmem_st16(a, r); }
-__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[32]) { tmem_st32(a, r); }
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
 // Zeroes the non-finite bf16 values of eight; whether there were any.
@@ -202,11 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = base + C::bar_off;
   const uint32_t q_full = bars, q_free = bars + 8, x_full = bars + 16, drain = bars + 24;
   auto s_full = [&](int w) { return bars + 32 + 8 * w; };
-  auto p_full = [&](int w) { return bars + 48 + 8 * w; };
-  auto o_full = [&](int w) { return bars + 64 + 8 * w; };
-  auto u_full = [&](uint32_t n) { return bars + 80 + 8 * (n % kUnits); };
-  auto u_free = [&](uint32_t n) { return bars + 80 + 8 * (kUnits + n % kUnits); };
-  constexpr int kStageBars = 80 + 16 * kUnits;
+  auto p_full = [&](int w, int half) { return bars + 48 + 16 * w + 8 * half; };
+  auto o_full = [&](int w) { return bars + 80 + 8 * w; };
+  auto u_full = [&](uint32_t n) { return bars + 96 + 8 * (n % kUnits); };
+  auto u_free = [&](uint32_t n) { return bars + 96 + 8 * (kUnits + n % kUnits); };
+  constexpr int kStageBars = 96 + 16 * kUnits;
   auto full = [&](int s) { return bars + kStageBars + 8 * s; };
   auto freed = [&](int s) { return bars + kStageBars + 8 * (NS + s); };
   auto clean = [&](int s) { return bars + kStageBars + 8 * (2 * NS + s); };
@@ -226,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full(w), 1);
-      mbar_init(p_full(w), 4);
+      mbar_init(p_full(w, 0), 4);
+      mbar_init(p_full(w, 1), 4);
       mbar_init(o_full(w), 1);
     }
     for (int k = 0; k < kUnits; ++k) {
@@ -499,14 +495,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             ready = need + 1;
           }
           if (held) {
-            if (!(ok = wait(p_full(w), np++ & 1u))) break;
-            tc_fence_after();
             const int s = nv % NS;
             const uint64_t vd = vd0 + s * (C::tile >> 4);
             const uint32_t o = tmem + C::o_col + w * C::o_step;
 #pragma unroll
-            for (int k = 0; k < kKT / 16; ++k)
-              tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
+            for (int half = 0; half < 2; ++half) {
+              if (!(ok = wait(p_full(w, half), np & 1u))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                tc_mma_ts(o, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k > 0);
+            }
+            if (!ok) break;
+            ++np;
             if (frees) tc_commit(freed(s));
             if (pair && !more) tc_commit(o_full(w));
             first = false;
@@ -615,20 +616,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
           }
-          // Two passes over the scores in tensor memory, in rolled loops: with
-          // all 128 in registers and one pass unrolled, the instructions of
-          // the eight warps did not fit the SM's instruction caches.
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = 0; c < 128; c += kCols) {
-            uint32_t s[kCols];
-            tmem_ld(ts + c, s);
+          uint32_t s[128];
+          tmem_ld128(ts, s);
+          float mx[4];
 #pragma unroll
-            for (int j = 0; j < kCols; j += 8)
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
-          }
+          for (int j = 8; j < 128; j += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool grow = (top - m) * p.sl2 > kRescale;  // -inf - -inf: NaN, no
           if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -650,31 +647,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float ref = m == -INFINITY ? 0.0f : m * p.sl2;
           const f32x2 a2 = pack2(p.sl2, p.sl2), b2 = pack2(-ref, -ref);
           f32x2 sum[2] = {0ull, 0ull};
-          // P's columns never pass the scores that have been read
-#pragma unroll 1
-          for (int c = 0; c < 128; c += kCols) {
-            uint32_t s[kCols], pk[kCols / 2];
-            tmem_ld(ts + c, s);
+          // P overwrites the first columns of S, and goes out in two halves:
+          // the tensor core starts on the first while the second is computed
 #pragma unroll
-            for (int j = 0; j < kCols / 2; ++j) {
-              float x0, x1;
-              unpack2(fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), a2, b2),
-                      x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-              sum[j & 1] = add2(sum[j & 1], pack2(x0, x1));
-              pk[j] = bf16x2(x0, x1);
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int c = 2 * half; c < 2 * half + 2; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int k = 32 * c + 2 * j;
+                float x0, x1;
+                unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), a2, b2), x0, x1);
+                x0 = ex2(x0);
+                x1 = ex2(x1);
+                sum[j & 1] = add2(sum[j & 1], pack2(x0, x1));
+                pk[j] = bf16x2(x0, x1);
+              }
+              tmem_st16(ts + 16 * c, pk);
             }
-            tmem_st(ts + c / 2, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(w, half));
           }
           float s0, s1;
           unpack2(add2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
-          tmem_wait_st();
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane < 2) mbar_arrive(p_full(w, lane));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(w));
       }
       if (!ok) break;
       const bool have = first < last;
