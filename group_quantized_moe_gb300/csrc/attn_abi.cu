@@ -140,7 +140,7 @@ cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t 
   AttnParts parts{reinterpret_cast<AttnOpen *>(base + l.open),
                   reinterpret_cast<float2 *>(base + l.ml), reinterpret_cast<float *>(base + l.o),
                   p.rows};
-  AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, log2i(p.KT), p.fixed, p.min_run,
+  AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, p.half, p.w_half, p.w_full, log2i(p.KT), p.fixed, p.min_run,
                ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, a.T,
                a.block_table ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, INT32_MAX)
                              : a.T};

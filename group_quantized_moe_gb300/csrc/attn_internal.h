@@ -21,9 +21,9 @@ struct AttnParts {
 
 // How a call is cut up: rows (query rows of a unit), the query heads gsub of
 // a group that one unit takes (nsub units cover the group), tokens U and keys
-// KT of a tile, workers (fixed, min_run: see AttnSched).
+// KT of a tile, workers (the rest: see AttnSched).
 struct AttnPlan {
-  int rows, gsub, nsub, U, KT, fixed, min_run, workers;
+  int rows, gsub, nsub, U, half, w_half, w_full, KT, fixed, min_run, workers;
 };
 
 AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R);

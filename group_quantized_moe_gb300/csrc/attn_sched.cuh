@@ -3,8 +3,9 @@
 // A call has R requests; request r has n new tokens (query rows) and L cache
 // rows, and token t of it sees the keys 0 .. L - n + t.  A unit of work is
 // (request, block of U consecutive tokens, key/value head); its cost is the
-// number of keys its last token sees, and `fixed` keys more for what a unit
-// costs besides them (loading its queries, writing its results).  The units
+// number of keys its last token sees, times `w_half` for a unit of up to `half`
+// tokens (one query tile) and `w_full` for a longer one (two), and `fixed` more
+// for what a unit costs besides (loading its queries, writing its results).  The units
 // are laid end to end in the order (request, token block, head) and the cost
 // W of the whole call is cut into equal runs of `step`, worker w's being
 // [w step, (w + 1) step): every worker gets the same work whatever the lengths
@@ -34,10 +35,11 @@ struct AttnSched {
   const int32_t *kvl;  // [R] cache rows, or nullptr: the new tokens themselves
   int R;
   int nvh;             // key/value heads (times the splits of a large query group)
-  int U;               // tokens per unit
+  int U, half;         // tokens per unit, and in the first of its query tiles
+  int w_half, w_full;  // cost of a key
   int kt_shift;        // log2 of the keys per tile
   int fixed;           // cost of a unit besides its keys
-  int min_run;         // a worker's run costs at least this much (one tile or more, so
+  int min_run;         // a worker's run costs at least this much (w_full KT or more, so
                        // that no run inside a unit is without a tile of it)
   uint64_t per_worker; // 2^64 / workers, rounded up
   int64_t T;           // query rows in the buffers
@@ -79,15 +81,22 @@ __device__ __forceinline__ int sched_tiles(const AttnSched &s, const AttnReq &q,
   return e > kt ? (e + kt - 1) >> s.kt_shift : 1;
 }
 
-// Cost of one unit of block i, and of one head's units in the blocks before
-// it (all of them full).  Rows that see no key (L < n) cost as if L = n.
+// Cost of a key for the units of block i, of one of these units, and of one
+// head's units in the blocks before it (all of them full).  Rows that see no
+// key (L < n) cost as if L = n.
+__device__ __forceinline__ int sched_weight(const AttnSched &s, const AttnReq &q, int i) {
+  return q.n - i * s.U > s.half ? s.w_full : s.w_half;
+}
+
 __device__ __forceinline__ int64_t sched_unit(const AttnSched &s, const AttnReq &q, int i) {
-  return static_cast<int64_t>(max(q.L - q.n, 0)) + min(q.n, (i + 1) * s.U) + s.fixed;
+  const int64_t keys = static_cast<int64_t>(max(q.L - q.n, 0)) + min(q.n, (i + 1) * s.U);
+  return keys * sched_weight(s, q, i) + s.fixed;
 }
 
 __device__ __forceinline__ int64_t sched_before(const AttnSched &s, const AttnReq &q, int i) {
   const int64_t n = i;
-  return n * (static_cast<int64_t>(max(q.L - q.n, 0)) + s.fixed) + n * (n + 1) / 2 * s.U;
+  return n * (static_cast<int64_t>(max(q.L - q.n, 0)) * s.w_full + s.fixed) +
+         n * (n + 1) / 2 * (s.U * s.w_full);
 }
 
 __device__ __forceinline__ int64_t sched_cost(const AttnSched &s, const AttnReq &q) {
@@ -175,20 +184,21 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
 }
 
 // The tiles [tile, stop) of a unit of ntile tiles at cost x whose first keys
-// the run holds (a cut inside the fixed cost leaves all tiles to the later run).
+// the run holds (weight: its sched_weight); a cut inside the fixed cost leaves
+// all tiles to the later run.
 __device__ __forceinline__ void sched_part(const AttnSched &s, const AttnRun &run, int64_t x,
-                                           int ntile, int &tile, int &stop) {
-  const int64_t up = (1 << s.kt_shift) - 1;
+                                           int weight, int ntile, int &tile, int &stop) {
+  const int64_t t = static_cast<int64_t>(weight) << s.kt_shift;
   const int64_t a = run.first - x - s.fixed, b = run.last - x - s.fixed;
-  tile = a <= 0 ? 0 : static_cast<int>((a + up) >> s.kt_shift);
-  stop = b <= 0 ? 0 : static_cast<int>((b + up) >> s.kt_shift);
-  if (stop > ntile) stop = ntile;
+  tile = a <= 0 ? 0 : small_quotient(a + t - 1, t);
+  stop = b <= 0 ? 0 : b > ntile * t ? ntile : small_quotient(b + t - 1, t);
 }
 
 // The worker that has a unit's last tile.
 __device__ __forceinline__ int sched_last(const AttnSched &s, const AttnRun &run, int64_t x,
-                                          int ntile) {
-  return small_quotient(x + s.fixed + (static_cast<int64_t>(ntile - 1) << s.kt_shift), run.step);
+                                          int weight, int ntile) {
+  return small_quotient(x + s.fixed + (static_cast<int64_t>(ntile - 1) * weight << s.kt_shift),
+                        run.step);
 }
 
 // What a worker leaves for the merge: the unit that is still open when its

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
     const int ntile = sched_tiles(sc, q, i);
     next = x + sched_unit(sc, q, i);
     int tile, stop;
-    sched_part(sc, run, x, ntile, tile, stop);
+    sched_part(sc, run, x, sched_weight(sc, q, i), ntile, tile, stop);
     if (tile >= stop) continue;
     const int h = vh / nsub, sub = vh - h * nsub;
     const int g = min(gsub, grp - sub * gsub);  // query heads of this unit
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
       }
     }
     if (tid == 0 && tile == 0 && !whole) {
-      parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, ntile)};
+      parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, sched_weight(sc, q, i), ntile)};
     }
   }
 }
@@ -338,6 +338,8 @@ AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim
   p.U = p.rows / p.gsub;
   const int nc = simt_nc(head_dim);
   p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
+  p.half = 0;
+  p.w_half = p.w_full = 1;
   p.fixed = p.KT;
   p.min_run = 2 * p.KT;
   p.workers = sm_count() * 2;

@@ -55,11 +55,13 @@ constexpr float kRescale = 8.0f;      // log2 of the growth of the maximum that 
 template <int NCH>  // 64-column chunks of the head size
 struct Tc {
   static constexpr uint32_t tile = NCH * kChunk;            // one Q, K or V tile
-  static constexpr int stages = NCH == 1 ? 10 : 5;          // K and V tiles in turn
-  static constexpr uint32_t q_off = 0, kv_off = 2 * tile, bar_off = kv_off + stages * tile;
-  // q_full, q_free, x_full, drain, s_full[2], p_full[2][2], o_full[2],
+  static constexpr int stages = NCH == 1 ? 10 : 4;          // K and V tiles in turn
+  static constexpr uint32_t q_off = 0, kv_off = 2 * tile;
+  static constexpr uint32_t out_off = kv_off + stages * tile;  // 4 KB a warp: 32 rows of 128 bytes
+  static constexpr uint32_t bar_off = out_off + 8 * 4096;
+  // q_full[2], q_free[2], x_full, drain, s_full[2], p_full[2][2], o_full[2],
   // u_full[kUnits], u_free[kUnits], then full, freed, clean [stages]
-  static constexpr int nbar = 12 + 2 * kUnits + 3 * stages;
+  static constexpr int nbar = 14 + 2 * kUnits + 3 * stages;
   static constexpr uint32_t unit_off = (bar_off + nbar * 8 + 15) & ~15u;
   static constexpr uint32_t misc_off = unit_off + kUnits * 64;  // tmem, abort, bad, -, marked[16]
   static constexpr uint32_t bytes = misc_off + 80 + 2 * 128 * 4 + 1024;
@@ -195,13 +197,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *gbase = smem_raw + (base - raw);
   const uint32_t bars = base + C::bar_off;
-  const uint32_t q_full = bars, q_free = bars + 8, x_full = bars + 16, drain = bars + 24;
-  auto s_full = [&](int w) { return bars + 32 + 8 * w; };
-  auto p_full = [&](int w, int half) { return bars + 48 + 16 * w + 8 * half; };
-  auto o_full = [&](int w) { return bars + 80 + 8 * w; };
-  auto u_full = [&](uint32_t n) { return bars + 96 + 8 * (n % kUnits); };
-  auto u_free = [&](uint32_t n) { return bars + 96 + 8 * (kUnits + n % kUnits); };
-  constexpr int kStageBars = 96 + 16 * kUnits;
+  const uint32_t x_full = bars, drain = bars + 8;
+  auto q_full = [&](int w) { return bars + 16 + 8 * w; };
+  auto q_free = [&](int w) { return bars + 32 + 8 * w; };
+  auto s_full = [&](int w) { return bars + 48 + 8 * w; };
+  auto p_full = [&](int w, int half) { return bars + 64 + 16 * w + 8 * half; };
+  auto o_full = [&](int w) { return bars + 96 + 8 * w; };
+  auto u_full = [&](uint32_t n) { return bars + 112 + 8 * (n % kUnits); };
+  auto u_free = [&](uint32_t n) { return bars + 112 + 8 * (kUnits + n % kUnits); };
+  constexpr int kStageBars = 112 + 16 * kUnits;
   auto full = [&](int s) { return bars + kStageBars + 8 * s; };
   auto freed = [&](int s) { return bars + kStageBars + 8 * (NS + s); };
   auto clean = [&](int s) { return bars + kStageBars + 8 * (2 * NS + s); };
@@ -215,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_free, 8);
     mbar_init(x_full, 4);
     mbar_init(drain, 1);
     for (int w = 0; w < 2; ++w) {
+      mbar_init(q_full(w), 1);
+      mbar_init(q_free(w), 4);
       mbar_init(s_full(w), 1);
       mbar_init(p_full(w, 0), 4);
       mbar_init(p_full(w, 1), 4);
@@ -277,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           u.ntile = sched_tiles(p.sc, q, i);
-          sched_part(p.sc, run, x, u.ntile, u.tile, u.stop);
+          const int weight = sched_weight(p.sc, q, i);
+          sched_part(p.sc, run, x, weight, u.ntile, u.tile, u.stop);
           if (u.tile < u.stop) {
             const int t0 = i * p.sc.U, ctx = q.L - q.n;
             u.valid = 1;
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             u.k_row = q.q0;
             if (lane == 0 && u.tile == 0 && u.stop < u.ntile)
               p.parts.open[blockIdx.x] =
-                  AttnOpen{u.q_row, u.nt, vh, sched_last(p.sc, run, x, u.ntile)};
+                  AttnOpen{u.q_row, u.nt, vh, sched_last(p.sc, run, x, weight, u.ntile)};
           }
           x += sched_unit(p.sc, q, i);
           if (++vh == p.sc.nvh) {
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         return u.valid != 0;
       };
-      uint32_t pub = 0, n = 0;  // units handed out, query tiles loaded
+      uint32_t pub = 0, n = 0, loads[2] = {0, 0};  // units handed out, served; tiles loaded
       bool more = true, ok = true;
       while (ok) {
         for (; ok && more && pub < n + 3; ++pub) {
@@ -320,20 +325,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) more = publish(pub);
         }
         if (!ok || (!more && n + 1 == pub)) break;
-        if (!wait_warp(q_free, (n & 1u) ^ 1u)) break;
         const Unit &u = units[n % kUnits];
-        const int tiles = u.pair ? 2 : 1;
-        if (lane == 0)
-          mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * nch * p.tpt * p.gsub * 128));
-        __syncwarp();
-        if (lane < tiles * nch) {
-          const int c = lane % nch, w = lane / nch;
-          tma_load_3d(base + C::q_off + w * C::tile + c * kChunk, &tm_q, c * 64, u.head0,
-                      u.q_row + w * p.tpt, q_full);
+        // a tile is loaded as soon as its warpgroup has no more use for the last one
+        for (int w = 0; w < (u.pair ? 2 : 1); ++w) {
+          if (!(ok = wait_warp(q_free(w), (n & 1u) ^ 1u))) break;
+          if (lane == 0)
+            mbar_arrive_expect_tx(q_full(w), static_cast<uint32_t>(nch * p.tpt * p.gsub * 128));
+          __syncwarp();
+          if (lane < nch)
+            tma_load_3d(base + C::q_off + w * C::tile + lane * kChunk, &tm_q, lane * 64, u.head0,
+                        u.q_row + w * p.tpt, q_full(w));
+          loads[w] += 1;
         }
         ++n;
       }
-      if (n > 0) mbar_wait_bounded(q_full, (n - 1) & 1u, p.status);
+      for (int w = 0; w < 2; ++w)
+        if (loads[w] > 0) mbar_wait_bounded(q_full(w), (loads[w] - 1) & 1u, p.status);
     } else if (warp == kWarpKv) {
       // ------------------------------------------------ key and value tiles
       uint32_t n = 0;  // tiles loaded so far; stage n % NS
@@ -462,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n0 = 0;                    // loads before the unit
       uint32_t ready = 0;                 // loads known to have passed warp 10
       uint32_t np = 0, np_other = 0;      // P tiles taken from this / the other warpgroup
+      uint32_t pairs = 0;                 // units with two query tiles so far
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return wait_ok(bar, parity, p.status, abort_flag);
@@ -477,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // other warpgroup; tile i's keys are load n0 + 2 i, its values the next
         int cur = 0, last = pair ? min(tiles, u.ntile_a - tile) : tiles;
         int cur_other = pair ? 0 : 1, last_other = tiles;
-        if (!(ok = wait(q_full, un & 1u))) break;
         // A turn of warpgroup w: P V of the tile whose scores it has had, then
         // Q K^T of its next tile.  The two take turns; cur, last, np, held
         // (scores out), first belong to w and change hands after every turn.
         // Warpgroup 1 is the last user of every tile of a pair.
         bool held = false, held_other = false, first = true, first_other = true;
         int w = 0;
+        if (!(ok = wait(q_full(0), un & 1u))) break;
         for (; held || held_other || cur < last || cur_other < last_other; w ^= 1) {
           const bool more = cur < last, frees = !pair || w;
           const uint32_t nk = n0 + 2 * cur, nv = n0 + 2 * (cur - step) + 1;
@@ -517,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = wait(clean(nk % NS), (nk / NS) & 1u))) break;
               ready = nk + 1;
             }
+            if (pair && w && cur == 0 && !(ok = wait(q_full(1), pairs & 1u))) break;
             const int s = nk % NS;
             const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
             const uint64_t kd = kd0 + s * (C::tile >> 4);
@@ -551,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tiles > 1) tc_commit(o_full(1));
         }
         mbar_arrive(u_free(un));
+        pairs += pair ? 1u : 0u;
         n0 += 2 * tiles;
       }
       tc_commit(drain);
@@ -586,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(s_full(w), nt & 1u))) break;
         tc_fence_after();
         // the last read of this query tile is done
-        if (pair && kt + step >= last && lane == 0) mbar_arrive(q_free);
+        if (pair && kt + step >= last && lane == 0) mbar_arrive(q_free(w));
         if (busy) {
           const int k0 = kt * kKT;
           uint32_t gone = 0;  // 16-key pieces in blocks outside the cache
@@ -685,11 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have) {
         if (!(ok = wait_warp(o_full(w), no++ & 1u))) break;
         tc_fence_after();
-      } else {
-        // no tile here: still one arrival per unit and warp, not before the
-        // unit's queries are in (so none counts for an earlier unit)
-        if (!(ok = wait_warp(q_full, un & 1u))) break;
-        if (pair && lane == 0) mbar_arrive(q_free);
+      } else if (pair) {
+        // no tile for warpgroup 0 here: its query tile is free, but not before
+        // it is in (so that the arrival counts for this unit)
+        if (!(ok = wait_warp(q_full(0), un & 1u))) break;
+        if (lane == 0) mbar_arrive(q_free(0));
       }
       // single: warpgroup 1's result to warpgroup 0 through the query tiles' memory
       const bool join = !pair && u.stop - u.tile > 1;
@@ -740,16 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t *out = !whole ? reinterpret_cast<uint8_t *>(p.parts.o + slot * hd)
                                 : static_cast<uint8_t *>(p.a.y) + y0 * (bf16 ? 2 : 4);
           if (!whole && live) p.parts.ml[slot] = make_float2(m == -INFINITY ? m : m * p.sl2, l);
-#pragma unroll 1
-          for (int c = 0; c < ochunks; ++c) {
+          // 32 columns of the result as floats
+          auto piece = [&](int c, float (&v)[32]) {
             uint32_t o[32];
             if (have)
               tmem_ld32(to + 32 * c, o);
             else
 #pragma unroll
               for (int j = 0; j < 32; ++j) o[j] = 0u;
-            if (!live) continue;
-            float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (f0 * inv);
             if (join) {
@@ -762,21 +770,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v[4 * j + 3] = fmaf(t.w, f1 * inv, v[4 * j + 3]);
               }
             }
+          };
+          // A thread holds a row, and rows lie far apart: stored from here, one
+          // instruction would touch 32 lines.  128 bytes of each row go through
+          // shared memory (16-byte units swizzled by the row), and eight lanes
+          // store one row's.
+          uint8_t *stage = gbase + C::out_off + warp * 4096;
+          auto put = [&](int j, uint4 t) {
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = t;
+          };
+          const uint32_t lives = __ballot_sync(0xFFFFFFFFu, live);
+          const int bytes = hd * (bf16 ? 2 : 4);  // of a row
+#pragma unroll 1
+          for (int b0 = 0; b0 < bytes; b0 += 128) {
+            float v[32];
+            if (bf16) {
+#pragma unroll 1
+              for (int k = 0; k < 2; ++k) {
+                const int c = (b0 >> 6) + k;
+                if (c >= ochunks) break;
+                piece(c, v);
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              const int d = 32 * c + j;
-              if (d < hd) {
-                if (bf16) {
-                  *reinterpret_cast<uint4 *>(out + d * 2) =
-                      make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
-                                 bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
-                } else {
-                  float4 *y4 = reinterpret_cast<float4 *>(out + d * 4);
-                  y4[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                  y4[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
-                }
+                for (int j = 0; j < 4; ++j)
+                  put(4 * k + j, make_uint4(bf16x2(v[8 * j], v[8 * j + 1]),
+                                            bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                            bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                            bf16x2(v[8 * j + 6], v[8 * j + 7])));
               }
+            } else {
+              piece(b0 >> 7, v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                put(j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                  __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = 4 * k + (lane >> 3), j = lane & 7;
+              uint8_t *to_row = reinterpret_cast<uint8_t *>(
+                  __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), r));
+              if ((lives >> r & 1u) && b0 + 16 * j < bytes)
+                *reinterpret_cast<uint4 *>(to_row + b0 + 16 * j) =
+                    *reinterpret_cast<const uint4 *>(stage + r * 128 + ((j ^ (r & 7)) << 4));
+            }
+            __syncwarp();
           }
           if (live && marked[un & 15u] == static_cast<int>(un + 1))
             add_marked<PAGED>(p, u, vis, out, bf16);
@@ -786,7 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (!pair) mbar_arrive(q_free);
+        // single: warpgroup 0 is the last to use the query tiles' memory
+        if (!pair && w == 0) {
+          mbar_arrive(q_free(0));
+          mbar_arrive(q_free(1));
+        }
         mbar_arrive(u_free(un));
       }
     }
@@ -859,8 +901,12 @@ AttnPlan attn_tc_plan(int n_head, int n_kv) {
   p.nsub = (grp + p.gsub - 1) / p.gsub;
   p.U = 2 * (128 / p.gsub);
   p.KT = kKT;
-  p.fixed = 2 * kKT;
-  p.min_run = 2 * kKT;
+  p.half = p.U / 2;
+  // measured: 1.44 us a tile of a pair, 0.99 us a tile of a single unit, 4.4 us a unit
+  p.w_half = 2;
+  p.w_full = 3;
+  p.fixed = 9 * kKT;
+  p.min_run = 4 * kKT;
   p.workers = sm_count();
   return p;
 }
