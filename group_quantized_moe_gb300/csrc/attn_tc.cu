@@ -52,13 +52,18 @@ constexpr uint32_t kChunk = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
 constexpr int kUnits = 4;             // units in the ring between warp 11 and the others
 constexpr float kRescale = 8.0f;      // log2 of the growth of the maximum that is let pass
 
-template <int NCH>  // 64-column chunks of the head size
+// NCH: 64-column chunks of the head size.  STAGED: results go out through
+// shared memory, which leaves room for four key and value tiles; without it
+// there are five, which decoding needs (it is bound by the loads in flight:
+// 64 requests 236 us with five tiles, 252 us with four) and can afford (few
+// rows to store).
+template <int NCH, bool STAGED>
 struct Tc {
   static constexpr uint32_t tile = NCH * kChunk;            // one Q, K or V tile
-  static constexpr int stages = NCH == 1 ? 10 : 4;          // K and V tiles in turn
+  static constexpr int stages = NCH == 1 ? (STAGED ? 8 : 10) : (STAGED ? 4 : 5);  // K, V in turn
   static constexpr uint32_t q_off = 0, kv_off = 2 * tile;
   static constexpr uint32_t out_off = kv_off + stages * tile;  // 4 KB a warp: 32 rows of 128 bytes
-  static constexpr uint32_t bar_off = out_off + 8 * 4096;
+  static constexpr uint32_t bar_off = out_off + (STAGED ? 8 * 4096 : 0);
   // q_full[2], q_free[2], x_full, drain, s_full[2], p_full[2][2], o_full[2],
   // u_full[kUnits], u_free[kUnits], then full, freed, clean [stages]
   static constexpr int nbar = 14 + 2 * kUnits + 3 * stages;
@@ -185,12 +190,12 @@ __device__ __noinline__ void add_marked(const TcAttn &p, const Unit &u, int vis,
   }
 }
 
-template <int NCH, bool PAGED>
+template <int NCH, bool PAGED, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcAttn p) {
-  using C = Tc<NCH>;
+  using C = Tc<NCH, STAGED>;
   constexpr int NS = C::stages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -771,50 +776,73 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           };
-          // A thread holds a row, and rows lie far apart: stored from here, one
-          // instruction would touch 32 lines.  128 bytes of each row go through
-          // shared memory (16-byte units swizzled by the row), and eight lanes
-          // store one row's.
-          uint8_t *stage = gbase + C::out_off + warp * 4096;
-          auto put = [&](int j, uint4 t) {
-            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = t;
-          };
-          const uint32_t lives = __ballot_sync(0xFFFFFFFFu, live);
-          const int bytes = hd * (bf16 ? 2 : 4);  // of a row
+          if constexpr (!STAGED) {
 #pragma unroll 1
-          for (int b0 = 0; b0 < bytes; b0 += 128) {
-            float v[32];
-            if (bf16) {
-#pragma unroll 1
-              for (int k = 0; k < 2; ++k) {
-                const int c = (b0 >> 6) + k;
-                if (c >= ochunks) break;
-                piece(c, v);
+            for (int c = 0; c < ochunks; ++c) {
+              float v[32];
+              piece(c, v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  put(4 * k + j, make_uint4(bf16x2(v[8 * j], v[8 * j + 1]),
-                                            bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                            bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                                            bf16x2(v[8 * j + 6], v[8 * j + 7])));
+              for (int j = 0; j < 32; j += 8) {
+                const int d = 32 * c + j;
+                if (live && d < hd) {
+                  if (bf16) {
+                    *reinterpret_cast<uint4 *>(out + d * 2) =
+                        make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
+                                   bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
+                  } else {
+                    float4 *y4 = reinterpret_cast<float4 *>(out + d * 4);
+                    y4[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    y4[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+                  }
+                }
               }
-            } else {
-              piece(b0 >> 7, v);
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                put(j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                  __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
             }
-            __syncwarp();
+          } else {
+            // A thread holds a row, and rows lie far apart: stored from here, one
+            // instruction would touch 32 lines.  128 bytes of each row go through
+            // shared memory (16-byte units swizzled by the row), and eight lanes
+            // store one row's.
+            uint8_t *stage = gbase + C::out_off + warp * 4096;
+            auto put = [&](int j, uint4 t) {
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = t;
+            };
+            const uint32_t lives = __ballot_sync(0xFFFFFFFFu, live);
+            const int bytes = hd * (bf16 ? 2 : 4);  // of a row
+#pragma unroll 1
+            for (int b0 = 0; b0 < bytes; b0 += 128) {
+              float v[32];
+              if (bf16) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                  const int c = (b0 >> 6) + k;
+                  if (c >= ochunks) break;
+                  piece(c, v);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int r = 4 * k + (lane >> 3), j = lane & 7;
-              uint8_t *to_row = reinterpret_cast<uint8_t *>(
-                  __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), r));
-              if ((lives >> r & 1u) && b0 + 16 * j < bytes)
-                *reinterpret_cast<uint4 *>(to_row + b0 + 16 * j) =
-                    *reinterpret_cast<const uint4 *>(stage + r * 128 + ((j ^ (r & 7)) << 4));
+                  for (int j = 0; j < 4; ++j)
+                    put(4 * k + j, make_uint4(bf16x2(v[8 * j], v[8 * j + 1]),
+                                              bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                              bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                              bf16x2(v[8 * j + 6], v[8 * j + 7])));
+                }
+              } else {
+                piece(b0 >> 7, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  put(j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                    __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int r = 4 * k + (lane >> 3), j = lane & 7;
+                uint8_t *to_row = reinterpret_cast<uint8_t *>(
+                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), r));
+                if ((lives >> r & 1u) && b0 + 16 * j < bytes)
+                  *reinterpret_cast<uint4 *>(to_row + b0 + 16 * j) =
+                      *reinterpret_cast<const uint4 *>(stage + r * 128 + ((j ^ (r & 7)) << 4));
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
           if (live && marked[un & 15u] == static_cast<int>(un + 1))
             add_marked<PAGED>(p, u, vis, out, bf16);
@@ -871,14 +899,15 @@ bool map_blocks(CUtensorMap *m, const void *p, const AttnBatch &a, int box_rows)
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NCH, bool PAGED>
+template <int NCH, bool PAGED, bool STAGED>
 cudaError_t run_tc(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const TcAttn &p,
                    int workers, cudaStream_t s) {
-  auto kern = attn_tc_kernel<NCH, PAGED>;
-  static_assert(Tc<NCH>::bytes <= 227 * 1024, "shared memory");
-  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), Tc<NCH>::bytes);
+  auto kern = attn_tc_kernel<NCH, PAGED, STAGED>;
+  constexpr uint32_t smem = Tc<NCH, STAGED>::bytes;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(workers), dim3(kThreads), Tc<NCH>::bytes, s, q, k, v, p);
+  return launch_pdl(kern, dim3(workers), dim3(kThreads), smem, s, q, k, v, p);
 }
 
 }  // namespace
@@ -906,7 +935,7 @@ AttnPlan attn_tc_plan(int n_head, int n_kv) {
   p.w_half = 2;
   p.w_full = 3;
   p.fixed = 9 * kKT;
-  p.min_run = 4 * kKT;
+  p.min_run = 3 * kKT;
   p.workers = sm_count();
   return p;
 }
@@ -933,11 +962,16 @@ cudaError_t launch_attn_tc(const AttnBatch &a, const AttnPlan &pl, const AttnSch
     ok = ok && map_rows(&k, a.k, a.T, a.k_stride, a.n_kv, a.head_dim, 1, kKT) &&
          map_rows(&v, a.v, a.T, a.v_stride, a.n_kv, a.head_dim, 1, kKT);
   if (!ok) return cudaErrorInvalidValue;
+  // requests of up to a query tile on average: the form for decoding
+  const bool few = a.T * p.gsub <= static_cast<int64_t>(128) * a.R;
+  if (!a.block_table)
+    return a.head_dim <= 64 ? run_tc<1, false, true>(q, k, v, p, pl.workers, s)
+                            : run_tc<2, false, true>(q, k, v, p, pl.workers, s);
   if (a.head_dim <= 64)
-    return a.block_table ? run_tc<1, true>(q, k, v, p, pl.workers, s)
-                         : run_tc<1, false>(q, k, v, p, pl.workers, s);
-  return a.block_table ? run_tc<2, true>(q, k, v, p, pl.workers, s)
-                       : run_tc<2, false>(q, k, v, p, pl.workers, s);
+    return few ? run_tc<1, true, false>(q, k, v, p, pl.workers, s)
+               : run_tc<1, true, true>(q, k, v, p, pl.workers, s);
+  return few ? run_tc<2, true, false>(q, k, v, p, pl.workers, s)
+             : run_tc<2, true, true>(q, k, v, p, pl.workers, s);
 }
 
 }  // namespace qmm
