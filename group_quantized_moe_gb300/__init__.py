@@ -95,6 +95,8 @@ def lib() -> ctypes.CDLL:
     """The loaded libqmm.so.  Raises if the library has not been built: there
     is deliberately no fallback implementation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -187,17 +189,17 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: building a torch.cuda.Stream costs microseconds
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return QMM_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return QMM_BF16
     raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
 
@@ -773,9 +775,21 @@ def _on_stream(stream, *ts) -> None:
             t.record_stream(s)
 
 
-def _lengths(t: torch.Tensor, numel: int, name: str) -> None:
-    if t.dtype != torch.int32 or t.numel() != numel:
-        _need(t, numel, (torch.int32,), name)
+# The calls of this section run once per layer and step, and at decode sizes
+# their kernels take a few microseconds: each tensor is passed by one short
+# expression, and only a tensor that fails it goes through the checks that
+# name what is wrong with it.
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+
+
+def _vec(t: torch.Tensor, dtype: torch.dtype, numel: int) -> bool:
+    return t.dtype is dtype and t.numel() == numel and t.is_cuda and t.is_contiguous()
+
+
+def _check_vec(t: torch.Tensor, dtype: torch.dtype, numel: int, name: str) -> None:
+    if not _vec(t, dtype, numel):
+        _need(t, numel, (dtype,), name)
+        _require_cuda(t)
 
 
 def _table(t: torch.Tensor, rows: int) -> None:
@@ -800,9 +814,13 @@ def _heads(t: torch.Tensor, name: str) -> int:
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
     T, h, d = t.shape
+    if T <= 1 or t.is_contiguous():
+        if T == 1 and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+            raise ValueError(f"the heads of a row of {name} must be contiguous")
+        return h * d
     if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return t.stride(0) if T > 1 else h * d
+    return t.stride(0)
 
 
 @dataclass
@@ -859,13 +877,10 @@ class KVPlan:
 
 
 def alloc_kv_plan(R: int, T: int, device="cuda") -> KVPlan:
-    """Uninitialised outputs for kv_plan (one allocation)."""
-    words = 2 * T + (R + 1) + R + T + 1
-    buf = torch.empty((words,), dtype=torch.int32, device=device)
-    o = 2 * T
-    return KVPlan(buf[o:o + R + 1], buf[o + R + 1:o + 2 * R + 1],
-                  buf[o + 2 * R + 1:o + 2 * R + 1 + T], buf[:2 * T].view(torch.int64),
-                  buf[words - 1:])
+    """Uninitialised outputs for kv_plan."""
+    def i32(n):  # five allocations cost less host time than one and its views
+        return torch.empty((n,), dtype=_I32, device=device)
+    return KVPlan(i32(R + 1), i32(R), i32(T), torch.empty((T,), dtype=_I64, device=device), i32(1))
 
 
 def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -875,28 +890,33 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     include/qmm.h): fills the new entries of block_table (int32 [R, columns])
     from free_blocks (int32) and returns the plan of num_tokens rows (as many
     as the new tokens, or more: padding rows get -1)."""
-    R, T = ctx_lens.numel(), num_tokens
-    _lengths(ctx_lens, R, "ctx_lens")
-    _lengths(new_lens, R, "new_lens")
-    _table(block_table, R)
-    _lengths(free_blocks, free_blocks.numel(), "free_blocks")
-    _on_device(block_table)
-    _require_cuda(ctx_lens, new_lens, free_blocks)
+    R, T, n_free = ctx_lens.numel(), num_tokens, free_blocks.numel()
+    if not (_vec(ctx_lens, _I32, R) and _vec(new_lens, _I32, R) and _vec(free_blocks, _I32, n_free)
+            and block_table.dtype is _I32 and block_table.is_cuda and block_table.is_contiguous()
+            and block_table.dim() == 2 and block_table.shape[0] == R):
+        _need(ctx_lens, R, (_I32,), "ctx_lens")
+        _need(new_lens, R, (_I32,), "new_lens")
+        _table(block_table, R)
+        _need(free_blocks, n_free, (_I32,), "free_blocks")
+        _on_device(block_table)
+        _require_cuda(ctx_lens, new_lens, free_blocks)
+    cols = block_table.shape[1]
     if out is None:
         out = alloc_kv_plan(R, T, ctx_lens.device)
-        _on_stream(stream, out.cu_new)
+        _on_stream(stream, out.cu_new, out.slots)
     else:
-        _lengths(out.cu_new, R + 1, "cu_new")
-        _lengths(out.kv_lens, R, "kv_lens")
-        _lengths(out.positions, T, "positions")
-        _need(out.slots, T, (torch.int64,), "slots")
-        _lengths(out.blocks_used, 1, "blocks_used")
-        _require_cuda(out.cu_new, out.kv_lens, out.positions, out.slots, out.blocks_used)
-    _check(lib().qmm_kv_plan(_ptr(ctx_lens), _ptr(new_lens), R, block_size, _ptr(block_table),
-                             block_table.stride(0) if R > 1 else block_table.shape[1],
-                             block_table.shape[1], _ptr(free_blocks), free_blocks.numel(), T,
-                             _ptr(out.cu_new), _ptr(out.kv_lens), _ptr(out.positions),
-                             _ptr(out.slots), _ptr(out.blocks_used), _stream(stream)))
+        _check_vec(out.cu_new, _I32, R + 1, "cu_new")
+        _check_vec(out.kv_lens, _I32, R, "kv_lens")
+        _check_vec(out.positions, _I32, T, "positions")
+        _check_vec(out.slots, _I64, T, "slots")
+        _check_vec(out.blocks_used, _I32, 1, "blocks_used")
+    rc = lib().qmm_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), R, block_size,
+                           block_table.data_ptr(), block_table.stride(0) if R > 1 else cols, cols,
+                           free_blocks.data_ptr(), n_free, T, out.cu_new.data_ptr(),
+                           out.kv_lens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+                           out.blocks_used.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -910,66 +930,77 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
     Returns (q, k, v): q [T, n_head, head_dim]; k, v [T, n_kv, head_dim] when
     keep_kv (or given), else None.  Without a cache, n_kv and y_dtype say the
     key/value heads and the output type."""
-    hd = 2 * rope_cos.shape[-1]
-    _need(rope_cos, rope_cos.shape[0] * rope_cos.shape[-1], (torch.float32,), "rope_cos")
-    _need(rope_sin, rope_cos.numel(), (torch.float32,), "rope_sin")
+    max_seq, half = rope_cos.shape
+    hd = 2 * half
+    plain = _vec(rope_cos, _F32, max_seq * half) and _vec(rope_sin, _F32, max_seq * half)
+    if not plain:
+        _need(rope_cos, max_seq * half, (_F32,), "rope_cos")
+        _need(rope_sin, max_seq * half, (_F32,), "rope_sin")
     if cache is not None:
         desc = cache._desc()
         if desc.head_dim != hd or (n_kv is not None and n_kv != desc.n_kv):
             raise ValueError(f"the cache has {desc.n_kv} heads of {desc.head_dim}, the call "
                              f"{n_kv} of {hd}")
-        n_kv, ref, y_dtype = desc.n_kv, ctypes.byref(desc), cache.k.dtype
+        n_kv, y_dtype = desc.n_kv, cache.k.dtype
         if slots is None:
             raise ValueError("a cache needs slots")
     else:
-        ref = None
+        desc = None
         if n_kv is None:
             raise ValueError("without a cache, n_kv must be given")
         y_dtype = qkv.dtype if y_dtype is None else y_dtype
     width = (n_head + 2 * n_kv) * hd
     if qkv.dim() != 2 or qkv.shape[1] != width:
         raise ValueError(f"qkv has shape {tuple(qkv.shape)}, expected [T, {width}]")
-    if qkv.numel() and qkv.stride(1) != 1:
-        raise ValueError("the rows of qkv must be contiguous")
     T = qkv.shape[0]
-    _lengths(positions, T, "positions")
-    _need(slots, T, (torch.int64,), "slots")
-    _need(q, T * n_head * hd, (y_dtype,), "q")
-    _need(k, T * n_kv * hd, (y_dtype,), "k")
-    _need(v, T * n_kv * hd, (y_dtype,), "v")
-    _on_device(qkv)
-    _require_cuda(positions, slots, rope_cos, rope_sin, q, k, v)
-    new = []
+    if not qkv.is_contiguous() and qkv.numel() and qkv.stride(1) != 1:
+        raise ValueError("the rows of qkv must be contiguous")
+    if not _vec(positions, _I32, T) or (slots is not None and not _vec(slots, _I64, T)):
+        plain = False
+        _need(positions, T, (_I32,), "positions")
+        _need(slots, T, (_I64,), "slots")
+    if q is not None:
+        _need(q, T * n_head * hd, (y_dtype,), "q")
+    if k is not None:
+        _need(k, T * n_kv * hd, (y_dtype,), "k")
+    if v is not None:
+        _need(v, T * n_kv * hd, (y_dtype,), "v")
+    if not (plain and qkv.is_cuda and q is None and k is None and v is None):
+        _on_device(qkv)
+        _require_cuda(positions, slots, rope_cos, rope_sin, q, k, v)
     if q is None:
         q = torch.empty((T, n_head, hd), dtype=y_dtype, device=qkv.device)
-        new.append(q)
+        _on_stream(stream, q)
     if keep_kv and k is None:
         k = torch.empty((T, n_kv, hd), dtype=y_dtype, device=qkv.device)
-        new.append(k)
+        _on_stream(stream, k)
     if keep_kv and v is None:
         v = torch.empty((T, n_kv, hd), dtype=y_dtype, device=qkv.device)
-        new.append(v)
-    _on_stream(stream, *new)
-    _check(lib().qmm_rope_append(_ptr(qkv), _dtype_code(qkv), T,
-                                 qkv.stride(0) if T > 1 else width, n_head, n_kv, hd,
-                                 _ptr(positions), _ptr(slots), _ptr(rope_cos), _ptr(rope_sin),
-                                 rope_cos.shape[0], ref, _ptr(q), _ptr(k), _ptr(v), _dtype_code(q),
-                                 _stream(stream)))
+        _on_stream(stream, v)
+    rc = lib().qmm_rope_append(qkv.data_ptr(), _dtype_code(qkv), T, qkv.stride(0) if T > 1 else width,
+                               n_head, n_kv, hd, positions.data_ptr(),
+                               None if slots is None else slots.data_ptr(), rope_cos.data_ptr(),
+                               rope_sin.data_ptr(), max_seq, desc, q.data_ptr(),
+                               None if k is None else k.data_ptr(), None if v is None else v.data_ptr(),
+                               _dtype_code(q), _stream(stream))
+    if rc:
+        _check(rc)
     return q, k, v
 
 
 def _attn_out(q, y, y_dtype, workspace, nbytes, stream):
-    T, nh, hd = q.shape
-    _need(y, T * nh * hd, (torch.float32, torch.bfloat16), "y")
-    _require_cuda(y, workspace)
-    new = []
-    if y is None:
-        y = torch.empty((T, nh, hd), dtype=y_dtype, device=q.device)
-        new.append(y)
-    if workspace is None:  # a caller's workspace is size-checked by the library
+    """The output and workspace of an attention call, checked or allocated."""
+    if y is not None:
+        _need(y, q.numel(), (_F32, torch.bfloat16), "y")
+        _require_cuda(y)
+    else:
+        y = torch.empty(q.shape, dtype=y_dtype, device=q.device)
+        _on_stream(stream, y)
+    if workspace is None:
         workspace = torch.empty((nbytes(),), dtype=torch.uint8, device=q.device)
-        new.append(workspace)
-    _on_stream(stream, *new)
+        _on_stream(stream, workspace)
+    else:  # a caller's workspace is size-checked by the library
+        _require_cuda(workspace)
     return y, workspace
 
 
@@ -995,15 +1026,18 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     B = cu_seqlens.numel() - 1
     if B < 0:
         raise ValueError("cu_seqlens must hold at least one element")
-    _lengths(cu_seqlens, B + 1, "cu_seqlens")
-    _on_device(q, k, v)
-    _require_cuda(cu_seqlens)
+    if not (_vec(cu_seqlens, _I32, B + 1) and q.is_cuda and k.is_cuda and v.is_cuda):
+        _need(cu_seqlens, B + 1, (_I32,), "cu_seqlens")
+        _on_device(q, k, v)
+        _require_cuda(cu_seqlens)
     y, workspace = _attn_out(q, y, y_dtype, workspace,
                              lambda: qmm_attn_prompt_workspace_bytes(q, k, B), stream)
-    _check(lib().qmm_attn_prompt(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), T, sq, sk, sv, nh, nkv,
-                                 hd, _ptr(cu_seqlens), B, 0.0 if scale is None else scale, _ptr(y),
-                                 _dtype_code(y), _ptr(workspace), _nbytes(workspace),
-                                 _stream(stream)))
+    rc = lib().qmm_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T, sq, sk, sv,
+                               nh, nkv, hd, cu_seqlens.data_ptr(), B, 0.0 if scale is None else scale,
+                               y.data_ptr(), _dtype_code(y), workspace.data_ptr(), _nbytes(workspace),
+                               _stream(stream))
+    if rc:
+        _check(rc)
     return y
 
 
@@ -1027,16 +1061,22 @@ def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q:
         raise ValueError(f"q is {q.dtype} with head_dim {hd}, the cache {cache.k.dtype} with "
                          f"{desc.head_dim}")
     R = kv_lens.numel()
-    _lengths(kv_lens, R, "kv_lens")
-    _lengths(cu_q, R + 1, "cu_q")
-    _table(block_table, R)
-    _on_device(q, block_table)
-    _require_cuda(cu_q, kv_lens)
+    if not (_vec(kv_lens, _I32, R) and _vec(cu_q, _I32, R + 1) and q.is_cuda
+            and block_table.dtype is _I32 and block_table.is_cuda and block_table.is_contiguous()
+            and block_table.dim() == 2 and block_table.shape[0] == R):
+        _need(kv_lens, R, (_I32,), "kv_lens")
+        _need(cu_q, R + 1, (_I32,), "cu_q")
+        _table(block_table, R)
+        _on_device(q, block_table)
+        _require_cuda(cu_q, kv_lens)
+    cols = block_table.shape[1]
     y, workspace = _attn_out(q, y, y_dtype, workspace,
                              lambda: qmm_attn_paged_workspace_bytes(q, cache, R), stream)
-    _check(lib().qmm_attn_paged(_ptr(q), T, sq, nh, ctypes.byref(desc), _ptr(block_table),
-                                block_table.stride(0) if R > 1 else block_table.shape[1],
-                                block_table.shape[1], _ptr(cu_q), _ptr(kv_lens), R,
-                                0.0 if scale is None else scale, _ptr(y), _dtype_code(y),
-                                _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    rc = lib().qmm_attn_paged(q.data_ptr(), T, sq, nh, desc, block_table.data_ptr(),
+                              block_table.stride(0) if R > 1 else cols, cols, cu_q.data_ptr(),
+                              kv_lens.data_ptr(), R, 0.0 if scale is None else scale, y.data_ptr(),
+                              _dtype_code(y), workspace.data_ptr(), _nbytes(workspace),
+                              _stream(stream))
+    if rc:
+        _check(rc)
     return y

@@ -195,6 +195,13 @@ def test_paged_cache_descriptor_checks(monkeypatch):
                    ((qq, cache, i(2, 4), i(3), i(2).float()), TypeError)):
         _raises(exc, q.attn_paged, *a)
     _raises(ValueError, q.attn_paged, qq, cache, i(2, 4), i(3), i(2), y=z(3, 4, 9))
+    _raises(ValueError, q.attn_paged, qq, cache, i(2, 4), i(6)[::2], i(2))
+    cos, x = z(50, 4), z(3, 64)
+    for a in ((i(6)[::2], i(3).long(), cos, cos), (i(3), i(6).long()[::2], cos, cos),
+              (i(3), i(3).long(), z(50, 8)[:, ::2], cos), (i(3), i(3).long(), cos, z(50, 8)[:, ::2])):
+        _raises(ValueError, q.rope_append, x, 4, *a, cache)
+    _raises(ValueError, q.kv_plan, i(4)[::2], i(2), i(2, 4), i(9), 16, 5)
+    _raises(ValueError, q.kv_plan, i(2), i(2), i(2, 4), i(18)[::2], 16, 5)
     _raises(TypeError, q.attn_paged, qq, cache, i(2, 4), i(3), i(2), y=z(3, 4, 8).half())
 
 
