@@ -125,16 +125,22 @@ PartsLayout parts_layout(const AttnPlan &p, int head_dim) {
 }  // namespace
 
 size_t attn_batch_workspace_bytes(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R) {
-  const size_t simt = parts_layout(attn_simt_plan(bf16, T, n_head, n_kv, head_dim, R), head_dim).total;
   // whether a bf16 call takes the tensor cores also depends on its strides
+  AttnPlan p;
+  if (!attn_rows_plan(T, n_head, n_kv, head_dim, R, &p))
+    p = attn_simt_plan(T, n_head, n_kv, head_dim, R);
+  const size_t simt = parts_layout(p, head_dim).total;
   const size_t tc = bf16 && head_dim <= 128 ? parts_layout(attn_tc_plan(n_head, n_kv), head_dim).total : 0;
   return simt > tc ? simt : tc;
 }
 
 cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t s) {
   const bool tc = attn_tc_takes(a);
-  const AttnPlan p = tc ? attn_tc_plan(a.n_head, a.n_kv)
-                        : attn_simt_plan(a.bf16, a.T, a.n_head, a.n_kv, a.head_dim, a.R);
+  AttnPlan p;
+  const bool rows = !tc && attn_rows_plan(a.T, a.n_head, a.n_kv, a.head_dim, a.R, &p);
+  if (!rows)
+    p = tc ? attn_tc_plan(a.n_head, a.n_kv)
+           : attn_simt_plan(a.T, a.n_head, a.n_kv, a.head_dim, a.R);
   const PartsLayout l = parts_layout(p, a.head_dim);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   AttnParts parts{reinterpret_cast<AttnOpen *>(base + l.open),
@@ -145,7 +151,8 @@ cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t 
                a.block_table ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, INT32_MAX)
                              : a.T};
   const cudaError_t e =
-      tc ? launch_attn_tc(a, p, sc, parts, s) : launch_attn_simt(a, p, sc, parts, s);
+      tc ? launch_attn_tc(a, p, sc, parts, s)
+         : rows ? launch_attn_rows(a, p, sc, parts, s) : launch_attn_simt(a, p, sc, parts, s);
   if (e != cudaSuccess) return e;
   return launch_attn_join(a, p, parts, s);
 }

@@ -26,8 +26,12 @@ struct AttnPlan {
   int rows, gsub, nsub, U, half, w_half, w_full, KT, fixed, min_run, workers;
 };
 
-AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R);
+AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R);
 cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
+                             const AttnParts &parts, cudaStream_t s);
+// The form for few rows; false: not for this call.
+bool attn_rows_plan(int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p);
+cudaError_t launch_attn_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                              const AttnParts &parts, cudaStream_t s);
 // The tensor-core form: whether it takes a call, its plan, its launch.
 bool attn_tc_takes(const AttnBatch &a);

@@ -1,0 +1,346 @@
+// attn_rows.cu -- batched attention for few query rows per key/value head
+// (decoding) in fp32 arithmetic: fp32 caches, and head sizes the tensor cores
+// do not take.
+//
+// The work is bound by reading the cache once, so the kernel keeps many wide
+// loads in flight and spends few instructions on a key.  A warp takes B
+// consecutive keys at a time (one block's; the eight warps of a CTA cover a
+// KT = 8 B key tile), lane l holding columns 4 l + 128 c of the keys, values,
+// queries and results in registers.  The RR x B partial dot products are
+// reduced over the lanes by halving (every step sends the half of the values
+// that the other lane keeps: RR B - 1 exchanges instead of 5 RR B), which
+// leaves the score of one (row, key) per lane; each lane keeps the running
+// maximum and sum of its row, and the weights go back to all lanes by shuffles.
+// The warps run independently and meet at the end of a unit.
+#include <cstdint>
+
+#include "attn_batch.h"
+#include "attn_internal.h"
+#include "attn_sched.cuh"
+#include "qmm_device.cuh"
+#include "qmm_internal.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// NC: 128-column groups of the head size; RR: query rows of a unit.
+template <int NC, int RR>
+struct Rows {
+  static constexpr int B = NC == 1 ? 8 : NC == 2 ? 4 : 2;  // keys of a warp at a time
+  static constexpr int KT = kWarps * B;
+  static constexpr int N = RR * B;                         // scores of a warp at a time
+  static constexpr int per_lane = N > 32 ? N / 32 : 1;     // ... of a lane
+  static constexpr int dup = N < 32 ? 32 / N : 1;          // lanes with the same score
+};
+
+// v[i] summed over the lanes: lane l is left with values per_lane (l / dup) + j.
+template <int N>
+__device__ __forceinline__ void reduce_scatter(float (&v)[N], int lane) {
+  int n = N;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    if (n > 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= n / 2) break;
+        const float send = up ? v[i] : v[i + n / 2], keep = up ? v[i + n / 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+      }
+      n /= 2;
+    } else {
+      v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    }
+  }
+}
+
+template <bool BF16, int NC, int RR>
+__global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, AttnSched sc, int gsub,
+                                                                int nsub, AttnParts parts,
+                                                                uint32_t *status) {
+  using C = Rows<NC, RR>;
+  constexpr int B = C::B, KT = C::KT, N = C::N, PL = C::per_lane;
+  __shared__ int64_t scratch[kWarps + 4];
+  __shared__ float wm[kWarps][RR], wl[kWarps][RR];
+  extern __shared__ __align__(16) float wo[];  // [warp][row][NC * 128]
+  pdl_enter();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hd = a.head_dim, grp = a.n_head / a.n_kv;
+  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
+  if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
+  const float sl2 = a.scale * 1.4426950408889634f;
+  // this lane's scores: row srow, keys skey + j
+  const int s0 = PL * (lane / C::dup), srow = s0 / B, skey = s0 % B;
+  int64_t x = run.unit;
+  int r = run.r, i = run.i, vh = run.h;
+  AttnReq q;
+  for (int64_t next = 0; x < run.last; x = next, vh = vh + 1 == sc.nvh ? 0 : vh + 1, i += vh == 0) {
+    q = sched_req(sc, r);
+    bool done = false;
+    while (i >= sched_blocks(sc, q)) {
+      if ((done = ++r >= sc.R)) break;  // lengths that changed during the call
+      i = 0;
+      q = sched_req(sc, r);
+    }
+    if (done) break;
+    const int ntile = sched_tiles(sc, q, i);
+    next = x + sched_unit(sc, q, i);
+    int tile, stop;
+    sched_part(sc, run, x, sched_weight(sc, q, i), ntile, tile, stop);
+    if (tile >= stop) continue;
+    const int h = vh / nsub, sub = vh - h * nsub;
+    const int g = min(gsub, grp - sub * gsub);
+    const int t0 = i * sc.U, nt = min(sc.U, q.n - t0);
+    const int rows = nt * g, head0 = h * grp + sub * gsub;
+    const int end = sched_end(sc, q, i), all = q.L - q.n + t0 + 1;
+    const int vis = all + (srow < rows ? srow / g : 0);  // keys this lane's row sees
+    float4 qv[RR][NC], o[RR][NC];
+#pragma unroll
+    for (int p = 0; p < RR; ++p) {
+      const int t = p / g, hq = p - t * g;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int d = 4 * lane + 128 * c;
+        qv[p][c] = p < rows && d < hd
+                       ? load_x4<BF16>(a.q, static_cast<int64_t>(q.q0 + t0 + t) * a.q_stride +
+                                                static_cast<int64_t>(head0 + hq) * hd + d)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        qv[p][c].x *= sl2;  // scores in log2 units
+        qv[p][c].y *= sl2;
+        qv[p][c].z *= sl2;
+        qv[p][c].w *= sl2;
+        o[p][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    float m = -INFINITY, l = 0.0f;  // of this lane's row; l over this lane's keys
+    const int32_t *table = a.block_table ? a.block_table + r * a.table_stride : nullptr;
+    // block of the first key of this warp's part of a tile (0 behind the end)
+    auto block_of = [&](int kt) {
+      const int k = kt * KT + warp * B;
+      return table && kt < stop && k < end ? table[k / a.block_size] : 0;
+    };
+    int id = block_of(tile);
+    for (int kt = tile; kt < stop; ++kt) {
+      const int k0 = kt * KT + warp * B, nk = min(B, end - k0);
+      const int mine = id;
+      id = block_of(kt + 1);
+      if (nk <= 0) continue;
+      if (table && (mine < 0 || mine >= a.num_blocks)) {
+        if (lane == 0) atomicOr(status, kDevBadBlock);
+        continue;
+      }
+      int64_t kp, vp, ks, vs;  // first row, distance of rows
+      if (table) {
+        kp = vp = mine * a.block_stride +
+                  static_cast<int64_t>(h * a.block_size + k0 % a.block_size) * hd;
+        ks = vs = hd;
+      } else {
+        ks = a.k_stride;
+        vs = a.v_stride;
+        kp = (static_cast<int64_t>(q.q0) + k0) * ks + static_cast<int64_t>(h) * hd;
+        vp = (static_cast<int64_t>(q.q0) + k0) * vs + static_cast<int64_t>(h) * hd;
+      }
+      float4 kv[B][NC], vv[B][NC];
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = 4 * lane + 128 * c;
+          kv[k][c] = k < nk && d < hd ? load_x4<BF16>(a.k, kp + k * ks + d)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = 4 * lane + 128 * c;
+          vv[k][c] = k < nk && d < hd ? load_x4<BF16>(a.v, vp + k * vs + d)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      float s[N];
+#pragma unroll
+      for (int p = 0; p < RR; ++p)
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          float acc = 0.0f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            acc = fmaf(qv[p][c].x, kv[k][c].x, acc);
+            acc = fmaf(qv[p][c].y, kv[k][c].y, acc);
+            acc = fmaf(qv[p][c].z, kv[k][c].z, acc);
+            acc = fmaf(qv[p][c].w, kv[k][c].w, acc);
+          }
+          s[p * B + k] = acc;
+        }
+      reduce_scatter<N>(s, lane);
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        if (k0 + skey + j >= vis || skey + j >= nk) s[j] = -INFINITY;
+        top = fmaxf(top, s[j]);
+      }
+#pragma unroll
+      for (int w = C::dup; w < C::dup * (B / PL); w <<= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
+      const bool grow = top > m;
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float f = grow ? ex2(m - top) : 1.0f;  // m = -inf: 0
+        if (grow) m = top;
+        l *= f;
+#pragma unroll
+        for (int p = 0; p < RR; ++p) {
+          const float fp = __shfl_sync(0xFFFFFFFFu, f, p * B / PL * C::dup);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            o[p][c].x *= fp;
+            o[p][c].y *= fp;
+            o[p][c].z *= fp;
+            o[p][c].w *= fp;
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        s[j] = ex2(s[j] - ref);
+        l += s[j];
+      }
+      const bool guard = k0 + B > all;  // some row misses some key: not even 0 * NaN
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int p = 0; p < RR; ++p) {
+          const int v = p * B + k;
+          const float w = __shfl_sync(0xFFFFFFFFu, s[v % PL], v / PL * C::dup);
+          if (guard && w == 0.0f) continue;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            o[p][c].x = fmaf(w, vv[k][c].x, o[p][c].x);
+            o[p][c].y = fmaf(w, vv[k][c].y, o[p][c].y);
+            o[p][c].z = fmaf(w, vv[k][c].z, o[p][c].z);
+            o[p][c].w = fmaf(w, vv[k][c].w, o[p][c].w);
+          }
+        }
+    }
+    // the row's sum over its lanes, then the warps' parts together
+#pragma unroll
+    for (int w = C::dup; w < C::dup * (B / PL); w <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, w);
+    if (skey == 0 && lane % C::dup == 0) {
+      wm[warp][srow] = m;
+      wl[warp][srow] = l;
+    }
+#pragma unroll
+    for (int p = 0; p < RR; ++p)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        *reinterpret_cast<float4 *>(wo + ((warp * RR + p) * NC + c) * 128 + 4 * lane) = o[p][c];
+    __syncthreads();
+    const bool whole = tile == 0 && stop == ntile;
+    const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);
+    for (int e = tid; e < RR * NC * 32; e += kThreads) {
+      const int p = e / (NC * 32), d = 4 * (e - p * (NC * 32));
+      if (p >= rows || d >= hd) continue;
+      float M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][p]);
+      const float ref = M == -INFINITY ? 0.0f : M;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(wm[w][p] - ref);
+        if (f == 0.0f) continue;
+        const float4 v = *reinterpret_cast<const float4 *>(wo + (w * RR + p) * NC * 128 + d);
+        L = fmaf(f, wl[w][p], L);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (whole) {
+        const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+        const int t = p / g, hq = p - t * g;
+        store_y4(a.y, (static_cast<int64_t>(q.q0 + t0 + t) * a.n_head + head0 + hq) * hd + d,
+                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), a.y_bf16);
+      } else {
+        const int64_t base = static_cast<int64_t>(slot) * parts.rows + p;
+        if (d == 0) parts.ml[base] = make_float2(M, L);
+        *reinterpret_cast<float4 *>(parts.o + base * hd + d) = acc;
+      }
+    }
+    __syncthreads();
+    if (tid == 0 && tile == 0 && !whole)
+      parts.open[blockIdx.x] =
+          AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, sched_weight(sc, q, i), ntile)};
+  }
+  zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
+}
+
+template <bool BF16, int NC, int RR>
+cudaError_t run_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
+                     const AttnParts &parts, cudaStream_t s) {
+  auto kern = attn_rows_kernel<BF16, NC, RR>;
+  constexpr int smem = kWarps * RR * NC * 128 * 4;
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
+  if (e != cudaSuccess) return e;
+  uint32_t *status = device_status();
+  if (!status) return cudaErrorInvalidDevice;
+  return launch_pdl(kern, dim3(p.workers), dim3(kThreads), smem, s, a, sc, p.gsub, p.nsub, parts,
+                    status);
+}
+
+template <bool BF16>
+cudaError_t pick_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
+                      const AttnParts &parts, cudaStream_t s) {
+  if (a.head_dim <= 128) {
+    if (p.rows == 1) return run_rows<BF16, 1, 1>(a, p, sc, parts, s);
+    if (p.rows == 2) return run_rows<BF16, 1, 2>(a, p, sc, parts, s);
+    if (p.rows == 4) return run_rows<BF16, 1, 4>(a, p, sc, parts, s);
+    return run_rows<BF16, 1, 8>(a, p, sc, parts, s);
+  }
+  if (a.head_dim <= 256) {
+    if (p.rows <= 2) return run_rows<BF16, 2, 2>(a, p, sc, parts, s);
+    return run_rows<BF16, 2, 4>(a, p, sc, parts, s);
+  }
+  return run_rows<BF16, 4, 2>(a, p, sc, parts, s);
+}
+
+}  // namespace
+
+// Calls with few query rows per request and key/value head: at most 8, 4 or 2
+// of them (what a thread's registers hold of queries and results at 128, 256
+// and 512 columns).
+bool attn_rows_plan(int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p) {
+  const int most = head_dim <= 128 ? 8 : head_dim <= 256 ? 4 : 2;
+  const int grp = n_head / n_kv;
+  if (R < 1 || grp > most || T * grp > static_cast<int64_t>(most) * R) return false;
+  const int avg = static_cast<int>((T * grp + R - 1) / R);
+  int rows = head_dim <= 128 ? 1 : 2;
+  while (rows < avg || rows < grp) rows *= 2;
+  p->rows = rows;
+  p->gsub = grp;
+  p->nsub = 1;
+  p->U = rows / grp;
+  p->half = 0;
+  p->w_half = p->w_full = 1;
+  p->KT = head_dim <= 128 ? 64 : head_dim <= 256 ? 32 : 16;
+  p->fixed = 2 * p->KT;
+  p->min_run = 2 * p->KT;
+  p->workers = sm_count() * 2;
+  return true;
+}
+
+cudaError_t launch_attn_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
+                             const AttnParts &parts, cudaStream_t s) {
+  return a.bf16 ? pick_rows<true>(a, p, sc, parts, s) : pick_rows<false>(a, p, sc, parts, s);
+}
+
+}  // namespace qmm

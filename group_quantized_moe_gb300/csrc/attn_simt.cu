@@ -328,8 +328,7 @@ int simt_nc(int head_dim) { return head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : he
 
 }  // namespace
 
-AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R) {
-  (void)bf16;
+AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R) {
   const int grp = n_head / n_kv;
   AttnPlan p;
   p.rows = T * grp <= static_cast<int64_t>(16) * R ? 16 : 64;
