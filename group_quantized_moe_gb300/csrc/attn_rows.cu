@@ -5,8 +5,9 @@
 // The work is bound by reading the cache once, so the kernel keeps many wide
 // loads in flight and spends few instructions on a key.  A warp takes B
 // consecutive keys at a time (one block's; the eight warps of a CTA cover a
-// KT = 8 B key tile), lane l holding columns 4 l + 128 c of the keys, values,
-// queries and results in registers.  The RR x B partial dot products are
+// KT = 8 B key tile; up to 64 columns, each half of a warp takes its own B
+// keys), lane l holding columns 4 l + 128 c of the keys, values, queries and
+// results in registers.  The RR x B partial dot products are
 // reduced over the lanes by halving (every step sends the half of the values
 // that the other lane keeps: RR B - 1 exchanges instead of 5 RR B), which
 // leaves the score of one (row, key) per lane; each lane keeps the running
@@ -32,22 +33,28 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// NC: 128-column groups of the head size; RR: query rows of a unit.
-template <int NC, int RR>
+// NC: 128-column groups of the head size; RR: query rows of a unit; LK: lanes
+// that share a key (a "team"; 16 for up to 64 columns).
+template <int NC, int RR, int LK>
 struct Rows {
-  static constexpr int B = NC == 1 ? 8 : NC == 2 ? 4 : 2;  // keys of a warp at a time
-  static constexpr int KT = kWarps * B;
-  static constexpr int N = RR * B;                         // scores of a warp at a time
-  static constexpr int per_lane = N > 32 ? N / 32 : 1;     // ... of a lane
-  static constexpr int dup = N < 32 ? 32 / N : 1;          // lanes with the same score
+  static constexpr int B = NC == 1 ? 8 : NC == 2 ? 4 : 2;  // keys of a team at a time
+  static constexpr int teams = kThreads / LK;
+  static constexpr int KT = teams * B;
+  static constexpr int N = RR * B;                         // scores of a team at a time
+  static constexpr int per_lane = N > LK ? N / LK : 1;     // ... of a lane
+  static constexpr int dup = N < LK ? LK / N : 1;          // lanes with the same score
+  // CTAs per SM: one where the registers of two would spill (measured: 4 rows
+  // of 128 columns gain from the second CTA in spite of a few spilled words)
+  static constexpr int per_sm = NC * RR <= 4 ? 2 : 1;
 };
 
-// v[i] summed over the lanes: lane l is left with values per_lane (l / dup) + j.
-template <int N>
+// v[i] summed over the team's lanes: lane l is left with values
+// per_lane (l / dup) + j.
+template <int N, int LK>
 __device__ __forceinline__ void reduce_scatter(float (&v)[N], int lane) {
   int n = N;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
+  for (int o = LK / 2; o >= 1; o >>= 1) {
     if (n > 1) {
       const bool up = lane & o;
 #pragma unroll
@@ -63,17 +70,18 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[N], int lane) {
   }
 }
 
-template <bool BF16, int NC, int RR>
-__global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, AttnSched sc, int gsub,
-                                                                int nsub, AttnParts parts,
-                                                                uint32_t *status) {
-  using C = Rows<NC, RR>;
-  constexpr int B = C::B, KT = C::KT, N = C::N, PL = C::per_lane;
+template <bool BF16, int NC, int RR, int LK>
+__global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
+    attn_rows_kernel(AttnBatch a, AttnSched sc, int gsub, int nsub, AttnParts parts,
+                     uint32_t *status) {
+  using C = Rows<NC, RR, LK>;
+  constexpr int B = C::B, KT = C::KT, N = C::N, PL = C::per_lane, CW = NC * 4 * LK;
   __shared__ int64_t scratch[kWarps + 4];
-  __shared__ float wm[kWarps][RR], wl[kWarps][RR];
-  extern __shared__ __align__(16) float wo[];  // [warp][row][NC * 128]
+  __shared__ float wm[C::teams][RR], wl[C::teams][RR];
+  extern __shared__ __align__(16) float wo[];  // [team][row][CW]
   pdl_enter();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, team = tid / LK, lane = tid % LK;
+  const int base_lane = (tid & 31) - lane;  // the team's first lane in its warp
   const int hd = a.head_dim, grp = a.n_head / a.n_kv;
   const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
@@ -110,34 +118,32 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, Att
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int d = 4 * lane + 128 * c;
-        qv[p][c] = p < rows && d < hd
-                       ? load_x4<BF16>(a.q, static_cast<int64_t>(q.q0 + t0 + t) * a.q_stride +
-                                                static_cast<int64_t>(head0 + hq) * hd + d)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-        qv[p][c].x *= sl2;  // scores in log2 units
-        qv[p][c].y *= sl2;
-        qv[p][c].z *= sl2;
-        qv[p][c].w *= sl2;
+        const float4 v = p < rows && d < hd
+                             ? load_x4<BF16>(a.q, static_cast<int64_t>(q.q0 + t0 + t) * a.q_stride +
+                                                      static_cast<int64_t>(head0 + hq) * hd + d)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        qv[p][c] = make_float4(v.x * sl2, v.y * sl2, v.z * sl2, v.w * sl2);  // scores in log2 units
         o[p][c] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
     float m = -INFINITY, l = 0.0f;  // of this lane's row; l over this lane's keys
     const int32_t *table = a.block_table ? a.block_table + r * a.table_stride : nullptr;
-    // block of the first key of this warp's part of a tile (0 behind the end)
+    // block of the first key of this team's part of a tile (0 behind the end)
     auto block_of = [&](int kt) {
-      const int k = kt * KT + warp * B;
+      const int k = kt * KT + team * B;
       return table && kt < stop && k < end ? table[k / a.block_size] : 0;
     };
     int id = block_of(tile);
     for (int kt = tile; kt < stop; ++kt) {
-      const int k0 = kt * KT + warp * B, nk = min(B, end - k0);
+      const int k0 = kt * KT + team * B;
+      int nk = max(0, min(B, end - k0));  // the team's keys; the warp's teams stay together
       const int mine = id;
       id = block_of(kt + 1);
-      if (nk <= 0) continue;
-      if (table && (mine < 0 || mine >= a.num_blocks)) {
+      if (table && nk > 0 && (mine < 0 || mine >= a.num_blocks)) {
         if (lane == 0) atomicOr(status, kDevBadBlock);
-        continue;
+        nk = 0;
       }
+      if (LK == 32 ? nk == 0 : !__any_sync(0xFFFFFFFFu, nk > 0)) continue;
       int64_t kp, vp, ks, vs;  // first row, distance of rows
       if (table) {
         kp = vp = mine * a.block_stride +
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, Att
           }
           s[p * B + k] = acc;
         }
-      reduce_scatter<N>(s, lane);
+      reduce_scatter<N, LK>(s, lane);
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < PL; ++j) {
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, Att
         l *= f;
 #pragma unroll
         for (int p = 0; p < RR; ++p) {
-          const float fp = __shfl_sync(0xFFFFFFFFu, f, p * B / PL * C::dup);
+          const float fp = __shfl_sync(0xFFFFFFFFu, f, base_lane + p * B / PL * C::dup);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             o[p][c].x *= fp;
@@ -214,13 +220,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, Att
         s[j] = ex2(s[j] - ref);
         l += s[j];
       }
-      const bool guard = k0 + B > all;  // some row misses some key: not even 0 * NaN
+      // some row of some team misses some key: not even 0 * NaN may enter
+      const bool guard = LK == 32 ? k0 + B > all : __any_sync(0xFFFFFFFFu, k0 + B > all || nk < B);
 #pragma unroll
       for (int k = 0; k < B; ++k)
 #pragma unroll
         for (int p = 0; p < RR; ++p) {
           const int v = p * B + k;
-          const float w = __shfl_sync(0xFFFFFFFFu, s[v % PL], v / PL * C::dup);
+          const float w = __shfl_sync(0xFFFFFFFFu, s[v % PL], base_lane + v / PL * C::dup);
           if (guard && w == 0.0f) continue;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
@@ -231,34 +238,34 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, Att
           }
         }
     }
-    // the row's sum over its lanes, then the warps' parts together
+    // the row's sum over its lanes, then the teams' parts together
 #pragma unroll
     for (int w = C::dup; w < C::dup * (B / PL); w <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, w);
     if (skey == 0 && lane % C::dup == 0) {
-      wm[warp][srow] = m;
-      wl[warp][srow] = l;
+      wm[team][srow] = m;
+      wl[team][srow] = l;
     }
 #pragma unroll
     for (int p = 0; p < RR; ++p)
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        *reinterpret_cast<float4 *>(wo + ((warp * RR + p) * NC + c) * 128 + 4 * lane) = o[p][c];
+        *reinterpret_cast<float4 *>(wo + (team * RR + p) * CW + c * 128 + 4 * lane) = o[p][c];
     __syncthreads();
     const bool whole = tile == 0 && stop == ntile;
     const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);
-    for (int e = tid; e < RR * NC * 32; e += kThreads) {
-      const int p = e / (NC * 32), d = 4 * (e - p * (NC * 32));
+    for (int e = tid; e < RR * CW / 4; e += kThreads) {
+      const int p = e / (CW / 4), d = 4 * (e - p * (CW / 4));
       if (p >= rows || d >= hd) continue;
       float M = -INFINITY, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][p]);
+      for (int w = 0; w < C::teams; ++w) M = fmaxf(M, wm[w][p]);
       const float ref = M == -INFINITY ? 0.0f : M;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < C::teams; ++w) {
         const float f = ex2(wm[w][p] - ref);
         if (f == 0.0f) continue;
-        const float4 v = *reinterpret_cast<const float4 *>(wo + (w * RR + p) * NC * 128 + d);
+        const float4 v = *reinterpret_cast<const float4 *>(wo + (w * RR + p) * CW + d);
         L = fmaf(f, wl[w][p], L);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
@@ -284,11 +291,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(AttnBatch a, Att
   zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
 }
 
-template <bool BF16, int NC, int RR>
+template <bool BF16, int NC, int RR, int LK = 32>
 cudaError_t run_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                      const AttnParts &parts, cudaStream_t s) {
-  auto kern = attn_rows_kernel<BF16, NC, RR>;
-  constexpr int smem = kWarps * RR * NC * 128 * 4;
+  using C = Rows<NC, RR, LK>;
+  auto kern = attn_rows_kernel<BF16, NC, RR, LK>;
+  constexpr int smem = C::teams * RR * NC * 4 * LK * 4;
   const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
   uint32_t *status = device_status();
@@ -300,6 +308,12 @@ cudaError_t run_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
 template <bool BF16>
 cudaError_t pick_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                       const AttnParts &parts, cudaStream_t s) {
+  if (a.head_dim <= 64) {
+    if (p.rows == 1) return run_rows<BF16, 1, 1, 16>(a, p, sc, parts, s);
+    if (p.rows == 2) return run_rows<BF16, 1, 2, 16>(a, p, sc, parts, s);
+    if (p.rows == 4) return run_rows<BF16, 1, 4, 16>(a, p, sc, parts, s);
+    return run_rows<BF16, 1, 8, 16>(a, p, sc, parts, s);
+  }
   if (a.head_dim <= 128) {
     if (p.rows == 1) return run_rows<BF16, 1, 1>(a, p, sc, parts, s);
     if (p.rows == 2) return run_rows<BF16, 1, 2>(a, p, sc, parts, s);
@@ -331,7 +345,7 @@ bool attn_rows_plan(int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPl
   p->U = rows / grp;
   p->half = 0;
   p->w_half = p->w_full = 1;
-  p->KT = head_dim <= 128 ? 64 : head_dim <= 256 ? 32 : 16;
+  p->KT = head_dim <= 64 ? 128 : head_dim <= 128 ? 64 : head_dim <= 256 ? 32 : 16;
   p->fixed = 2 * p->KT;
   p->min_run = 2 * p->KT;
   p->workers = sm_count() * 2;
