@@ -122,25 +122,36 @@ PartsLayout parts_layout(const AttnPlan &p, int head_dim) {
   return l;
 }
 
+// Which kernel runs a call, and its plan.
+using Launch = cudaError_t (*)(const AttnBatch &, const AttnPlan &, const AttnSched &,
+                               const AttnParts &, cudaStream_t);
+Launch pick_plan(bool bf16, bool tc, int64_t T, int n_head, int n_kv, int head_dim, int R,
+                 AttnPlan *p) {
+  if (tc) {
+    *p = attn_tc_plan(n_head, n_kv);
+    return launch_attn_tc;
+  }
+  if (attn_rows_plan(T, n_head, n_kv, head_dim, R, p)) return launch_attn_rows;
+  if (attn_tile_plan(bf16, T, n_head, n_kv, head_dim, R, p)) return launch_attn_tile;
+  *p = attn_simt_plan(T, n_head, n_kv, head_dim, R);
+  return launch_attn_simt;
+}
+
 }  // namespace
 
 size_t attn_batch_workspace_bytes(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R) {
   // whether a bf16 call takes the tensor cores also depends on its strides
   AttnPlan p;
-  if (!attn_rows_plan(T, n_head, n_kv, head_dim, R, &p))
-    p = attn_simt_plan(T, n_head, n_kv, head_dim, R);
+  pick_plan(bf16, false, T, n_head, n_kv, head_dim, R, &p);
   const size_t simt = parts_layout(p, head_dim).total;
   const size_t tc = bf16 && head_dim <= 128 ? parts_layout(attn_tc_plan(n_head, n_kv), head_dim).total : 0;
   return simt > tc ? simt : tc;
 }
 
 cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t s) {
-  const bool tc = attn_tc_takes(a);
   AttnPlan p;
-  const bool rows = !tc && attn_rows_plan(a.T, a.n_head, a.n_kv, a.head_dim, a.R, &p);
-  if (!rows)
-    p = tc ? attn_tc_plan(a.n_head, a.n_kv)
-           : attn_simt_plan(a.T, a.n_head, a.n_kv, a.head_dim, a.R);
+  const Launch launch =
+      pick_plan(a.bf16, attn_tc_takes(a), a.T, a.n_head, a.n_kv, a.head_dim, a.R, &p);
   const PartsLayout l = parts_layout(p, a.head_dim);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   AttnParts parts{reinterpret_cast<AttnOpen *>(base + l.open),
@@ -150,9 +161,7 @@ cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t 
                ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, a.T,
                a.block_table ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, INT32_MAX)
                              : a.T};
-  const cudaError_t e =
-      tc ? launch_attn_tc(a, p, sc, parts, s)
-         : rows ? launch_attn_rows(a, p, sc, parts, s) : launch_attn_simt(a, p, sc, parts, s);
+  const cudaError_t e = launch(a, p, sc, parts, s);
   if (e != cudaSuccess) return e;
   return launch_attn_join(a, p, parts, s);
 }

@@ -33,6 +33,10 @@ cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSc
 bool attn_rows_plan(int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p);
 cudaError_t launch_attn_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                              const AttnParts &parts, cudaStream_t s);
+// The form for many rows in fp32; false: not for this call.
+bool attn_tile_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p);
+cudaError_t launch_attn_tile(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
+                             const AttnParts &parts, cudaStream_t s);
 // The tensor-core form: whether it takes a call, its plan, its launch.
 bool attn_tc_takes(const AttnBatch &a);
 AttnPlan attn_tc_plan(int n_head, int n_kv);
