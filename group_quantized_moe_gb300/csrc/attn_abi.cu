@@ -72,6 +72,8 @@ int log2i(int v) {
   return s;
 }
 
+constexpr int64_t kMaxKeys = (int64_t(1) << 29) - 1;  // of one request (costs of a unit fit 32 bits)
+
 // What both attention calls check: T query rows, the lengths, scale, output,
 // workspace.
 int check_attn(const char *who, const void *q, int64_t T, int64_t q_stride, int n_head, int n_kv,
@@ -83,6 +85,7 @@ int check_attn(const char *who, const void *q, int64_t T, int64_t q_stride, int 
     return refuse(QMM_ERR_INVALID_ARG, "%s: dtypes must be QMM_F32 or QMM_BF16", who);
   if (T < 0 || T > (int64_t(1) << 31) - 1 || R < 0)
     return refuse(QMM_ERR_SHAPE, "%s: T must be in [0, 2^31) and the request count >= 0", who);
+  if (T > kMaxKeys) return refuse(QMM_ERR_UNSUPPORTED, "%s: 2^29 rows or more", who);
   if (!(scale >= 0.0f) || std::isinf(scale))
     return refuse(QMM_ERR_INVALID_ARG, "%s: scale must be finite and positive (0: 1 / sqrt(head_dim))",
                   who);
@@ -159,7 +162,7 @@ cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t 
                   p.rows};
   AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, p.half, p.w_half, p.w_full, log2i(p.KT), p.fixed, p.min_run,
                ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, a.T,
-               a.block_table ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, INT32_MAX)
+               a.block_table ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, kMaxKeys)
                              : a.T};
   const cudaError_t e = launch(a, p, sc, parts, s);
   if (e != cudaSuccess) return e;

@@ -36,14 +36,14 @@ struct AttnSched {
   int R;
   int nvh;             // key/value heads (times the splits of a large query group)
   int U, half;         // tokens per unit, and in the first of its query tiles
-  int w_half, w_full;  // cost of a key
+  int w_half, w_full;  // cost of a key, 1 to 3
   int kt_shift;        // log2 of the keys per tile
   int fixed;           // cost of a unit besides its keys
   int min_run;         // a worker's run costs at least this much (w_full KT or more, so
                        // that no run inside a unit is without a tile of it)
   uint64_t per_worker; // 2^64 / workers, rounded up
   int64_t T;           // query rows in the buffers
-  int64_t cap;         // largest cache length the block table can hold
+  int64_t cap;         // largest cache length the block table can hold (below 2^29)
 };
 
 struct AttnReq {
@@ -115,13 +115,17 @@ struct AttnRun {
 // head): the quotient in fp32, put right; far shorter than a 64-bit division.
 __device__ __forceinline__ int small_quotient(int64_t a, int64_t b) {
   int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+#pragma unroll 1
   while (static_cast<int64_t>(q) * b > a) --q;
+#pragma unroll 1
   while ((static_cast<int64_t>(q) + 1) * b <= a) ++q;
   return q;
 }
 
 // The run of worker w, by all NT threads of a block.  scratch: 8 (NT / 32 + 4)
-// bytes of shared memory.  A worker without work gets first >= last.
+// bytes of shared memory.  A worker without work gets first >= last.  (Written
+// for few instructions: at the start of a call all of them are fetched from
+// far, which costs more than executing them.)
 template <int NT>
 __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t *scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -139,11 +143,10 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
   int64_t lo = inc - mine, W = 0;  // lo: cost before this thread's requests
-#pragma unroll 4
+#pragma unroll 1
   for (int k = 0; k < NT / 32; ++k) {
-    const int64_t v = scratch[k];
-    if (k < warp) lo += v;
-    W += v;
+    if (k == warp) lo += W;
+    W += scratch[k];
   }
   AttnRun run;
   const int64_t even = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(W), s.per_worker)) + 1;
@@ -153,20 +156,30 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
   int64_t *found = scratch + NT / 32;
   if (run.first < run.last && run.first >= lo && run.first < lo + mine) {
     int r = r0;
-    AttnReq q = sched_req(s, r);
+    AttnReq q;
 #pragma unroll 1
-    for (int64_t c = sched_cost(s, q); run.first >= lo + c && r + 1 < r1; c = sched_cost(s, q)) {
+    for (;; ++r) {
+      q = sched_req(s, r);
+      const int64_t c = sched_cost(s, q);
+      if (run.first < lo + c || r + 1 >= r1) break;
       lo += c;
-      q = sched_req(s, ++r);
     }
-    int a = 0, b = sched_blocks(s, q);  // the block whose units hold the start
+    // the block whose units hold the start: all heads of the blocks before
+    // block a cost `before`
+    int a = 0, b = sched_blocks(s, q);
+    int64_t before = 0;
 #pragma unroll 1
     while (b - a > 1) {
       const int mid = (a + b) >> 1;
-      if (lo + sched_before(s, q, mid) * s.nvh <= run.first) a = mid;
-      else b = mid;
+      const int64_t c = sched_before(s, q, mid) * s.nvh;
+      if (lo + c <= run.first) {
+        a = mid;
+        before = c;
+      } else {
+        b = mid;
+      }
     }
-    lo += sched_before(s, q, a) * s.nvh;
+    lo += before;
     const int64_t cost = sched_unit(s, q, a);
     const int h = small_quotient(run.first - lo, cost);
     found[0] = r;
@@ -184,14 +197,21 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
 }
 
 // The tiles [tile, stop) of a unit of ntile tiles at cost x whose first keys
-// the run holds (weight: its sched_weight); a cut inside the fixed cost leaves
-// all tiles to the later run.
+// the run holds (weight: its sched_weight, 1 to 3); a cut inside the fixed
+// cost leaves all tiles to the later run.
+__device__ __forceinline__ int sched_cut(const AttnSched &s, int64_t at, int weight, int ntile) {
+  const int64_t all = static_cast<int64_t>(ntile) * weight << s.kt_shift;
+  if (at <= 0) return 0;
+  if (at >= all) return ntile;
+  // ceil(at / (weight KT)); a unit's cost fits 32 bits (L < 2^29)
+  const uint32_t t = (static_cast<uint32_t>(at) + (1u << s.kt_shift) - 1) >> s.kt_shift;
+  return static_cast<int>(weight == 3 ? (t + 2) / 3 : (t + weight - 1) >> (weight - 1));
+}
+
 __device__ __forceinline__ void sched_part(const AttnSched &s, const AttnRun &run, int64_t x,
                                            int weight, int ntile, int &tile, int &stop) {
-  const int64_t t = static_cast<int64_t>(weight) << s.kt_shift;
-  const int64_t a = run.first - x - s.fixed, b = run.last - x - s.fixed;
-  tile = a <= 0 ? 0 : small_quotient(a + t - 1, t);
-  stop = b <= 0 ? 0 : b > ntile * t ? ntile : small_quotient(b + t - 1, t);
+  tile = sched_cut(s, run.first - x - s.fixed, weight, ntile);
+  stop = sched_cut(s, run.last - x - s.fixed, weight, ntile);
 }
 
 // The worker that has a unit's last tile.

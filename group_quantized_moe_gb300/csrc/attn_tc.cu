@@ -113,19 +113,20 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
-// Zeroes the non-finite bf16 values of eight; whether there were any.
-__device__ __forceinline__ bool drop_nonfinite(uint4 &t) {
+// Not zero when one of eight bf16 values is not finite (its exponent, all ones,
+// carries into the sign's place).
+__device__ __forceinline__ uint32_t nonfinite_bits(uint4 t) {
+  return (((t.x & 0x7FFF7FFFu) + 0x00800080u) | ((t.y & 0x7FFF7FFFu) + 0x00800080u) |
+          ((t.z & 0x7FFF7FFFu) + 0x00800080u) | ((t.w & 0x7FFF7FFFu) + 0x00800080u)) & 0x80008000u;
+}
+__device__ __forceinline__ uint4 drop_nonfinite(uint4 t) {
   uint32_t w[4] = {t.x, t.y, t.z, t.w};
-  uint32_t hit = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t m = (nonfinite_bf16(w[k]) ? 0xFFFFu : 0u) |
-                       (nonfinite_bf16(w[k] >> 16) ? 0xFFFF0000u : 0u);
-    w[k] &= ~m;
-    hit |= m;
+    if (nonfinite_bf16(w[k])) w[k] &= 0xFFFF0000u;
+    if (nonfinite_bf16(w[k] >> 16)) w[k] &= 0xFFFFu;
   }
-  t = make_uint4(w[0], w[1], w[2], w[3]);
-  return hit != 0;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Value tiles are [key][column] in shared memory, columns contiguous: for the
@@ -142,6 +143,25 @@ __device__ __forceinline__ uint64_t desc_values(uint32_t addr) {
 __device__ __forceinline__ uint32_t idesc_bf16(int n, bool values) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (values ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// wait_ok in few instructions (there are many waits, and the roles' code shares
+// the instruction caches).
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t *status,
+                                         volatile int *abort_flag) {
+  uint32_t since = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    uint32_t now;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+    if (since == 0) since = now & ~1u;
+    if (*abort_flag || now - since > static_cast<uint32_t>(kWaitLimitNs)) {
+      *abort_flag = 1;
+      atomicOr(status, kDevWaitTimeout);
+      return false;
+    }
+  }
+  return true;
 }
 
 // One unit of this worker's run, as the roles see it.
@@ -260,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nch = NCH == 1 ? 1 : (hd + 63) / 64;  // chunks that hold columns
   // the whole warp waits for a barrier
   auto wait_warp = [&](uint32_t bar, uint32_t parity) {
-    return __all_sync(0xFFFFFFFFu, wait_ok(bar, parity, p.status, abort_flag)) != 0;
+    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, p.status, abort_flag)) != 0;
   };
 
   // 384 threads launched with 168 registers: 2 x 208 + 88 = 3 x 168
@@ -325,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pub = 0, n = 0, loads[2] = {0, 0};  // units handed out, served; tiles loaded
       bool more = true, ok = true;
       while (ok) {
-        for (; ok && more && pub < n + 3; ++pub) {
+        // the first unit's queries go out before the next units are looked up
+        for (; ok && more && pub < (n == 0 ? 1 : n + 3); ++pub) {
           ok = wait_warp(u_free(pub), ((pub / kUnits) & 1u) ^ 1u);
           if (ok) more = publish(pub);
         }
@@ -422,29 +443,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const int k0 = kt * kKT;
             if (kv && k0 + kKT > all) {
-              const int lo = max(0, all - k0), hi = max(lo, min(kKT, end - k0));
+              // Keys from `lo` on are missed by some row, from `hi` on by all of
+              // them (their rows may hold anything).  Eight lanes read a row of
+              // a chunk, eight reads in flight.
+              const int lo = max(0, all - k0), hi = end - k0;
               uint8_t *v = gbase + C::kv_off + s * C::tile + (lane & 7) * 16;
               bool found = false;
-              // eight lanes a row of a chunk, four rows a step, four steps at once
 #pragma unroll 1
               for (int c = 0; c < nch; ++c, v += kChunk) {
 #pragma unroll 1
-                for (int r0 = lo + (lane >> 3); r0 < hi; r0 += 16) {
-                  uint4 t[4];
+                for (int r0 = (lo & ~3) + (lane >> 3); r0 < kKT; r0 += 32) {
+                  uint32_t hit = 0;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    t[k] = r0 + 4 * k < hi ? *reinterpret_cast<const uint4 *>(v + (r0 + 4 * k) * 128)
-                                           : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if (drop_nonfinite(t[k])) {
-                      *reinterpret_cast<uint4 *>(v + (r0 + 4 * k) * 128) = t[k];
-                      found = true;
+                  for (int k = 0; k < 8; ++k) {
+                    const int r = min(r0 + 4 * k, kKT - 1);
+                    hit |= nonfinite_bits(*reinterpret_cast<const uint4 *>(v + r * 128));
+                  }
+                  if (hit) {
+#pragma unroll 1
+                    for (int r = r0; r < min(r0 + 32, kKT); r += 4) {
+                      if (r < lo) continue;
+                      uint4 *t = reinterpret_cast<uint4 *>(v + r * 128);
+                      const uint4 x = *t;
+                      if (!nonfinite_bits(x)) continue;
+                      *t = drop_nonfinite(x);
+                      if (r < hi) found = true;
                     }
                   }
                 }
-                for (int r = hi + (lane >> 3); r < kKT; r += 4)
-                  *reinterpret_cast<uint4 *>(v + r * 128) = make_uint4(0u, 0u, 0u, 0u);
               }
               if (found) marked[un & 15u] = static_cast<int>(un + 1);
               fence_proxy_async_smem();
@@ -477,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pairs = 0;                 // units with two query tiles so far
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        return wait_ok(bar, parity, p.status, abort_flag);
+        return wait_bar(bar, parity, p.status, abort_flag);
       };
       for (uint32_t un = 0; ok; ++un) {
         if (!wait(u_full(un), (un / kUnits) & 1u)) break;
@@ -748,98 +774,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (busy) {
           const bool whole = u.tile == 0 && u.stop == u.ntile;
           const float inv = whole ? (l > 0.0f || l != l ? 1.0f / l : 0.0f) : 1.0f;
+          // row `line` of the partial result's slot, or of the output from the
+          // unit's first row on
+          const int line = whole ? (tw + tok) * p.a.n_head + hq : (tw + tok) * u.g + hq;
           const int64_t slot = (2 * blockIdx.x + (u.tile == 0 ? 1 : 0)) *
-                                   static_cast<int64_t>(p.parts.rows) + (tw + tok) * u.g + hq;
-          const int64_t y0 = (static_cast<int64_t>(u.q_row + tw + tok) * p.a.n_head + u.head0 + hq) * hd;
+                               static_cast<int64_t>(p.parts.rows);
           const bool bf16 = whole && p.a.y_bf16;
-          uint8_t *out = !whole ? reinterpret_cast<uint8_t *>(p.parts.o + slot * hd)
-                                : static_cast<uint8_t *>(p.a.y) + y0 * (bf16 ? 2 : 4);
-          if (!whole && live) p.parts.ml[slot] = make_float2(m == -INFINITY ? m : m * p.sl2, l);
-          // 32 columns of the result as floats
-          auto piece = [&](int c, float (&v)[32]) {
-            uint32_t o[32];
-            if (have)
+          const int esize = bf16 ? 2 : 4, bytes = hd * esize;  // of an element, of a row
+          uint8_t *out0 =
+              whole ? static_cast<uint8_t *>(p.a.y) +
+                          (static_cast<int64_t>(u.q_row) * p.a.n_head + u.head0) * bytes
+                    : reinterpret_cast<uint8_t *>(p.parts.o + slot * hd);
+          uint8_t *out = out0 + static_cast<int64_t>(line) * bytes;
+          if (!whole && live)
+            p.parts.ml[slot + line] = make_float2(m == -INFINITY ? m : m * p.sl2, l);
+          const float k0 = f0 * inv, k1 = f1 * inv;
+          // STAGED: a thread holds a row, and rows lie far apart: stored from
+          // here, one instruction would touch 32 lines.  128 bytes of each row
+          // go through shared memory (16-byte units swizzled by the row), and
+          // eight lanes store one row's.
+          uint8_t *stage = gbase + C::out_off + warp * 4096;
+#pragma unroll 1
+          for (int c = 0; c < ochunks; ++c) {
+            float v[32];
+            {
+              uint32_t o[32];
               tmem_ld32(to + 32 * c, o);
-            else
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = 0u;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (f0 * inv);
+              for (int j = 0; j < 32; ++j) v[j] = have ? __uint_as_float(o[j]) * k0 : 0.0f;
+            }
             if (join) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const float4 t = *reinterpret_cast<const float4 *>(xat(8 * c + j));
-                v[4 * j] = fmaf(t.x, f1 * inv, v[4 * j]);
-                v[4 * j + 1] = fmaf(t.y, f1 * inv, v[4 * j + 1]);
-                v[4 * j + 2] = fmaf(t.z, f1 * inv, v[4 * j + 2]);
-                v[4 * j + 3] = fmaf(t.w, f1 * inv, v[4 * j + 3]);
+                v[4 * j] = fmaf(t.x, k1, v[4 * j]);
+                v[4 * j + 1] = fmaf(t.y, k1, v[4 * j + 1]);
+                v[4 * j + 2] = fmaf(t.z, k1, v[4 * j + 2]);
+                v[4 * j + 3] = fmaf(t.w, k1, v[4 * j + 3]);
               }
             }
-          };
-          if constexpr (!STAGED) {
-#pragma unroll 1
-            for (int c = 0; c < ochunks; ++c) {
-              float v[32];
-              piece(c, v);
-#pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                const int d = 32 * c + j;
-                if (live && d < hd) {
-                  if (bf16) {
-                    *reinterpret_cast<uint4 *>(out + d * 2) =
-                        make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
-                                   bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
-                  } else {
-                    float4 *y4 = reinterpret_cast<float4 *>(out + d * 4);
-                    y4[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                    y4[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
-                  }
-                }
-              }
-            }
-          } else {
-            // A thread holds a row, and rows lie far apart: stored from here, one
-            // instruction would touch 32 lines.  128 bytes of each row go through
-            // shared memory (16-byte units swizzled by the row), and eight lanes
-            // store one row's.
-            uint8_t *stage = gbase + C::out_off + warp * 4096;
+            // 16-byte unit j of this piece of the row
             auto put = [&](int j, uint4 t) {
-              *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = t;
+              if constexpr (STAGED)
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = t;
+              else if (live && c * 32 * esize + 16 * j < bytes)
+                *reinterpret_cast<uint4 *>(out + c * 32 * esize + 16 * j) = t;
             };
-            const uint32_t lives = __ballot_sync(0xFFFFFFFFu, live);
-            const int bytes = hd * (bf16 ? 2 : 4);  // of a row
-#pragma unroll 1
-            for (int b0 = 0; b0 < bytes; b0 += 128) {
-              float v[32];
-              if (bf16) {
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                  const int c = (b0 >> 6) + k;
-                  if (c >= ochunks) break;
-                  piece(c, v);
+            if (bf16) {
 #pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    put(4 * k + j, make_uint4(bf16x2(v[8 * j], v[8 * j + 1]),
-                                              bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                              bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                                              bf16x2(v[8 * j + 6], v[8 * j + 7])));
-                }
-              } else {
-                piece(b0 >> 7, v);
+              for (int j = 0; j < 4; ++j)
+                put(STAGED ? 4 * (c & 1) + j : j,
+                    make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                               bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7])));
+            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  put(j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                    __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
-              }
+              for (int j = 0; j < 8; ++j)
+                put(j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                  __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+            }
+            if constexpr (STAGED) {
+              if (bf16 && !(c & 1) && c + 1 < ochunks) continue;  // 128 bytes not full yet
+              const int b0 = c * 32 * esize & ~127, j = lane & 7;
+              const bool in = b0 + 16 * j < bytes;
+              uint8_t *col = out0 + b0 + 16 * j;
               __syncwarp();
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const int r = 4 * k + (lane >> 3), j = lane & 7;
-                uint8_t *to_row = reinterpret_cast<uint8_t *>(
-                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), r));
-                if ((lives >> r & 1u) && b0 + 16 * j < bytes)
-                  *reinterpret_cast<uint4 *>(to_row + b0 + 16 * j) =
-                      *reinterpret_cast<const uint4 *>(stage + r * 128 + ((j ^ (r & 7)) << 4));
+                const int r = 4 * k + (lane >> 3);
+                const uint4 t = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((j ^ (r & 7)) << 4));
+                const int at = __shfl_sync(0xFFFFFFFFu, live ? line : -1, r);
+                if (at >= 0 && in) *reinterpret_cast<uint4 *>(col + static_cast<int64_t>(at) * bytes) = t;
               }
               __syncwarp();
             }

@@ -406,7 +406,7 @@ int qmm_attn_prompt(const void *q, const void *k, const void *v, int32_t dtype, 
  * y, scale, workspace and the rest as for qmm_attn_prompt.  Rows of a block
  * beyond L are not used, whatever they hold.  A block index outside the cache
  * leaves its keys out and sets QMM_DEV_BAD_BLOCK; L is held to max_blocks *
- * block_size.
+ * block_size, and to 2^29 - 1.
  */
 size_t qmm_attn_paged_workspace_bytes(const qmm_kv_cache *cache, int64_t T, int32_t n_head,
                                       int32_t R);
