@@ -128,10 +128,10 @@ PartsLayout parts_layout(const AttnPlan &p, int head_dim) {
 // Which kernel runs a call, and its plan.
 using Launch = cudaError_t (*)(const AttnBatch &, const AttnPlan &, const AttnSched &,
                                const AttnParts &, cudaStream_t);
-Launch pick_plan(bool bf16, bool tc, int64_t T, int n_head, int n_kv, int head_dim, int R,
+Launch pick_plan(bool bf16, bool tc, bool paged, int64_t T, int n_head, int n_kv, int head_dim, int R,
                  AttnPlan *p) {
   if (tc) {
-    *p = attn_tc_plan(n_head, n_kv);
+    *p = attn_tc_plan(paged, T, n_head, n_kv, R);
     return launch_attn_tc;
   }
   if (attn_rows_plan(T, n_head, n_kv, head_dim, R, p)) return launch_attn_rows;
@@ -145,22 +145,22 @@ Launch pick_plan(bool bf16, bool tc, int64_t T, int n_head, int n_kv, int head_d
 size_t attn_batch_workspace_bytes(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R) {
   // whether a bf16 call takes the tensor cores also depends on its strides
   AttnPlan p;
-  pick_plan(bf16, false, T, n_head, n_kv, head_dim, R, &p);
+  pick_plan(bf16, false, false, T, n_head, n_kv, head_dim, R, &p);
   const size_t simt = parts_layout(p, head_dim).total;
-  const size_t tc = bf16 && head_dim <= 128 ? parts_layout(attn_tc_plan(n_head, n_kv), head_dim).total : 0;
+  const size_t tc = bf16 && head_dim <= 128 ? parts_layout(attn_tc_plan(false, T, n_head, n_kv, R), head_dim).total : 0;
   return simt > tc ? simt : tc;
 }
 
 cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t s) {
   AttnPlan p;
   const Launch launch =
-      pick_plan(a.bf16, attn_tc_takes(a), a.T, a.n_head, a.n_kv, a.head_dim, a.R, &p);
+      pick_plan(a.bf16, attn_tc_takes(a), a.block_table != nullptr, a.T, a.n_head, a.n_kv, a.head_dim, a.R, &p);
   const PartsLayout l = parts_layout(p, a.head_dim);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   AttnParts parts{reinterpret_cast<AttnOpen *>(base + l.open),
                   reinterpret_cast<float2 *>(base + l.ml), reinterpret_cast<float *>(base + l.o),
                   p.rows};
-  AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, p.half, p.w_half, p.w_full, log2i(p.KT), p.fixed, p.min_run,
+  AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, log2i(p.KT), p.fixed, p.min_run,
                ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, a.T,
                a.block_table ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, kMaxKeys)
                              : a.T};

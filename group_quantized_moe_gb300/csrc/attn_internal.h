@@ -21,9 +21,9 @@ struct AttnParts {
 
 // How a call is cut up: rows (query rows of a unit), the query heads gsub of
 // a group that one unit takes (nsub units cover the group), tokens U and keys
-// KT of a tile, workers (the rest: see AttnSched).
+// KT of a tile, workers (fixed, min_run: see AttnSched).
 struct AttnPlan {
-  int rows, gsub, nsub, U, half, w_half, w_full, KT, fixed, min_run, workers;
+  int rows, gsub, nsub, U, KT, fixed, min_run, workers;
 };
 
 AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R);
@@ -39,7 +39,7 @@ cudaError_t launch_attn_tile(const AttnBatch &a, const AttnPlan &p, const AttnSc
                              const AttnParts &parts, cudaStream_t s);
 // The tensor-core form: whether it takes a call, its plan, its launch.
 bool attn_tc_takes(const AttnBatch &a);
-AttnPlan attn_tc_plan(int n_head, int n_kv);
+AttnPlan attn_tc_plan(bool paged, int64_t T, int n_head, int n_kv, int R);
 cudaError_t launch_attn_tc(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                            const AttnParts &parts, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnBatch &a, const AttnPlan &p, const AttnParts &parts,

@@ -79,11 +79,10 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
   __shared__ int64_t scratch[kWarps + 4];
   __shared__ float wm[C::teams][RR], wl[C::teams][RR];
   extern __shared__ __align__(16) float wo[];  // [team][row][CW]
-  pdl_enter();
   const int tid = threadIdx.x, team = tid / LK, lane = tid % LK;
   const int base_lane = (tid & 31) - lane;  // the team's first lane in its warp
   const int hd = a.head_dim, grp = a.n_head / a.n_kv;
-  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
+  const AttnRun run = sched_start<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
   // this lane's scores: row srow, keys skey + j
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
     const int ntile = sched_tiles(sc, q, i);
     next = x + sched_unit(sc, q, i);
     int tile, stop;
-    sched_part(sc, run, x, sched_weight(sc, q, i), ntile, tile, stop);
+    sched_part(sc, run, x, ntile, tile, stop);
     if (tile >= stop) continue;
     const int h = vh / nsub, sub = vh - h * nsub;
     const int g = min(gsub, grp - sub * gsub);
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
     __syncthreads();
     if (tid == 0 && tile == 0 && !whole)
       parts.open[blockIdx.x] =
-          AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, sched_weight(sc, q, i), ntile)};
+          AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, ntile)};
   }
   zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
 }
@@ -343,8 +342,6 @@ bool attn_rows_plan(int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPl
   p->gsub = grp;
   p->nsub = 1;
   p->U = rows / grp;
-  p->half = 0;
-  p->w_half = p->w_full = 1;
   p->KT = head_dim <= 64 ? 128 : head_dim <= 128 ? 64 : head_dim <= 256 ? 32 : 16;
   p->fixed = 2 * p->KT;
   p->min_run = 2 * p->KT;

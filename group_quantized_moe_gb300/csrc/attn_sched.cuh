@@ -3,9 +3,8 @@
 // A call has R requests; request r has n new tokens (query rows) and L cache
 // rows, and token t of it sees the keys 0 .. L - n + t.  A unit of work is
 // (request, block of U consecutive tokens, key/value head); its cost is the
-// number of keys its last token sees, times `w_half` for a unit of up to `half`
-// tokens (one query tile) and `w_full` for a longer one (two), and `fixed` more
-// for what a unit costs besides (loading its queries, writing its results).  The units
+// number of keys its last token sees, and `fixed` keys more for what a unit
+// costs besides them (loading its queries, writing its results).  The units
 // are laid end to end in the order (request, token block, head) and the cost
 // W of the whole call is cut into equal runs of `step`, worker w's being
 // [w step, (w + 1) step): every worker gets the same work whatever the lengths
@@ -35,11 +34,10 @@ struct AttnSched {
   const int32_t *kvl;  // [R] cache rows, or nullptr: the new tokens themselves
   int R;
   int nvh;             // key/value heads (times the splits of a large query group)
-  int U, half;         // tokens per unit, and in the first of its query tiles
-  int w_half, w_full;  // cost of a key, 1 to 3
+  int U;               // tokens per unit
   int kt_shift;        // log2 of the keys per tile
   int fixed;           // cost of a unit besides its keys
-  int min_run;         // a worker's run costs at least this much (w_full KT or more, so
+  int min_run;         // a worker's run costs at least this much (KT or more, so
                        // that no run inside a unit is without a tile of it)
   uint64_t per_worker; // 2^64 / workers, rounded up
   int64_t T;           // query rows in the buffers
@@ -51,15 +49,17 @@ struct AttnReq {
   int L;      // cache rows
 };
 
-// Request r, held inside the buffers whatever the lengths say.
+// Request r, held inside the buffers whatever the lengths say.  Read past L1: a
+// kernel may look before the one that writes the lengths has ended (see
+// sched_start), and must not find that value again afterwards.
 __device__ __forceinline__ AttnReq sched_req(const AttnSched &s, int r) {
   AttnReq q;
-  const int64_t a = s.cu[r], b = s.cu[r + 1];
+  const int64_t a = __ldcg(s.cu + r), b = __ldcg(s.cu + r + 1);
   const int64_t lo = a < 0 ? 0 : (a > s.T ? s.T : a);
   const int64_t hi = b < lo ? lo : (b > s.T ? s.T : b);
   q.q0 = static_cast<int>(lo);
   q.n = static_cast<int>(hi - lo);
-  int64_t L = s.kvl ? s.kvl[r] : q.n;
+  int64_t L = s.kvl ? __ldcg(s.kvl + r) : q.n;
   if (L < 0) L = 0;
   if (L > s.cap) L = s.cap;
   q.L = static_cast<int>(L);
@@ -81,22 +81,15 @@ __device__ __forceinline__ int sched_tiles(const AttnSched &s, const AttnReq &q,
   return e > kt ? (e + kt - 1) >> s.kt_shift : 1;
 }
 
-// Cost of a key for the units of block i, of one of these units, and of one
-// head's units in the blocks before it (all of them full).  Rows that see no
-// key (L < n) cost as if L = n.
-__device__ __forceinline__ int sched_weight(const AttnSched &s, const AttnReq &q, int i) {
-  return q.n - i * s.U > s.half ? s.w_full : s.w_half;
-}
-
+// Cost of one unit of block i, and of one head's units in the blocks before
+// it (all of them full).  Rows that see no key (L < n) cost as if L = n.
 __device__ __forceinline__ int64_t sched_unit(const AttnSched &s, const AttnReq &q, int i) {
-  const int64_t keys = static_cast<int64_t>(max(q.L - q.n, 0)) + min(q.n, (i + 1) * s.U);
-  return keys * sched_weight(s, q, i) + s.fixed;
+  return static_cast<int64_t>(max(q.L - q.n, 0)) + min(q.n, (i + 1) * s.U) + s.fixed;
 }
 
 __device__ __forceinline__ int64_t sched_before(const AttnSched &s, const AttnReq &q, int i) {
   const int64_t n = i;
-  return n * (static_cast<int64_t>(max(q.L - q.n, 0)) * s.w_full + s.fixed) +
-         n * (n + 1) / 2 * (s.U * s.w_full);
+  return n * (max(q.L - q.n, 0) + s.fixed) + n * (n + 1) / 2 * s.U;
 }
 
 __device__ __forceinline__ int64_t sched_cost(const AttnSched &s, const AttnReq &q) {
@@ -196,29 +189,39 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
   return run;
 }
 
+// sched_run behind the wait for the kernel before (pdl_enter).  It is run once
+// before the wait as well, with whatever lengths are there, and that result
+// dropped: its instructions, which come from far at the start of a call, are
+// then fetched while the kernel before is still at work.
+template <int NT>
+__device__ __forceinline__ AttnRun sched_start(const AttnSched &s, int w, int64_t *scratch) {
+  AttnRun run;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) pdl_enter();
+    run = sched_run<NT>(s, w, scratch);
+  }
+  return run;
+}
+
 // The tiles [tile, stop) of a unit of ntile tiles at cost x whose first keys
-// the run holds (weight: its sched_weight, 1 to 3); a cut inside the fixed
-// cost leaves all tiles to the later run.
-__device__ __forceinline__ int sched_cut(const AttnSched &s, int64_t at, int weight, int ntile) {
-  const int64_t all = static_cast<int64_t>(ntile) * weight << s.kt_shift;
+// the run holds; a cut inside the fixed cost leaves all tiles to the later run.
+__device__ __forceinline__ int sched_cut(const AttnSched &s, int64_t at, int ntile) {
   if (at <= 0) return 0;
-  if (at >= all) return ntile;
-  // ceil(at / (weight KT)); a unit's cost fits 32 bits (L < 2^29)
-  const uint32_t t = (static_cast<uint32_t>(at) + (1u << s.kt_shift) - 1) >> s.kt_shift;
-  return static_cast<int>(weight == 3 ? (t + 2) / 3 : (t + weight - 1) >> (weight - 1));
+  const int64_t t = (at + (1 << s.kt_shift) - 1) >> s.kt_shift;
+  return t < ntile ? static_cast<int>(t) : ntile;
 }
 
 __device__ __forceinline__ void sched_part(const AttnSched &s, const AttnRun &run, int64_t x,
-                                           int weight, int ntile, int &tile, int &stop) {
-  tile = sched_cut(s, run.first - x - s.fixed, weight, ntile);
-  stop = sched_cut(s, run.last - x - s.fixed, weight, ntile);
+                                           int ntile, int &tile, int &stop) {
+  tile = sched_cut(s, run.first - x - s.fixed, ntile);
+  stop = sched_cut(s, run.last - x - s.fixed, ntile);
 }
 
 // The worker that has a unit's last tile.
 __device__ __forceinline__ int sched_last(const AttnSched &s, const AttnRun &run, int64_t x,
-                                          int weight, int ntile) {
-  return small_quotient(x + s.fixed + (static_cast<int64_t>(ntile - 1) * weight << s.kt_shift),
-                        run.step);
+                                          int ntile) {
+  return small_quotient(x + s.fixed + (static_cast<int64_t>(ntile - 1) << s.kt_shift), run.step);
 }
 
 // What a worker leaves for the merge: the unit that is still open when its

@@ -51,12 +51,11 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
   float *Qs = sm, *Ks = Qs + TR * LD, *Vs = Ks + KT * LD, *Ps = Vs + KT * NC * 64;
   int64_t *krow = reinterpret_cast<int64_t *>(Ps + TR * PLD);  // element offset of a key row, -1: none
   __shared__ int64_t scratch[kThreads / 32 + 4];
-  pdl_enter();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int hd = a.head_dim, d4 = hd / 4;
   const int grp = a.n_head / a.n_kv;
   zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
-  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
+  const AttnRun run = sched_start<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
   int64_t x = run.unit;
@@ -72,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
     const int ntile = sched_tiles(sc, q, i);
     next = x + sched_unit(sc, q, i);
     int tile, stop;
-    sched_part(sc, run, x, sched_weight(sc, q, i), ntile, tile, stop);
+    sched_part(sc, run, x, ntile, tile, stop);
     if (tile >= stop) continue;
     const int h = vh / nsub, sub = vh - h * nsub;
     const int g = min(gsub, grp - sub * gsub);  // query heads of this unit
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
       }
     }
     if (tid == 0 && tile == 0 && !whole) {
-      parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, sched_weight(sc, q, i), ntile)};
+      parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, ntile)};
     }
   }
 }
@@ -337,8 +336,6 @@ AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R) {
   p.U = p.rows / p.gsub;
   const int nc = simt_nc(head_dim);
   p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
-  p.half = 0;
-  p.w_half = p.w_full = 1;
   p.fixed = p.KT;
   p.min_run = 2 * p.KT;
   p.workers = sm_count() * 2;
@@ -357,7 +354,9 @@ cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSc
 
 cudaError_t launch_attn_join(const AttnBatch &a, const AttnPlan &p, const AttnParts &parts,
                              cudaStream_t s) {
-  const int ny = p.rows <= 16 ? 4 : 8;
+  // rows of the largest unit, 32 to a block
+  const int64_t rows = a.T * p.gsub < p.rows ? a.T * p.gsub : p.rows;
+  const int ny = static_cast<int>((rows + 31) / 32);
   return launch_pdl(attn_join_kernel, dim3(p.workers, ny), dim3(128), 0, s, a, p.gsub, p.nsub,
                     parts);
 }

@@ -145,25 +145,6 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n, bool values) {
          (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
-// wait_ok in few instructions (there are many waits, and the roles' code shares
-// the instruction caches).
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t *status,
-                                         volatile int *abort_flag) {
-  uint32_t since = 0;
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    uint32_t now;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
-    if (since == 0) since = now & ~1u;
-    if (*abort_flag || now - since > static_cast<uint32_t>(kWaitLimitNs)) {
-      *abort_flag = 1;
-      atomicOr(status, kDevWaitTimeout);
-      return false;
-    }
-  }
-  return true;
-}
-
 // One unit of this worker's run, as the roles see it.
 struct __align__(16) Unit {
   int valid, pair, q_row, nt;      // 0: no unit any more; first query row, tokens
@@ -269,9 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < 16; ++k) marked[k] = 0;
   }
   if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_slot), 512);
-  pdl_enter();
+  const AttnRun run = sched_start<kThreads>(p.sc, blockIdx.x, scratch);
   if (threadIdx.x == 0) p.parts.open[blockIdx.x].rows_tok = 0;
-  const AttnRun run = sched_run<kThreads>(p.sc, blockIdx.x, scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -280,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nch = NCH == 1 ? 1 : (hd + 63) / 64;  // chunks that hold columns
   // the whole warp waits for a barrier
   auto wait_warp = [&](uint32_t bar, uint32_t parity) {
-    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, p.status, abort_flag)) != 0;
+    return __all_sync(0xFFFFFFFFu, wait_ok(bar, parity, p.status, abort_flag)) != 0;
   };
 
   // 384 threads launched with 168 registers: 2 x 208 + 88 = 3 x 168
@@ -306,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           u.ntile = sched_tiles(p.sc, q, i);
-          const int weight = sched_weight(p.sc, q, i);
-          sched_part(p.sc, run, x, weight, u.ntile, u.tile, u.stop);
+          sched_part(p.sc, run, x, u.ntile, u.tile, u.stop);
           if (u.tile < u.stop) {
             const int t0 = i * p.sc.U, ctx = q.L - q.n;
             u.valid = 1;
@@ -326,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             u.k_row = q.q0;
             if (lane == 0 && u.tile == 0 && u.stop < u.ntile)
               p.parts.open[blockIdx.x] =
-                  AttnOpen{u.q_row, u.nt, vh, sched_last(p.sc, run, x, weight, u.ntile)};
+                  AttnOpen{u.q_row, u.nt, vh, sched_last(p.sc, run, x, u.ntile)};
           }
           x += sched_unit(p.sc, q, i);
           if (++vh == p.sc.nvh) {
@@ -503,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pairs = 0;                 // units with two query tiles so far
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        return wait_bar(bar, parity, p.status, abort_flag);
+        return wait_ok(bar, parity, p.status, abort_flag);
       };
       for (uint32_t un = 0; ok; ++un) {
         if (!wait(u_full(un), (un / kUnits) & 1u)) break;
@@ -926,7 +905,12 @@ bool attn_tc_takes(const AttnBatch &a) {
   return a.k_stride % 8 == 0 && a.v_stride % 8 == 0 && a.k_stride < most && a.v_stride < most;
 }
 
-AttnPlan attn_tc_plan(int n_head, int n_kv) {
+// Requests of up to a query tile on average: the form for decoding.
+static bool tc_few(bool paged, int64_t T, int gsub, int R) {
+  return paged && T * gsub <= static_cast<int64_t>(128) * R;
+}
+
+AttnPlan attn_tc_plan(bool paged, int64_t T, int n_head, int n_kv, int R) {
   const int grp = n_head / n_kv;
   AttnPlan p;
   p.rows = 256;
@@ -934,12 +918,11 @@ AttnPlan attn_tc_plan(int n_head, int n_kv) {
   p.nsub = (grp + p.gsub - 1) / p.gsub;
   p.U = 2 * (128 / p.gsub);
   p.KT = kKT;
-  p.half = p.U / 2;
-  // measured: 1.44 us a tile of a pair, 0.99 us a tile of a single unit, 4.4 us a unit
-  p.w_half = 2;
-  p.w_full = 3;
-  p.fixed = 9 * kKT;
-  p.min_run = 3 * kKT;
+  const bool few = tc_few(paged, T, p.gsub, R);
+  // a unit costs about three tiles besides its own (4.4 us of 1.4 us each);
+  // one with a single query tile less, as do its tiles
+  p.fixed = few ? 5 * kKT / 2 : 3 * kKT;
+  p.min_run = 2 * kKT;
   p.workers = sm_count();
   return p;
 }
@@ -966,8 +949,7 @@ cudaError_t launch_attn_tc(const AttnBatch &a, const AttnPlan &pl, const AttnSch
     ok = ok && map_rows(&k, a.k, a.T, a.k_stride, a.n_kv, a.head_dim, 1, kKT) &&
          map_rows(&v, a.v, a.T, a.v_stride, a.n_kv, a.head_dim, 1, kKT);
   if (!ok) return cudaErrorInvalidValue;
-  // requests of up to a query tile on average: the form for decoding
-  const bool few = a.T * p.gsub <= static_cast<int64_t>(128) * a.R;
+  const bool few = tc_few(a.block_table != nullptr, a.T, p.gsub, a.R);
   if (!a.block_table)
     return a.head_dim <= 64 ? run_tc<1, false, true>(q, k, v, p, pl.workers, s)
                             : run_tc<2, false, true>(q, k, v, p, pl.workers, s);

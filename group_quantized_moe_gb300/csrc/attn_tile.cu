@@ -57,12 +57,11 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
   __shared__ int64_t scratch[kThreads / 32 + 4];
   __shared__ int bad[3];  // keys of tile kt in blocks outside the cache, one bit each, in kt % 3
   float *Qs = sm, *stages = sm + kRows * LD;
-  pdl_enter();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x8 = lane & 7, y4 = lane >> 3;
   float *Pw = stages + 2 * C::stage + warp * 16 * kPld;
   const int hd = a.head_dim, d4 = hd / 4, grp = a.n_head / a.n_kv;
   const float *gk = static_cast<const float *>(a.k), *gv = static_cast<const float *>(a.v);
-  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
+  const AttnRun run = sched_start<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
   int64_t x = run.unit;
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
     const int ntile = sched_tiles(sc, q, i);
     next = x + sched_unit(sc, q, i);
     int tile, stop;
-    sched_part(sc, run, x, sched_weight(sc, q, i), ntile, tile, stop);
+    sched_part(sc, run, x, ntile, tile, stop);
     if (tile >= stop) continue;
     const int h = vh / nsub, sub = vh - h * nsub;
     const int g = min(gsub, grp - sub * gsub);
@@ -312,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
     }
     if (tid == 0 && tile == 0 && !whole)
       parts.open[blockIdx.x] =
-          AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, sched_weight(sc, q, i), ntile)};
+          AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, ntile)};
   }
   zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
 }
@@ -340,8 +339,6 @@ bool attn_tile_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, in
   p->gsub = grp < kRows ? grp : kRows;
   p->nsub = (grp + p->gsub - 1) / p->gsub;
   p->U = kRows / p->gsub;
-  p->half = 0;
-  p->w_half = p->w_full = 1;
   p->KT = kKeys;
   p->fixed = kKeys;
   p->min_run = 4 * kKeys;
