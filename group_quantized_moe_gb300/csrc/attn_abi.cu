@@ -227,7 +227,8 @@ int qmm_rope_append(const void *qkv, int32_t x_dtype, int64_t T, int64_t row_str
   const int64_t row = (static_cast<int64_t>(n_head) + 2 * n_kv) * head_dim;
   if (row_stride < row || row_stride > (int64_t(1) << 40))
     return refuse(QMM_ERR_SHAPE, "%s: row_stride is smaller than a row, or larger than 2^40", who);
-  if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || row_stride % 4)
+  if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(rope_cos, 16) || !aligned(rope_sin, 16) || row_stride % 4)
     return refuse(QMM_ERR_ALIGN,
                   "%s: tensors must be 16-byte aligned and rows a multiple of 4 elements apart", who);
   RopeAppend a{};

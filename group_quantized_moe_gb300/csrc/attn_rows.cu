@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
   const int tid = threadIdx.x, team = tid / LK, lane = tid % LK;
   const int base_lane = (tid & 31) - lane;  // the team's first lane in its warp
   const int hd = a.head_dim, grp = a.n_head / a.n_kv;
-  const AttnRun run = sched_start<kThreads>(sc, blockIdx.x, scratch);
+  pdl_enter();
+  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
   // this lane's scores: row srow, keys skey + j

@@ -49,17 +49,15 @@ struct AttnReq {
   int L;      // cache rows
 };
 
-// Request r, held inside the buffers whatever the lengths say.  Read past L1: a
-// kernel may look before the one that writes the lengths has ended (see
-// sched_start), and must not find that value again afterwards.
+// Request r, held inside the buffers whatever the lengths say.
 __device__ __forceinline__ AttnReq sched_req(const AttnSched &s, int r) {
   AttnReq q;
-  const int64_t a = __ldcg(s.cu + r), b = __ldcg(s.cu + r + 1);
+  const int64_t a = s.cu[r], b = s.cu[r + 1];
   const int64_t lo = a < 0 ? 0 : (a > s.T ? s.T : a);
   const int64_t hi = b < lo ? lo : (b > s.T ? s.T : b);
   q.q0 = static_cast<int>(lo);
   q.n = static_cast<int>(hi - lo);
-  int64_t L = s.kvl ? __ldcg(s.kvl + r) : q.n;
+  int64_t L = s.kvl ? s.kvl[r] : q.n;
   if (L < 0) L = 0;
   if (L > s.cap) L = s.cap;
   q.L = static_cast<int>(L);
@@ -186,21 +184,6 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
   run.i = work ? static_cast<int>(found[1]) : 0;
   run.h = work ? static_cast<int>(found[2]) : 0;
   run.unit = work ? found[3] : run.last;
-  return run;
-}
-
-// sched_run behind the wait for the kernel before (pdl_enter).  It is run once
-// before the wait as well, with whatever lengths are there, and that result
-// dropped: its instructions, which come from far at the start of a call, are
-// then fetched while the kernel before is still at work.
-template <int NT>
-__device__ __forceinline__ AttnRun sched_start(const AttnSched &s, int w, int64_t *scratch) {
-  AttnRun run;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass) pdl_enter();
-    run = sched_run<NT>(s, w, scratch);
-  }
   return run;
 }
 

@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
   const int hd = a.head_dim, d4 = hd / 4;
   const int grp = a.n_head / a.n_kv;
   zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
-  const AttnRun run = sched_start<kThreads>(sc, blockIdx.x, scratch);
+  pdl_enter();
+  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
   int64_t x = run.unit;

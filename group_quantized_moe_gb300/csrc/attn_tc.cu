@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < 16; ++k) marked[k] = 0;
   }
   if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_slot), 512);
-  const AttnRun run = sched_start<kThreads>(p.sc, blockIdx.x, scratch);
+  pdl_enter();
+  const AttnRun run = sched_run<kThreads>(p.sc, blockIdx.x, scratch);
   if (threadIdx.x == 0) p.parts.open[blockIdx.x].rows_tok = 0;
   tc_fence_before();
   __syncthreads();

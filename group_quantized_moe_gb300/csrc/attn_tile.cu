@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
   float *Pw = stages + 2 * C::stage + warp * 16 * kPld;
   const int hd = a.head_dim, d4 = hd / 4, grp = a.n_head / a.n_kv;
   const float *gk = static_cast<const float *>(a.k), *gv = static_cast<const float *>(a.v);
-  const AttnRun run = sched_start<kThreads>(sc, blockIdx.x, scratch);
+  pdl_enter();
+  const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
   int64_t x = run.unit;

@@ -74,6 +74,7 @@ def test_rope_append_refuses(L):
                      (dict(T=-1), q.QMM_ERR_SHAPE), (dict(max=-1), q.QMM_ERR_SHAPE),
                      (dict(stride=511), q.QMM_ERR_SHAPE), (dict(stride=514), q.QMM_ERR_ALIGN),
                      (dict(x=P + 4), q.QMM_ERR_ALIGN), (dict(k=P + 8), q.QMM_ERR_ALIGN),
+                     (dict(cos=P + 8), q.QMM_ERR_ALIGN),
                      (dict(x=None), q.QMM_ERR_INVALID_ARG), (dict(pos=None), q.QMM_ERR_INVALID_ARG),
                      (dict(slots=None), q.QMM_ERR_INVALID_ARG), (dict(sin=None), q.QMM_ERR_INVALID_ARG),
                      (dict(q=None), q.QMM_ERR_INVALID_ARG)):
