@@ -8,9 +8,12 @@
 // that use them inside the warp, and the only block-wide barriers are the two
 // that hand the stages over.  Lane (y, x), y < 4, x < 8: scores of rows
 // 4 p + y and keys x + 8 k (4 x 4), results of those rows in columns
-// 4 x + 32 j.  Per four columns a warp reads 8 lines of shared memory for 64
-// multiply-adds a lane in Q K^T, and per key 5 for 64 in P V, so the FMA pipe
-// is the bound.  A warp skips the tiles that none of its rows sees.
+// 4 x + 32 j.  A load from shared memory costs the SM a cycle per 4 bytes a
+// lane, whoever shares them, and four multiply-adds a lane take one: with 4 x 4
+// scores a lane Q K^T reads 8 floats for 16 multiply-adds, which bounds it at
+// half the FMA rate (measured 38 TFLOP/s at 4096 tokens, 48% of the FMA pipe).
+// Multiply-adds are issued in pairs (f32x2), 8% on short prompts.  A warp skips
+// the tiles that none of its rows sees.
 #include <cstdint>
 
 #include "attn_batch.h"
@@ -31,6 +34,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 // 16 bytes global -> shared, or zeros.
 __device__ __forceinline__ void copy16(float *dst, const float *src, bool real) {
@@ -141,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
     // this lane's rows 16 warp + 4 p + y4: keys they see, running maximum and sum, results
     int vis[4];
     float m[4], l[4];
-    float4 o[4][NJ];
+    ulonglong2 o[4][NJ];  // four columns as two packed pairs
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const int row = 16 * warp + 4 * p + y4;
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
       m[p] = -INFINITY;
       l[p] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) o[p][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < NJ; ++j) o[p][j] = make_ulonglong2(0ull, 0ull);
     }
     const int first_row = 16 * warp, last_row = min(rows, first_row + 16) - 1;
     const int most = last_row >= first_row ? all + last_row / g : 0;  // keys any row of the warp sees
@@ -166,29 +174,36 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
       if (k0 < most) {
         const float *Ks = stages + st * C::stage, *Vs = Ks + kKeys * LD;
         const float *Qw = Qs + (16 * warp + y4) * LD;
-        float s[4][4];
+        f32x2 s2[4][4];
 #pragma unroll
         for (int p = 0; p < 4; ++p)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[p][k] = 0.0f;
+          for (int k = 0; k < 4; ++k) s2[p][k] = 0ull;
 #pragma unroll 4
         for (int c = 0; c < W / 4; ++c) {
-          float4 kk[4], qq[4];
+          ulonglong2 kk[4], qq[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            kk[k] = *reinterpret_cast<const float4 *>(Ks + (x8 + 8 * k) * LD + 4 * c);
+            kk[k] = *reinterpret_cast<const ulonglong2 *>(Ks + (x8 + 8 * k) * LD + 4 * c);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) qq[p] = *reinterpret_cast<const float4 *>(Qw + 4 * p * LD + 4 * c);
+          for (int p = 0; p < 4; ++p) qq[p] = *reinterpret_cast<const ulonglong2 *>(Qw + 4 * p * LD + 4 * c);
 #pragma unroll
           for (int p = 0; p < 4; ++p)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              s[p][k] = fmaf(qq[p].x, kk[k].x, s[p][k]);
-              s[p][k] = fmaf(qq[p].y, kk[k].y, s[p][k]);
-              s[p][k] = fmaf(qq[p].z, kk[k].z, s[p][k]);
-              s[p][k] = fmaf(qq[p].w, kk[k].w, s[p][k]);
+              s2[p][k] = fma2(qq[p].x, kk[k].x, s2[p][k]);
+              s2[p][k] = fma2(qq[p].y, kk[k].y, s2[p][k]);
             }
         }
+        float s[4][4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            unpack2(s2[p][k], lo, hi);
+            s[p][k] = lo + hi;
+          }
         const uint32_t gone = static_cast<uint32_t>(bad[kt % 3]);
         const bool guard = k0 + kKeys > least || gone;
 #pragma unroll
@@ -216,21 +231,19 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
           l[p] = fmaf(l[p], f, sum);  // this lane's keys; summed over the lanes at the end
           m[p] = mn;
           if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+            const f32x2 f2 = pack2(f, f);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-              o[p][j].x *= f;
-              o[p][j].y *= f;
-              o[p][j].z *= f;
-              o[p][j].w *= f;
+              o[p][j].x = mul2(o[p][j].x, f2);
+              o[p][j].y = mul2(o[p][j].y, f2);
             }
           }
         }
         __syncwarp();
-        auto add = [&](float w, const float4 &v, float4 &t) {
-          t.x = fmaf(w, v.x, t.x);
-          t.y = fmaf(w, v.y, t.y);
-          t.z = fmaf(w, v.z, t.z);
-          t.w = fmaf(w, v.w, t.w);
+        auto add = [&](float w, const ulonglong2 &v, ulonglong2 &t) {
+          const f32x2 w2 = pack2(w, w);
+          t.x = fma2(w2, v.x, t.x);
+          t.y = fma2(w2, v.y, t.y);
         };
         // Where some row misses some key, P is 0 there, which a non-finite value
         // would still turn into NaN: then (and only then) key by key.
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
               for (int j = 0; j < NJ; ++j) {
-                const float4 v = *reinterpret_cast<const float4 *>(Vs + (k + kk) * W + 32 * j + 4 * x8);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(Vs + (k + kk) * W + 32 * j + 4 * x8);
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
                   add(kk == 0 ? w[p].x : kk == 1 ? w[p].y : kk == 2 ? w[p].z : w[p].w, v, o[p][j]);
@@ -273,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
             for (int p = 0; p < 4; ++p) w[p] = Pw[(4 * p + y4) * kPld + k];
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-              const float4 v = *reinterpret_cast<const float4 *>(Vs + k * W + 32 * j + 4 * x8);
+              const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(Vs + k * W + 32 * j + 4 * x8);
 #pragma unroll
               for (int p = 0; p < 4; ++p)
                 if (w[p] != 0.0f) add(w[p], v, o[p][j]);
@@ -303,7 +316,10 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
       for (int j = 0; j < NJ; ++j) {
         const int d = 32 * j + 4 * x8;
         if (d >= hd) continue;
-        const float4 v = make_float4(o[p][j].x * inv, o[p][j].y * inv, o[p][j].z * inv, o[p][j].w * inv);
+        float4 v;
+        unpack2(o[p][j].x, v.x, v.y);
+        unpack2(o[p][j].y, v.z, v.w);
+        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
         if (whole)
           store_y4(a.y, y0 + d, v, a.y_bf16);
         else
