@@ -1080,3 +1080,24 @@ def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q:
     if rc:
         _check(rc)
     return y
+
+
+def attn_layer_paged(x: torch.Tensor, wqkv: QWeight, wo: QWeight, n_head: int,
+                     rope_cos: torch.Tensor, rope_sin: torch.Tensor, cache: PagedKV, plan: KVPlan,
+                     block_table: torch.Tensor, prompts: bool = False,
+                     y_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """One attention layer for a batch of requests' new tokens x [T, D], as
+    kv_plan has planned them: the quantised q/k/v projection (wqkv: the rows of
+    wq, wk and wv as one weight), rotary positions and the cache write, the
+    attention and the quantised output projection.  prompts: no request has
+    earlier context, so the attention reads the new keys and values as they
+    lie instead of through the cache.  Returns y [T, wo.N]."""
+    qkv = qmm_linear_batched(x, wqkv, y_dtype=cache.k.dtype, stream=stream)
+    q, k, v = rope_append(qkv, n_head, plan.positions, plan.slots, rope_cos, rope_sin, cache,
+                          keep_kv=prompts, stream=stream)
+    if prompts:
+        a = attn_prompt(q, k, v, plan.cu_new, y_dtype=q.dtype, stream=stream)
+    else:
+        a = attn_paged(q, cache, block_table, plan.cu_new, plan.kv_lens, y_dtype=q.dtype,
+                       stream=stream)
+    return qmm_linear_batched(a.view(x.shape[0], -1), wo, y_dtype=y_dtype, stream=stream)

@@ -54,7 +54,6 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int hd = a.head_dim, d4 = hd / 4;
   const int grp = a.n_head / a.n_kv;
-  zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
   pdl_enter();
   const AttnRun run = sched_run<kThreads>(sc, blockIdx.x, scratch);
   if (tid == 0) parts.open[blockIdx.x].rows_tok = 0;
@@ -64,11 +63,13 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
   AttnReq q;
   for (int64_t next = 0; x < run.last; x = next, vh = vh + 1 == sc.nvh ? 0 : vh + 1, i += vh == 0) {
     q = sched_req(sc, r);
+    bool done = false;
     while (i >= sched_blocks(sc, q)) {
-      if (++r >= sc.R) return;  // lengths that changed during the call
+      if ((done = ++r >= sc.R)) break;  // lengths that changed during the call
       i = 0;
       q = sched_req(sc, r);
     }
+    if (done) break;
     const int ntile = sched_tiles(sc, q, i);
     next = x + sched_unit(sc, q, i);
     int tile, stop;
@@ -252,6 +253,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
       parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, vh, sched_last(sc, run, x, ntile)};
     }
   }
+  zero_loose_rows(a, sc, blockIdx.x, gridDim.x, kThreads);
 }
 
 // Units divided between workers: worker w (blockIdx.x) started one and left

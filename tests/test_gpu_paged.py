@@ -429,3 +429,62 @@ def test_prompt_and_paged_agree(dev):
                 done += m
                 out.append(q.attn_paged(qq[done - m:done], cache, table, cu_of([m]), i32([done])))
             assert_within(num(torch.cat(out)), whole, b + ref.U * np.abs(whole))
+
+
+# -------------------------------------------------- the layer and the example
+
+def test_layer_step_within_the_decode_oracles_bound(dev):
+    """One decode step of a layer over a paged fp32 cache, beside another
+    request, against the oracle of the single-sequence decode step: the same
+    weights, token, position and earlier cache rows."""
+    import oracle
+    import synth
+
+    D, nh, nkv, hd, S, pos, max_seq = 256, 8, 2, 32, 16, 70, 128
+    r = synth.normal
+    ow = [oracle.quantize(r(5, i, n * kk, 0.05).reshape(n, kk), 8, 64)
+          for i, (n, kk) in enumerate(((nh * hd, D), (nkv * hd, D), (nkv * hd, D), (D, nh * hd)))]
+
+    def weight(os_):
+        cat = [np.concatenate([getattr(o, f).reshape(o.N, -1) for o in os_])
+               for f in ("codes", "scales", "zps")]
+        t = [torch.from_numpy(np.ascontiguousarray(c)).cuda() for c in (cat[0].view(np.int8), *cat[1:])]
+        return q.QWeight(8, 64, sum(o.N for o in os_), os_[0].K, *t)
+
+    wqkv, wo = weight(ow[:3]), weight(ow[3:])
+    oc, os_ = oracle.rope_table(max_seq, hd, 10000.0)
+    cos, sin = q.rope_table(max_seq, hd, device=dev)
+    old = r(6, 1, 2 * nkv * max_seq * hd).reshape(2, nkv, max_seq, hd)
+    cache = q.PagedKV(*(torch.zeros((12, nkv, S, hd), device="cuda") for _ in range(2)))
+    used = [7, 0, 9, 4, 11]  # the request's earlier blocks
+    for b, i in enumerate(used):
+        for t, c in ((0, cache.k), (1, cache.v)):
+            c[i] = torch.from_numpy(old[t][:, b * S:(b + 1) * S].copy()).cuda()
+    table = torch.full((2, 6), -1, dtype=torch.int32, device="cuda")
+    table[0, :5] = torch.tensor(used)
+    xs = np.stack([r(7, 1, D), r(7, 2, D)])
+    plan = q.kv_plan(i32([pos, 0]), i32([1, 1]), table, i32([3, 5]), S, 2)
+    y = q.attn_layer_paged(torch.from_numpy(xs).cuda(), wqkv, wo, nh, cos, sin, cache, plan, table)
+    assert plan.blocks_used.tolist() == [1] and table[1, 0] == 3
+    for row, (p, c) in enumerate(((pos, old), (0, np.zeros_like(old)))):
+        want, bound, kv, kvb = oracle.attn_decode(xs[row], p, nh, nkv, hd, *ow, oc, os_, c)
+        assert_within(num(y[row]), want, bound, f"row {row}")
+        slot = int(plan.slots[row])
+        for t, got in ((0, cache.k), (1, cache.v)):
+            assert_within(num(got[slot // S, :, slot % S]), kv[t], kvb[t], f"cache {row}")
+
+
+def test_example_serves_requests(dev):
+    """examples/serve_paged.py: prompts, decoding and a chunked prompt through
+    the cache agree with each whole sequence at once.  Both round the same
+    values to bf16 at the same places (queries, keys, values, weights, rows),
+    so a row differs by a few of those roundings, each at most 2^-8 of what it
+    rounds: 4 x 2^-8."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "serve_paged.py")
+    spec = importlib.util.spec_from_file_location("serve_paged", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.main(["--quiet", "--width", "1024", "--heads", "8", "--kv-heads", "2"]) <= 4 * 2.0 ** -8
