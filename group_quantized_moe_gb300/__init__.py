@@ -988,20 +988,26 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
     return q, k, v
 
 
-def _attn_out(q, y, y_dtype, workspace, nbytes, stream):
-    """The output and workspace of an attention call, checked or allocated."""
-    if y is not None:
+_CODES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16}
+
+
+def _attn_y(q, y, y_dtype, stream):
+    """The output of an attention call, checked or allocated."""
+    if y is None:
+        y = torch.empty(q.shape, dtype=y_dtype, device=q.device)
+        if stream is not None:
+            _on_stream(stream, y)
+    else:
         _need(y, q.numel(), (_F32, torch.bfloat16), "y")
         _require_cuda(y)
-    else:
-        y = torch.empty(q.shape, dtype=y_dtype, device=q.device)
-        _on_stream(stream, y)
-    if workspace is None:
-        workspace = torch.empty((nbytes(),), dtype=torch.uint8, device=q.device)
-        _on_stream(stream, workspace)
-    else:  # a caller's workspace is size-checked by the library
-        _require_cuda(workspace)
-    return y, workspace
+    return y
+
+
+def _workspace(nbytes, q, stream):
+    w = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+    if stream is not None:
+        _on_stream(stream, w)
+    return w
 
 
 def qmm_attn_prompt_workspace_bytes(q: torch.Tensor, k: torch.Tensor, n_seqs: int) -> int:
@@ -1030,12 +1036,15 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
         _need(cu_seqlens, B + 1, (_I32,), "cu_seqlens")
         _on_device(q, k, v)
         _require_cuda(cu_seqlens)
-    y, workspace = _attn_out(q, y, y_dtype, workspace,
-                             lambda: qmm_attn_prompt_workspace_bytes(q, k, B), stream)
+    y = _attn_y(q, y, y_dtype, stream)
+    if workspace is None:
+        workspace = _workspace(qmm_attn_prompt_workspace_bytes(q, k, B), q, stream)
+    elif not workspace.is_cuda or not workspace.is_contiguous():  # its size is the library's check
+        _require_cuda(workspace)
     rc = lib().qmm_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T, sq, sk, sv,
                                nh, nkv, hd, cu_seqlens.data_ptr(), B, 0.0 if scale is None else scale,
-                               y.data_ptr(), _dtype_code(y), workspace.data_ptr(), _nbytes(workspace),
-                               _stream(stream))
+                               y.data_ptr(), _CODES[y.dtype], workspace.data_ptr(),
+                               workspace.nbytes, _stream(stream))
     if rc:
         _check(rc)
     return y
@@ -1070,12 +1079,15 @@ def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q:
         _on_device(q, block_table)
         _require_cuda(cu_q, kv_lens)
     cols = block_table.shape[1]
-    y, workspace = _attn_out(q, y, y_dtype, workspace,
-                             lambda: qmm_attn_paged_workspace_bytes(q, cache, R), stream)
+    y = _attn_y(q, y, y_dtype, stream)
+    if workspace is None:
+        workspace = _workspace(qmm_attn_paged_workspace_bytes(q, cache, R), q, stream)
+    elif not workspace.is_cuda or not workspace.is_contiguous():  # its size is the library's check
+        _require_cuda(workspace)
     rc = lib().qmm_attn_paged(q.data_ptr(), T, sq, nh, desc, block_table.data_ptr(),
                               block_table.stride(0) if R > 1 else cols, cols, cu_q.data_ptr(),
                               kv_lens.data_ptr(), R, 0.0 if scale is None else scale, y.data_ptr(),
-                              _dtype_code(y), workspace.data_ptr(), _nbytes(workspace),
+                              _CODES[y.dtype], workspace.data_ptr(), workspace.nbytes,
                               _stream(stream))
     if rc:
         _check(rc)

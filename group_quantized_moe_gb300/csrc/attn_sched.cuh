@@ -40,6 +40,7 @@ struct AttnSched {
   int min_run;         // a worker's run costs at least this much (KT or more, so
                        // that no run inside a unit is without a tile of it)
   uint64_t per_worker; // 2^64 / workers, rounded up
+  bool whole;          // units are not divided: each goes to the run that holds its start
   int64_t T;           // query rows in the buffers
   int64_t cap;         // largest cache length the block table can hold (below 2^29)
 };
@@ -197,6 +198,11 @@ __device__ __forceinline__ int sched_cut(const AttnSched &s, int64_t at, int nti
 
 __device__ __forceinline__ void sched_part(const AttnSched &s, const AttnRun &run, int64_t x,
                                            int ntile, int &tile, int &stop) {
+  if (s.whole) {
+    tile = x >= run.first ? 0 : ntile;
+    stop = ntile;
+    return;
+  }
   tile = sched_cut(s, run.first - x - s.fixed, ntile);
   stop = sched_cut(s, run.last - x - s.fixed, ntile);
 }
