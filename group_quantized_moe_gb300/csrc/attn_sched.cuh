@@ -127,7 +127,7 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) mine += sched_cost(s, sched_req(s, r));
   int64_t inc = mine;  // inclusive over the warp
-#pragma unroll 1
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += v;
@@ -135,7 +135,7 @@ __device__ __forceinline__ AttnRun sched_run(const AttnSched &s, int w, int64_t 
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
   int64_t lo = inc - mine, W = 0;  // lo: cost before this thread's requests
-#pragma unroll 1
+#pragma unroll
   for (int k = 0; k < NT / 32; ++k) {
     if (k == warp) lo += W;
     W += scratch[k];

@@ -250,6 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < 16; ++k) marked[k] = 0;
   }
   if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_slot), 512);
+  if (threadIdx.x == kWarpKv * 32) {
+    prefetch_map(&tm_q);
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
+  }
   pdl_enter();
   const AttnRun run = sched_run<kThreads>(p.sc, blockIdx.x, scratch);
   if (threadIdx.x == 0) p.parts.open[blockIdx.x].rows_tok = 0;
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             u.nt = min(p.sc.U, q.n - t0);
             u.pair = u.nt > p.tpt;
             u.q_row = q.q0 + t0;
-            u.h = vh / p.nsub;
+            u.h = p.nsub == 1 ? vh : vh / p.nsub;
             const int sub = vh - u.h * p.nsub;
             u.head0 = u.h * grp + sub * p.gsub;
             u.g = min(p.gsub, grp - sub * p.gsub);
