@@ -488,3 +488,86 @@ def test_example_serves_requests(dev):
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     assert m.main(["--quiet", "--width", "1024", "--heads", "8", "--kv-heads", "2"]) <= 4 * 2.0 ** -8
+
+
+# ------------------------------------------------------------- further edges
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_requests_and_given_scale(dev, dtype):
+    run_prompt([], 4, 2, 64, dtype, pad=2)
+    run_paged([], 4, 2, 64, 16, dtype, pad=3)
+    n, nh, nkv, hd = 140, 4, 2, 64
+    qq, k, v = (rnd(s, (n, h, hd), dtype).cuda() for s, h in ((1, nh), (2, nkv), (3, nkv)))
+    y = q.attn_prompt(qq, k, v, cu_of([n]), scale=0.3)
+    want, b = ref.prompt(num(qq), num(k), num(v), [n], float(np.float32(0.3)), tensor_core(dtype))
+    assert_within(num(y), want, round_bound(want, b, F32))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_cache_offsets_beyond_32_bits(dev, dtype):
+    """A cache of more than 2^31 elements (and 2^32 bytes), the requests'
+    blocks at its end: written by rope_append, read by attn_paged."""
+    nh, nkv, hd, S, nb, n = 8, 8, 128, 16, 140000, 40
+    assert nb * nkv * S * hd > 2 ** 31
+    cache = q.paged_kv(nb, nkv, S, hd, dtype)
+    x = rnd(1, (n, (nh + 2 * nkv) * hd), dtype).cuda()
+    cos, sin = q.rope_table(n, hd, device=dev)
+    table = torch.tensor([[nb - 1, nb - 3, 131072]], dtype=torch.int32, device="cuda")
+    plan = q.kv_plan(i32([0]), i32([n]), torch.full((1, 3), -1, dtype=torch.int32, device="cuda"),
+                     table[0].contiguous(), S, n)
+    gq, gk, gv = q.rope_append(x, nh, plan.positions, plan.slots, cos, sin, cache, keep_kv=True)
+    for j in (0, 15, 16, 39):
+        b = int(table[0, j // S])
+        assert torch.equal(cache.k[b, :, j % S], gk[j]) and torch.equal(cache.v[b, :, j % S], gv[j])
+    y = q.attn_paged(gq, cache, table, plan.cu_new, plan.kv_lens)
+    want, b = ref.prompt(num(gq), num(gk), num(gv), [n], hd ** -0.5, tensor_core(dtype))
+    assert_within(num(y), want, round_bound(want, b, F32))
+    last = q.attn_paged(gq[-1:], cache, table, cu_of([1]), plan.kv_lens)
+    assert_within(num(last), want[-1:], round_bound(want, b, F32)[-1:])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_captured_serving_step(dev, dtype):
+    """kv_plan, rope_append and attn_paged in one graph, replayed step by step
+    with the lengths updated in place, against the same steps run eagerly."""
+    nh, nkv, hd, S, R = 4, 2, 64, 16, 3
+    cos, sin = q.rope_table(256, hd, device=dev)
+    free = torch.arange(40, dtype=torch.int32, device="cuda")
+
+    def server():
+        cache = q.PagedKV(*(torch.zeros((40, nkv, S, hd), dtype=dtype, device="cuda") for _ in range(2)))
+        table = torch.full((R, 40), -1, dtype=torch.int32, device="cuda")
+        return cache, table, i32([0, 0, 0]), i32([1, 1, 1]), free.clone(), \
+            torch.empty((R, (nh + 2 * nkv) * hd), dtype=dtype, device="cuda")
+
+    def step(s, plan=None, y=None, ws=None):
+        cache, table, ctx, new, pool, x = s
+        p = q.kv_plan(ctx, new, table, pool, S, R, out=plan)
+        gq, _, _ = q.rope_append(x, nh, p.positions, p.slots, cos, sin, cache)
+        return p, q.attn_paged(gq, cache, table, p.cu_new, p.kv_lens, y=y, workspace=ws)
+
+    a, b = server(), server()
+    plan, y = q.alloc_kv_plan(R, R), torch.empty((R, nh, hd), device="cuda")
+    x0 = rnd(50, tuple(b[5].shape), dtype).cuda()
+    b[5].copy_(x0)
+    ws = torch.empty((q.qmm_attn_paged_workspace_bytes(
+        torch.empty((R, nh, hd), dtype=dtype, device="cuda"), b[0], R),), dtype=torch.uint8, device="cuda")
+    step(b, plan, y, ws)  # warm-up; the lengths stay as they are
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(b, plan, y, ws)
+    for t in range(40):
+        x = rnd(100 + t, tuple(x0.shape), dtype).cuda()
+        for s in (a, b):
+            s[5].copy_(x)
+        p, want = step(a)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(a[1], b[1])
+        assert torch.equal(a[0].k, b[0].k) and torch.equal(a[0].v, b[0].v)
+        used = int(p.blocks_used)
+        for s in (a, b):
+            s[2].copy_(p.kv_lens)
+            s[4].copy_(torch.roll(s[4], -used))
+    assert a[2].tolist() == [40, 40, 40]
