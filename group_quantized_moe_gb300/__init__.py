@@ -355,9 +355,11 @@ def qmm_linear_batched(x: torch.Tensor, w: QWeight, y: torch.Tensor | None = Non
     desc = w._c()
     if y is None:
         y = torch.empty((M, w.N), dtype=y_dtype, device=x.device)
+        _on_stream(stream, y)
     if workspace is None:  # a caller's workspace is size-checked by the library
         nbytes = int(lib().qmm_linear_batched_workspace_bytes(M, ctypes.byref(desc)))
         workspace = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
+        _on_stream(stream, workspace)
     _check(lib().qmm_linear_batched(_ptr(x2), _dtype_code(x2), M, ctypes.byref(desc), _ptr(y),
                                     _dtype_code(y), _ptr(workspace), _nbytes(workspace),
                                     _stream(stream)))
@@ -903,7 +905,7 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     cols = block_table.shape[1]
     if out is None:
         out = alloc_kv_plan(R, T, ctx_lens.device)
-        _on_stream(stream, out.cu_new, out.slots)
+        _on_stream(stream, out.cu_new, out.kv_lens, out.positions, out.slots, out.blocks_used)
     else:
         _check_vec(out.cu_new, _I32, R + 1, "cu_new")
         _check_vec(out.kv_lens, _I32, R, "kv_lens")
@@ -1112,4 +1114,4 @@ def attn_layer_paged(x: torch.Tensor, wqkv: QWeight, wo: QWeight, n_head: int,
     else:
         a = attn_paged(q, cache, block_table, plan.cu_new, plan.kv_lens, y_dtype=q.dtype,
                        stream=stream)
-    return qmm_linear_batched(a.view(x.shape[0], -1), wo, y_dtype=y_dtype, stream=stream)
+    return qmm_linear_batched(a.flatten(1), wo, y_dtype=y_dtype, stream=stream)

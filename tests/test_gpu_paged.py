@@ -474,6 +474,60 @@ def test_layer_step_within_the_decode_oracles_bound(dev):
             assert_within(num(got[slot // S, :, slot % S]), kv[t], kvb[t], f"cache {row}")
 
 
+@pytest.mark.parametrize("dtype", (F32, BF16))
+def test_memory_of_a_call_on_another_stream_is_recorded_there(dev, monkeypatch, dtype):
+    """Every tensor that a call allocates belongs to the current stream; a call
+    on another one has to record them all there, or their memory could be
+    handed out again while that stream still uses it."""
+    D, nh, nkv, hd, S, T = 128, 4, 2, 32, 16, 12
+    g = torch.Generator().manual_seed(3)
+
+    def weight(N, K):
+        return q.qmm_quantize_groupwise(torch.randn((N, K), generator=g).cuda(), 8, 64)
+
+    wqkv, wo = weight((nh + 2 * nkv) * hd, D), weight(D, nh * hd)
+    cos, sin = q.rope_table(64, hd, device=dev)
+    cache = q.paged_kv(4, nkv, S, hd, dtype=dtype, device=dev)
+    table = torch.full((2, 2), -1, dtype=torch.int32, device="cuda")
+    x = torch.randn((T, D), generator=g).to(dtype).cuda()
+    args = i32([0, 0]), i32([5, 7]), table, i32([0, 1, 2, 3]), S, T
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    made, seen, empty, record = [], set(), torch.empty, q._on_stream
+
+    def spy_empty(*a, **kw):
+        t = empty(*a, **kw)
+        made.append(t)  # kept, so that no address comes twice
+        return t
+
+    def spy_record(stream, *ts):
+        seen.update(t.data_ptr() for t in ts if t is not None and stream is not None)
+        record(stream, *ts)
+
+    monkeypatch.setattr(torch, "empty", spy_empty)
+    monkeypatch.setattr(q, "_on_stream", spy_record)
+    plan = q.kv_plan(*args, stream=s)
+    for prompts in (True, False):
+        q.attn_layer_paged(x, wqkv, wo, nh, cos, sin, cache, plan, table, prompts=prompts, stream=s)
+    s.synchronize()
+    missing = [(t.shape, t.dtype) for t in made if t.numel() and t.data_ptr() not in seen]
+    assert len(made) >= 5 and not missing, missing
+
+
+def test_layer_without_tokens(dev):
+    nh, nkv, hd, S = 4, 2, 32, 16
+    w = [q.qmm_quantize_groupwise(torch.ones((n, k), device="cuda"), 8, 64) for n, k in ((256, 128), (128, 128))]
+    cos, sin = q.rope_table(16, hd, device=dev)
+    cache = q.paged_kv(2, nkv, S, hd, dtype=F32, device=dev)
+    table = torch.full((1, 1), -1, dtype=torch.int32, device="cuda")
+    plan = q.kv_plan(i32([0]), i32([0]), table, i32([0, 1]), S, 0)
+    x = torch.zeros((0, 128), device="cuda")
+    for prompts in (True, False):
+        y = q.attn_layer_paged(x, *w, nh, cos, sin, cache, plan, table, prompts=prompts)
+        assert y.shape == (0, 128)
+    assert plan.blocks_used.tolist() == [0]
+
+
 def test_example_serves_requests(dev):
     """examples/serve_paged.py: prompts, decoding and a chunked prompt through
     the cache agree with each whole sequence at once.  Both round the same
