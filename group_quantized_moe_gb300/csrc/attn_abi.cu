@@ -135,7 +135,7 @@ Launch pick_plan(bool bf16, bool tc, bool paged, int64_t T, int n_head, int n_kv
     *p = attn_tc_plan(paged, T, n_head, n_kv, R);
     return launch_attn_tc;
   }
-  if (attn_rows_plan(T, n_head, n_kv, head_dim, R, p)) return launch_attn_rows;
+  if (attn_rows_plan(paged, T, n_head, n_kv, head_dim, R, p)) return launch_attn_rows;
   if (attn_tile_plan(bf16, T, n_head, n_kv, head_dim, R, p)) return launch_attn_tile;
   *p = attn_simt_plan(T, n_head, n_kv, head_dim, R);
   return launch_attn_simt;
@@ -143,12 +143,12 @@ Launch pick_plan(bool bf16, bool tc, bool paged, int64_t T, int n_head, int n_kv
 
 }  // namespace
 
-size_t attn_batch_workspace_bytes(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R) {
+size_t attn_batch_workspace_bytes(bool bf16, bool paged, int64_t T, int n_head, int n_kv, int head_dim, int R) {
   // whether a bf16 call takes the tensor cores also depends on its strides
   AttnPlan p;
-  pick_plan(bf16, false, false, T, n_head, n_kv, head_dim, R, &p);
+  pick_plan(bf16, false, paged, T, n_head, n_kv, head_dim, R, &p);
   const size_t simt = parts_layout(p, head_dim).total;
-  const size_t tc = bf16 && head_dim <= 128 ? parts_layout(attn_tc_plan(false, T, n_head, n_kv, R), head_dim).total : 0;
+  const size_t tc = bf16 && head_dim <= 128 ? parts_layout(attn_tc_plan(paged, T, n_head, n_kv, R), head_dim).total : 0;
   return simt > tc ? simt : tc;
 }
 
@@ -269,7 +269,7 @@ size_t qmm_attn_prompt_workspace_bytes(int32_t dtype, int64_t T, int32_t n_head,
   if (!dtype_ok(dtype) || check_heads("qmm_attn_prompt_workspace_bytes", n_head, n_kv, head_dim) ||
       T < 0 || n_seqs < 0)
     return 0;
-  return attn_batch_workspace_bytes(dtype == QMM_BF16, T, n_head, n_kv, head_dim, n_seqs);
+  return attn_batch_workspace_bytes(dtype == QMM_BF16, false, T, n_head, n_kv, head_dim, n_seqs);
 }
 
 int qmm_attn_prompt(const void *q, const void *k, const void *v, int32_t dtype, int64_t T,
@@ -320,7 +320,7 @@ size_t qmm_attn_paged_workspace_bytes(const qmm_kv_cache *cache, int64_t T, int3
   if (!cache || !dtype_ok(cache->dtype) || check_heads(who, n_head, cache->n_kv, cache->head_dim) ||
       T < 0 || R < 0)
     return 0;
-  return attn_batch_workspace_bytes(cache->dtype == QMM_BF16, T, n_head, cache->n_kv,
+  return attn_batch_workspace_bytes(cache->dtype == QMM_BF16, true, T, n_head, cache->n_kv,
                                     cache->head_dim, R);
 }
 

@@ -29,7 +29,8 @@ struct AttnBatch {
 };
 
 // Bytes of workspace for a call with these sizes.
-size_t attn_batch_workspace_bytes(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R);
+size_t attn_batch_workspace_bytes(bool bf16, bool paged, int64_t T, int n_head, int n_kv,
+                                  int head_dim, int R);
 cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t s);
 
 cudaError_t launch_kv_plan(const int32_t *ctx, const int32_t *add, int R, int block_shift,

@@ -30,7 +30,7 @@ AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R);
 cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                              const AttnParts &parts, cudaStream_t s);
 // The form for few rows; false: not for this call.
-bool attn_rows_plan(int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p);
+bool attn_rows_plan(bool paged, int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p);
 cudaError_t launch_attn_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                              const AttnParts &parts, cudaStream_t s);
 // The form for many rows in fp32; false: not for this call.

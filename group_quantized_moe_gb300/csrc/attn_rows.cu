@@ -3,21 +3,32 @@
 // do not take.
 //
 // The work is bound by reading the cache once, so the kernel keeps many wide
-// loads in flight and spends few instructions on a key.  A warp takes B
-// consecutive keys at a time (one block's; the eight warps of a CTA cover a
-// KT = 8 B key tile; up to 64 columns, each half of a warp takes its own B
-// keys), lane l holding columns 4 l + 128 c of the keys, values, queries and
-// results in registers.  The RR x B partial dot products are
+// loads in flight and spends few instructions on a key.  A team of LK lanes
+// takes B consecutive keys at a time (one block's; the teams of a CTA cover a
+// KT key tile), lane l holding columns 4 l + 4 LK c of the keys, values,
+// queries and results in registers.  The RR x B partial dot products are
 // reduced over the lanes by halving (every step sends the half of the values
-// that the other lane keeps: RR B - 1 exchanges instead of 5 RR B), which
-// leaves the score of one (row, key) per lane; each lane keeps the running
-// maximum and sum of its row, and the weights go back to all lanes by shuffles.
-// The warps run independently and meet at the end of a unit.
+// that the other lane keeps: RR B - 1 exchanges instead of log2(LK) RR B),
+// which leaves the scores of one or a few (row, key) per lane; each lane keeps
+// the running maximum and sum of its row, and the weights go back to all lanes
+// by shuffles.  The warps run independently and meet at the end of a unit.
+//
+// One or two rows: a team is as many lanes as the row has pieces of four
+// columns, which keeps the registers free for loads in flight.  Four rows and
+// more: half as many lanes with two pieces each, which halves the exchanges of
+// a key (16 heads over 4 of 64 columns, 128 requests: 5.8 TB/s instead of 4.2;
+// 64 over 8 of 128: 5.4 instead of 4.8; 12 over 4 of 96: 5.2 instead of 4.8).
 //
 // Measured: 12 single tokens of 32 heads of 128 columns over 32 key/value
-// heads' fp32 caches (623 MB) 98 us, 6.4 TB/s, 94% of a copy.  More rows per key are bound
-// by the reduction: eight query heads to a key/value head of 128 columns 4.8
-// TB/s, of 64 columns 4.6.
+// heads' fp32 caches (623 MB) 98 us, 6.4 TB/s, 94% of a copy.  Eight rows a key are bound by
+// the latency of reduction, maximum and weights at two warps a scheduler: 80% of
+// a copy.
+//
+// A request's rows beyond a unit's are further units that read its keys again,
+// which over long caches still is cheaper up to four units (24 requests of 2048
+// keys, 32 rows each: 282 us against attn_tile_kernel's 387; 256 columns, 16
+// rows: 132 against attn_simt_kernel's 163); packed prompts, whose keys are few,
+// go there at once (16 prompts of 32 tokens, 32 heads: 37 us against 74).
 #include <cstdint>
 
 #include "attn_batch.h"
@@ -38,8 +49,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// NC: 128-column groups of the head size; RR: query rows of a unit; LK: lanes
-// that share a key (a "team"; 16 for up to 64 columns).
+// NC: 4 LK-column groups of the head size; RR: query rows of a unit; LK: lanes
+// that share a key (a "team").
 template <int NC, int RR, int LK>
 struct Rows {
   static constexpr int B = NC == 1 ? 8 : NC == 2 ? 4 : 2;  // keys of a team at a time
@@ -48,10 +59,38 @@ struct Rows {
   static constexpr int N = RR * B;                         // scores of a team at a time
   static constexpr int per_lane = N > LK ? N / LK : 1;     // ... of a lane
   static constexpr int dup = N < LK ? LK / N : 1;          // lanes with the same score
-  // CTAs per SM: one where the registers of two would spill (measured: 4 rows
-  // of 128 columns gain from the second CTA in spite of a few spilled words)
+  // CTAs per SM: one where the registers of two would spill
   static constexpr int per_sm = NC * RR <= 4 ? 2 : 1;
+  // With one CTA's eight warps an SM, the registers of a lane hold too few
+  // loads: these copy their keys and values to shared memory, two tiles ahead.
+  // Every lane copies what it reads itself, so no barrier is needed.
+  static constexpr int stages = per_sm == 1 ? 3 : 0;
+  static constexpr int out_bytes = teams * RR * NC * 4 * LK * 4;  // results of the teams
+  static constexpr int pieces = B * NC * kThreads;  // four elements each: a stage's keys, or values
 };
+
+// Four elements, global -> shared, asynchronously.
+template <bool BF16>
+__device__ __forceinline__ void copy_x4(uint32_t dst, const void *base, int64_t i) {
+  if constexpr (BF16)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst),
+                 "l"(static_cast<const uint16_t *>(base) + i)
+                 : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                 "l"(static_cast<const float *>(base) + i)
+                 : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ float4 shared_x4(const uint8_t *p) {
+  if constexpr (BF16) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+  } else {
+    return *reinterpret_cast<const float4 *>(p);
+  }
+}
 
 // v[i] summed over the team's lanes: lane l is left with values
 // per_lane (l / dup) + j.
@@ -83,7 +122,9 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
   constexpr int B = C::B, KT = C::KT, N = C::N, PL = C::per_lane, CW = NC * 4 * LK;
   __shared__ int64_t scratch[kWarps + 4];
   __shared__ float wm[C::teams][RR], wl[C::teams][RR];
-  extern __shared__ __align__(16) float wo[];  // [team][row][CW]
+  extern __shared__ __align__(16) float wo[];  // [team][row][CW], and the stages, then the stages
+  constexpr int W = BF16 ? 8 : 16, HALF = C::pieces * W;
+  uint8_t *const stages = reinterpret_cast<uint8_t *>(wo) + threadIdx.x * W;
   const int tid = threadIdx.x, team = tid / LK, lane = tid % LK;
   const int base_lane = (tid & 31) - lane;  // the team's first lane in its warp
   const int hd = a.head_dim, grp = a.n_head / a.n_kv;
@@ -122,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
       const int t = p / g, hq = p - t * g;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int d = 4 * lane + 128 * c;
+        const int d = 4 * lane + 4 * LK * c;
         const float4 v = p < rows && d < hd
                              ? load_x4<BF16>(a.q, static_cast<int64_t>(q.q0 + t0 + t) * a.q_stride +
                                                       static_cast<int64_t>(head0 + hq) * hd + d)
@@ -138,45 +179,101 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
       const int k = kt * KT + team * B;
       return table && kt < stop && k < end ? table[k / a.block_size] : 0;
     };
-    int id = block_of(tile);
-    for (int kt = tile; kt < stop; ++kt) {
+    // keys of this team's part of a tile that lie in the cache, and their place
+    int64_t kp = 0, vp = 0, ks = hd, vs = hd;  // first row, distance of rows
+    auto locate = [&](int kt, int id) {
       const int k0 = kt * KT + team * B;
-      int nk = max(0, min(B, end - k0));  // the team's keys; the warp's teams stay together
-      const int mine = id;
-      id = block_of(kt + 1);
-      if (table && nk > 0 && (mine < 0 || mine >= a.num_blocks)) {
-        if (lane == 0) atomicOr(status, kDevBadBlock);
-        nk = 0;
-      }
-      if (LK == 32 ? nk == 0 : !__any_sync(0xFFFFFFFFu, nk > 0)) continue;
-      int64_t kp, vp, ks, vs;  // first row, distance of rows
+      const int nk = kt < stop ? max(0, min(B, end - k0)) : 0;
       if (table) {
-        kp = vp = mine * a.block_stride +
+        if (nk > 0 && (id < 0 || id >= a.num_blocks)) {
+          if (lane == 0) atomicOr(status, kDevBadBlock);
+          return 0;
+        }
+        kp = vp = id * a.block_stride +
                   static_cast<int64_t>(h * a.block_size + k0 % a.block_size) * hd;
-        ks = vs = hd;
       } else {
         ks = a.k_stride;
         vs = a.v_stride;
         kp = (static_cast<int64_t>(q.q0) + k0) * ks + static_cast<int64_t>(h) * hd;
         vp = (static_cast<int64_t>(q.q0) + k0) * vs + static_cast<int64_t>(h) * hd;
       }
+      return nk;
+    };
+    int slot3 = 0;  // stage of the current tile
+    auto fetch = [&](int kt, int id, int stage) {
+      const int nk = locate(kt, id);
+      uint8_t *const at = stages + stage * 2 * HALF;
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = 4 * lane + 4 * LK * c;
+          uint8_t *const kd = at + (k * NC + c) * kThreads * W, *const vd = kd + HALF;
+          if (k < nk && d < hd) {
+            copy_x4<BF16>(smem_addr(kd), a.k, kp + k * ks + d);
+            copy_x4<BF16>(smem_addr(vd), a.v, vp + k * vs + d);
+          } else if constexpr (BF16) {
+            *reinterpret_cast<uint2 *>(kd) = *reinterpret_cast<uint2 *>(vd) = make_uint2(0, 0);
+          } else {
+            *reinterpret_cast<float4 *>(kd) = *reinterpret_cast<float4 *>(vd) =
+                make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return nk;
+    };
+    int id = block_of(tile), nk0 = 0, nk1 = 0;
+    if constexpr (C::stages > 0) {
+      const int id1 = block_of(tile + 1), id2 = block_of(tile + 2);
+      nk0 = fetch(tile, id, 0);
+      nk1 = fetch(tile + 1, id1, 1);
+      id = id2;
+    }
+    for (int kt = tile; kt < stop; ++kt) {
+      const int k0 = kt * KT + team * B;
+      int nk;  // the team's keys; the warp's teams stay together
+      const uint8_t *at = nullptr;
+      if constexpr (C::stages > 0) {
+        const int two = id, ahead = slot3 == 0 ? 2 : slot3 - 1;
+        id = block_of(kt + 3);
+        const int nk2 = fetch(kt + 2, two, ahead);
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        at = stages + slot3 * 2 * HALF;
+        slot3 = slot3 == 2 ? 0 : slot3 + 1;
+        nk = nk0;
+        nk0 = nk1;
+        nk1 = nk2;
+      } else {
+        const int mine = id;
+        id = block_of(kt + 1);
+        nk = locate(kt, mine);
+      }
+      if (LK == 32 ? nk == 0 : !__any_sync(0xFFFFFFFFu, nk > 0)) continue;
       float4 kv[B][NC], vv[B][NC];
+      if constexpr (C::stages > 0) {
 #pragma unroll
-      for (int k = 0; k < B; ++k)
+        for (int k = 0; k < B; ++k)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int d = 4 * lane + 128 * c;
-          kv[k][c] = k < nk && d < hd ? load_x4<BF16>(a.k, kp + k * ks + d)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+          for (int c = 0; c < NC; ++c)
+            kv[k][c] = shared_x4<BF16>(at + (k * NC + c) * kThreads * W);
+      } else {
 #pragma unroll
-      for (int k = 0; k < B; ++k)
+        for (int k = 0; k < B; ++k)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int d = 4 * lane + 128 * c;
-          vv[k][c] = k < nk && d < hd ? load_x4<BF16>(a.v, vp + k * vs + d)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+          for (int c = 0; c < NC; ++c) {
+            const int d = 4 * lane + 4 * LK * c;
+            kv[k][c] = k < nk && d < hd ? load_x4<BF16>(a.k, kp + k * ks + d)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int d = 4 * lane + 4 * LK * c;
+            vv[k][c] = k < nk && d < hd ? load_x4<BF16>(a.v, vp + k * vs + d)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+      }
       float s[N];
 #pragma unroll
       for (int p = 0; p < RR; ++p)
@@ -228,7 +325,12 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
       // some row of some team misses some key: not even 0 * NaN may enter
       const bool guard = LK == 32 ? k0 + B > all : __any_sync(0xFFFFFFFFu, k0 + B > all || nk < B);
 #pragma unroll
-      for (int k = 0; k < B; ++k)
+      for (int k = 0; k < B; ++k) {
+        if constexpr (C::stages > 0) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            vv[k][c] = shared_x4<BF16>(at + HALF + (k * NC + c) * kThreads * W);
+        }
 #pragma unroll
         for (int p = 0; p < RR; ++p) {
           const int v = p * B + k;
@@ -242,10 +344,12 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
             o[p][c].w = fmaf(w, vv[k][c].w, o[p][c].w);
           }
         }
+      }
     }
     // the row's sum over its lanes, then the teams' parts together
 #pragma unroll
     for (int w = C::dup; w < C::dup * (B / PL); w <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, w);
+    if (C::stages > 0) __syncthreads();  // the stages' memory takes the results
     if (skey == 0 && lane % C::dup == 0) {
       wm[team][srow] = m;
       wl[team][srow] = l;
@@ -254,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
     for (int p = 0; p < RR; ++p)
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        *reinterpret_cast<float4 *>(wo + (team * RR + p) * CW + c * 128 + 4 * lane) = o[p][c];
+        *reinterpret_cast<float4 *>(wo + (team * RR + p) * CW + 4 * LK * c + 4 * lane) = o[p][c];
     __syncthreads();
     const bool whole = tile == 0 && stop == ntile;
     const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);
@@ -301,7 +405,8 @@ cudaError_t run_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                      const AttnParts &parts, cudaStream_t s) {
   using C = Rows<NC, RR, LK>;
   auto kern = attn_rows_kernel<BF16, NC, RR, LK>;
-  constexpr int smem = C::teams * RR * NC * 4 * LK * 4;
+  constexpr int staged = C::stages * 2 * C::pieces * (BF16 ? 8 : 16);
+  constexpr int smem = staged > C::out_bytes ? staged : C::out_bytes;
   const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
   uint32_t *status = device_status();
@@ -316,14 +421,14 @@ cudaError_t pick_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc
   if (a.head_dim <= 64) {
     if (p.rows == 1) return run_rows<BF16, 1, 1, 16>(a, p, sc, parts, s);
     if (p.rows == 2) return run_rows<BF16, 1, 2, 16>(a, p, sc, parts, s);
-    if (p.rows == 4) return run_rows<BF16, 1, 4, 16>(a, p, sc, parts, s);
-    return run_rows<BF16, 1, 8, 16>(a, p, sc, parts, s);
+    if (p.rows == 4) return run_rows<BF16, 2, 4, 8>(a, p, sc, parts, s);
+    return run_rows<BF16, 2, 8, 8>(a, p, sc, parts, s);
   }
   if (a.head_dim <= 128) {
     if (p.rows == 1) return run_rows<BF16, 1, 1>(a, p, sc, parts, s);
     if (p.rows == 2) return run_rows<BF16, 1, 2>(a, p, sc, parts, s);
-    if (p.rows == 4) return run_rows<BF16, 1, 4>(a, p, sc, parts, s);
-    return run_rows<BF16, 1, 8>(a, p, sc, parts, s);
+    if (p.rows == 4) return run_rows<BF16, 2, 4, 16>(a, p, sc, parts, s);
+    return run_rows<BF16, 2, 8, 16>(a, p, sc, parts, s);
   }
   if (a.head_dim <= 256) {
     if (p.rows <= 2) return run_rows<BF16, 2, 2>(a, p, sc, parts, s);
@@ -337,21 +442,23 @@ cudaError_t pick_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc
 // Calls with few query rows per request and key/value head: at most 8, 4 or 2
 // of them (what a thread's registers hold of queries and results at 128, 256
 // and 512 columns).
-bool attn_rows_plan(int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p) {
-  const int most = head_dim <= 128 ? 8 : head_dim <= 256 ? 4 : 2;
+bool attn_rows_plan(bool paged, int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p) {
+  const int most = head_dim <= 128 ? 8 : head_dim <= 256 ? 4 : 2;  // rows of a unit
+  const int take = paged ? 4 * most : most;  // rows of a request
   const int grp = n_head / n_kv;
-  if (R < 1 || grp > most || T * grp > static_cast<int64_t>(most) * R) return false;
+  if (R < 1 || grp > take || T * grp > static_cast<int64_t>(take) * R) return false;
   const int avg = static_cast<int>((T * grp + R - 1) / R);
   int rows = head_dim <= 128 ? 1 : 2;
-  while (rows < avg || rows < grp) rows *= 2;
+  while (rows < most && (rows < avg || rows < grp)) rows *= 2;
   p->rows = rows;
-  p->gsub = grp;
-  p->nsub = 1;
-  p->U = rows / grp;
+  p->gsub = grp < rows ? grp : rows;
+  p->nsub = (grp + p->gsub - 1) / p->gsub;
+  p->U = rows / p->gsub;
   p->KT = head_dim <= 64 ? 128 : head_dim <= 128 ? 64 : head_dim <= 256 ? 32 : 16;
   p->fixed = 2 * p->KT;
   p->min_run = 2 * p->KT;
-  p->workers = sm_count() * 2;
+  // CTAs an SM: two, or one that stages its loads
+  p->workers = sm_count() * (rows * (head_dim <= 256 ? 2 : 4) <= 4 ? 2 : 1);
   return true;
 }
 

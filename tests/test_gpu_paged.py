@@ -344,6 +344,26 @@ def test_paged_other_heads(dev, nh, nkv, hd, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", [(12, 1, 128), (32, 2, 64), (20, 1, 84), (32, 1, 36), (16, 2, 256),
+                                       (13, 1, 200), (8, 1, 512), (5, 1, 260)])
+def test_paged_rows_of_several_units(dev, nh, nkv, hd, dtype):
+    """More query rows to a key/value head than one unit of the kernel for few
+    rows takes: whole and ragged shares of a group, single tokens and several,
+    rows that see no key, blocks outside the cache."""
+    run_paged([(700, 1), (33, 1), (1, 1), (0, 1), (258, 1), (0, 0)], nh, nkv, hd, 16, dtype,
+              bad=[(0, 2), (4, 16)])
+    few = max(1, 32 // (nh // nkv) * 4 // 5) if hd <= 128 else 1
+    run_paged([(700, few + 1), (few - 1, few), (64, few)], nh, nkv, hd, 32, dtype, pad=2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [3, 5, 7, 8])
+def test_paged_few_tokens_each(dev, n, dtype):
+    run_paged([(900, n), (n, n), (40, n), (2, n)], 8, 2, 128, 16, dtype, bad=[(0, 50)])
+    run_paged([(900, n), (n, n), (40, n), (2, n)], 16, 2, 60, 64, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_paged_rows_that_see_no_key(dev, dtype):
     """Fewer cache rows than new tokens: the first of them see nothing."""
     run_paged([(3, 10), (0, 4), (130, 140), (1, 300), (-5, 2)], 4, 2, 64, 16, dtype)
