@@ -89,15 +89,25 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
     const int end = sched_end(sc, q, i);        // keys the last token sees
     const int all = q.L - q.n + t0 + 1;         // keys the first token sees
     __syncthreads();                            // the previous unit is done with Qs
-    for (int e = tid; e < TR * NC * 16; e += kThreads) {
-      const int row = e / (NC * 16), c = e - row * (NC * 16);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row < rows && c < d4) {
-        const int t = row / g, hq = row - t * g;
-        v = load_x4<BF16>(a.q, static_cast<int64_t>(q.q0 + t0 + t) * a.q_stride +
-                                   static_cast<int64_t>(head0 + hq) * hd + 4 * c);
+    constexpr int QB = TR * NC / 16 < 8 ? TR * NC / 16 : 8;  // loads in flight a thread
+#pragma unroll 1
+    for (int e0 = tid; e0 < TR * NC * 16; e0 += QB * kThreads) {
+      float4 v[QB];
+#pragma unroll
+      for (int j = 0; j < QB; ++j) {
+        const int e = e0 + j * kThreads, row = e / (NC * 16), c = e - row * (NC * 16);
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < rows && c < d4) {
+          const int t = row / g, hq = row - t * g;
+          v[j] = load_x4<BF16>(a.q, static_cast<int64_t>(q.q0 + t0 + t) * a.q_stride +
+                                        static_cast<int64_t>(head0 + hq) * hd + 4 * c);
+        }
       }
-      *reinterpret_cast<float4 *>(Qs + row * LD + 4 * c) = v;
+#pragma unroll
+      for (int j = 0; j < QB; ++j) {
+        const int e = e0 + j * kThreads, row = e / (NC * 16), c = e - row * (NC * 16);
+        *reinterpret_cast<float4 *>(Qs + row * LD + 4 * c) = v[j];
+      }
     }
     float m[RP], l[RP];
     float4 o[RP][NC];
@@ -131,22 +141,32 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
       // keys without a block, or that some row does not see: the guarded form
       const bool guard = __syncthreads_or(bad) || k0 + KT > all;
       if (bad) atomicOr(status, kDevBadBlock);
-      for (int e = tid; e < KT * NC * 16; e += kThreads) {
-        const int k = e / (NC * 16), c = e - k * (NC * 16);
-        const int64_t off = krow[k];
-        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-        if (off >= 0 && c < d4) {
-          if (a.block_table) {
-            kv = load_x4<BF16>(a.k, off + 4 * c);
-            vv = load_x4<BF16>(a.v, off + 4 * c);
-          } else {
-            const int64_t row = q.q0 + off;
-            kv = load_x4<BF16>(a.k, row * a.k_stride + static_cast<int64_t>(h) * hd + 4 * c);
-            vv = load_x4<BF16>(a.v, row * a.v_stride + static_cast<int64_t>(h) * hd + 4 * c);
+      constexpr int KB = KT * NC / 16 < 4 ? KT * NC / 16 : 4;  // keys and values in flight a thread
+#pragma unroll 1
+      for (int e0 = tid; e0 < KT * NC * 16; e0 += KB * kThreads) {
+        float4 kv[KB], vv[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const int e = e0 + j * kThreads, k = e / (NC * 16), c = e - k * (NC * 16);
+          const int64_t off = krow[k];
+          kv[j] = vv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (off >= 0 && c < d4) {
+            if (a.block_table) {
+              kv[j] = load_x4<BF16>(a.k, off + 4 * c);
+              vv[j] = load_x4<BF16>(a.v, off + 4 * c);
+            } else {
+              const int64_t row = q.q0 + off, col = static_cast<int64_t>(h) * hd + 4 * c;
+              kv[j] = load_x4<BF16>(a.k, row * a.k_stride + col);
+              vv[j] = load_x4<BF16>(a.v, row * a.v_stride + col);
+            }
           }
         }
-        *reinterpret_cast<float4 *>(Ks + k * LD + 4 * c) = kv;
-        *reinterpret_cast<float4 *>(Vs + k * NC * 64 + 4 * c) = vv;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const int e = e0 + j * kThreads, k = e / (NC * 16), c = e - k * (NC * 16);
+          *reinterpret_cast<float4 *>(Ks + k * LD + 4 * c) = kv[j];
+          *reinterpret_cast<float4 *>(Vs + k * NC * 64 + 4 * c) = vv[j];
+        }
       }
       __syncthreads();
       float s[RP][KP];
@@ -330,7 +350,7 @@ cudaError_t launch_simt(const AttnBatch &a, const AttnSched &sc, int gsub, int n
 template <bool BF16, int TR>
 cudaError_t launch_simt_nc(int nc, const AttnBatch &a, const AttnSched &sc, int gsub, int nsub,
                            const AttnParts &parts, int workers, cudaStream_t s) {
-  if constexpr (BF16 || TR == 16) {  // fp32, 64 rows, up to 128 columns: attn_tile_kernel's
+  if constexpr (BF16) {  // fp32, up to 128 columns: attn_rows_kernel or attn_tile_kernel
     if (nc == 1) return launch_simt<BF16, 1, TR>(a, sc, gsub, nsub, parts, workers, s);
     if (nc == 2) return launch_simt<BF16, 2, TR>(a, sc, gsub, nsub, parts, workers, s);
   }
@@ -352,7 +372,7 @@ AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R) {
   const int nc = simt_nc(head_dim);
   p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
   p.fixed = p.KT;
-  p.min_run = 2 * p.KT;
+  p.min_run = p.KT;
   p.workers = sm_count() * 2;
   return p;
 }
