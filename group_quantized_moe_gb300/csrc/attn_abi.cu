@@ -72,7 +72,6 @@ int log2i(int v) {
   return s;
 }
 
-constexpr int64_t kWholeKeys = 512;  // see launch_attn_batch
 constexpr int64_t kMaxKeys = (int64_t(1) << 29) - 1;  // of one request (costs of a unit fit 32 bits)
 
 // What both attention calls check: T query rows, the lengths, scale, output,
@@ -164,9 +163,8 @@ cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t 
   const int64_t cap = a.block_table
                           ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, kMaxKeys)
                           : a.T;
-  // Where no request can have more than a few tiles of keys, dividing a unit
-  // gains less than the second launch costs.
-  const bool whole = cap <= kWholeKeys;
+  const int64_t usual = a.block_table || a.R < 1 ? cap : a.T / a.R;
+  const bool whole = cap <= kWholeKeys && usual <= p.whole;
   AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, log2i(p.KT), p.fixed, p.min_run,
                ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, whole, a.T, cap};
   const cudaError_t e = launch(a, p, sc, parts, s);

@@ -19,11 +19,14 @@ struct AttnParts {
   int rows;
 };
 
+constexpr int kWholeKeys = 512;
 // How a call is cut up: rows (query rows of a unit), the query heads gsub of
 // a group that one unit takes (nsub units cover the group), tokens U and keys
-// KT of a tile, workers (fixed, min_run: see AttnSched).
+// KT of a tile, workers (fixed, min_run: see AttnSched).  Where requests have up
+// to `whole` keys on average, and none can have more than kWholeKeys, dividing a unit
+// gains less than the second launch costs, and units stay whole.
 struct AttnPlan {
-  int rows, gsub, nsub, U, KT, fixed, min_run, workers;
+  int rows, gsub, nsub, U, KT, fixed, min_run, workers, whole;
 };
 
 AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R);

@@ -28,7 +28,11 @@
 // which over long caches still is cheaper up to four units (24 requests of 2048
 // keys, 32 rows each: 282 us against attn_tile_kernel's 387; 256 columns, 16
 // rows: 132 against attn_simt_kernel's 163); packed prompts, whose keys are few,
-// go there at once (16 prompts of 32 tokens, 32 heads: 37 us against 74).
+// go there at once (16 prompts of 32 tokens, 32 heads: 37 us against 74), unless
+// all of their units are at most three to an SM: attn_tile_kernel's units of 128
+// rows would leave SMs idle (a prompt of 37 tokens, 6 heads 8.2 us against 19; of
+// 100 tokens, 32 heads, 400 units 22 against 32; 4 of 32 tokens, 512 units 22
+// against 16).
 #include <cstdint>
 
 #include "attn_batch.h"
@@ -444,9 +448,11 @@ cudaError_t pick_rows(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc
 // and 512 columns).
 bool attn_rows_plan(bool paged, int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p) {
   const int most = head_dim <= 128 ? 8 : head_dim <= 256 ? 4 : 2;  // rows of a unit
-  const int take = paged ? 4 * most : most;  // rows of a request
+  const int take = paged ? 4 * most : most;                        // rows of a request
   const int grp = n_head / n_kv;
-  if (R < 1 || grp > take || T * grp > static_cast<int64_t>(take) * R) return false;
+  const int64_t total = T * n_head;
+  const bool few = grp <= take && T * grp <= static_cast<int64_t>(take) * R;
+  if (R < 1 || !(few || (!paged && total <= static_cast<int64_t>(3) * most * sm_count()))) return false;
   const int avg = static_cast<int>((T * grp + R - 1) / R);
   int rows = head_dim <= 128 ? 1 : 2;
   while (rows < most && (rows < avg || rows < grp)) rows *= 2;
@@ -457,6 +463,7 @@ bool attn_rows_plan(bool paged, int64_t T, int n_head, int n_kv, int head_dim, i
   p->KT = head_dim <= 64 ? 128 : head_dim <= 128 ? 64 : head_dim <= 256 ? 32 : 16;
   p->fixed = 2 * p->KT;
   p->min_run = 2 * p->KT;
+  p->whole = kWholeKeys;
   // CTAs an SM: two, or one that stages its loads
   p->workers = sm_count() * (rows * (head_dim <= 256 ? 2 : 4) <= 4 ? 2 : 1);
   return true;

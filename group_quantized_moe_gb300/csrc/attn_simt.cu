@@ -373,6 +373,7 @@ AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R) {
   p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
   p.fixed = p.KT;
   p.min_run = p.KT;
+  p.whole = 128;  // four prompts of 40 tokens, 512 columns: whole 47 us, divided 64
   p.workers = sm_count() * 2;
   return p;
 }

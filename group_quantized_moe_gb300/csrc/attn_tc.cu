@@ -936,6 +936,7 @@ AttnPlan attn_tc_plan(bool paged, int64_t T, int n_head, int n_kv, int R) {
   // one with a single query tile less, as do its tiles
   p.fixed = few ? 5 * kKT / 2 : 3 * kKT;
   p.min_run = 2 * kKT;
+  p.whole = kWholeKeys;  // a prompt of 37 tokens 8.1 us, 10.7 with a launch to join
   p.workers = sm_count();
   return p;
 }

@@ -373,6 +373,9 @@ bool attn_tile_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, in
   // (6 heads over one, 2 prompts of 300 tokens: 47 us; runs of four tiles 58).
   p->fixed = kKeys;
   p->min_run = kKeys;
+  // a prompt of 200 tokens (32 heads over 8) divided 39 us, whole 54; four of 64
+  // tokens 35 and 24
+  p->whole = 128;
   p->workers = sm_count() * (head_dim <= 64 ? 2 : 1);
   return true;
 }
