@@ -233,6 +233,23 @@ def test_prompt_long_and_many(dev, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", [(32, 8, 64), (32, 32, 128), (40, 4, 20), (24, 24, 100), (30, 5, 80),
+                                       (16, 4, 132), (12, 12, 256), (8, 2, 260), (8, 1, 512)])
+def test_prompt_many_rows(dev, nh, nkv, hd, dtype):
+    """More query rows than the kernel for few rows takes, whole units and divided ones."""
+    run_prompt([300, 1, 0, 77, 150, 64], nh, nkv, hd, dtype, pad=3, strided=hd % 8 == 0)
+    run_prompt([700], nh, nkv, hd, dtype, qs=50.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", [(8, 8, 20), (8, 8, 100), (4, 4, 256), (4, 4, 512)])
+def test_prompt_many_short_ones(dev, nh, nkv, hd, dtype):
+    """8 to 16 query rows a request and head."""
+    rng = np.random.default_rng(4)
+    run_prompt([int(n) for n in rng.integers(0, 24, 100)], nh, nkv, hd, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_prompt_sharp_scores(dev, dtype):
     """Scores of hundreds: the running maximum moves by far more than one weight's range."""
     run_prompt([400], 4, 2, 64, dtype, qs=100.0)
@@ -257,6 +274,20 @@ def test_prompt_unseen_values_do_not_matter(dev, dtype):
     y = q.attn_prompt(qq, k, v2, cu_of([n, n]))
     assert torch.equal(y[:200], clean[:200])
     assert (y[200:n, :, 5] == float("inf")).all() and y[200:n, :, :5].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", [(32, 8, 64), (8, 4, 256), (40, 8, 100)])
+def test_prompt_unseen_values_do_not_matter_with_many_rows(dev, nh, nkv, hd, dtype):
+    n = 300
+    qq, k, v = (rnd(s, (2 * n, h, hd), dtype).cuda() for s, h in ((1, nh), (2, nkv), (3, nkv)))
+    clean = q.attn_prompt(qq, k, v, cu_of([n, n]))
+    for j, what in ((0, "v"), (150, "v"), (150, "k"), (299, "v")):
+        k2, v2 = k.clone(), v.clone()
+        (v2 if what == "v" else k2)[j] = float("nan")
+        y = q.attn_prompt(qq, k2, v2, cu_of([n, n]))
+        assert torch.equal(y[:j], clean[:j]) and torch.equal(y[n:], clean[n:]), (j, what)
+        assert y[j:n].isnan().all(), (j, what)
 
 
 def test_prompt_repeats_bit_for_bit_on_any_stream(dev):
@@ -354,6 +385,13 @@ def test_paged_rows_of_several_units(dev, nh, nkv, hd, dtype):
               bad=[(0, 2), (4, 16)])
     few = max(1, 32 // (nh // nkv) * 4 // 5) if hd <= 128 else 1
     run_paged([(700, few + 1), (few - 1, few), (64, few)], nh, nkv, hd, 32, dtype, pad=2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", [(16, 4, 256), (8, 2, 512), (8, 8, 132)])
+def test_paged_chunks_of_wide_heads(dev, nh, nkv, hd, dtype):
+    run_paged(MIXED, nh, nkv, hd, 32, dtype, bad=[(0, 3), (2, 9)])
+    run_paged([(300, 12), (12, 12), (5, 12)], nh, nh, hd, 16, dtype)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
