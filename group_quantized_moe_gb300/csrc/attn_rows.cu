@@ -17,12 +17,12 @@
 // columns, which keeps the registers free for loads in flight.  Four rows and
 // more: half as many lanes with two pieces each, which halves the exchanges of
 // a key (16 heads over 4 of 64 columns, 128 requests: 5.8 TB/s instead of 4.2;
-// 64 over 8 of 128: 5.4 instead of 4.8; 12 over 4 of 96: 5.2 instead of 4.8).
+// 64 over 8 of 128: 5.5 instead of 4.8; 12 over 4 of 96: 5.2 instead of 4.8).
 //
 // Measured: 12 single tokens of 32 heads of 128 columns over 32 key/value
 // heads' fp32 caches (623 MB) 98 us, 6.4 TB/s, 94% of a copy.  Eight rows a key are bound by
-// the latency of reduction, maximum and weights at two warps a scheduler: 80% of
-// a copy.
+// instructions and their latency at two warps a scheduler (they issue 63% of the
+// cycles; 47% of the instructions are the products): 82% of a copy.
 //
 // A request's rows beyond a unit's are further units that read its keys again,
 // which over long caches still is cheaper up to four units (24 requests of 2048
@@ -342,10 +342,12 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
           if (guard && w == 0.0f) continue;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            o[p][c].x = fmaf(w, vv[k][c].x, o[p][c].x);
-            o[p][c].y = fmaf(w, vv[k][c].y, o[p][c].y);
-            o[p][c].z = fmaf(w, vv[k][c].z, o[p][c].z);
-            o[p][c].w = fmaf(w, vv[k][c].w, o[p][c].w);
+            // pairs: 64 heads over 8 149 -> 145 us (the scores gain nothing from them)
+            const f32x2 w2 = pack2(w, w);
+            unpack2(fma2(w2, pack2(vv[k][c].x, vv[k][c].y), pack2(o[p][c].x, o[p][c].y)), o[p][c].x,
+                    o[p][c].y);
+            unpack2(fma2(w2, pack2(vv[k][c].z, vv[k][c].w), pack2(o[p][c].z, o[p][c].w)), o[p][c].z,
+                    o[p][c].w);
           }
         }
       }
