@@ -9,6 +9,7 @@ library's CUDA kernels; there is no other implementation behind these names.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import operator
 import os
@@ -196,6 +197,44 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _stream_of(stream) -> torch.cuda.Stream:
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if int(stream) in (0, 1):  # the legacy default stream (torch takes the handle 0 for "a new stream")
+        return torch.cuda.default_stream()
+    return torch.cuda.ExternalStream(int(stream))
+
+
+def _memory_of(stream):
+    """The context in which a call on `stream` allocates: memory from that
+    stream's own pool, whose earlier uses that stream has in its order.  Memory
+    of the current stream's pool may still be in use by work queued there,
+    which nothing orders before the call's."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_stream_of(stream))
+
+
+def _on_stream(stream, *ts) -> None:
+    """Tensors that a call on `stream` uses, or makes there and hands out: their
+    memory must not be used again before that stream, and the current one on
+    which the caller reads them, are done with it."""
+    if stream is None:
+        return
+    for s in (_stream_of(stream), torch.cuda.current_stream()):
+        for t in ts:
+            if t is not None and t.numel():
+                t.record_stream(s)
+
+
+def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An uninitialised output or workspace of a call on `stream`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _memory_of(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    _on_stream(stream, t)
+    return t
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype is torch.float32:
         return QMM_F32
@@ -293,7 +332,9 @@ def qmm_quantize_groupwise(w: torch.Tensor, bits: int, group: int, out: QWeight 
     if out is not None:
         _require_cuda(*_qweight_tensors(out))
     if out is None:
-        out = alloc_qweight(N, K, bits, group, device=w.device)
+        with _memory_of(stream):
+            out = alloc_qweight(N, K, bits, group, device=w.device)
+        _on_stream(stream, *_qweight_tensors(out))
     _check(lib().qmm_quantize_groupwise(_ptr(w), N, K, bits, group, _ptr(out.codes),
                                         _ptr(out.scales), _ptr(out.zps), _stream(stream)))
     return out
@@ -328,7 +369,7 @@ def qmm_linear(x: torch.Tensor, w: QWeight, y: torch.Tensor | None = None,
         w.__dict__["_desc_for"] = (codes, scales, zps, codes.data_ptr(), scales.data_ptr(),
                                    zps.data_ptr(), desc, shape)
     if y is None:
-        y = torch.empty((M, w.N), dtype=y_dtype, device=x.device)
+        y = _new((M, w.N), y_dtype, x.device, stream)
     _check(lib().qmm_linear(_ptr(x2), _dtype_code(x2), M, ctypes.byref(desc), _ptr(y),
                             _dtype_code(y), _stream(stream)))
     return y
@@ -354,12 +395,10 @@ def qmm_linear_batched(x: torch.Tensor, w: QWeight, y: torch.Tensor | None = Non
     _require_cuda(x, y, workspace, *_qweight_tensors(w))
     desc = w._c()
     if y is None:
-        y = torch.empty((M, w.N), dtype=y_dtype, device=x.device)
-        _on_stream(stream, y)
+        y = _new((M, w.N), y_dtype, x.device, stream)
     if workspace is None:  # a caller's workspace is size-checked by the library
         nbytes = int(lib().qmm_linear_batched_workspace_bytes(M, ctypes.byref(desc)))
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
-        _on_stream(stream, workspace)
+        workspace = _new((nbytes,), torch.uint8, x.device, stream)
     _check(lib().qmm_linear_batched(_ptr(x2), _dtype_code(x2), M, ctypes.byref(desc), _ptr(y),
                                     _dtype_code(y), _ptr(workspace), _nbytes(workspace),
                                     _stream(stream)))
@@ -396,13 +435,13 @@ def moe_route_topk(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor |
     _require_cuda(workspace)
     dev = x.device
     if topk_idx is None:
-        topk_idx = torch.empty((M, k), dtype=torch.int32, device=dev)
+        topk_idx = _new((M, k), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = torch.empty((M, k), dtype=torch.float32, device=dev)
+        topk_w = _new((M, k), torch.float32, dev, stream)
     if expert_counts is None and with_counts:
-        expert_counts = torch.empty((E,), dtype=torch.int32, device=dev)
+        expert_counts = _new((E,), torch.int32, dev, stream)
     if workspace is None:  # a caller's workspace is size-checked by the library
-        workspace = torch.empty((moe_route_workspace_bytes(M, E),), dtype=torch.uint8, device=dev)
+        workspace = _new((moe_route_workspace_bytes(M, E),), torch.uint8, dev, stream)
     _check(lib().moe_route_topk(_ptr(x), _dtype_code(x), M, H, _ptr(w_router), _ptr(bias), E, k,
                                 _ptr(topk_idx), _ptr(topk_w), _ptr(expert_counts),
                                 _ptr(workspace), _nbytes(workspace), _stream(stream)))
@@ -511,10 +550,10 @@ def moe_ffn_forward(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tenso
         desc = experts._c()
         experts.__dict__["_desc_for"] = (ts, tuple(t.data_ptr() for t in ts), shape, desc)
     if y is None:
-        y = torch.empty((M, H), dtype=y_dtype, device=x.device)
+        y = _new((M, H), y_dtype, x.device, stream)
     if workspace is None:  # a caller's workspace is size-checked by the library
         nbytes = int(lib().moe_ffn_workspace_bytes(M, k, ctypes.byref(desc)))
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
+        workspace = _new((nbytes,), torch.uint8, x.device, stream)
     _check(lib().moe_ffn_forward(_ptr(x), _dtype_code(x), M, _ptr(topk_idx), _ptr(topk_w), k,
                                  ctypes.byref(desc), _ptr(y), _dtype_code(y), _ptr(workspace),
                                  _nbytes(workspace), _stream(stream)))
@@ -554,10 +593,10 @@ def moe_decode_forward(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tens
     _require_cuda(y, workspace)
     desc = _experts_desc(experts)
     if y is None:
-        y = torch.empty((M, H), dtype=y_dtype, device=x.device)
+        y = _new((M, H), y_dtype, x.device, stream)
     if workspace is None:  # a caller's workspace is size-checked by the library
         nbytes = int(lib().moe_decode_workspace_bytes(M, k, ctypes.byref(desc)))
-        workspace = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=x.device)
+        workspace = _new((max(nbytes, 1),), torch.uint8, x.device, stream)
     _check(lib().moe_decode_forward(_ptr(x), _dtype_code(x), M, _ptr(w_router), _ptr(bias), k,
                                     ctypes.byref(desc), _ptr(y), _dtype_code(y), _ptr(topk_idx),
                                     _ptr(topk_w), _ptr(expert_counts), _ptr(workspace),
@@ -575,11 +614,11 @@ def moe_route_topk_noalloc(x: torch.Tensor, w_router: torch.Tensor, bias: torch.
     M, H, E = _check_route(x, w_router, bias, k, topk_idx, topk_w, expert_counts)
     dev = x.device
     if topk_idx is None:
-        topk_idx = torch.empty((M, k), dtype=torch.int32, device=dev)
+        topk_idx = _new((M, k), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = torch.empty((M, k), dtype=torch.float32, device=dev)
+        topk_w = _new((M, k), torch.float32, dev, stream)
     if expert_counts is None and with_counts:
-        expert_counts = torch.empty((E,), dtype=torch.int32, device=dev)
+        expert_counts = _new((E,), torch.int32, dev, stream)
     _check(lib().moe_route_topk_noalloc(_ptr(x), _dtype_code(x), M, H, _ptr(w_router), _ptr(bias),
                                         E, k, _ptr(topk_idx), _ptr(topk_w), _ptr(expert_counts),
                                         _stream(stream)))
@@ -598,7 +637,7 @@ def moe_route_load_stats(expert_counts: torch.Tensor, threshold: int, stats=None
     _need(stats, 4, (torch.int64,), "stats")
     _require_cuda(expert_counts, stats)
     if stats is None:
-        stats = torch.empty((4,), dtype=torch.int64, device=expert_counts.device)
+        stats = _new((4,), torch.int64, expert_counts.device, stream)
     _check(lib().moe_route_load_stats(_ptr(expert_counts), E, int(threshold), _ptr(stats),
                                       _stream(stream)))
     return stats
@@ -646,11 +685,13 @@ def quantize_experts(E: int, H: int, I: int, bits: int, group: int, rows_fn, dev
     matrix is staged through pinned host memory to the device and quantised
     there by qmm_quantize_groupwise, so no fp32 copy of the experts stays
     resident."""
-    ex = alloc_experts(E, H, I, bits, group, device=device)
     n = I * H
     pinned = [torch.empty((n,), dtype=torch.float32).pin_memory() for _ in range(2)]
-    staging = [torch.empty((n,), dtype=torch.float32, device=device) for _ in range(2)]
-    s = torch.cuda.current_stream(device) if stream is None else stream
+    s = torch.cuda.current_stream(device) if stream is None else _stream_of(stream)
+    with torch.cuda.stream(s):
+        ex = alloc_experts(E, H, I, bits, group, device=device)
+        staging = [torch.empty((n,), dtype=torch.float32, device=device) for _ in range(2)]
+    _on_stream(stream, *_experts_tensors(ex))
     events = [None, None]
     j = 0
     for e in range(E):
@@ -680,8 +721,8 @@ def rope_table(max_seq: int, head_dim: int, base: float = 10000.0, device="cuda"
     """cos, sin fp32 [max_seq, head_dim / 2] of pos * base^(-2i / head_dim)
     (see include/qmm.h)."""
     hp = head_dim // 2
-    c = torch.empty((max_seq, hp), dtype=torch.float32, device=device)
-    s = torch.empty((max_seq, hp), dtype=torch.float32, device=device)
+    c = _new((max_seq, hp), torch.float32, device, stream)
+    s = _new((max_seq, hp), torch.float32, device, stream)
     _check(lib().qmm_rope_table(max_seq, head_dim, float(base), _ptr(c), _ptr(s),
                                 _stream(stream)))
     return c, s
@@ -720,8 +761,9 @@ def quantize_attn_layer(wq: torch.Tensor, wk: torch.Tensor, wv: torch.Tensor, wo
     matrix (so that the decode step runs the three projections as one
     launch), wo on its own, and the RoPE table."""
     nq, nk = wq.shape[0], wk.shape[0]
-    qkv = qmm_quantize_groupwise(torch.cat([wq, wk, wv], dim=0).contiguous(), bits, group,
-                                 stream=stream)
+    with _memory_of(stream):  # the stacking runs where the quantisation reads it
+        qkv = torch.cat([wq, wk, wv], dim=0).contiguous()
+    qkv = qmm_quantize_groupwise(qkv, bits, group, stream=stream)
     c, s = rope_table(max_seq, head_dim, base, device=wq.device, stream=stream)
     return AttnLayer(n_head, n_head_kv, head_dim, max_seq, qkv.rows(0, nq),
                      qkv.rows(nq, nq + nk), qkv.rows(nq + nk, nq + 2 * nk),
@@ -753,10 +795,10 @@ def attn_decode(x: torch.Tensor, pos: int, layer: AttnLayer, kv_cache: torch.Ten
     _require_cuda(x, kv_cache, y, workspace, layer.rope_cos, layer.rope_sin, *ts)
     desc = layer._c()
     if y is None:
-        y = torch.empty((layer.wo.N,), dtype=y_dtype, device=x.device)
+        y = _new((layer.wo.N,), y_dtype, x.device, stream)
     if workspace is None:  # a caller's workspace is size-checked by the library
         nbytes = int(lib().qmm_attn_decode_workspace_bytes(ctypes.byref(desc)))
-        workspace = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=x.device)
+        workspace = _new((max(nbytes, 1),), torch.uint8, x.device, stream)
     _check(lib().qmm_attn_decode(_ptr(x), _dtype_code(x), pos, ctypes.byref(desc), _ptr(kv_cache),
                                  _ptr(y), _dtype_code(y), _ptr(workspace), _nbytes(workspace),
                                  _stream(stream)))
@@ -764,18 +806,6 @@ def attn_decode(x: torch.Tensor, pos: int, layer: AttnLayer, kv_cache: torch.Ten
 
 
 # ------------------------------------------------------- paged cache, batches
-
-def _on_stream(stream, *ts) -> None:
-    """Outputs and workspaces allocated here belong to torch's current stream;
-    when the work runs on another one, their memory must not be reused before
-    that stream is done with it."""
-    if stream is None:
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    for t in ts:
-        if t is not None and t.numel():
-            t.record_stream(s)
-
 
 # The calls of this section run once per layer and step, and at decode sizes
 # their kernels take a few microseconds: each tensor is passed by one short
@@ -904,7 +934,8 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
         _require_cuda(ctx_lens, new_lens, free_blocks)
     cols = block_table.shape[1]
     if out is None:
-        out = alloc_kv_plan(R, T, ctx_lens.device)
+        with _memory_of(stream):
+            out = alloc_kv_plan(R, T, ctx_lens.device)
         _on_stream(stream, out.cu_new, out.kv_lens, out.positions, out.slots, out.blocks_used)
     else:
         _check_vec(out.cu_new, _I32, R + 1, "cu_new")
@@ -971,14 +1002,11 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
         _on_device(qkv)
         _require_cuda(positions, slots, rope_cos, rope_sin, q, k, v)
     if q is None:
-        q = torch.empty((T, n_head, hd), dtype=y_dtype, device=qkv.device)
-        _on_stream(stream, q)
+        q = _new((T, n_head, hd), y_dtype, qkv.device, stream)
     if keep_kv and k is None:
-        k = torch.empty((T, n_kv, hd), dtype=y_dtype, device=qkv.device)
-        _on_stream(stream, k)
+        k = _new((T, n_kv, hd), y_dtype, qkv.device, stream)
     if keep_kv and v is None:
-        v = torch.empty((T, n_kv, hd), dtype=y_dtype, device=qkv.device)
-        _on_stream(stream, v)
+        v = _new((T, n_kv, hd), y_dtype, qkv.device, stream)
     rc = lib().qmm_rope_append(qkv.data_ptr(), _dtype_code(qkv), T, qkv.stride(0) if T > 1 else width,
                                n_head, n_kv, hd, positions.data_ptr(),
                                None if slots is None else slots.data_ptr(), rope_cos.data_ptr(),
@@ -996,20 +1024,11 @@ _CODES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16}
 def _attn_y(q, y, y_dtype, stream):
     """The output of an attention call, checked or allocated."""
     if y is None:
-        y = torch.empty(q.shape, dtype=y_dtype, device=q.device)
-        if stream is not None:
-            _on_stream(stream, y)
+        y = _new(q.shape, y_dtype, q.device, stream)
     else:
         _need(y, q.numel(), (_F32, torch.bfloat16), "y")
         _require_cuda(y)
     return y
-
-
-def _workspace(nbytes, q, stream):
-    w = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
-    if stream is not None:
-        _on_stream(stream, w)
-    return w
 
 
 def qmm_attn_prompt_workspace_bytes(q: torch.Tensor, k: torch.Tensor, n_seqs: int) -> int:
@@ -1040,7 +1059,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
         _require_cuda(cu_seqlens)
     y = _attn_y(q, y, y_dtype, stream)
     if workspace is None:
-        workspace = _workspace(qmm_attn_prompt_workspace_bytes(q, k, B), q, stream)
+        workspace = _new((qmm_attn_prompt_workspace_bytes(q, k, B),), torch.uint8, q.device, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():  # its size is the library's check
         _require_cuda(workspace)
     rc = lib().qmm_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T, sq, sk, sv,
@@ -1083,7 +1102,8 @@ def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q:
     cols = block_table.shape[1]
     y = _attn_y(q, y, y_dtype, stream)
     if workspace is None:
-        workspace = _workspace(qmm_attn_paged_workspace_bytes(q, cache, R), q, stream)
+        workspace = _new((qmm_attn_paged_workspace_bytes(q, cache, R),), torch.uint8, q.device,
+                         stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():  # its size is the library's check
         _require_cuda(workspace)
     rc = lib().qmm_attn_paged(q.data_ptr(), T, sq, nh, desc, block_table.data_ptr(),
