@@ -175,8 +175,9 @@ cudaError_t launch_kv_plan(const int32_t *ctx, const int32_t *add, int R, int bl
   const int smem = 2 * (R + 1) * 4;
   cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kv_plan_kernel), smem);
   if (e != cudaSuccess) return e;
+  // an idle step, without requests and tokens, still writes cu[0] and *used
   const int64_t work = T > R ? T : R;
-  int64_t blocks = (work + kPlanThreads - 1) / kPlanThreads;
+  int64_t blocks = work > 0 ? (work + kPlanThreads - 1) / kPlanThreads : 1;
   if (blocks > sm_count()) blocks = sm_count();
   return launch_pdl(kv_plan_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kPlanThreads), smem,
                     s, a);
