@@ -921,7 +921,9 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     """Block tables and slot maps from the requests' lengths (int32 [R]; see
     include/qmm.h): fills the new entries of block_table (int32 [R, columns])
     from free_blocks (int32) and returns the plan of num_tokens rows (as many
-    as the new tokens, or more: padding rows get -1)."""
+    as the new tokens, or more: padding rows get -1).  out's tensors must not
+    be those of the lengths: kv_lens is copied to ctx_lens when the step is
+    over."""
     R, T, n_free = ctx_lens.numel(), num_tokens, free_blocks.numel()
     if not (_vec(ctx_lens, _I32, R) and _vec(new_lens, _I32, R) and _vec(free_blocks, _I32, n_free)
             and block_table.dtype is _I32 and block_table.is_cuda and block_table.is_contiguous()

@@ -66,6 +66,29 @@ int check_cache(const char *who, const qmm_kv_cache *c) {
   return QMM_OK;
 }
 
+// Memory of an argument: rows of `len` bytes, `stride` bytes apart (one row for
+// a vector).
+struct Span {
+  const char *name;
+  const void *p;
+  int64_t rows, stride, len;
+};
+
+Span vec_span(const char *name, const void *p, int64_t n, int size) {
+  return {name, p, 1, n * size, n * size};
+}
+
+// Whether a vector and the rows of b share a byte.
+bool overlap(const Span &a, const Span &b) {
+  if (a.len <= 0 || b.len <= 0 || b.rows <= 0) return false;
+  const int64_t lo = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p) - reinterpret_cast<uintptr_t>(b.p));
+  const int64_t hi = lo + a.len;
+  // the first row of b that ends behind lo
+  int64_t r = lo <= 0 ? 0 : lo / b.stride;
+  if (r * b.stride + b.len <= lo) ++r;
+  return r < b.rows && r * b.stride < hi;
+}
+
 int log2i(int v) {
   int s = 0;
   while ((1 << s) < v) ++s;
@@ -198,6 +221,24 @@ int qmm_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int32_t R, int
       (R > 0 && max_blocks > 0 && !block_table) || (n_free > 0 && !free_blocks) ||
       (T > 0 && (!positions || !slots)))
     return refuse(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
+  // Every block of the launch reads the lengths and the free list from first to
+  // last, so none of the outputs may lie on them (or on one another).
+  const Span span[] = {vec_span("cu_new", cu_new, R + int64_t(1), 4),
+                       vec_span("kv_lens", kv_lens, R, 4),
+                       vec_span("positions", positions, T, 4),
+                       vec_span("slots", slots, T, 8),
+                       vec_span("blocks_used", blocks_used, 1, 4),
+                       vec_span("ctx_lens", ctx_lens, R, 4),
+                       vec_span("new_lens", new_lens, R, 4),
+                       vec_span("free_blocks", free_blocks, n_free, 4)};
+  const Span table{"block_table", block_table, R, table_stride * 4, int64_t(max_blocks) * 4};
+  for (int i = 0; i < 8; ++i) {
+    for (int j = i + 1; i < 5 && j < 8; ++j)
+      if (overlap(span[i], span[j]))
+        return refuse(QMM_ERR_INVALID_ARG, "%s: %s overlaps %s", who, span[i].name, span[j].name);
+    if (overlap(span[i], table))
+      return refuse(QMM_ERR_INVALID_ARG, "%s: %s overlaps %s", who, span[i].name, table.name);
+  }
   const cudaError_t e = launch_kv_plan(
       ctx_lens, new_lens, R, log2i(block_size), block_table, table_stride, max_blocks, free_blocks,
       n_free, T, cu_new, kv_lens, positions, slots, blocks_used, static_cast<cudaStream_t>(stream));

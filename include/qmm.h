@@ -341,6 +341,8 @@ typedef struct qmm_kv_cache {
  * positions and slots (may exceed the tokens).  Lengths below 0 count as 0.
  * When the free list, the table's columns or T are too short, entries become
  * -1, the tokens concerned get slot -1 and QMM_DEV_KV_SHORT is set.
+ * Outputs must not overlap the inputs, the table or one another (refused): a
+ * step that keeps its buffers copies kv_lens to ctx_lens when it is over.
  * R <= 16384.  One kernel launch.
  */
 int qmm_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int32_t R, int32_t block_size,

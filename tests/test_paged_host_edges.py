@@ -1,0 +1,57 @@
+"""Further refusals of the paged-cache entry points, on the CPU (see
+tests/test_paged_host.py: addresses that are never dereferenced, and only
+where no GPU is visible)."""
+import pytest
+
+import group_quantized_moe_gb300 as q
+from test_paged_host import L  # noqa: F401 (fixture)
+
+P = 0x7F0000000000
+GAP = 1 << 32
+NAMES = ["ctx", "new", "R", "S", "table", "stride", "cols", "free", "nfree", "T", "cu", "kvl", "pos",
+         "slots", "used", "s"]
+BYTES = dict(ctx=16, new=16, free=40, cu=20, kvl=16, pos=80, slots=160, used=4)
+OUT = ("cu", "kvl", "pos", "slots", "used")
+
+
+def _plan(L, **kw):
+    """qmm_kv_plan of 4 requests, 20 token rows, a table of 4 x 8 in rows of 12."""
+    a = dict(R=4, S=16, stride=12, cols=8, nfree=10, T=20, s=None)
+    for i, k in enumerate(("ctx", "new", "table", "free") + OUT):
+        a[k] = P + i * GAP
+    a.update(kw)
+    return L.qmm_kv_plan(*(a[k] for k in NAMES)), a
+
+
+@pytest.mark.parametrize("out", OUT)
+def test_kv_plan_refuses_outputs_on_its_inputs(L, out):
+    base = _plan(L)[1]
+    for other in BYTES:
+        if other == out:
+            continue
+        for at in (0, BYTES[other] - 4, 4 - BYTES[out]):  # same start, its last word, our last word
+            rc, _ = _plan(L, **{out: base[other] + at})
+            assert rc == q.QMM_ERR_INVALID_ARG and "overlaps" in q.qmm_last_error(), (out, other, at)
+        for at in (BYTES[other], -BYTES[out]):  # side by side: nothing shared
+            rc, _ = _plan(L, **{out: base[other] + at})
+            assert rc == q.QMM_ERR_CUDA, (out, other, at, q.qmm_last_error())
+
+
+@pytest.mark.parametrize("name", sorted(BYTES))
+def test_kv_plan_refuses_vectors_in_the_table(L, name):
+    t = _plan(L)[1]["table"]
+    n = BYTES[name]
+    for at in (0, 31, 48, 3 * 48 + 28, 4 - n):
+        at &= ~3
+        assert _plan(L, **{name: t + at})[0] == q.QMM_ERR_INVALID_ARG, (name, at)
+    for at in (3 * 48 + 32, -n):  # behind the last row's columns, before the first
+        assert _plan(L, **{name: t + at})[0] == q.QMM_ERR_CUDA, (name, at)
+    if n <= 16:  # between two rows' columns
+        assert _plan(L, **{name: t + 48 + 32})[0] == q.QMM_ERR_CUDA, name
+
+
+def test_kv_plan_without_rows_overlaps_nothing(L):
+    """Vectors of no elements have no memory."""
+    p = P + 100 * GAP
+    assert _plan(L, R=0, T=0, nfree=0, ctx=p, new=p, kvl=p, pos=p, slots=p, free=p, table=p)[0] \
+        == q.QMM_ERR_CUDA
