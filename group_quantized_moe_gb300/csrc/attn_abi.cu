@@ -183,13 +183,14 @@ cudaError_t launch_attn_batch(const AttnBatch &a, void *workspace, cudaStream_t 
   AttnParts parts{reinterpret_cast<AttnOpen *>(base + l.open),
                   reinterpret_cast<float2 *>(base + l.ml), reinterpret_cast<float *>(base + l.o),
                   p.rows};
-  const int64_t cap = a.block_table
+  const int64_t cap = a.block_table  // at most kMaxKeys: T is checked to be
                           ? min64(static_cast<int64_t>(a.max_blocks) * a.block_size, kMaxKeys)
                           : a.T;
   const int64_t usual = a.block_table || a.R < 1 ? cap : a.T / a.R;
   const bool whole = cap <= kWholeKeys && usual <= p.whole;
   AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, log2i(p.KT), p.fixed, p.min_run,
-               ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, whole, a.T, cap};
+               ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, whole, a.T,
+               static_cast<int>(cap)};
   const cudaError_t e = launch(a, p, sc, parts, s);
   if (e != cudaSuccess || whole) return e;
   return launch_attn_join(a, p, parts, s);

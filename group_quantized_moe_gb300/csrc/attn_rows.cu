@@ -159,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
     const int g = min(gsub, grp - sub * gsub);
     const int t0 = i * sc.U, nt = min(sc.U, q.n - t0);
     const int rows = nt * g, head0 = h * grp + sub * gsub;
-    const int end = sched_end(sc, q, i), all = q.L - q.n + t0 + 1;
-    const int vis = all + (srow < rows ? srow / g : 0);  // keys this lane's row sees
+    const int end = sched_end(sc, q, i), all = sched_seen(sc, q, t0);
+    const int vis = min(all + (srow < rows ? srow / g : 0), end);  // keys this lane's row sees
+    if (tid == 0 && sched_short(sc, q, i)) atomicOr(status, kDevBadBlock);
     float4 qv[RR][NC], o[RR][NC];
 #pragma unroll
     for (int p = 0; p < RR; ++p) {

@@ -1,7 +1,9 @@
 // attn_sched.cuh -- how the batched attention kernels share their work out.
 //
 // A call has R requests; request r has n new tokens (query rows) and L cache
-// rows, and token t of it sees the keys 0 .. L - n + t.  A unit of work is
+// rows, and token t of it sees the keys 0 .. L - n + t that the block table can
+// hold (where L is beyond it, the later keys are left out and the rest of the
+// mask stays where it is).  A unit of work is
 // (request, block of U consecutive tokens, key/value head); its cost is the
 // number of keys its last token sees, and `fixed` keys more for what a unit
 // costs besides them (loading its queries, writing its results).  The units
@@ -42,12 +44,12 @@ struct AttnSched {
   uint64_t per_worker; // 2^64 / workers, rounded up
   bool whole;          // units are not divided: each goes to the run that holds its start
   int64_t T;           // query rows in the buffers
-  int64_t cap;         // largest cache length the block table can hold (below 2^29)
+  int cap;             // keys the block table can hold (below 2^29)
 };
 
 struct AttnReq {
   int q0, n;  // first query row, new tokens
-  int L;      // cache rows
+  int ctx;    // cache rows before them (L - n): token t sees ctx + t + 1 keys
 };
 
 // Request r, held inside the buffers whatever the lengths say.
@@ -58,10 +60,14 @@ __device__ __forceinline__ AttnReq sched_req(const AttnSched &s, int r) {
   const int64_t hi = b < lo ? lo : (b > s.T ? s.T : b);
   q.q0 = static_cast<int>(lo);
   q.n = static_cast<int>(hi - lo);
-  int64_t L = s.kvl ? s.kvl[r] : q.n;
+  // tokens of the request, those behind the buffers' end included: the rows
+  // that there are keep their keys.  2^30 rows: more than any table holds, for
+  // each of its tokens
+  const int64_t tokens = (b < lo ? lo : b) - lo;
+  int64_t L = s.kvl ? s.kvl[r] : tokens;
   if (L < 0) L = 0;
-  if (L > s.cap) L = s.cap;
-  q.L = static_cast<int>(L);
+  if (L > (1 << 30)) L = 1 << 30;
+  q.ctx = static_cast<int>(L - tokens);
   return q;
 }
 
@@ -69,10 +75,18 @@ __device__ __forceinline__ int sched_blocks(const AttnSched &s, const AttnReq &q
   return (q.n + s.U - 1) / s.U;
 }
 
-// Keys that the last token of block i sees (0 or less: none).
+// Keys that the last token of block i sees (0 or less: none), that token t
+// sees, and whether the table is too short for the former.
 __device__ __forceinline__ int sched_end(const AttnSched &s, const AttnReq &q, int i) {
-  const int last = min(q.n, (i + 1) * s.U);
-  return q.L - q.n + last;
+  return min(q.ctx + min(q.n, (i + 1) * s.U), s.cap);
+}
+
+__device__ __forceinline__ int sched_seen(const AttnSched &s, const AttnReq &q, int t) {
+  return min(q.ctx + t + 1, s.cap);
+}
+
+__device__ __forceinline__ bool sched_short(const AttnSched &s, const AttnReq &q, int i) {
+  return q.ctx + min(q.n, (i + 1) * s.U) > s.cap;
 }
 
 __device__ __forceinline__ int sched_tiles(const AttnSched &s, const AttnReq &q, int i) {
@@ -81,14 +95,15 @@ __device__ __forceinline__ int sched_tiles(const AttnSched &s, const AttnReq &q,
 }
 
 // Cost of one unit of block i, and of one head's units in the blocks before
-// it (all of them full).  Rows that see no key (L < n) cost as if L = n.
+// it (all of them full).  Rows that see no key (L < n) cost as if L = n; keys
+// beyond the table count, so that a unit's tiles always fit its cost.
 __device__ __forceinline__ int64_t sched_unit(const AttnSched &s, const AttnReq &q, int i) {
-  return static_cast<int64_t>(max(q.L - q.n, 0)) + min(q.n, (i + 1) * s.U) + s.fixed;
+  return static_cast<int64_t>(max(q.ctx, 0)) + min(q.n, (i + 1) * s.U) + s.fixed;
 }
 
 __device__ __forceinline__ int64_t sched_before(const AttnSched &s, const AttnReq &q, int i) {
   const int64_t n = i;
-  return n * (max(q.L - q.n, 0) + s.fixed) + n * (n + 1) / 2 * s.U;
+  return n * (max(q.ctx, 0) + s.fixed) + n * (n + 1) / 2 * s.U;
 }
 
 __device__ __forceinline__ int64_t sched_cost(const AttnSched &s, const AttnReq &q) {

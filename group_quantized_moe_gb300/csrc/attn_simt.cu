@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
     const int t0 = i * sc.U, nt = min(sc.U, q.n - t0);
     const int rows = nt * g, head0 = h * grp + sub * gsub;
     const int end = sched_end(sc, q, i);        // keys the last token sees
-    const int all = q.L - q.n + t0 + 1;         // keys the first token sees
+    const int all = sched_seen(sc, q, t0);      // keys the first token sees
+    if (tid == 0 && sched_short(sc, q, i)) atomicOr(status, kDevBadBlock);
     __syncthreads();                            // the previous unit is done with Qs
     constexpr int QB = TR * NC / 16 < 8 ? TR * NC / 16 : 8;  // loads in flight a thread
 #pragma unroll 1
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
 #pragma unroll
       for (int p = 0; p < RP; ++p) {
         const int row = ty * RP + p;
-        const int vis = all + row / g;  // keys this row sees
+        const int vis = min(all + row / g, end);  // keys this row sees
         float mx = -INFINITY;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           u.ntile = sched_tiles(p.sc, q, i);
           sched_part(p.sc, run, x, u.ntile, u.tile, u.stop);
           if (u.tile < u.stop) {
-            const int t0 = i * p.sc.U, ctx = q.L - q.n;
+            const int t0 = i * p.sc.U;
             u.valid = 1;
             u.nt = min(p.sc.U, q.n - t0);
             u.pair = u.nt > p.tpt;
@@ -311,10 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             u.head0 = u.h * grp + sub * p.gsub;
             u.g = min(p.gsub, grp - sub * p.gsub);
             u.r = r;
-            const int end_a = ctx + t0 + min(u.nt, p.tpt);
+            const int end_a = sched_seen(p.sc, q, t0 + min(u.nt, p.tpt) - 1);
             u.ntile_a = end_a > kKT ? (end_a + kKT - 1) / kKT : 1;
-            u.all = ctx + t0 + 1;
-            u.end = ctx + t0 + u.nt;
+            u.all = sched_seen(p.sc, q, t0);
+            u.end = sched_end(p.sc, q, i);
+            if (lane == 0 && sched_short(p.sc, q, i)) atomicOr(p.status, kDevBadBlock);
             u.k_row = q.q0;
             if (lane == 0 && u.tile == 0 && u.stop < u.ntile)
               p.parts.open[blockIdx.x] =
@@ -611,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tw = pair ? w * p.tpt : 0;    // first token of this warpgroup's query tile
       const bool live = tok < min(p.tpt, u.nt - tw) && hq < u.g;
       const bool busy = __any_sync(0xFFFFFFFFu, live);
-      const int all = u.all + tw;             // keys every row of the tile sees
-      const int vis = all + tok;              // keys this row sees
+      const int all = min(u.all + tw, u.end);  // keys every row of the tile sees
+      const int vis = min(all + tok, u.end);   // keys this row sees
       float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
       for (int kt = first; kt < last; kt += step, ++nt) {

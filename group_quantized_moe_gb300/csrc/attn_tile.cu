@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
     const int g = min(gsub, grp - sub * gsub);
     const int t0 = i * sc.U, nt = min(sc.U, q.n - t0);
     const int rows = nt * g, head0 = h * grp + sub * gsub;
-    const int end = sched_end(sc, q, i), all = q.L - q.n + t0 + 1;
+    const int end = sched_end(sc, q, i), all = sched_seen(sc, q, t0);
+    if (tid == 0 && sched_short(sc, q, i)) atomicOr(status, kDevBadBlock);
     // Copies tile kt into stage kt & 1: eight threads a key.
     const int ck = tid >> 3;  // this thread's key
     auto fetch = [&](int kt) {
@@ -165,15 +166,16 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const int row = 16 * warp + 4 * p + y4;
-      vis[p] = row < rows ? all + row / g : 0;
+      vis[p] = row < rows ? min(all + row / g, end) : 0;
       m[p] = -INFINITY;
       l[p] = 0.0f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) o[p][j] = make_ulonglong2(0ull, 0ull);
     }
     const int first_row = 16 * warp, last_row = min(rows, first_row + 16) - 1;
-    const int most = last_row >= first_row ? all + last_row / g : 0;  // keys any row of the warp sees
-    const int least = last_row == first_row + 15 ? all + first_row / g : 0;  // ... every row sees
+    // keys any row of the warp sees, and every row
+    const int most = last_row >= first_row ? min(all + last_row / g, end) : 0;
+    const int least = last_row == first_row + 15 ? min(all + first_row / g, end) : 0;
     for (int kt = tile; kt < stop; ++kt) {
       const int st = kt & 1, k0 = kt * kKeys;
       if (kt + 1 < stop) {

@@ -75,7 +75,8 @@ enum {
   QMM_DEV_EXPERT_OVERLOAD = 4u, /* moe_route_load_stats found an expert chosen
                                 more often than its threshold             */
   QMM_DEV_BAD_BLOCK = 8u,   /* a block table entry that was needed, or a slot,
-                               lay outside the cache: those keys were left out
+                               lay outside the cache, or keys outside the
+                               table: those keys were left out
                                (qmm_attn_paged), that row was not written
                                (qmm_rope_append)                           */
   QMM_DEV_KV_SHORT = 16u,   /* qmm_kv_plan ran out of free blocks, table
@@ -407,8 +408,9 @@ int qmm_attn_prompt(const void *q, const void *k, const void *v, int32_t dtype, 
  * keys j <= L - n + i; a query that sees none (L < n) gives a row of zeros.
  * y, scale, workspace and the rest as for qmm_attn_prompt.  Rows of a block
  * beyond L are not used, whatever they hold.  A block index outside the cache
- * leaves its keys out and sets QMM_DEV_BAD_BLOCK; L is held to max_blocks *
- * block_size, and to 2^29 - 1.
+ * leaves its keys out and sets QMM_DEV_BAD_BLOCK, and so do keys that are needed
+ * beyond the table (from max_blocks * block_size on, or 2^29 - 1).  Where cu_q
+ * goes beyond T, the rows that there are see the same keys.
  */
 size_t qmm_attn_paged_workspace_bytes(const qmm_kv_cache *cache, int64_t T, int32_t n_head,
                                       int32_t R);

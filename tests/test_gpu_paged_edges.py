@@ -1,0 +1,72 @@
+"""attn_paged and attn_prompt where a call's lengths, table or values are at
+their ends, against plain 64-bit numpy (tests/paged_reference.py): every kernel
+behind the two calls, whole units and divided ones."""
+import numpy as np
+import pytest
+import torch
+
+import group_quantized_moe_gb300 as q
+import paged_reference as ref
+from parity_checks import assert_within
+from test_gpu_paged import BF16, F32, cu_of, dev, i32, num, rnd, round_bound  # noqa: F401 (dev: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def tensor_core(dtype, hd):
+    """The calls whose weights are rounded to bf16 where they meet the values."""
+    return dtype == BF16 and hd <= 128 and hd % 8 == 0
+
+
+# query heads, key/value heads, head size, tokens a request: few rows (attn_rows_kernel;
+# attn_tc_kernel, one query tile), many (attn_tile_kernel; attn_tc_kernel, two), and
+# the sizes that attn_simt_kernel takes
+FORMS = [(4, 2, 64, 1), (8, 1, 128, 1), (8, 2, 64, 60), (2, 2, 80, 200), (8, 2, 256, 1), (16, 2, 256, 20),
+         (4, 1, 512, 40), (3, 3, 20, 2), (6, 1, 36, 70)]
+
+
+def make(seed, R, n, nh, nkv, hd, S, cols, dtype):
+    """R requests of n tokens each over a table of `cols` columns; behind them
+    the row holds more blocks of the cache, which no call may use."""
+    nb = R * (cols + 4)
+    k, v = (rnd(seed + i, (nb, nkv, S, hd), dtype).cuda() for i in (1, 2))
+    wide = np.random.default_rng(seed).permutation(nb).astype(np.int32).reshape(R, cols + 4)
+    x = rnd(seed, (R * n, nh, hd), dtype, 2.0).cuda()
+    return x, k, v, wide, torch.from_numpy(wide).cuda()[:, :cols]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd,n", FORMS)
+def test_more_cache_rows_than_the_table_holds(dev, nh, nkv, hd, n, dtype):
+    """Query i sees the keys j <= L - n + i that the table holds, whatever L is
+    beyond it, and the missing keys are reported."""
+    for S, cols in ((16, 3), (32, 21), (16, 130)):
+        cap = S * cols
+        lens = [cap, cap + 1, max(cap - 1, 0), cap + n, cap + n // 2, cap + 7 * n + 900, 2 ** 31 - 1, 5]
+        x, k, v, wide, table = make(hd + n, len(lens), n, nh, nkv, hd, S, cols, dtype)
+        y = q.attn_paged(x, q.PagedKV(k, v), table, cu_of([n] * len(lens)), i32(lens))
+        assert q.qmm_device_status(clear=True) == q.QMM_DEV_BAD_BLOCK
+        # the reference takes the keys behind the table for ones in blocks outside the cache
+        short = [min(L, cap + 2 * n) for L in lens]
+        full = np.full((len(lens), -(-max(short) // S)), -1, dtype=np.int32)
+        full[:, :cols] = wide[:, :cols]
+        want, b = ref.paged(num(x), num(k), num(v), full, [(L, n) for L in short], hd ** -0.5,
+                            tensor_core(dtype, hd))
+        assert_within(num(y), want, round_bound(want, b, F32), f"S{S} cols{cols}")
+        # lengths up to the table's end, and idle requests beyond it, report nothing
+        q.attn_paged(x[:n], q.PagedKV(k, v), table[:2], cu_of([n, 0]), i32([cap, cap + 99]))
+        assert q.qmm_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd,n", FORMS)
+def test_fewer_rows_than_the_tokens(dev, nh, nkv, hd, n, dtype):
+    """cu_q beyond the rows of q: the rows there are see the same keys."""
+    S, cols, more = 16, 40, 37
+    L = 300 + n + more
+    x, k, v, wide, table = make(hd, 2, n, nh, nkv, hd, S, cols, dtype)
+    cache = q.PagedKV(k, v)
+    y = q.attn_paged(x, cache, table, i32([0, n, 2 * n + more]), i32([n, L]))
+    want, b = ref.paged(num(x), num(k), num(v), wide, [(n, n), (L - more, n)], hd ** -0.5,
+                        tensor_core(dtype, hd))
+    assert_within(num(y), want, round_bound(want, b, F32))
