@@ -379,10 +379,12 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < C::teams; ++w) {
-        const float f = ex2(wm[w][p] - ref);
-        if (f == 0.0f) continue;
+        const float f = ex2(wm[w][p] - ref), lw = wl[w][p];
+        // nothing to add; but a sum that is NaN (a NaN among the scores, which
+        // the maximum does not show) makes the row NaN whatever its factor is
+        if (f == 0.0f && lw == lw) continue;
         const float4 v = *reinterpret_cast<const float4 *>(wo + (w * RR + p) * CW + d);
-        L = fmaf(f, wl[w][p], L);
+        L = fmaf(f, lw, L);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);

@@ -321,7 +321,9 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnBatch a, int gsub, i
         const float2 ml = parts.ml[at(w)];
         const float4 v = *reinterpret_cast<const float4 *>(parts.o + at(w) * hd + 4 * c);
         const float f = ex2(ml.x - ref);
-        if (f == 0.0f) continue;  // a part that saw no key, or only negligible ones
+        // a part that saw no key, or only negligible ones; a NaN sum (a NaN among
+        // the scores, which the maximum does not show) makes the row NaN
+        if (f == 0.0f && ml.y == ml.y) continue;
         L = fmaf(f, ml.y, L);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);

@@ -70,3 +70,53 @@ def test_fewer_rows_than_the_tokens(dev, nh, nkv, hd, n, dtype):
     want, b = ref.paged(num(x), num(k), num(v), wide, [(n, n), (L - more, n)], hd ** -0.5,
                         tensor_core(dtype, hd))
     assert_within(num(y), want, round_bound(want, b, F32))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd,n", FORMS)
+def test_nan_queries_and_keys_reach_their_rows(dev, nh, nkv, hd, n, dtype):
+    """A row whose scores hold a NaN is NaN, wherever the NaN lies (alone in its
+    part of a divided unit, behind every key of the row's maximum) and however
+    small that part's weight is; the other rows are as without it."""
+    S = 16
+    for L in (n, n + 8, n + 128, 4000 + n):  # parts of one key, and of many
+        cols = -(-L // S)
+        x, k, v, wide, table = make(hd + L, 2, n, nh, nkv, hd, S, cols, dtype)
+        cache, cu, kvl = q.PagedKV(k, v), cu_of([n, n]), i32([L, L])
+        clean = q.attn_paged(x, cache, table, cu, kvl)
+        x2 = x.clone()
+        x2[n - 1] = float("nan")
+        y = q.attn_paged(x2, cache, table, cu, kvl)
+        assert y[n - 1].isnan().all(), L
+        y[n - 1] = clean[n - 1]
+        assert torch.equal(y, clean), L
+        for j in (L - 1, L - n, (L - n) // 2, 0):
+            k2 = k.clone()
+            k2[wide[0, j // S], :, j % S] = float("nan")
+            y = q.attn_paged(x, q.PagedKV(k2, v), table, cu, kvl)
+            first = max(0, j - (L - n))  # the first row that sees key j
+            assert y[first:n].isnan().all(), (L, j)
+            assert torch.equal(y[:first], clean[:first]) and torch.equal(y[n:], clean[n:]), (L, j)
+        # a part of little weight: one key far above the others, the NaN far away
+        k2, x2 = k.clone(), x.clone()
+        k2[wide[0, (L - n) // 2 // S], :, (L - n) // 2 % S] = 100.0
+        x2[:n] = x2[:n].abs() + 1.0
+        k2[wide[0, (L - n) // S], :, (L - n) % S] = float("nan")
+        y = q.attn_paged(x2, q.PagedKV(k2, v), table, cu, kvl)
+        assert y[:n].isnan().all(), L
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", [(4, 4, 64), (8, 1, 128), (32, 8, 64), (24, 24, 100), (4, 4, 256)])
+def test_nan_queries_of_prompts_reach_their_rows(dev, nh, nkv, hd, dtype):
+    for lens in ([9, 40], [300, 700], [1500]):
+        T = sum(lens)
+        x, k, v = (rnd(s, (T, h, hd), dtype).cuda() for s, h in ((1, nh), (2, nkv), (3, nkv)))
+        clean = q.attn_prompt(x, k, v, cu_of(lens))
+        for t in (0, lens[0] - 1, T - 1):
+            x2 = x.clone()
+            x2[t] = float("nan")
+            y = q.attn_prompt(x2, k, v, cu_of(lens))
+            assert y[t].isnan().all(), (lens, t)
+            y[t] = clean[t]
+            assert torch.equal(y, clean), (lens, t)
