@@ -17,6 +17,10 @@
 // this call hands out is read from the free list, never from the table rows
 // that another CTA may be writing.
 //
+// Sums and positions are formed in 64 bits and stop at 2^31 - 1 where they are
+// kept, so that lengths beyond all reason end in tokens without a slot and a
+// flag, not in negative lengths.
+//
 // A few hundred kilobytes at most: bound by latency.  3.8 us for 256 single
 // tokens, 6.8 us for 4096 requests (a launch that does nothing takes 2).
 #include <cstdint>
@@ -44,6 +48,26 @@ struct PlanArgs {
   uint32_t *status;
 };
 
+__device__ __forceinline__ int held(int64_t v) { return static_cast<int>(min64(v, 0x7FFFFFFF)); }
+
+struct Sums {
+  int64_t tokens, blocks;
+};
+
+// Inclusive sums over the lanes of a warp.
+__device__ __forceinline__ Sums warp_sums(Sums v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, v.tokens, o);
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, v.blocks, o);
+    if (lane >= o) {
+      v.tokens += x;
+      v.blocks += y;
+    }
+  }
+  return v;
+}
+
 // Largest index r in [0, n) with v[r] <= x (v ascending, v[0] <= x).
 __device__ __forceinline__ int last_at_most(const int32_t *v, int n, int x) {
   int a = 0, b = n;
@@ -58,7 +82,7 @@ __device__ __forceinline__ int last_at_most(const int32_t *v, int n, int x) {
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
   extern __shared__ int32_t sm[];
   int32_t *cu = sm, *blk = sm + a.R + 1;  // exclusive prefixes, [R + 1] each
-  __shared__ int2 warp_tot[kPlanThreads / 32];
+  __shared__ Sums warp_tot[kPlanThreads / 32];
   __shared__ uint32_t flags;
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -78,49 +102,33 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
     fresh = max(need - have, 0);
     return end > cap;
   };
-  int2 sum = make_int2(0, 0);
+  Sums sum{0, 0};
   bool over = false;
   for (int r = r0; r < r1; ++r) {
     int c, n, fresh;
     over |= lens(r, c, n, fresh);
-    sum.x += n;
-    sum.y += fresh;
+    sum.tokens += n;
+    sum.blocks += fresh;
   }
-  int2 inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xFFFFFFFFu, inc.x, o), y = __shfl_up_sync(0xFFFFFFFFu, inc.y, o);
-    if (lane >= o) {
-      inc.x += x;
-      inc.y += y;
-    }
-  }
+  const Sums inc = warp_sums(sum, lane);
   if (lane == 31) warp_tot[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int2 t = warp_tot[lane];
-    const int2 own = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xFFFFFFFFu, t.x, o), y = __shfl_up_sync(0xFFFFFFFFu, t.y, o);
-      if (lane >= o) {
-        t.x += x;
-        t.y += y;
-      }
-    }
+    const Sums own = warp_tot[lane], t = warp_sums(own, lane);
     if (lane == 31) {
-      cu[a.R] = t.x;
-      blk[a.R] = t.y;
+      cu[a.R] = held(t.tokens);
+      blk[a.R] = held(t.blocks);
     }
-    warp_tot[lane] = make_int2(t.x - own.x, t.y - own.y);
+    warp_tot[lane] = Sums{t.tokens - own.tokens, t.blocks - own.blocks};
   }
   __syncthreads();
-  int at = warp_tot[warp].x + inc.x - sum.x, bt = warp_tot[warp].y + inc.y - sum.y;
+  int64_t at = warp_tot[warp].tokens + inc.tokens - sum.tokens;
+  int64_t bt = warp_tot[warp].blocks + inc.blocks - sum.blocks;
   for (int r = r0; r < r1; ++r) {
     int c, n, fresh;
     lens(r, c, n, fresh);
-    cu[r] = at;
-    blk[r] = bt;
+    cu[r] = held(at);
+    blk[r] = held(bt);
     at += n;
     bt += fresh;
   }
@@ -129,14 +137,14 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
   const int total = cu[a.R], fresh_total = blk[a.R];
   const int g = blockIdx.x * kPlanThreads + tid, gs = gridDim.x * kPlanThreads;
   for (int r = g; r <= a.R; r += gs) a.cu[r] = cu[r];
-  for (int r = g; r < a.R; r += gs) a.kvl[r] = max(a.ctx[r], 0) + max(a.add[r], 0);
+  for (int r = g; r < a.R; r += gs) a.kvl[r] = held(static_cast<int64_t>(max(a.ctx[r], 0)) + max(a.add[r], 0));
   if (g == 0) {
     *a.used = fresh_total;
     if (flags || fresh_total > a.n_free || total > a.T) atomicOr(a.status, kDevKvShort);
   }
   // the blocks handed out (beyond the free list: -1)
-  for (int f = g; f < fresh_total; f += gs) {
-    const int r = last_at_most(blk, a.R, f);
+  for (int64_t f = g; f < fresh_total; f += gs) {
+    const int r = last_at_most(blk, a.R, static_cast<int>(f));
     const int have = static_cast<int>(min64(static_cast<int64_t>(max(a.ctx[r], 0)) + S1, cap) >> a.shift);
     a.table[r * a.table_stride + have + (f - blk[r])] = f < a.n_free ? a.free_blocks[f] : -1;
   }
@@ -147,14 +155,14 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
     if (t < total) {
       const int r = last_at_most(cu, a.R, static_cast<int>(t));
       const int c = max(a.ctx[r], 0);
-      p = c + (static_cast<int>(t) - cu[r]);
-      const int b = p >> a.shift;
-      if (b >= 0 && b < a.max_blocks) {
-        const int have = static_cast<int>((static_cast<int64_t>(c) + S1) >> a.shift);
-        const int f = blk[r] + b - have;
+      const int64_t pos = c + (t - cu[r]), b = pos >> a.shift;
+      p = held(pos);
+      if (b < a.max_blocks) {
+        const int64_t have = (static_cast<int64_t>(c) + S1) >> a.shift;
+        const int64_t f = blk[r] + b - have;
         const int id = b < have ? a.table[r * a.table_stride + b]
                                 : (f >= 0 && f < a.n_free ? a.free_blocks[f] : -1);
-        if (id >= 0) slot = (static_cast<int64_t>(id) << a.shift) + (p & S1);
+        if (id >= 0) slot = (static_cast<int64_t>(id) << a.shift) + (pos & S1);
       }
     }
     a.positions[t] = p;

@@ -339,7 +339,8 @@ typedef struct qmm_kv_cache {
  *                   for token t of request r; -1 for t >= cu_new[R]
  * block_table [R, max_blocks] int32, rows table_stride elements apart; its
  * earlier entries are read, those behind the new ones left alone.  T: rows of
- * positions and slots (may exceed the tokens).  Lengths below 0 count as 0.
+ * positions and slots (may exceed the tokens).  Lengths below 0 count as 0;
+ * sums and positions stop at 2^31 - 1.
  * When the free list, the table's columns or T are too short, entries become
  * -1, the tokens concerned get slot -1 and QMM_DEV_KV_SHORT is set.
  * Outputs must not overlap the inputs, the table or one another (refused): a
