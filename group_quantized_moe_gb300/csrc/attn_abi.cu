@@ -293,7 +293,8 @@ int qmm_rope_append(const void *qkv, int32_t x_dtype, int64_t T, int64_t row_str
   a.k = k;
   a.v = v;
   a.y_bf16 = y_dtype == QMM_BF16;
-  if (cache && cache->num_blocks > 0) {
+  if (cache) {
+    a.cached = true;
     a.k_cache = cache->k;
     a.v_cache = cache->v;
     a.num_blocks = cache->num_blocks;

@@ -39,7 +39,8 @@ cudaError_t launch_kv_plan(const int32_t *ctx, const int32_t *add, int R, int bl
                            int32_t *kvl, int32_t *positions, int64_t *slots, int32_t *used,
                            cudaStream_t s);
 
-// Rotary positions and the cache write (k_cache == nullptr: no cache).
+// Rotary positions and the cache write (cached: there is a cache, of num_blocks
+// blocks, which may be none).
 struct RopeAppend {
   const void *qkv;
   bool x_bf16;
@@ -51,6 +52,7 @@ struct RopeAppend {
   int64_t max_seq;
   void *q, *k, *v;
   bool y_bf16;
+  bool cached;
   void *k_cache, *v_cache;
   int block_shift;
   int64_t num_blocks, block_stride;

@@ -102,10 +102,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rope_append_kernel(RopeAppen
     const int64_t slot_next = next < a.T && a.slots ? a.slots[next] : -1;
     // a padding row (position below 0) or one the table does not reach: zeros, no cache row
     const bool live = p >= 0 && p < a.max_seq;
-    const bool put = live && a.k_cache && slot >= 0 && slot < rows;
+    const bool put = live && a.cached && slot >= 0 && slot < rows;
     if (threadIdx.x == 0) {
       if (p >= a.max_seq) atomicOr(status, kDevBadPosition);
-      if (a.k_cache && live && slot >= rows) atomicOr(status, kDevBadBlock);
+      if (a.cached && live && slot >= rows) atomicOr(status, kDevBadBlock);
     }
     float c[V / 2], s[V / 2];
     const int64_t at = live ? p * (a.head_dim / 2) + u * (V / 2) : 0;
