@@ -54,13 +54,13 @@ class Server:
 
     def whole(self, x):
         """The same layer over one request's whole sequence, without the cache."""
-        qkv = lib.qmm_linear_batched(x, self.wqkv, y_dtype=self.cache.k.dtype)
+        qkv = lib.qmm_linear_batched(x, self.wqkv)
         n = x.shape[0]
         q, k, v = lib.rope_append(qkv, self.heads, torch.arange(n, dtype=torch.int32, device="cuda"),
                                   None, self.cos, self.sin, None, keep_kv=True, n_kv=self.kv_heads,
                                   y_dtype=self.cache.k.dtype)
         cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
-        a = lib.attn_prompt(q, k, v, cu, y_dtype=q.dtype)
+        a = lib.attn_prompt(q, k, v, cu, y_dtype=x.dtype)
         return lib.qmm_linear_batched(a.view(n, -1), self.wo)
 
 

@@ -1127,13 +1127,19 @@ def attn_layer_paged(x: torch.Tensor, wqkv: QWeight, wo: QWeight, n_head: int,
     wq, wk and wv as one weight), rotary positions and the cache write, the
     attention and the quantised output projection.  prompts: no request has
     earlier context, so the attention reads the new keys and values as they
-    lie instead of through the cache.  Returns y [T, wo.N]."""
-    qkv = qmm_linear_batched(x, wqkv, y_dtype=cache.k.dtype, stream=stream)
+    lie instead of through the cache.  Returns y [T, wo.N].
+
+    Queries, keys and values stay in fp32 up to the rotation and are rounded
+    once, to the cache's type (bf16 before it, too, would double that error).
+    The attention's rows go to the output projection in the type of x, with
+    which the caller chooses the projections' arithmetic: fp32 rows are not
+    rounded, bf16 ones are (that projection takes bf16 on the tensor cores)."""
+    qkv = qmm_linear_batched(x, wqkv, stream=stream)
     q, k, v = rope_append(qkv, n_head, plan.positions, plan.slots, rope_cos, rope_sin, cache,
                           keep_kv=prompts, stream=stream)
     if prompts:
-        a = attn_prompt(q, k, v, plan.cu_new, y_dtype=q.dtype, stream=stream)
+        a = attn_prompt(q, k, v, plan.cu_new, y_dtype=x.dtype, stream=stream)
     else:
-        a = attn_paged(q, cache, block_table, plan.cu_new, plan.kv_lens, y_dtype=q.dtype,
+        a = attn_paged(q, cache, block_table, plan.cu_new, plan.kv_lens, y_dtype=x.dtype,
                        stream=stream)
     return qmm_linear_batched(a.flatten(1), wo, y_dtype=y_dtype, stream=stream)
