@@ -1020,12 +1020,11 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
     return q, k, v
 
 
-_CODES = {torch.float32: QMM_F32, torch.bfloat16: QMM_BF16}
-
-
 def _attn_y(q, y, y_dtype, stream):
     """The output of an attention call, checked or allocated."""
     if y is None:
+        if y_dtype is not _F32 and y_dtype is not torch.bfloat16:
+            raise TypeError(f"unsupported y_dtype {y_dtype} (float32 or bfloat16)")
         y = _new(q.shape, y_dtype, q.device, stream)
     else:
         _need(y, q.numel(), (_F32, torch.bfloat16), "y")
@@ -1066,7 +1065,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
         _require_cuda(workspace)
     rc = lib().qmm_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), T, sq, sk, sv,
                                nh, nkv, hd, cu_seqlens.data_ptr(), B, 0.0 if scale is None else scale,
-                               y.data_ptr(), _CODES[y.dtype], workspace.data_ptr(),
+                               y.data_ptr(), _dtype_code(y), workspace.data_ptr(),
                                workspace.nbytes, _stream(stream))
     if rc:
         _check(rc)
@@ -1111,7 +1110,7 @@ def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q:
     rc = lib().qmm_attn_paged(q.data_ptr(), T, sq, nh, desc, block_table.data_ptr(),
                               block_table.stride(0) if R > 1 else cols, cols, cu_q.data_ptr(),
                               kv_lens.data_ptr(), R, 0.0 if scale is None else scale, y.data_ptr(),
-                              _CODES[y.dtype], workspace.data_ptr(), workspace.nbytes,
+                              _dtype_code(y), workspace.data_ptr(), workspace.nbytes,
                               _stream(stream))
     if rc:
         _check(rc)

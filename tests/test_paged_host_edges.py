@@ -2,6 +2,7 @@
 tests/test_paged_host.py: addresses that are never dereferenced, and only
 where no GPU is visible)."""
 import pytest
+import torch
 
 import group_quantized_moe_gb300 as q
 from test_paged_host import L  # noqa: F401 (fixture)
@@ -55,3 +56,22 @@ def test_kv_plan_without_rows_overlaps_nothing(L):
     p = P + 100 * GAP
     assert _plan(L, R=0, T=0, nfree=0, ctx=p, new=p, kvl=p, pos=p, slots=p, free=p, table=p)[0] \
         == q.QMM_ERR_CUDA
+
+
+# ---------------------------------------------------------------- the binding
+
+def _ints(*s):
+    return torch.zeros(s, dtype=torch.int32)
+
+
+def test_attention_refuses_other_output_types(monkeypatch):
+    """A type that the library cannot write is a TypeError before any memory is made."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(q, "_new", lambda *a: pytest.fail("allocated"))
+    x, kv = torch.zeros(3, 4, 64), torch.zeros(3, 2, 64)
+    cache = q.PagedKV(torch.zeros(2, 2, 16, 64), torch.zeros(2, 2, 16, 64))
+    for bad in (torch.float16, torch.float64, torch.int32, None):
+        with pytest.raises(TypeError, match="float32 or bfloat16"):
+            q.attn_prompt(x, kv, kv, _ints(2), y_dtype=bad)
+        with pytest.raises(TypeError, match="float32 or bfloat16"):
+            q.attn_paged(x, cache, _ints(1, 2), _ints(2), _ints(1), y_dtype=bad)
