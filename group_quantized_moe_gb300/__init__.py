@@ -877,8 +877,9 @@ class PagedKV:
             raise ValueError("k and v must share a dtype and live on a CUDA device")
         nb, nkv, bs, hd = k.shape
         block = nkv * bs * hd
-        for t in (k, v):
-            if nb and block and t.stride()[1:] != (bs * hd, hd, 1):
+        for t in (k, v):  # (the stride of a dimension of one element means nothing)
+            if nb and block and any(t.shape[d] > 1 and t.stride(d) != s
+                                    for d, s in ((1, bs * hd), (2, hd), (3, 1))):
                 raise ValueError("the rows of a block must be contiguous")
         if nb > 1 and k.stride(0) != v.stride(0):
             raise ValueError("k and v must have the same block stride")

@@ -120,3 +120,18 @@ def test_nan_queries_of_prompts_reach_their_rows(dev, nh, nkv, hd, dtype):
             assert y[t].isnan().all(), (lens, t)
             y[t] = clean[t]
             assert torch.equal(y, clean), (lens, t)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("hd", [64, 512])
+def test_cache_of_one_head_laid_out_by_rows(dev, hd, dtype):
+    """One key/value head: blocks made as [rows, 1, columns] and seen as [1, rows,
+    columns]."""
+    nh, S, nb, L = 4, 16, 9, 130
+    k, v = (rnd(i, (nb, S, 1, hd), dtype).cuda().transpose(1, 2) for i in (1, 2))
+    x = rnd(3, (3, nh, hd), dtype).cuda()
+    table = torch.arange(nb, dtype=torch.int32, device="cuda").flip(0)[None].contiguous()
+    y = q.attn_paged(x, q.PagedKV(k, v), table, cu_of([3]), i32([L]))
+    want, b = ref.paged(num(x), num(k), num(v), table.cpu().numpy(), [(L, 3)], hd ** -0.5,
+                        tensor_core(dtype, hd))
+    assert_within(num(y), want, round_bound(want, b, F32))

@@ -75,3 +75,20 @@ def test_attention_refuses_other_output_types(monkeypatch):
             q.attn_prompt(x, kv, kv, _ints(2), y_dtype=bad)
         with pytest.raises(TypeError, match="float32 or bfloat16"):
             q.attn_paged(x, cache, _ints(1, 2), _ints(2), _ints(1), y_dtype=bad)
+
+
+def test_cache_of_one_head_may_have_any_stride_there(monkeypatch):
+    """[blocks, rows, 1, columns] seen as [blocks, 1, rows, columns] is the same memory."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    rows = [torch.zeros(5, 16, 1, 64) for _ in range(2)]
+    k, v = (t.transpose(1, 2) for t in rows)
+    assert k.stride(1) == 64 and k.is_contiguous()
+    d = q.PagedKV(k, v)._desc()
+    assert (d.num_blocks, d.n_kv, d.block_size, d.head_dim, d.block_stride) == (5, 1, 16, 64, 1024)
+    both = torch.zeros(5, 2, 16, 1, 64)
+    d = q.PagedKV(both[:, 0].transpose(1, 2), both[:, 1].transpose(1, 2))._desc()
+    assert d.block_stride == 2048
+    for t in (torch.zeros(5, 16, 2, 64).transpose(1, 2), torch.zeros(5, 1, 64, 16).transpose(2, 3),
+              torch.zeros(5, 1, 16, 128)[..., ::2]):
+        with pytest.raises(ValueError):
+            q.PagedKV(t, t)._desc()
