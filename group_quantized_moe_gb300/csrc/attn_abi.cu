@@ -159,7 +159,7 @@ Launch pick_plan(bool bf16, bool tc, bool paged, int64_t T, int n_head, int n_kv
   }
   if (attn_rows_plan(paged, T, n_head, n_kv, head_dim, R, p)) return launch_attn_rows;
   if (attn_tile_plan(bf16, T, n_head, n_kv, head_dim, R, p)) return launch_attn_tile;
-  *p = attn_simt_plan(T, n_head, n_kv, head_dim, R);
+  *p = attn_simt_plan(bf16, T, n_head, n_kv, head_dim, R);
   return launch_attn_simt;
 }
 

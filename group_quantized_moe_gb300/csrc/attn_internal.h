@@ -29,7 +29,7 @@ struct AttnPlan {
   int rows, gsub, nsub, U, KT, fixed, min_run, workers, whole;
 };
 
-AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R);
+AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R);
 cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                              const AttnParts &parts, cudaStream_t s);
 // The form for few rows; false: not for this call.

@@ -1,6 +1,7 @@
 // attn_simt.cu -- batched causal attention (packed prompts, or new tokens over
-// a paged cache) in fp32 on the CUDA cores, for every type and head size the
-// library takes, and the merge of divided units.
+// a paged cache) in fp32 on the CUDA cores, for the types and head sizes that
+// the faster kernels leave (bf16 of any head size, fp32 of more than 128
+// columns), and the merge of divided units.
 //
 //   s_j = scale q . k_j,  m = max_j s_j,  l = sum_j 2^((s_j - m) log2 e),
 //   o = sum_j 2^((s_j - m) log2 e) v_j / l
@@ -350,10 +351,18 @@ cudaError_t launch_simt(const AttnBatch &a, const AttnSched &sc, int gsub, int n
   return launch_pdl(kern, dim3(workers), dim3(kThreads), smem, s, a, sc, gsub, nsub, parts, status);
 }
 
+// Column groups of the form that takes a call: the plan's tiles and the launch
+// both follow from it.  fp32 has no forms below four (such calls go to
+// attn_rows_kernel or attn_tile_kernel); the wider one would compute the same.
+int simt_nc(bool bf16, int head_dim) {
+  if (head_dim > 256) return 8;
+  return head_dim > 128 || !bf16 ? 4 : head_dim > 64 ? 2 : 1;
+}
+
 template <bool BF16, int TR>
 cudaError_t launch_simt_nc(int nc, const AttnBatch &a, const AttnSched &sc, int gsub, int nsub,
                            const AttnParts &parts, int workers, cudaStream_t s) {
-  if constexpr (BF16) {  // fp32, up to 128 columns: attn_rows_kernel or attn_tile_kernel
+  if constexpr (BF16) {
     if (nc == 1) return launch_simt<BF16, 1, TR>(a, sc, gsub, nsub, parts, workers, s);
     if (nc == 2) return launch_simt<BF16, 2, TR>(a, sc, gsub, nsub, parts, workers, s);
   }
@@ -361,18 +370,16 @@ cudaError_t launch_simt_nc(int nc, const AttnBatch &a, const AttnSched &sc, int 
   return launch_simt<BF16, 8, TR>(a, sc, gsub, nsub, parts, workers, s);
 }
 
-int simt_nc(int head_dim) { return head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : head_dim <= 256 ? 4 : 8; }
-
 }  // namespace
 
-AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R) {
+AttnPlan attn_simt_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R) {
   const int grp = n_head / n_kv;
   AttnPlan p;
   p.rows = T * grp <= static_cast<int64_t>(16) * R ? 16 : 64;
   p.gsub = grp < p.rows ? grp : p.rows;
   p.nsub = (grp + p.gsub - 1) / p.gsub;
   p.U = p.rows / p.gsub;
-  const int nc = simt_nc(head_dim);
+  const int nc = simt_nc(bf16, head_dim);
   p.KT = nc <= 2 ? 64 : (nc == 4 ? 32 : 16);
   p.fixed = p.KT;
   p.min_run = p.KT;
@@ -383,7 +390,7 @@ AttnPlan attn_simt_plan(int64_t T, int n_head, int n_kv, int head_dim, int R) {
 
 cudaError_t launch_attn_simt(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
                              const AttnParts &parts, cudaStream_t s) {
-  const int nc = simt_nc(a.head_dim);
+  const int nc = simt_nc(a.bf16, a.head_dim);
   if (a.bf16)
     return p.rows == 16 ? launch_simt_nc<true, 16>(nc, a, sc, p.gsub, p.nsub, parts, p.workers, s)
                         : launch_simt_nc<true, 64>(nc, a, sc, p.gsub, p.nsub, parts, p.workers, s);
