@@ -16,10 +16,11 @@
 //
 // Bound by reading shared memory: each product of 4 x 4 scores (or rows by
 // columns) takes eight 16-byte reads.  It serves what the faster kernels do
-// not take; where attn_tile_kernel takes over (three fp32 prompts of 1500
-// tokens together, 32 heads of 128: 274 us), it needs 392 us, 17 TFLOP/s.  Single
-// bf16 tokens, 64 query heads over one key/value head of 512 columns: 0.27
-// TB/s of the cache, bound by the same reads.
+// not take; where attn_tile_kernel takes over (three fp32 prompts, 1500 tokens
+// together, 32 heads of 128: 263 us), it needed 392 us, 17 TFLOP/s.  Prompts of
+// three times 300 tokens, 8 heads of 256: 115 us (bf16), 107 us (fp32).  Single
+// bf16 tokens, 64 query heads over one key/value head of 512 columns, 48 requests
+// of 4096 keys: 1547 us, 0.26 TB/s of the cache, bound by the same reads.
 #include <cstdint>
 
 #include "attn_batch.h"

@@ -12,7 +12,7 @@
 // lane, whoever shares them, and four multiply-adds a lane take one: with 4 x 4
 // scores a lane Q K^T reads 8 floats for 16 multiply-adds, which bounds it at
 // half the FMA rate (measured 38 TFLOP/s at 4096 tokens, 48% of the FMA pipe;
-// three prompts of 1500 tokens together, 32 heads of 128, 275 us or 24 TFLOP/s; 8 x 4 and
+// three prompts, 1500 tokens together, 32 heads of 128, 263 us or 25 TFLOP/s; 8 x 4 and
 // 8 x 8 scores a lane, which spill, gain nothing).
 // Multiply-adds are issued in pairs (f32x2), 8% on short prompts.  A warp skips
 // the tiles that none of its rows sees.
@@ -54,6 +54,8 @@ struct Tile {
   static constexpr int W = NC * 64, LD = W + 4;  // rows of Q and K 4 banks apart
   static constexpr int stage = kKeys * LD + kKeys * W;
   static constexpr int smem = (kRows * LD + 2 * stage + 8 * 16 * kPld) * 4;
+  // two CTAs of 128 registers a thread spill ten words of them: three prompts of 500
+  // tokens, 32 heads over 8 of 64 columns, 115 us; 130 us with one that spills none
   static constexpr int per_sm = NC == 1 ? 2 : 1;
 };
 
@@ -361,8 +363,9 @@ cudaError_t run_tile(const AttnBatch &a, const AttnPlan &p, const AttnSched &sc,
 
 }  // namespace
 
-// fp32, head sizes up to 128, more than 16 query rows a request and key/value
-// head on average (below, a 128-row unit would be mostly empty).
+// fp32, head sizes up to 128, with more query rows a request and key/value head
+// than attn_rows_plan, which is asked first, takes: 8 on average of packed
+// prompts, 32 over a paged cache (below, a 128-row unit would be mostly empty).
 bool attn_tile_plan(bool bf16, int64_t T, int n_head, int n_kv, int head_dim, int R, AttnPlan *p) {
   const int grp = n_head / n_kv;
   if (bf16 || head_dim > 128) return false;

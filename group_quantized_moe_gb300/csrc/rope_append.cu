@@ -27,7 +27,10 @@ namespace {
 
 constexpr int kThreads = 256;
 // Resident CTAs per SM, each over many tokens (16384 tokens of 48 heads of 128, bf16,
-// three heads in flight a thread: 74 us, 6.4 TB/s; one or two heads in flight 83 to 90)
+// three heads in flight a thread: 74 us, 6.4 TB/s; one or two heads in flight 83 to 90).
+// Five leave a thread 48 registers, and up to 31 words of it are spilled and read again from
+// L1; with four CTAs almost nothing is, and the same call takes 83 us (fp32 rows into a bf16
+// cache, which spill most: 104 us with five, 96 with four).
 constexpr int kPerSm = 5;
 
 // V elements as they lie in memory, and as floats.

@@ -135,3 +135,39 @@ def test_cache_of_one_head_laid_out_by_rows(dev, hd, dtype):
     want, b = ref.paged(num(x), num(k), num(v), table.cpu().numpy(), [(L, 3)], hd ** -0.5,
                         tensor_core(dtype, hd))
     assert_within(num(y), want, round_bound(want, b, F32))
+
+
+# bf16 on the CUDA cores: weights in fp32, so none of the allowance for weights
+# rounded to bf16
+CORES = [(2, 1, 4), (3, 3, 20), (16, 2, 60), (20, 1, 84), (24, 24, 100), (4, 2, 132), (2, 1, 256), (8, 4, 256),
+         (2, 2, 260), (4, 1, 512), (64, 1, 512)]
+
+
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd", CORES)
+def test_bf16_on_the_cuda_cores_keeps_its_weights_in_fp32(dev, monkeypatch, nh, nkv, hd, y_dtype):
+    import test_gpu_paged as t
+    monkeypatch.setattr(t, "tensor_core", lambda dtype: False)
+    t.run_prompt([37, 1, 0, 150], nh, nkv, hd, BF16, y_dtype, pad=2)
+    t.run_prompt([500], nh, nkv, hd, BF16, y_dtype, seed=3)
+    t.run_paged(t.DECODE, nh, nkv, hd, 16, BF16, y_dtype)
+    t.run_paged([(3000, 1)], nh, nkv, hd, 64, BF16, y_dtype)
+    t.run_paged([(300, 40), (64, 64), (17, 5), (3, 9)], nh, nkv, hd, 32, BF16, y_dtype, bad=[(0, 2)])
+
+
+@pytest.mark.parametrize("nh,nkv,hd", [(4, 2, 64), (16, 8, 128)])
+def test_bf16_rows_of_8_bytes_take_the_cuda_cores(dev, nh, nkv, hd):
+    """Rows a multiple of 8 bytes apart, not of 16: no tensor map, the same results."""
+    n, L = 90, 200
+    pad = lambda seed, h: rnd(seed, (n, h * hd + 4), BF16).cuda()[:, :h * hd].view(n, h, hd)
+    x, k, v = pad(1, nh), pad(2, nkv), pad(3, nkv)
+    y = q.attn_prompt(x, k, v, cu_of([50, 40]))
+    want, b = ref.prompt(num(x), num(k), num(v), [50, 40], hd ** -0.5)
+    assert_within(num(y), want, round_bound(want, b, F32))
+    S, nb = 16, 13
+    both = rnd(4, (nb, 2 * nkv * S * hd + 8), BF16).cuda()  # blocks of 16-byte distance, queries not
+    kc, vc = (both[:, i * nkv * S * hd:(i + 1) * nkv * S * hd].view(nb, nkv, S, hd) for i in range(2))
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    y = q.attn_paged(x, q.PagedKV(kc, vc), table, cu_of([n]), i32([L]))
+    want, b = ref.paged(num(x), num(kc), num(vc), table.cpu().numpy(), [(L, n)], hd ** -0.5)
+    assert_within(num(y), want, round_bound(want, b, F32))
