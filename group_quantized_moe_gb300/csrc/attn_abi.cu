@@ -2,6 +2,7 @@
 // batched attention over it: argument validation, workspace carving and
 // kernel selection.  Declared in include/qmm.h.
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/qmm.h"
 #include "attn_batch.h"
@@ -87,6 +88,14 @@ bool overlap(const Span &a, const Span &b) {
   int64_t r = lo <= 0 ? 0 : lo / b.stride;
   if (r * b.stride + b.len <= lo) ++r;
   return r < b.rows && r * b.stride < hi;
+}
+
+// Lengths, tables, positions and slots lie at multiples of their element.
+int check_ints(const char *who, std::initializer_list<const void *> i32, const void *i64 = nullptr) {
+  for (const void *p : i32)
+    if (!aligned(p, 4)) return refuse(QMM_ERR_ALIGN, "%s: int32 arrays must be 4-byte aligned", who);
+  if (!aligned(i64, 8)) return refuse(QMM_ERR_ALIGN, "%s: int64 arrays must be 8-byte aligned", who);
+  return QMM_OK;
 }
 
 int log2i(int v) {
@@ -222,6 +231,9 @@ int qmm_kv_plan(const int32_t *ctx_lens, const int32_t *new_lens, int32_t R, int
       (R > 0 && max_blocks > 0 && !block_table) || (n_free > 0 && !free_blocks) ||
       (T > 0 && (!positions || !slots)))
     return refuse(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
+  const int rc = check_ints(who, {ctx_lens, new_lens, block_table, free_blocks, cu_new, kv_lens,
+                                  positions, blocks_used}, slots);
+  if (rc) return rc;
   // Every block of the launch reads the lengths and the free list from first to
   // last, so none of the outputs may lie on them (or on one another).
   const Span span[] = {vec_span("cu_new", cu_new, R + int64_t(1), 4),
@@ -276,6 +288,7 @@ int qmm_rope_append(const void *qkv, int32_t x_dtype, int64_t T, int64_t row_str
       !aligned(rope_cos, 16) || !aligned(rope_sin, 16) || row_stride % 4)
     return refuse(QMM_ERR_ALIGN,
                   "%s: tensors must be 16-byte aligned and rows a multiple of 4 elements apart", who);
+  if ((rc = check_ints(who, {positions}, slots))) return rc;
   RopeAppend a{};
   a.qkv = qkv;
   a.x_bf16 = x_dtype == QMM_BF16;
@@ -334,6 +347,7 @@ int qmm_attn_prompt(const void *q, const void *k, const void *v, int32_t dtype, 
   if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 4 || v_stride % 4)
     return refuse(QMM_ERR_ALIGN, "%s: k and v must be 16-byte aligned, rows a multiple of 4 elements "
                   "apart", who);
+  if ((rc = check_ints(who, {cu_seqlens}))) return rc;
   AttnBatch a{};
   a.q = q;
   a.k = k;
@@ -383,6 +397,7 @@ int qmm_attn_paged(const void *q, int64_t T, int64_t q_stride, int32_t n_head,
   if (T == 0) return QMM_OK;
   if (R > 0 && (!kv_lens || !block_table))
     return refuse(QMM_ERR_INVALID_ARG, "%s: null pointer", who);
+  if ((rc = check_ints(who, {cu_q, kv_lens, block_table}))) return rc;
   AttnBatch a{};
   a.q = q;
   a.k = cache->k;

@@ -316,7 +316,8 @@ int qmm_attn_decode(const void *x, int32_t x_dtype, int64_t pos, const qmm_attn_
  * or bf16, consecutive blocks block_stride elements apart (at least one
  * block; more where one allocation interleaves keys and values or layers).
  * block_size 16, 32, 64, 128 or 256; pointers and block_stride multiples of
- * 16 bytes. */
+ * 16 bytes.  Lengths, tables, positions and slots of the calls below lie at
+ * multiples of their element's size. */
 typedef struct qmm_kv_cache {
   int32_t dtype;           /* QMM_F32 or QMM_BF16                            */
   int32_t n_kv, head_dim;  /* head_dim a multiple of 4 in [4, 512]           */

@@ -1,6 +1,8 @@
 """Further refusals of the paged-cache entry points, on the CPU (see
 tests/test_paged_host.py: addresses that are never dereferenced, and only
 where no GPU is visible)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -30,10 +32,12 @@ def test_kv_plan_refuses_outputs_on_its_inputs(L, out):
     for other in BYTES:
         if other == out:
             continue
-        for at in (0, BYTES[other] - 4, 4 - BYTES[out]):  # same start, its last word, our last word
+        word = 8 if "slots" in (out, other) else 4  # (slots lie at multiples of 8)
+        size = {k: -(-BYTES[k] // word) * word for k in (out, other)}
+        for at in (0, size[other] - word, word - size[out]):  # same start, its last word, our last word
             rc, _ = _plan(L, **{out: base[other] + at})
             assert rc == q.QMM_ERR_INVALID_ARG and "overlaps" in q.qmm_last_error(), (out, other, at)
-        for at in (BYTES[other], -BYTES[out]):  # side by side: nothing shared
+        for at in (size[other], -size[out]):  # side by side: nothing shared
             rc, _ = _plan(L, **{out: base[other] + at})
             assert rc == q.QMM_ERR_CUDA, (out, other, at, q.qmm_last_error())
 
@@ -42,8 +46,9 @@ def test_kv_plan_refuses_outputs_on_its_inputs(L, out):
 def test_kv_plan_refuses_vectors_in_the_table(L, name):
     t = _plan(L)[1]["table"]
     n = BYTES[name]
-    for at in (0, 31, 48, 3 * 48 + 28, 4 - n):
-        at &= ~3
+    word = 8 if name == "slots" else 4
+    for at in (0, 31, 48, 3 * 48 + 28, word - n):
+        at -= at % word
         assert _plan(L, **{name: t + at})[0] == q.QMM_ERR_INVALID_ARG, (name, at)
     for at in (3 * 48 + 32, -n):  # behind the last row's columns, before the first
         assert _plan(L, **{name: t + at})[0] == q.QMM_ERR_CUDA, (name, at)
@@ -56,6 +61,33 @@ def test_kv_plan_without_rows_overlaps_nothing(L):
     p = P + 100 * GAP
     assert _plan(L, R=0, T=0, nfree=0, ctx=p, new=p, kvl=p, pos=p, slots=p, free=p, table=p)[0] \
         == q.QMM_ERR_CUDA
+
+
+def test_misaligned_integer_arrays_are_refused(L):
+    for name in ("ctx", "new", "table", "free", "cu", "kvl", "pos", "used"):
+        for at in (1, 2):
+            assert _plan(L, **{name: _plan(L)[1][name] + at})[0] == q.QMM_ERR_ALIGN, name
+    assert _plan(L, slots=_plan(L)[1]["slots"] + 4)[0] == q.QMM_ERR_ALIGN
+    cache = q._KvCache(q.QMM_BF16, 2, 64, 16, 10, P, P, 2 * 16 * 64)
+    c = ctypes.byref(cache)
+
+    def append(pos=P, slots=P):
+        return L.qmm_rope_append(P, q.QMM_F32, 3, 512, 4, 2, 64, pos, slots, P, P, 100, c, P, P, P,
+                                 q.QMM_BF16, None)
+    assert append(pos=P + 2) == append(slots=P + 4) == q.QMM_ERR_ALIGN
+    assert append() == q.QMM_ERR_CUDA
+
+    def prompt(cu=P):
+        n = L.qmm_attn_prompt_workspace_bytes(q.QMM_BF16, 5, 4, 2, 64, 1)
+        return L.qmm_attn_prompt(P, P, P, q.QMM_BF16, 5, 256, 128, 128, 4, 2, 64, cu, 1, 0.0, P, q.QMM_F32,
+                                 P, n, None)
+    assert prompt(P + 1) == q.QMM_ERR_ALIGN and prompt() == q.QMM_ERR_CUDA
+
+    def paged(table=P, cu=P, kvl=P):
+        n = L.qmm_attn_paged_workspace_bytes(c, 3, 4, 3)
+        return L.qmm_attn_paged(P, 3, 256, 4, c, table, 9, 9, cu, kvl, 3, 0.0, P, q.QMM_F32, P, n, None)
+    assert paged(table=P + 2) == paged(cu=P + 2) == paged(kvl=P + 1) == q.QMM_ERR_ALIGN
+    assert paged() == q.QMM_ERR_CUDA
 
 
 # ---------------------------------------------------------------- the binding
