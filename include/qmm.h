@@ -386,10 +386,17 @@ int qmm_rope_append(const void *qkv, int32_t x_dtype, int64_t T, int64_t row_str
  * y [T, n_head, head_dim] fp32 or bf16 (y_dtype), contiguous; rows that
  * belong to no sequence become zeros.  scale 0: 1 / sqrt(head_dim).  dtype:
  * of q, k and v.  A key that a row does not see never touches it, whatever it
- * holds (NaN included).  Strides are multiples of 4 elements, pointers
- * 16-byte aligned; workspace: qmm_attn_prompt_workspace_bytes bytes, 256-byte
- * aligned, contents on entry do not matter.  Two kernel launches; results are
- * reproducible bit for bit.
+ * holds (NaN included); a NaN among a row's scores makes the row NaN.
+ * Arithmetic: scores, maxima, sums and results in fp32.  bf16 with head_dim a
+ * multiple of 8 up to 128 and rows 16 bytes apart runs on the tensor cores,
+ * whose operands are bf16: there each weight is rounded to bf16 where it
+ * multiplies its value (at most 2^-8 of it; not in the sum it is divided by),
+ * whatever y_dtype is.  All other calls keep the weights in fp32.
+ * Strides are multiples of 4 elements, pointers 16-byte aligned; workspace:
+ * qmm_attn_prompt_workspace_bytes bytes, 256-byte aligned, contents on entry do
+ * not matter.  One kernel launch where no request can have more than a few
+ * hundred keys and its work is not divided, else two; results are reproducible
+ * bit for bit.
  */
 size_t qmm_attn_prompt_workspace_bytes(int32_t dtype, int64_t T, int32_t n_head, int32_t n_kv,
                                        int32_t head_dim, int32_t n_seqs);
