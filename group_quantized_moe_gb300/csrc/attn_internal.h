@@ -48,6 +48,13 @@ cudaError_t launch_attn_tc(const AttnBatch &a, const AttnPlan &p, const AttnSche
 cudaError_t launch_attn_join(const AttnBatch &a, const AttnPlan &p, const AttnParts &parts,
                              cudaStream_t s);
 
+// The weight of a key that a row does not see, where some row of the tile sees
+// it: a zero that the exponential never gives (its own, of a key far below the
+// maximum, is +0).  A key with this weight is left out of the row's sums, since
+// its value may be NaN; a NaN behind a weight of +0 is the row's to have.
+__device__ __forceinline__ float unseen_weight() { return -0.0f; }
+__device__ __forceinline__ bool is_unseen(float w) { return __float_as_uint(w) == 0x80000000u; }
+
 // Four consecutive outputs, fp32 or rounded to bf16 (nearest even).
 __device__ __forceinline__ void store_y4(void *y, int64_t i, float4 v, bool bf16) {
   if (bf16) {

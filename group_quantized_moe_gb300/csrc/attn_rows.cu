@@ -322,13 +322,13 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-      for (int j = 0; j < PL; ++j) {
-        s[j] = ex2(s[j] - ref);
-        l += s[j];
-      }
       // some row of some team misses some key: not even 0 * NaN may enter
       const bool guard = LK == 32 ? k0 + B > all : __any_sync(0xFFFFFFFFu, k0 + B > all || nk < B);
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        s[j] = s[j] == -INFINITY ? unseen_weight() : ex2(s[j] - ref);
+        l += s[j];
+      }
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         if constexpr (C::stages > 0) {
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
         for (int p = 0; p < RR; ++p) {
           const int v = p * B + k;
           const float w = __shfl_sync(0xFFFFFFFFu, s[v % PL], base_lane + v / PL * C::dup);
-          if (guard && w == 0.0f) continue;
+          if (guard && is_unseen(w)) continue;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             // pairs: 64 heads over 8 149 -> 145 us (the scores gain nothing from them)
@@ -379,12 +379,11 @@ __global__ void __launch_bounds__(kThreads, Rows<NC, RR, LK>::per_sm)
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < C::teams; ++w) {
-        const float f = ex2(wm[w][p] - ref), lw = wl[w][p];
-        // nothing to add; but a sum that is NaN (a NaN among the scores, which
-        // the maximum does not show) makes the row NaN whatever its factor is
-        if (f == 0.0f && lw == lw) continue;
+        // (zeros of a team that saw no key count nothing; a NaN makes the row NaN,
+        // however small its team's factor is)
+        const float f = ex2(wm[w][p] - ref);
         const float4 v = *reinterpret_cast<const float4 *>(wo + (w * RR + p) * CW + d);
-        L = fmaf(f, lw, L);
+        L = fmaf(f, wl[w][p], L);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);

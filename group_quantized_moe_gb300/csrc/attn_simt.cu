@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-          const float e = ex2(s[p][k] - ref);
+          const float e = guard && s[p][k] == -INFINITY ? unseen_weight() : ex2(s[p][k] - ref);
           sum += e;
           Ps[row * PLD + tx + 16 * k] = e;
         }
@@ -242,8 +242,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnBatch a, AttnSc
           const float4 vv = *reinterpret_cast<const float4 *>(Vs + k * NC * 64 + 64 * c + 4 * tx);
 #pragma unroll
           for (int p = 0; p < RP; ++p) {
-            // a key the row does not see must not enter even as 0 * NaN
-            if (guard && pr[p] == 0.0f) continue;
+            if (guard && is_unseen(pr[p])) continue;  // not even as 0 * NaN
             o[p][c].x = fmaf(pr[p], vv.x, o[p][c].x);
             o[p][c].y = fmaf(pr[p], vv.y, o[p][c].y);
             o[p][c].z = fmaf(pr[p], vv.z, o[p][c].z);
@@ -322,10 +321,10 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnBatch a, int gsub, i
       for (int w = w0; w <= u.last; ++w) {
         const float2 ml = parts.ml[at(w)];
         const float4 v = *reinterpret_cast<const float4 *>(parts.o + at(w) * hd + 4 * c);
+        // A part that saw no key is all zeros, and counts nothing; one that holds a
+        // NaN makes the row NaN, however small its factor is (NaN scores do not
+        // show in the maximum).
         const float f = ex2(ml.x - ref);
-        // a part that saw no key, or only negligible ones; a NaN sum (a NaN among
-        // the scores, which the maximum does not show) makes the row NaN
-        if (f == 0.0f && ml.y == ml.y) continue;
         L = fmaf(f, ml.y, L);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);

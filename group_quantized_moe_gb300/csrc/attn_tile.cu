@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
           float sum = 0.0f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float e = ex2(s[p][k] - ref);
+            const float e = s[p][k] == -INFINITY ? unseen_weight() : ex2(s[p][k] - ref);
             sum += e;
             Pw[(4 * p + y4) * kPld + x8 + 8 * k] = e;
           }
@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
           t.x = fma2(w2, v.x, t.x);
           t.y = fma2(w2, v.y, t.y);
         };
-        // Where some row misses some key, P is 0 there, which a non-finite value
-        // would still turn into NaN: then (and only then) key by key.
+        // Where some row misses some key, P is a zero there, which a non-finite
+        // value would still turn into NaN: then (and only then) key by key.
         bool plain = true;
         if (guard) {
           float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, Tile<NC>::per_sm)
               const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(Vs + k * W + 32 * j + 4 * x8);
 #pragma unroll
               for (int p = 0; p < 4; ++p)
-                if (w[p] != 0.0f) add(w[p], v, o[p][j]);
+                if (!is_unseen(w[p])) add(w[p], v, o[p][j]);
             }
           }
         }

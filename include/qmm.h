@@ -386,7 +386,8 @@ int qmm_rope_append(const void *qkv, int32_t x_dtype, int64_t T, int64_t row_str
  * y [T, n_head, head_dim] fp32 or bf16 (y_dtype), contiguous; rows that
  * belong to no sequence become zeros.  scale 0: 1 / sqrt(head_dim).  dtype:
  * of q, k and v.  A key that a row does not see never touches it, whatever it
- * holds (NaN included); a NaN among a row's scores makes the row NaN.
+ * holds (NaN included); a NaN among a row's scores, or in the values of keys
+ * that it sees, makes it NaN.
  * Arithmetic: scores, maxima, sums and results in fp32.  bf16 with head_dim a
  * multiple of 8 up to 128 and rows 16 bytes apart runs on the tensor cores,
  * whose operands are bf16: there each weight is rounded to bf16 where it

@@ -171,3 +171,28 @@ def test_bf16_rows_of_8_bytes_take_the_cuda_cores(dev, nh, nkv, hd):
     y = q.attn_paged(x, q.PagedKV(kc, vc), table, cu_of([n]), i32([L]))
     want, b = ref.paged(num(x), num(kc), num(vc), table.cpu().numpy(), [(L, n)], hd ** -0.5)
     assert_within(num(y), want, round_bound(want, b, F32))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nh,nkv,hd,n", FORMS)
+def test_nan_values_reach_every_row_that_sees_them(dev, nh, nkv, hd, n, dtype):
+    """A NaN value makes the rows NaN that see its key, also where the key lies so
+    far below the row's maximum that its weight, or its whole part's, is zero
+    in fp32; rows that do not see it are as without it."""
+    S = 16
+    for L in (n + 8, n + 131, 4000 + n):
+        cols = -(-L // S)
+        x, k, v, wide, table = make(hd + L, 2, n, nh, nkv, hd, S, cols, dtype)
+        x = x.abs() + 1.0
+        top = 0  # every row sees key 0, far above the others
+        k[wide[0, top // S], :, top % S] = 100.0
+        cache, cu, kvl = q.PagedKV(k, v), cu_of([n, n]), i32([L, L])
+        clean = q.attn_paged(x, cache, table, cu, kvl)
+        assert torch.isfinite(clean).all()
+        for j in (L - 1, L - n, (L - n) // 2, 1):
+            v2 = v.clone()
+            v2[wide[0, j // S], :, j % S] = float("nan")
+            y = q.attn_paged(x, q.PagedKV(k, v2), table, cu, kvl)
+            first = max(0, j - (L - n))
+            assert y[first:n].isnan().all(), (L, j)
+            assert torch.equal(y[:first], clean[:first]) and torch.equal(y[n:], clean[n:]), (L, j)
