@@ -45,7 +45,9 @@ EXPORTED = ("qmm_quantize_groupwise", "qmm_linear", "moe_route_workspace_bytes",
             "qmm_attn_decode", "moe_decode_workspace_bytes", "moe_decode_forward",
             "qmm_tc_timing", "qmm_tc_timing_ms", "qmm_kv_plan", "qmm_rope_append",
             "qmm_attn_prompt_workspace_bytes", "qmm_attn_prompt",
-            "qmm_attn_paged_workspace_bytes", "qmm_attn_paged")
+            "qmm_attn_paged_workspace_bytes", "qmm_attn_paged", "qmm_kv4_block_bytes",
+            "qmm_rope_append_kv4", "qmm_kv4_read", "qmm_attn_paged_kv4_workspace_bytes",
+            "qmm_attn_paged_kv4")
 QMM_NOALLOC_MAX_LOGITS = 262144
 
 
@@ -81,6 +83,12 @@ class _KvCache(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int64),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_stride", ctypes.c_int64)]
+
+
+class _Kv4Cache(ctypes.Structure):
+    _fields_ = [("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int64),
+                ("data", ctypes.c_void_p), ("block_stride", ctypes.c_int64)]
 
 
 class _Experts(ctypes.Structure):
@@ -172,6 +180,19 @@ def lib() -> ctypes.CDLL:
             L.qmm_attn_paged.argtypes = [vp, i64, i64, i32, kvp, vp, i64, i32, vp, vp, i32, f32, vp,
                                          i32, vp, sz, vp]
             L.qmm_attn_paged.restype = ctypes.c_int
+            kv4 = ctypes.POINTER(_Kv4Cache)
+            L.qmm_kv4_block_bytes.argtypes = [i32, i32, i32, i32]
+            L.qmm_kv4_block_bytes.restype = i64
+            L.qmm_rope_append_kv4.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, vp, i64, kv4, vp, vp,
+                                              vp, i32, vp]
+            L.qmm_rope_append_kv4.restype = ctypes.c_int
+            L.qmm_kv4_read.argtypes = [kv4, vp, i64, vp, vp, i32, vp]
+            L.qmm_kv4_read.restype = ctypes.c_int
+            L.qmm_attn_paged_kv4_workspace_bytes.argtypes = [kv4, i32, i64, i32, i32]
+            L.qmm_attn_paged_kv4_workspace_bytes.restype = sz
+            L.qmm_attn_paged_kv4.argtypes = [vp, i32, i64, i64, i32, kv4, vp, i64, i32, vp, vp, i32, f32,
+                                             vp, i32, vp, sz, vp]
+            L.qmm_attn_paged_kv4.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -899,6 +920,66 @@ def paged_kv(num_blocks: int, n_kv: int, block_size: int, head_dim: int,
 
 
 @dataclass
+class PagedKV4:
+    """One layer's paged cache held in 4 bits (see include/qmm.h for its form):
+    data uint8 [num_blocks, n_kv, bytes of a block's head], codes in groups of
+    32 or 64 dimensions with a scale and a zero point each.  Blocks may lie
+    apart (views of one allocation that interleaves layers).  Takes PagedKV's
+    place in rope_append, attn_paged and attn_layer_paged; kv4_read gives rows
+    of it as numbers."""
+    data: torch.Tensor
+    head_dim: int
+    group: int
+    block_size: int
+
+    def _desc(self) -> _Kv4Cache:
+        d = self.data
+        c = self.__dict__.get("_desc_for")
+        if (c is not None and c[0] is d and c[1] == d.data_ptr() and c[2] == d.shape
+                and c[3] == d.stride() and c[4] == (self.head_dim, self.group, self.block_size)):
+            return c[5]
+        if d.dtype != torch.uint8 or d.dim() != 3:
+            raise TypeError("data must be uint8 [num_blocks, n_kv, bytes]")
+        if not d.is_cuda:
+            raise ValueError("data must live on a CUDA device")
+        nb, nkv, n = d.shape
+        want = qmm_kv4_block_bytes(nkv, self.head_dim, self.group, self.block_size)
+        if nkv * n != want:
+            raise ValueError(f"a block has {nkv * n} bytes, expected {want}")
+        if nb and (n > 1 and d.stride(2) != 1 or nkv > 1 and d.stride(1) != n):
+            raise ValueError("a block must be contiguous")
+        desc = _Kv4Cache(nkv, self.head_dim, self.group, self.block_size, nb, d.data_ptr(),
+                         d.stride(0) if nb > 1 else nkv * n)
+        self.__dict__["_desc_for"] = (d, d.data_ptr(), d.shape, d.stride(),
+                                      (self.head_dim, self.group, self.block_size), desc)
+        return desc
+
+
+def qmm_kv4_block_bytes(n_kv: int, head_dim: int, group: int, block_size: int) -> int:
+    """Bytes of a block of a 4-bit cache."""
+    n = int(lib().qmm_kv4_block_bytes(n_kv, head_dim, group, block_size))
+    if n == 0:
+        raise QmmError(QMM_ERR_UNSUPPORTED, lib().qmm_last_error().decode(errors="replace"))
+    return n
+
+
+def paged_kv4(num_blocks: int, n_kv: int, block_size: int, head_dim: int, group: int = 64,
+              device="cuda") -> PagedKV4:
+    """An uninitialised paged cache of one layer, held in 4 bits."""
+    n = qmm_kv4_block_bytes(n_kv, head_dim, group, block_size) // n_kv
+    return PagedKV4(torch.empty((num_blocks, n_kv, n), dtype=torch.uint8, device=device), head_dim,
+                    group, block_size)
+
+
+def _same_device(*ts) -> None:
+    """The calls over a 4-bit cache run on the current device: tensors of
+    another one are refused."""
+    for t in ts:
+        if t is not None and t.numel() and t.get_device() != torch._C._cuda_getDevice():
+            raise ValueError("tensors must live on the current CUDA device")
+
+
+@dataclass
 class KVPlan:
     """What kv_plan computes: cu_new int32 [R + 1], kv_lens int32 [R],
     positions int32 [T], slots int64 [T], blocks_used int32 [1]."""
@@ -957,15 +1038,16 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
 
 
 def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: torch.Tensor | None,
-                rope_cos: torch.Tensor, rope_sin: torch.Tensor, cache: PagedKV | None,
-                keep_kv: bool = False, n_kv: int | None = None, y_dtype: torch.dtype | None = None,
-                q: torch.Tensor | None = None, k: torch.Tensor | None = None,
-                v: torch.Tensor | None = None, stream=None):
+                rope_cos: torch.Tensor, rope_sin: torch.Tensor,
+                cache: PagedKV | PagedKV4 | None, keep_kv: bool = False, n_kv: int | None = None,
+                y_dtype: torch.dtype | None = None, q: torch.Tensor | None = None,
+                k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
     """Rotates the queries and keys of qkv [T, (n_head + 2 n_kv) head_dim] and
     stores keys and values into their rows of the cache (see include/qmm.h).
     Returns (q, k, v): q [T, n_head, head_dim]; k, v [T, n_kv, head_dim] when
     keep_kv (or given), else None.  Without a cache, n_kv and y_dtype say the
-    key/value heads and the output type."""
+    key/value heads and the output type.  A PagedKV4 is written in 4 bits; there
+    y_dtype says the type of q, k and v (bf16 if it is not given)."""
     max_seq, half = rope_cos.shape
     hd = 2 * half
     plain = _vec(rope_cos, _F32, max_seq * half) and _vec(rope_sin, _F32, max_seq * half)
@@ -977,7 +1059,15 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
         if desc.head_dim != hd or (n_kv is not None and n_kv != desc.n_kv):
             raise ValueError(f"the cache has {desc.n_kv} heads of {desc.head_dim}, the call "
                              f"{n_kv} of {hd}")
-        n_kv, y_dtype = desc.n_kv, cache.k.dtype
+        n_kv = desc.n_kv
+        if cache.__class__ is not PagedKV4:
+            y_dtype = cache.k.dtype
+        else:
+            if y_dtype is None:
+                y_dtype = torch.bfloat16
+            elif y_dtype not in (_F32, torch.bfloat16):
+                raise TypeError(f"unsupported y_dtype {y_dtype} (float32 or bfloat16)")
+            _same_device(cache.data, qkv, positions, slots, rope_cos, rope_sin, q, k, v)
         if slots is None:
             raise ValueError("a cache needs slots")
     else:
@@ -1010,6 +1100,16 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
         k = _new((T, n_kv, hd), y_dtype, qkv.device, stream)
     if keep_kv and v is None:
         v = _new((T, n_kv, hd), y_dtype, qkv.device, stream)
+    if cache.__class__ is PagedKV4:
+        rc = lib().qmm_rope_append_kv4(qkv.data_ptr(), _dtype_code(qkv), T,
+                                       qkv.stride(0) if T > 1 else width, n_head, positions.data_ptr(),
+                                       slots.data_ptr(), rope_cos.data_ptr(), rope_sin.data_ptr(),
+                                       max_seq, desc, q.data_ptr(), None if k is None else k.data_ptr(),
+                                       None if v is None else v.data_ptr(), _dtype_code(q),
+                                       _stream(stream))
+        if rc:
+            _check(rc)
+        return q, k, v
     rc = lib().qmm_rope_append(qkv.data_ptr(), _dtype_code(qkv), T, qkv.stride(0) if T > 1 else width,
                                n_head, n_kv, hd, positions.data_ptr(),
                                None if slots is None else slots.data_ptr(), rope_cos.data_ptr(),
@@ -1019,6 +1119,30 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
     if rc:
         _check(rc)
     return q, k, v
+
+
+def kv4_read(cache: PagedKV4, slots: torch.Tensor, y_dtype: torch.dtype = torch.float32,
+             k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """The values that rows slots (int64 [n]; below 0: zeros) of a 4-bit cache
+    stand for (see include/qmm.h): k, v [n, n_kv, head_dim] of y_dtype."""
+    desc = cache._desc()
+    n = slots.numel()
+    shape = (n, desc.n_kv, desc.head_dim)
+    _check_vec(slots, _I64, n, "slots")
+    _same_device(cache.data, slots, k, v)
+    if y_dtype not in (_F32, torch.bfloat16):
+        raise TypeError(f"unsupported y_dtype {y_dtype} (float32 or bfloat16)")
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _need(t, n * desc.n_kv * desc.head_dim, (y_dtype,), name)
+            _require_cuda(t)
+    k = _new(shape, y_dtype, slots.device, stream) if k is None else k
+    v = _new(shape, y_dtype, slots.device, stream) if v is None else v
+    rc = lib().qmm_kv4_read(desc, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _dtype_code(k),
+                            _stream(stream))
+    if rc:
+        _check(rc)
+    return k, v
 
 
 def _attn_y(q, y, y_dtype, stream):
@@ -1073,23 +1197,33 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     return y
 
 
-def qmm_attn_paged_workspace_bytes(q: torch.Tensor, cache: PagedKV, n_requests: int) -> int:
+def qmm_attn_paged_workspace_bytes(q: torch.Tensor, cache: PagedKV | PagedKV4,
+                                   n_requests: int) -> int:
+    if cache.__class__ is PagedKV4:
+        return int(lib().qmm_attn_paged_kv4_workspace_bytes(ctypes.byref(cache._desc()), _dtype_code(q),
+                                                            q.shape[0], q.shape[1], n_requests))
     return int(lib().qmm_attn_paged_workspace_bytes(ctypes.byref(cache._desc()), q.shape[0],
                                                     q.shape[1], n_requests))
 
 
-def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q: torch.Tensor,
+def attn_paged(q: torch.Tensor, cache: PagedKV | PagedKV4, block_table: torch.Tensor, cu_q: torch.Tensor,
                kv_lens: torch.Tensor, scale: float | None = None, y: torch.Tensor | None = None,
                y_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """Attention of each request's new tokens (one or many) over its blocks of
     the cache (see include/qmm.h): q [T, n_head, head_dim] of the cache's
     dtype, block_table int32 [R, columns], cu_q int32 [R + 1], kv_lens int32
-    [R] (cache rows with the new tokens)."""
+    [R] (cache rows with the new tokens).  Over a PagedKV4, q is fp32 or bf16:
+    that chooses the arithmetic."""
     sq = _heads(q, "q")
     T, nh, hd = q.shape
     desc = cache._desc()
-    if hd != desc.head_dim or q.dtype != cache.k.dtype:
+    kv4 = cache.__class__ is PagedKV4
+    if kv4:
+        if hd != desc.head_dim:
+            raise ValueError(f"q has head_dim {hd}, the cache {desc.head_dim}")
+        _same_device(cache.data, q, block_table, cu_q, kv_lens, y, workspace)
+    elif hd != desc.head_dim or q.dtype != cache.k.dtype:
         raise ValueError(f"q is {q.dtype} with head_dim {hd}, the cache {cache.k.dtype} with "
                          f"{desc.head_dim}")
     R = kv_lens.numel()
@@ -1108,6 +1242,15 @@ def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q:
                          stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():  # its size is the library's check
         _require_cuda(workspace)
+    if kv4:
+        rc = lib().qmm_attn_paged_kv4(q.data_ptr(), _dtype_code(q), T, sq, nh, desc,
+                                      block_table.data_ptr(), block_table.stride(0) if R > 1 else cols,
+                                      cols, cu_q.data_ptr(), kv_lens.data_ptr(), R,
+                                      0.0 if scale is None else scale, y.data_ptr(), _dtype_code(y),
+                                      workspace.data_ptr(), workspace.nbytes, _stream(stream))
+        if rc:
+            _check(rc)
+        return y
     rc = lib().qmm_attn_paged(q.data_ptr(), T, sq, nh, desc, block_table.data_ptr(),
                               block_table.stride(0) if R > 1 else cols, cols, cu_q.data_ptr(),
                               kv_lens.data_ptr(), R, 0.0 if scale is None else scale, y.data_ptr(),
@@ -1119,8 +1262,8 @@ def attn_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor, cu_q:
 
 
 def attn_layer_paged(x: torch.Tensor, wqkv: QWeight, wo: QWeight, n_head: int,
-                     rope_cos: torch.Tensor, rope_sin: torch.Tensor, cache: PagedKV, plan: KVPlan,
-                     block_table: torch.Tensor, prompts: bool = False,
+                     rope_cos: torch.Tensor, rope_sin: torch.Tensor, cache: PagedKV | PagedKV4,
+                     plan: KVPlan, block_table: torch.Tensor, prompts: bool = False,
                      y_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """One attention layer for a batch of requests' new tokens x [T, D], as
     kv_plan has planned them: the quantised q/k/v projection (wqkv: the rows of
@@ -1133,10 +1276,12 @@ def attn_layer_paged(x: torch.Tensor, wqkv: QWeight, wo: QWeight, n_head: int,
     once, to the cache's type (bf16 before it, too, would double that error).
     The attention's rows go to the output projection in the type of x, with
     which the caller chooses the projections' arithmetic: fp32 rows are not
-    rounded, bf16 ones are (that projection takes bf16 on the tensor cores)."""
+    rounded, bf16 ones are (that projection takes bf16 on the tensor cores).
+    Over a PagedKV4 the queries (and the prompts' keys and values) have the type
+    of x too; what is stored is quantised from fp32."""
     qkv = qmm_linear_batched(x, wqkv, stream=stream)
     q, k, v = rope_append(qkv, n_head, plan.positions, plan.slots, rope_cos, rope_sin, cache,
-                          keep_kv=prompts, stream=stream)
+                          keep_kv=prompts, y_dtype=x.dtype, stream=stream)
     if prompts:
         a = attn_prompt(q, k, v, plan.cu_new, y_dtype=x.dtype, stream=stream)
     else:

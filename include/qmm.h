@@ -432,6 +432,81 @@ int qmm_attn_paged(const void *q, int64_t T, int64_t q_stride, int32_t n_head,
                    qmm_stream_t stream);
 
 /*
+ * A layer's paged cache held in 4 bits: keys and values quantised per row, head
+ * and group of 32 or 64 dimensions [P1 section 3.2's group-wise codes, for the
+ * cache of section 3.4], a quarter to a third of the bytes of bf16.  Per group
+ *   lo, hi = min, max;  top = max(|lo|, |hi|)
+ *   s  = the next bf16 at or above max((hi - lo) / 15, top / 2048, 2^-100)
+ *   zp = -rint(lo / s),  code = clamp(rint(v / s) + zp, 0, 15)
+ *   value = (code - zp) s
+ * in fp32, ties to even, 1 / s rounded once and multiplied ((hi - lo) / 15 as
+ * (hi / 16 - lo / 16) (16 / 15)).  A value is off by at most s / 2, a little
+ * more at a group's ends; a group with a NaN or an infinity reads as NaN.
+ * data: num_blocks blocks, block_stride bytes apart, of qmm_kv4_block_bytes
+ * bytes each: for every key/value head its rows in strips of 16, and in a strip
+ * (NC = ceil(head_dim / 32), beyond 4 the next even number; G groups)
+ *   key codes     32-bit words [16][4][NC]; nibble j (low ones first) of word
+ *                 (r, t, c) is dimension 32 c + 8 t + j of row r
+ *   value codes   words [2][8][4][NC]; the low half of word (h, g, t, c) belongs
+ *                 to row 8 h + 2 t, the high half to the row after it; nibble j
+ *                 of a half is dimension 32 c + 4 g + j
+ *   key scales    words [16][G]: zp (fp16) in the low half, s (bf16) in the high
+ *   value scales  the same
+ * Lengths, tables and slots are those of the other caches (qmm_kv_plan).
+ */
+typedef struct qmm_kv4_cache {
+  int32_t n_kv, head_dim;  /* head_dim a multiple of 8 in [8, 256]           */
+  int32_t group;           /* 32 or 64; the last group of a row may be short */
+  int32_t block_size;      /* 16, 32, 64, 128 or 256                         */
+  int64_t num_blocks;
+  void *data;              /* 16-byte aligned                                */
+  int64_t block_stride;    /* bytes, a multiple of 16                        */
+} qmm_kv4_cache;
+
+/* Bytes of a block; 0 for sizes that are not supported. */
+int64_t qmm_kv4_block_bytes(int32_t n_kv, int32_t head_dim, int32_t group, int32_t block_size);
+
+/*
+ * qmm_rope_append into a 4-bit cache: the same rotation, q, k and v (of
+ * y_dtype, whatever the cache holds; k, v NULL: skip), padding rows and status
+ * bits; the rotated keys and the values are quantised from fp32.  Rows are a
+ * multiple of 16 bytes apart.  Two tokens must not share a slot.  One launch.
+ */
+int qmm_rope_append_kv4(const void *qkv, int32_t x_dtype, int64_t T, int64_t row_stride, int32_t n_head,
+                        const int32_t *positions, const int64_t *slots, const float *rope_cos,
+                        const float *rope_sin, int64_t max_seq, const qmm_kv4_cache *cache, void *q, void *k,
+                        void *v, int32_t y_dtype, qmm_stream_t stream);
+
+/*
+ * Rows of a 4-bit cache as numbers: k, v [n, n_kv, head_dim] of y_dtype (either
+ * may be NULL) <- the values of row slots[i].  A slot below 0 gives zeros; one
+ * beyond the cache does the same and sets QMM_DEV_BAD_BLOCK.  One launch.
+ */
+int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, void *k, void *v, int32_t y_dtype,
+                 qmm_stream_t stream);
+
+/*
+ * qmm_attn_paged over a 4-bit cache; q_dtype: of q.  Masks, lengths, tables,
+ * rows of no request, NaNs and status bits as there; a row of the cache that is
+ * seen must have been written by qmm_rope_append_kv4.
+ * Arithmetic: the products multiply codes, which fp16 holds exactly, on the
+ * tensor cores, and scales and zero points are applied in fp32; scores, maxima,
+ * sums and results are fp32.  A query row is scaled by a power of two to fp16
+ * (bf16 rows: exact for elements down to 2^-29 of the row's largest; fp32 rows:
+ * in two parts, 2^-22; an element of 2^114 or more counts as infinite).  With
+ * bf16 queries each weight times its value's scale is rounded to 16 bits
+ * (2^-11 in fp16; not in the sum it is divided by), whatever y_dtype is; with
+ * fp32 queries it has two parts, 2^-22.
+ */
+size_t qmm_attn_paged_kv4_workspace_bytes(const qmm_kv4_cache *cache, int32_t q_dtype, int64_t T, int32_t n_head,
+                                          int32_t R);
+
+int qmm_attn_paged_kv4(const void *q, int32_t q_dtype, int64_t T, int64_t q_stride, int32_t n_head,
+                       const qmm_kv4_cache *cache, const int32_t *block_table, int64_t table_stride,
+                       int32_t max_blocks, const int32_t *cu_q, const int32_t *kv_lens, int32_t R, float scale,
+                       void *y, int32_t y_dtype, void *workspace, size_t workspace_bytes, qmm_stream_t stream);
+
+/*
  * The routed MoE layer of a decode batch in one launch [P1 section 3.5: the
  * router, the grouping of tokens by expert and the experts' weighted sum as
  * one step]: computes exactly what moe_route_topk followed by
