@@ -21,8 +21,8 @@
 // [2^14, 2^15): bf16 queries are exact down to 2^-29 of the largest; fp32 ones
 // are split into two fp16.  The weights p s_g c are rounded to fp16 (2^-11;
 // fp32 queries: split in two as well), c a power of two per query row that
-// keeps them below 2^15 and moves when the maximum moves or a product would
-// leave the range.  The tensor cores cut their sums off instead of rounding,
+// keeps them below 2^15 and moves when the maximum moves or the scale of a
+// value is so large that a product could leave the range.  The tensor cores cut their sums off instead of rounding,
 // so they run over 32 keys only and are added up in fp32.
 #include <cuda_fp16.h>
 
@@ -34,12 +34,14 @@
 #include "kv4.h"
 #include "qmm_device.cuh"
 #include "qmm_internal.h"
+#include "tc_device.cuh"
 
 namespace qmm {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kKT = 32;           // keys of a step: two strips
+constexpr int kUnits = 16;          // units in the ring between the loading warp and the others
+constexpr int kAlone = 6;            // tiles of a unit that one warp takes alone
 constexpr float kRescale = 8.0f;  // log2 of the growth of the maximum that is let pass
 constexpr float kTop = 32768.0f;  // of a weight
 
@@ -59,13 +61,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// d += a b, a [16 x 16], b [16 x 8] fp16, d fp32.
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
+// d += a b (first: d = a b), a [16 x 16], b [16 x 8] fp16, d fp32.
+__device__ __forceinline__ void mma(bool first, float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first ? 0.0f : d[0]), "f"(first ? 0.0f : d[1]),
+        "f"(first ? 0.0f : d[2]), "f"(first ? 0.0f : d[3]));
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -95,43 +98,51 @@ __device__ __forceinline__ float column_sum(float v) {
   return v;
 }
 
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Whether the phase with the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Keeps a rarely taken block behind a branch (not predicated, which would cost
+// its instructions every time).
+__device__ __forceinline__ void branch() { asm volatile("" ::: "memory"); }
+
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// N words of shared memory, 16 bytes at a time where they lie so.
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint32_t *p) {
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int c = 0; c < N; c += 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + c));
+      const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * c);
       w[c] = v.x, w[c + 1] = v.y, w[c + 2] = v.z, w[c + 3] = v.w;
     }
   } else if constexpr (N % 2 == 0) {
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p + c));
+      const uint2 v = *reinterpret_cast<const uint2 *>(p + 4 * c);
       w[c] = v.x, w[c + 1] = v.y;
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < N; ++c) w[c] = __ldg(p + c);
+    for (int c = 0; c < N; ++c) w[c] = *reinterpret_cast<const uint32_t *>(p + 4 * c);
   }
 }
-
-// NC: chunks of 32 dimensions; CPG: chunks of a group; NQ: tiles of eight query
-// rows; F32: the queries' type (else bf16).
-template <int NC, int CPG, int NQ, bool F32>
-struct Form {
-  static constexpr int G = (NC + CPG - 1) / CPG, R = 8 * NQ, P = F32 ? 2 : 1, HD = 32 * NC;
-  // an operand of code c is (c - centre) / unit
-  static constexpr float unit = F32 ? 1.0f : 0x1p20f, centre = F32 ? 8.0f : 0.0f;
-  // queries as operands [P][NQ][NC][32 lanes] of 16 bytes, their group sums
-  // [R][G] in an operand's unit, unit / 2^E times the scale [R], then the warps' results
-  static constexpr int q_bytes = P * NQ * NC * 512;
-  static constexpr int sum_off = q_bytes, ke_off = sum_off + R * G * 4;
-  static constexpr int ml_off = (ke_off + R * 4 + 15) & ~15;
-  static constexpr int o_off = ml_off + kWarps * R * 8;
-  static constexpr int bytes = o_off + kWarps * R * HD * 4;
-};
 
 // The four operand registers of a word of codes: its nibbles (0, 4), (1, 5),
 // (2, 6), (3, 7), each as code 2^-20, or with fp32 queries as code - 8: sums of
@@ -156,408 +167,715 @@ __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) {
   a[3] = x & 0x00F000F0u;
 }
 
-// A unit's query rows as operands.  Thread t of a column's eight holds
-// dimensions 32 c + 8 t + j of chunk c: pairs (0, 4), (1, 5), (2, 6), (3, 7).
+// NC: chunks of 32 dimensions; CPG: chunks of a group; NQ: tiles of eight query
+// rows; F32: the queries' type (else bf16).
 template <int NC, int CPG, int NQ, bool F32>
-__device__ __forceinline__ void stage_queries(const Attn4 &p, uint8_t *smem, int row0, int head0, int g, int rows) {
+struct Form {
+  static constexpr int G = (NC + CPG - 1) / CPG, R = 8 * NQ, P = F32 ? 2 : 1, HD = 32 * NC;
+  // an operand of code c is (c - centre) / unit
+  static constexpr float unit = F32 ? 1.0f : 0x1p20f, centre = F32 ? 8.0f : 0.0f;
+  // warps that multiply, and one that loads: three to a scheduler leave a thread
+  // 168 registers, two 255
+  static constexpr int warps = NQ == 1 && NC <= 4 && !(F32 && NC == 4 && CPG == 1) ? 11 : 7, threads = 32 * (warps + 1);
+  static constexpr int stage = 2 * (512 * NC + 128 * G);  // a tile of the cache
+  static constexpr bool qreg = NQ * P == 1 && NC <= 4;    // queries in registers, else in shared memory
+  static constexpr int q_warp = qreg ? 0 : P * NQ * NC * 512, q_bytes = warps * q_warp;
+  static constexpr int OS = HD + 4;  // floats between rows of results (four lanes store one each)
+  static constexpr int o_bytes = warps * R * OS * 4, ml_bytes = warps * R * 8;
+  static constexpr int fixed = q_bytes + o_bytes + ml_bytes + kUnits * 64 + 2048;
+  static constexpr int room = (225 * 1024 - fixed) / (stage * warps);
+  static constexpr int depth = room < 4 ? room : 4;  // tiles in flight a warp
+  static constexpr int stages = depth * warps;
+  static constexpr int o_off = stages * stage, ml_off = o_off + o_bytes, q_off = ml_off + ml_bytes;
+  static constexpr int unit_off = (q_off + q_bytes + 15) & ~15, bar_off = unit_off + kUnits * 64;
+  // full [stages], u_full, joined, wrote [kUnits], the abort flag
+  static constexpr int flag_off = bar_off + 8 * (stages + 3 * kUnits);
+  static constexpr int bytes = flag_off + 16;
+  static_assert(depth >= 1 && bytes <= 227 * 1024, "shared memory");
+};
+
+// One unit of this worker's run, as the warps see it.
+struct __align__(16) Unit4 {
+  int valid, q_row, rows, g;    // 0: no unit any more; first query row, rows, heads
+  int h, head0, r, pad;         // key/value head, first query head, request
+  int tile, stop, whole, slot;  // this worker's tiles [tile, stop); all of them: not divided; its slot if not
+  int all, end, alone, n0;      // keys the first / last token sees; one warp has all tiles; turn of its first
+};
+
+// A query row's elements as operands: lane 4 col + t holds dimensions
+// 32 c + 8 t + j of row `col` of tile n, in pairs (0, 4), (1, 5), (2, 6), (3, 7).
+// ke: unit / 2^E scale log2 e, sum: by group, both of that row.
+template <int NC, int CPG, int NQ, bool F32>
+__device__ __forceinline__ void make_queries(const Attn4 &p, const Unit4 &u, int n, uint32_t (&op)[F32 ? 2 : 1][NC][4],
+                                             float (&sum)[Form<NC, CPG, NQ, F32>::G], float &ke) {
   using C = Form<NC, CPG, NQ, F32>;
-  const int lane = threadIdx.x & 31, hd = p.a.head_dim;
-  for (int row = threadIdx.x >> 5; row < C::R; row += kWarps) {
-    const int t = row / g, h = head0 + row - t * g;
-    float x[NC], top = 0.0f;
-    bool bad = false;
+  const int lane = threadIdx.x & 31, row = 8 * n + (lane >> 2), t4 = lane & 3, hd = p.a.head_dim;
+  const int t = row / u.g;
+  const int64_t i = static_cast<int64_t>(u.q_row + t) * p.a.q_stride + static_cast<int64_t>(u.head0 + row - t * u.g) * hd;
+  float x[NC][8], top = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int d = 32 * c + lane;
-      x[c] = 0.0f;
-      if (row < rows && d < hd) {
-        const int64_t i = static_cast<int64_t>(row0 + t) * p.a.q_stride + static_cast<int64_t>(h) * hd + d;
-        x[c] = F32 ? __ldg(static_cast<const float *>(p.a.q) + i)
-                   : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t *>(p.a.q) + i)) << 16);
+  for (int c = 0; c < NC; ++c) {
+    const int d = 32 * c + 8 * t4;
+    const bool in = row < u.rows && d < hd;
+    if constexpr (F32) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 v = in ? __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.a.q) + i + d) + k)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[c][4 * k] = v.x, x[c][4 * k + 1] = v.y, x[c][4 * k + 2] = v.z, x[c][4 * k + 3] = v.w;
       }
-      top = fmaxf(top, fabsf(x[c]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // (rows are multiples of 8 bytes apart)
+        const uint2 v = in ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.a.q) + i + d) + k)
+                           : make_uint2(0, 0);
+        x[c][4 * k] = __uint_as_float(v.x << 16), x[c][4 * k + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+        x[c][4 * k + 2] = __uint_as_float(v.y << 16), x[c][4 * k + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[c][j]));
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  int E = 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+  E = top > 0.0f ? max(-100, min(E, 100)) : 0;
+  const float up = pow2i(E);
+  ke = p.sl2 * C::unit * pow2i(-E);
+#pragma unroll
+  for (int k = 0; k < C::G; ++k) sum[k] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[c][j] *= up;
+      sum[c / CPG] += x[c][j];
     }
 #pragma unroll
-    for (int o = 1; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    int E = 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-    E = top > 0.0f ? max(-100, min(E, 100)) : 0;
-    const float up = pow2i(E);
-    const int n = row >> 3, col = row & 7, t4 = (lane >> 3) & 3, j = lane & 7;
-    float sum = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const float v = x[c] * up;
-      float s = v;
-#pragma unroll
-      for (int o = 1; o <= 16; o <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      sum = c % CPG == 0 ? s : sum + s;
-      if ((c % CPG == CPG - 1 || c == NC - 1) && lane == 0)
-        reinterpret_cast<float *>(smem + C::sum_off)[row * C::G + c / CPG] = sum * (1.0f / C::unit);
-      // nibble j: pair j & 3, place j >> 2 of it
-      const __half hi = __float2half_rn(v);
-      const int at = ((n * NC + c) * 32 + col * 4 + t4) * 16 + (j & 3) * 4 + (j >> 2) * 2;
-      *reinterpret_cast<__half *>(smem + at) = hi;
+    for (int j = 0; j < 4; ++j) {
+      op[0][c][j] = half2_of(x[c][j], x[c][j + 4]);
       if constexpr (F32)
-        *reinterpret_cast<__half *>(smem + NQ * NC * 512 + at) = __float2half_rn(v - __half2float(hi));
+        op[C::P - 1][c][j] = half2_of(x[c][j] - low_half(op[0][c][j]), x[c][j + 4] - low_half(op[0][c][j] >> 16));
     }
-    if (lane == 0) reinterpret_cast<float *>(smem + C::ke_off)[row] = p.sl2 * C::unit * pow2i(-E);
+  }
+#pragma unroll
+  for (int k = 0; k < C::G; ++k) {
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) sum[k] += __shfl_xor_sync(0xFFFFFFFFu, sum[k], o);
+    sum[k] *= 1.0f / C::unit;
   }
 }
 
-template <int NC, int CPG, int NQ, bool F32>
-__global__ void __launch_bounds__(kThreads) attn4_rows_kernel(const __grid_constant__ Attn4 p) {
-  using C = Form<NC, CPG, NQ, F32>;
-  constexpr int G = C::G;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t scratch[kWarps + 4];
-  pdl_enter();
-  const AttnRun run = sched_run<kThreads>(p.sc, blockIdx.x, scratch);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
-  const int hd = p.a.head_dim, grp = p.a.n_head / p.a.n_kv;
-  const int strip = kv4_strip(p.c), head_bytes = kv4_head_bytes(p.c), bshift = p.c.block_shift;
-  if (tid == 0) p.parts.open[blockIdx.x].rows_tok = 0;
-  int64_t x = run.unit;
-  int r = run.r, i = run.i, vh = run.h;
-  AttnReq q{};
-  bool fresh = true;
-  while (x < run.last) {
-    if (fresh) q = sched_req(p.sc, r);
-    fresh = false;
-    if (i >= sched_blocks(p.sc, q)) {
-      if (++r >= p.sc.R) break;  // lengths that changed during the call
-      i = 0;
-      fresh = true;
-      continue;
-    }
-    const int ntile = sched_tiles(p.sc, q, i), block = i, v = vh;
-    const int64_t x0 = x;
-    int tile, stop;
-    sched_part(p.sc, run, x, ntile, tile, stop);
-    x += sched_unit(p.sc, q, i);
-    if (++vh == p.sc.nvh) {
-      vh = 0;
-      ++i;
-    }
-    if (tile >= stop) continue;
-    const int h = v / p.nsub, sub = v - h * p.nsub, g = min(p.gsub, grp - sub * p.gsub);
-    const int t0 = block * p.sc.U, nt = min(p.sc.U, q.n - t0), rows = nt * g, head0 = h * grp + sub * p.gsub;
-    const int all = sched_seen(p.sc, q, t0), end = sched_end(p.sc, q, block);
-    if (tid == 0 && sched_short(p.sc, q, block)) atomicOr(p.status, kDevBadBlock);
-    stage_queries<NC, CPG, NQ, F32>(p, smem, q.q0 + t0, head0, g, rows);
-    __syncthreads();
+// Four elements of row `row` of a unit: of the output, or of its partial result.
+__device__ __forceinline__ void store_row4(const Attn4 &p, const Unit4 &u, int row, int d, float4 v) {
+  const int hd = p.a.head_dim, t = row / u.g;
+  if (u.whole)
+    store_y4(p.a.y, (static_cast<int64_t>(u.q_row + t) * p.a.n_head + u.head0 + row - t * u.g) * hd + d, v, p.a.y_bf16);
+  else
+    *reinterpret_cast<float4 *>(p.parts.o + (static_cast<int64_t>(u.slot) * p.parts.rows + row) * hd + d) = v;
+}
 
-    // this thread's columns of tile n: query rows 8 n + 2 t4 and the next
-    float o[NQ][2 * NC][4], z[NQ][G][2], qs[NQ][G][2], m[NQ][2], l[NQ][2], cw[NQ][2], top_w[NQ][2], ke[NQ][2];
-    int vis[NQ][2];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-      for (int k = 0; k < 2 * NC; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][k][e] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 8 * n + 2 * t4 + e;
-        m[n][e] = -INFINITY;
-        l[n][e] = top_w[n][e] = 0.0f;
-        cw[n][e] = 1.0f;
-        ke[n][e] = reinterpret_cast<const float *>(smem + C::ke_off)[row];
-        vis[n][e] = row < rows ? min(all + row / g, end) : 0;
-#pragma unroll
-        for (int k = 0; k < G; ++k) {
-          z[n][k][e] = 0.0f;
-          qs[n][k][e] = reinterpret_cast<const float *>(smem + C::sum_off)[row * G + k];
-        }
-      }
+template <int NC, int CPG, int NQ, bool F32>
+__global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
+    attn4_rows_kernel(const __grid_constant__ Attn4 p) {
+  using C = Form<NC, CPG, NQ, F32>;
+  constexpr int G = C::G, NW = C::warps, NS = C::stages, D = C::depth, P = C::P;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scratch[NW + 1 + 4];
+  const uint32_t base = smem_addr(smem), bars = base + C::bar_off;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto u_full = [&](uint32_t n) { return bars + 8 * (NS + n % kUnits); };
+  auto joined = [&](uint32_t n) { return bars + 8 * (NS + kUnits + n % kUnits); };
+  auto wrote = [&](uint32_t n) { return bars + 8 * (NS + 2 * kUnits + n % kUnits); };
+  volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + C::flag_off);
+  Unit4 *const units = reinterpret_cast<Unit4 *>(smem + C::unit_off);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) mbar_init(full(s), 1);
+    for (int k = 0; k < kUnits; ++k) {
+      mbar_init(u_full(k), 1);
+      mbar_init(joined(k), 1);
+      mbar_init(wrote(k), NW);
     }
-    const int32_t *table = p.a.block_table + r * p.a.table_stride;
-    for (int kt = tile + warp; kt < stop; kt += kWarps) {
-      const int k0 = kt * kKT;
-      // strip u of the step: its place, and its first key that is not there
-      const uint8_t *src[2];
-      int lim[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int k = k0 + 16 * u;
-        src[u] = p.c.data;
-        lim[u] = k;
-        if (k >= end) continue;
-        const int32_t id = table[k >> bshift];
-        if (id < 0 || id >= p.c.num_blocks) {
-          if (lane == 0) atomicOr(p.status, kDevBadBlock);
+    mbar_fence_init();
+    *abort_flag = 0;
+  }
+  pdl_enter();
+  const AttnRun run = sched_run<C::threads>(p.sc, blockIdx.x, scratch);
+  if (tid == 0) p.parts.open[blockIdx.x].rows_tok = 0;
+  __syncthreads();
+  const int hd = p.a.head_dim, strip = 512 * NC + 128 * (NC <= 4 ? G : p.c.ng);
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, wait_ok(bar, parity, p.status, abort_flag)) != 0;
+  };
+
+  if (warp == NW) {
+    // -------------------- units of the run, and the warps' results of them joined
+    const int grp = p.a.n_head / p.a.n_kv;
+    int64_t x = run.unit;
+    int r = run.r, i = run.i, vh = run.h;
+    AttnReq q{};
+    bool fresh = true;
+    uint32_t n = 0;  // the warps' turns so far
+    // Short units of a long run go to one warp each: nothing to join, and others
+    // run beside it.
+    const bool many = run.last - run.first >= 4 * NW * kAlone * kKT;
+    // the next unit of the run with tiles of it
+    auto next_unit = [&]() {
+      Unit4 u{};
+      while (x < run.last) {
+        if (fresh) q = sched_req(p.sc, r);
+        fresh = false;
+        if (i >= sched_blocks(p.sc, q)) {
+          if (++r >= p.sc.R) break;  // lengths that changed during the call
+          i = 0;
+          fresh = true;
           continue;
         }
-        src[u] += id * p.c.block_stride + static_cast<int64_t>(h) * head_bytes +
-                  ((k & ((1 << bshift) - 1)) >> 4) * strip;
-        lim[u] = min(end, k + 16);
+        const int ntile = sched_tiles(p.sc, q, i);
+        sched_part(p.sc, run, x, ntile, u.tile, u.stop);
+        if (u.tile < u.stop) {
+          u.valid = 1;
+          u.h = vh / p.nsub;
+          const int sub = vh - u.h * p.nsub, t0 = i * p.sc.U, nt = min(p.sc.U, q.n - t0);
+          u.g = min(p.gsub, grp - sub * p.gsub);
+          u.q_row = q.q0 + t0;
+          u.rows = nt * u.g;
+          u.head0 = u.h * grp + sub * p.gsub;
+          u.r = r;
+          u.whole = u.tile == 0 && u.stop == ntile;
+          u.slot = 2 * blockIdx.x + (u.tile == 0 ? 1 : 0);
+          u.all = sched_seen(p.sc, q, t0);
+          u.end = sched_end(p.sc, q, i);
+          u.n0 = static_cast<int>(n);
+          u.alone = many && u.stop - u.tile <= kAlone;
+          if (lane == 0 && sched_short(p.sc, q, i)) atomicOr(p.status, kDevBadBlock);
+          if (lane == 0 && u.tile == 0 && !u.whole)
+            p.parts.open[blockIdx.x] = AttnOpen{u.q_row, nt, vh, sched_last(p.sc, run, x, ntile)};
+        }
+        x += sched_unit(p.sc, q, i);
+        if (++vh == p.sc.nvh) {
+          vh = 0;
+          ++i;
+        }
+        if (u.valid) break;
       }
-      float s[NQ][2][4];
-      uint32_t kp[2][2][G], vp[2][2][G];  // parameters of rows g8 and g8 + 8 of the strips
+      return u;
+    };
+    uint32_t made = 0, done = 0;  // units handed out, joined
+    bool more = true;
+    while (true) {
+      while (more && made - done < kUnits) {
+        const Unit4 u = next_unit();
+        if (lane == 0) {
+          units[made % kUnits] = u;
+          mbar_arrive(u_full(made));
+        }
+        __syncwarp();
+        n += u.alone ? 1 : u.stop - u.tile;
+        more = u.valid != 0;
+        if (more) ++made;
+      }
+      if (done == made || !wait_warp(wrote(done), (done / kUnits) & 1u)) break;
+      // the warps' results of a unit: part k is warp (n0 + k) % NW's
+      const Unit4 u = units[done % kUnits];
+      const int parts = u.alone ? 1 : min(NW, u.stop - u.tile), first = static_cast<uint32_t>(u.n0) % NW;
+      if (parts > 1) {
+        const float2 *const ml = reinterpret_cast<const float2 *>(smem + C::ml_off);
+        auto part = [&](int k) { return first + k < NW ? first + k : first + k - NW; };
+        // lane = row: its maximum and sum
+        float M = -INFINITY, L = 0.0f;
+        const int mine = min(lane, C::R - 1);
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) M = fmaxf(M, ml[part(k) * C::R + mine].x);
+        const float ref = M == -INFINITY ? 0.0f : M;
+        // (zeros of a warp that saw no key count nothing; a NaN makes the row NaN,
+        // however small its warp's factor is)
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+          const float2 v = ml[part(k) * C::R + mine];
+          L = fmaf(ex2(v.x - ref), v.y, L);
+        }
+        const float inv = u.whole ? (L > 0.0f || L != L ? 1.0f / L : 0.0f) : 1.0f;
+        if (!u.whole && lane < u.rows)
+          p.parts.ml[static_cast<int64_t>(u.slot) * p.parts.rows + lane] = make_float2(M, L);
+        const int from = part(min(lane, parts - 1));
+#pragma unroll 2
+        for (int row = 0; row < u.rows; ++row) {
+          // lane = part: its factor
+          const float f = ex2(ml[from * C::R + row].x - __shfl_sync(0xFFFFFFFFu, ref, row)) *
+                          __shfl_sync(0xFFFFFFFFu, inv, row);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bool there = lim[u] > k0 + 16 * u;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][u][e] = 0.0f;
-        uint32_t kw[2][NC];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t *const par = reinterpret_cast<const uint32_t *>(src[u] + 512 * NC) + (8 * w + g8) * p.c.ng;
-          // rows behind the last key may hold anything
-          const bool in = k0 + 16 * u + 8 * w + g8 < lim[u];
-#pragma unroll
-          for (int k = 0; k < G; ++k) {
-            kp[u][w][k] = in && k < p.c.ng ? __ldg(par + k) : 0u;
-            vp[u][w][k] = in && k < p.c.ng ? __ldg(par + 16 * p.c.ng + k) : 0u;
-          }
-          if (there) {
-            load_words<NC>(kw[w], reinterpret_cast<const uint32_t *>(src[u]) + (32 * w + lane) * NC);
-          } else {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) kw[w][c] = 0u;
+          for (int c0 = 0; c0 < 8 * NC; c0 += 32) {
+            const int d = 4 * (c0 + lane);
+            const float *const o = reinterpret_cast<const float *>(smem + C::o_off) + row * C::OS + min(d, C::HD - 4);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = 0; k < parts; ++k) {
+              const float4 v = *reinterpret_cast<const float4 *>(o + part(k) * C::R * C::OS);
+              const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+              acc.x = fmaf(fk, v.x, acc.x);
+              acc.y = fmaf(fk, v.y, acc.y);
+              acc.z = fmaf(fk, v.z, acc.z);
+              acc.w = fmaf(fk, v.w, acc.w);
+            }
+            if (d < hd) store_row4(p, u, row, d, acc);
           }
         }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(joined(done));
+      ++done;
+    }
+  } else {
+    // ---------------------------------------------------------------- products
+    // Tile n of the worker is warp n % NW's, which also fetches it, up to D tiles
+    // ahead and across units, into a stage of its own.
+    const int bshift = p.c.block_shift, bmask = (1 << bshift) - 1;
+    const int64_t head_bytes = kv4_head_bytes(p.c);
+    int ahead = 0, f_stage = 0;    // tiles fetched and not used; stage of the next one
+    int stage = 0;                 // of the next one to be used, and its barrier's parity
+    uint32_t parity = 0;
+    uint32_t here = 0;             // two bits a stage: its strips that are in the cache
+    // the unit that is being fetched, this warp's tiles left of it and their
+    // distance; sixteen of them at a time: lane 2 i + u has the place of strip u of
+    // tile i, and the block of that strip of the next sixteen
+    uint32_t f_un = 0xFFFFFFFFu, f_have = 0;
+    int f_key = 0, f_end = 0, f_left = 0, f_step = NW, f_batch = 0;
+    const int32_t *f_table = nullptr;
+    const uint8_t *f_head = nullptr, *f_src = nullptr;
+    int32_t f_id = 0;
+    bool f_more = true, ok = true;
+    auto look = [&](int key) {
+      const int k = key + (lane >> 1) * f_step * kKT + 16 * (lane & 1);
+      return k < f_end ? f_table[k >> bshift] : 0;
+    };
+    // places of the sixteen tiles from f_key on, whose blocks have been looked up
+    auto place = [&]() {
+      const int k = f_key + (lane >> 1) * f_step * kKT + 16 * (lane & 1);
+      const bool in = k < f_end, there = in && f_id >= 0 && f_id < p.c.num_blocks;
+      if (in && !there) atomicOr(p.status, kDevBadBlock);
+      f_have = __ballot_sync(0xFFFFFFFFu, there);
+      f_src = f_head + f_id * p.c.block_stride + ((k & bmask) >> 4) * strip;
+      f_batch = 0;
+      f_id = look(f_key + 16 * f_step * kKT);
+    };
+    // fetches this warp's next tile, if there is one before unit `limit`
+    auto fetch = [&](uint32_t limit) {
+      while (f_left <= 0) {
+        // (a unit that is not there yet is left for later: this may run ahead)
+        if (!f_more || f_un + 1 >= limit ||
+            !__all_sync(0xFFFFFFFFu, mbar_test(u_full(f_un + 1), ((f_un + 1) / kUnits) & 1u)))
+          return;
+        ++f_un;
+        const Unit4 &u = units[f_un % kUnits];
+        if (!(f_more = u.valid != 0)) return;
+        const int rank = (warp + NW - static_cast<uint32_t>(u.n0) % NW) % NW;
+        f_step = u.alone ? 1 : NW;
+        f_left = u.alone ? (rank == 0 ? u.stop - u.tile : 0) : (u.stop - u.tile - rank + NW - 1) / NW;
+        if (f_left <= 0) continue;
+        f_key = (u.tile + rank) * kKT;
+        f_end = min(u.end, u.stop * kKT);
+        f_head = p.c.data + u.h * head_bytes;
+        f_table = p.a.block_table + u.r * p.a.table_stride;
+        f_id = look(f_key);
+        place();
+      }
+      const uint32_t have = f_have >> (2 * f_batch) & 3u;
+      here = (here & ~(3u << (2 * f_stage))) | have << (2 * f_stage);
+      if ((lane >> 1) == f_batch) {
+        const int s = warp * D + f_stage, u = lane & 1;
+        if (u == 0) mbar_arrive_expect_tx(full(s), __popc(have) * strip);
+        // strips of one block follow one another
+        const int bytes = (bshift > 4 ? (u ? 0 : __popc(have)) : have >> u & 1) * strip;
+        if (bytes) bulk_g2s(base + s * C::stage + u * strip, f_src, bytes, full(s));
+      }
+      __syncwarp();
+      ++ahead;
+      f_stage = f_stage + 1 == D ? 0 : f_stage + 1;
+      --f_left;
+      f_key += f_step * kKT;
+      if (++f_batch == 16) place();
+    };
+    uint32_t last_un = 0;  // the unit whose results this warp has in shared memory, plus one
+    for (uint32_t un = 0;; ++un) {
+      if (!ok || !wait_warp(u_full(un), (un / kUnits) & 1u)) break;
+      const Unit4 &us = units[un % kUnits];
+      if (!us.valid) break;
+      // as far ahead as the ring of units goes (this unit is there: its first tile is not missed)
+#pragma unroll 1
+      for (int k = 0; k < D && ahead < D; ++k) fetch(un + kUnits);
+      // the warps from n0 % NW on have its tiles; the others go on to the next unit
+      const int rank = (warp + NW - static_cast<uint32_t>(us.n0) % NW) % NW;
+      const int parts = us.alone ? 1 : min(NW, us.stop - us.tile), step = us.alone ? 1 : NW;
+      if (rank >= parts) {
+        if (lane == 0) mbar_arrive(wrote(un));
+        continue;
+      }
+      const Unit4 u = us;
+      // this thread's columns of query tile n: rows 8 n + 2 t4 and the next
+      uint32_t qop[P][C::qreg ? NC : 1][4];
+      float o[NQ][2 * NC][4], z[NQ][G][2], qs[NQ][G][2], m[NQ][2], l[NQ][2], cw[NQ][2], lim_s[NQ][2], top_w[NQ][2], ke[NQ][2];
+      int vis[NQ][2];
+      uint8_t *const qmem = smem + C::q_off + warp * C::q_warp;
 #pragma unroll
-        for (int k = 0; k < G; ++k) {
-          float acc[NQ][4];
+      for (int n = 0; n < NQ; ++n) {
+        float sum[G], k;
+        if constexpr (C::qreg) {
+          make_queries<NC, CPG, NQ, F32>(p, u, n, qop, sum, k);
+        } else {
+          uint32_t op[P][NC][4];
+          make_queries<NC, CPG, NQ, F32>(p, u, n, op, sum, k);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+          for (int part = 0; part < P; ++part)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+            for (int c = 0; c < NC; ++c)
+              *reinterpret_cast<uint4 *>(qmem + (((part * NQ + n) * NC + c) * 32 + lane) * 16) =
+                  make_uint4(op[part][c][0], op[part][c][1], op[part][c][2], op[part][c][3]);
+        }
 #pragma unroll
-          for (int c = k * CPG; c < (k + 1) * CPG && c < NC; ++c) {
+        for (int e = 0; e < 2; ++e) {
+          const int from = 4 * (2 * t4 + e);
+          ke[n][e] = __shfl_sync(0xFFFFFFFFu, k, from);
+#pragma unroll
+          for (int j = 0; j < G; ++j) qs[n][j][e] = __shfl_sync(0xFFFFFFFFu, sum[j], from);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int k = 0; k < 2 * NC; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][k][e] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * n + 2 * t4 + e;
+          m[n][e] = -INFINITY;
+          l[n][e] = top_w[n][e] = 0.0f;
+          cw[n][e] = 1.0f;
+          lim_s[n][e] = kTop / 256.0f;
+          vis[n][e] = row < u.rows ? min(u.all + row / u.g, u.end) : 0;
+#pragma unroll
+          for (int k = 0; k < G; ++k) z[n][k][e] = 0.0f;
+        }
+      }
+#pragma unroll 1
+      for (int kt = u.tile + rank; kt < u.stop; kt += step) {
+        const int s = warp * D + stage;
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(full(s), parity)) && !(ok = wait_warp(full(s), parity))) break;
+        const int k0 = kt * kKT;
+        const uint8_t *const at = smem + s * C::stage;
+        const uint32_t have = here >> (2 * stage) & 3u;
+        // some row misses some key of the tile
+        const bool guard = k0 + kKT > u.all || have != 3u;
+        float sc[NQ][2][4];
+        uint32_t vp[2][2][G];  // value parameters of rows g8 and g8 + 8 of the strips
+#pragma unroll
+        for (int w2 = 0; w2 < 2; ++w2) {
+          const uint8_t *const src = at + w2 * strip;
+          uint32_t kw[2][NC], kp[2][G];
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            load_words<NC>(kw[w], src + (32 * w + lane) * 4 * NC);
+            if constexpr (NC <= 4) {
+              load_words<G>(kp[w], src + 512 * NC + (8 * w + g8) * 4 * G);
+              load_words<G>(vp[w2][w], src + 512 * NC + 64 * G + (8 * w + g8) * 4 * G);
+            } else {
+#pragma unroll
+              for (int k = 0; k < G; ++k) {
+                const int kk = min(k, p.c.ng - 1);  // (a chunk of padding has no group: its codes are zeros)
+                kp[w][k] = reinterpret_cast<const uint32_t *>(src + 512 * NC)[(8 * w + g8) * p.c.ng + kk];
+                vp[w2][w][k] = reinterpret_cast<const uint32_t *>(src + 512 * NC)[(16 + 8 * w + g8) * p.c.ng + kk];
+              }
+            }
+          }
+          if (guard) {
+            branch();
+            // rows behind the last key may hold anything
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const bool in = (have >> w2 & 1u) && k0 + 16 * w2 + 8 * w + g8 < u.end;
+#pragma unroll
+              for (int k = 0; k < G; ++k)
+                if (!in) kp[w][k] = vp[w2][w][k] = 0u;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            float acc[NQ][4];
+#pragma unroll
+            for (int c = k * CPG; c < (k + 1) * CPG && c < NC; ++c) {
+              uint32_t lo[4], hi[4];
+              operands<F32>(kw[0][c], lo);
+              operands<F32>(kw[1][c], hi);
+#pragma unroll
+              for (int n_ = 0; n_ < NQ; ++n_)
+#pragma unroll
+                for (int part = 0; part < P; ++part) {
+                  uint32_t b[4];
+                  if constexpr (C::qreg) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) b[j] = qop[part][c][j];
+                  } else {
+                    load_words<4>(b, qmem + (((part * NQ + n_) * NC + c) * 32 + lane) * 16);
+                  }
+                  mma(c == k * CPG && part == 0, acc[n_], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+                  mma(false, acc[n_], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              float zp = low_half(kp[w][k]);
+              if constexpr (F32) zp -= C::centre;
+              const float ks = __uint_as_float(kp[w][k] & 0xFFFF0000u);
+#pragma unroll
+              for (int n_ = 0; n_ < NQ; ++n_)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float t = fmaf(-zp, qs[n_][k][e], acc[n_][2 * w + e]);
+                  float &y = sc[n_][w2][2 * w + e];
+                  y = k == 0 ? ks * t : fmaf(ks, t, y);
+                }
+            }
+          }
+        }
+        // weights
+        float most_s = 0.0f;  // largest scale of a value
+#pragma unroll
+        for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < G; ++k) most_s = fmaxf(most_s, __uint_as_float(vp[w2][half][k]));
+        uint32_t b[NQ][2][G][2][P];
+#pragma unroll
+        for (int n_ = 0; n_ < NQ; ++n_) {
+          uint32_t gone = 0;  // keys that the rows do not see
+          if (guard) {
+            branch();
+#pragma unroll
+            for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = k0 + 16 * w2 + 8 * (e >> 1) + g8;
+                if (key >= vis[n_][e & 1] || !(have >> w2 & 1u)) {
+                  sc[n_][w2][e] = -INFINITY;
+                  gone |= 1u << (4 * w2 + e);
+                }
+              }
+          }
+          float top[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            top[e] = fmaxf(fmaxf(sc[n_][0][e], sc[n_][0][2 + e]), fmaxf(sc[n_][1][e], sc[n_][1][2 + e])) * ke[n_][e];
+          // A row's maximum moves on by more than kRescale, or the scale of some
+          // value is so large that a weight could leave fp16's range.
+          const bool move = __any_sync(0xFFFFFFFFu, top[0] > m[n_][0] + kRescale || top[1] > m[n_][1] + kRescale ||
+                                                        most_s > lim_s[n_][0] || most_s > lim_s[n_][1]);
+          float f[2] = {1.0f, 1.0f};
+          if (move) {
+            branch();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float t = column_max(top[e]);
+              if (t > m[n_][e] + kRescale) {
+                f[e] = ex2(m[n_][e] - t);
+                m[n_][e] = t;
+                l[n_][e] *= f[e];
+                top_w[n_][e] *= f[e];
+              }
+            }
+          }
+          float w[2][4];
+#pragma unroll
+          for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float mm = m[n_][e & 1] == -INFINITY ? 0.0f : m[n_][e & 1];
+              w[w2][e] = ex2(fmaf(sc[n_][w2][e], ke[n_][e & 1], -mm));
+              l[n_][e & 1] += w[w2][e];
+            }
+          if (move) {
+            branch();
+            // c anew: the largest product so far to [2^4, 2^5)
+            float most[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int k = 0; k < G; ++k)
+                  if (!(gone >> (4 * w2 + e) & 1u))  // (2^-10: scales up to 2^125)
+                    most[e & 1] = fmaxf(most[e & 1], w[w2][e] * 0x1p-10f * __uint_as_float(vp[w2][e >> 1][k] & 0xFFFF0000u));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float t = fmaxf(column_max(most[e]), top_w[n_][e]);
+              top_w[n_][e] = t;
+              int turn = 0;  // log2 of what c moves by
+              if (t > 0.0f) {
+                const int old = static_cast<int>(__float_as_uint(cw[n_][e]) >> 23);  // biased exponents
+                const int now = max(5, min(248 - static_cast<int>(__float_as_uint(t) >> 23), 249));
+                turn = now - old;
+                cw[n_][e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+                lim_s[n_][e] = __uint_as_float(static_cast<uint32_t>(min(261 - now, 254)) << 23);  // kTop / 2^8 / c
+              }
+              const float f0 = f[e] * pow2i(turn / 2), f1 = pow2i(turn - turn / 2);
+#pragma unroll
+              for (int k = 0; k < G; ++k) z[n_][k][e] = z[n_][k][e] * f0 * f1;
+#pragma unroll
+              for (int k = 0; k < 2 * NC; ++k) {
+                o[n_][k][e] = o[n_][k][e] * f0 * f1;
+                o[n_][k][2 + e] = o[n_][k][2 + e] * f0 * f1;
+              }
+            }
+          }
+#pragma unroll
+          for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[w2][e] *= cw[n_][e & 1];
+          float ws[2][G][4];
+#pragma unroll
+          for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+            for (int k = 0; k < G; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                ws[w2][k][e] = w[w2][e] * __uint_as_float(vp[w2][e >> 1][k] & 0xFFFF0000u);
+          if (guard) {
+            branch();
+            // not even 0 * NaN of a key that is not seen
+#pragma unroll
+            for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (gone >> (4 * w2 + e) & 1u)
+#pragma unroll
+                  for (int k = 0; k < G; ++k) ws[w2][k][e] = 0.0f;
+          }
+#pragma unroll
+          for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+            for (int k = 0; k < G; ++k)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const float w0 = ws[w2][k][2 * half], w1 = ws[w2][k][2 * half + 1];
+                float zp = low_half(vp[w2][half][k]);
+                if constexpr (F32) zp -= C::centre;
+                z[n_][k][0] = fmaf(w0, zp, z[n_][k][0]);
+                z[n_][k][1] = fmaf(w1, zp, z[n_][k][1]);
+                const uint32_t hi = half2_of(w0, w1);
+                b[n_][w2][k][half][0] = transpose8(hi);
+                if constexpr (F32)
+                  b[n_][w2][k][half][P - 1] = transpose8(half2_of(w0 - low_half(hi), w1 - low_half(hi >> 16)));
+              }
+        }
+        uint32_t vw[2][2][NC];
+#pragma unroll
+        for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            load_words<NC>(vw[w2][half], at + w2 * strip + 256 * NC + (32 * half + lane) * 4 * NC);
+        __syncwarp();
+        --ahead;
+        if (++stage == D) {
+          stage = 0;
+          parity ^= 1u;
+        }
+        fetch(un + kUnits);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float acc[NQ][2][4];
+#pragma unroll
+          for (int w2 = 0; w2 < 2; ++w2) {
             uint32_t lo[4], hi[4];
-            operands<F32>(kw[0][c], lo);
-            operands<F32>(kw[1][c], hi);
+            operands<F32>(vw[w2][0][c], lo);
+            operands<F32>(vw[w2][1][c], hi);
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int n_ = 0; n_ < NQ; ++n_)
 #pragma unroll
-              for (int part = 0; part < C::P; ++part) {
-                const uint4 b = *reinterpret_cast<const uint4 *>(smem + (((part * NQ + n) * NC + c) * 32 + lane) * 16);
-                mma(acc[n], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                mma(acc[n], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+              for (int part = 0; part < P; ++part) {
+                const uint32_t b0 = b[n_][w2][c / CPG][0][part], b1 = b[n_][w2][c / CPG][1][part];
+                mma(w2 == 0 && part == 0, acc[n_][0], lo[0], lo[1], hi[0], hi[1], b0, b1);
+                mma(w2 == 0 && part == 0, acc[n_][1], lo[2], lo[3], hi[2], hi[3], b0, b1);
               }
           }
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const float zp = low_half(kp[u][w][k]) - C::centre, sc = __uint_as_float(kp[u][w][k] & 0xFFFF0000u);
+          for (int n_ = 0; n_ < NQ; ++n_)
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                s[n][u][2 * w + e] = fmaf(sc, fmaf(-zp, qs[n][k][e], acc[n][2 * w + e]), s[n][u][2 * w + e]);
-          }
+              for (int e = 0; e < 4; e += 2)
+                unpack2(add2(pack2(o[n_][2 * c + k][e], o[n_][2 * c + k][e + 1]), pack2(acc[n_][k][e], acc[n_][k][e + 1])),
+                        o[n_][2 * c + k][e], o[n_][2 * c + k][e + 1]);
         }
       }
-      // weights
-      uint32_t b[NQ][2][G][2][C::P];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        float top[2] = {-INFINITY, -INFINITY};
-        uint32_t gone = 0;  // keys that the rows do not see
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = k0 + 16 * u + 8 * (e >> 1) + g8;
-            float y = s[n][u][e] * ke[n][e & 1];
-            if (key >= min(vis[n][e & 1], lim[u])) {
-              y = -INFINITY;
-              gone |= 1u << (4 * u + e);
-            }
-            s[n][u][e] = y;
-            top[e & 1] = fmaxf(top[e & 1], y);
-          }
-        float f[2] = {1.0f, 1.0f};
-        bool move = false;
-        if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] + kRescale || top[1] > m[n][1] + kRescale)) {
-          move = true;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float t = column_max(top[e]);
-            if (t > m[n][e] + kRescale) {
-              f[e] = ex2(m[n][e] - t);
-              m[n][e] = t;
-              l[n][e] *= f[e];
-              top_w[n][e] *= f[e];
-            }
-          }
-        }
-        float w[2][G][4], most[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float ref = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1];
-            const float pr = ex2(s[n][u][e] - ref);
-            l[n][e & 1] += pr;
-            const float pc = pr * cw[n][e & 1];
-#pragma unroll
-            for (int k = 0; k < G; ++k) {
-              float t = pc * __uint_as_float(vp[u][e >> 1][k] & 0xFFFF0000u);
-              if (gone >> (4 * u + e) & 1u) t = 0.0f;
-              w[u][k][e] = t;
-              most[e & 1] = fmaxf(most[e & 1], t);
-            }
-          }
-        if (__any_sync(0xFFFFFFFFu, move || most[0] > kTop || most[1] > kTop)) {
-          // c anew: the largest weight so far to [2^7, 2^8)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float t = fmaxf(column_max(most[e]), top_w[n][e]);
-            float turn = 1.0f;
-            if (t > 0.0f) {
-              const int old = static_cast<int>(__float_as_uint(cw[n][e]) >> 23);  // biased exponents
-              const int E = old + 7 - (static_cast<int>(__float_as_uint(t) >> 23) - 127);
-              const float cn = __uint_as_float(static_cast<uint32_t>(max(2, min(min(E, old + 100), 252))) << 23);
-              turn = cn / cw[n][e];
-              cw[n][e] = cn;
-            }
-            top_w[n][e] = t * turn;
-            f[e] *= turn;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int k = 0; k < G; ++k)
-#pragma unroll
-                for (int j = e; j < 4; j += 2) w[u][k][j] *= turn;
-#pragma unroll
-            for (int k = 0; k < G; ++k) z[n][k][e] *= f[e];
-#pragma unroll
-            for (int k = 0; k < 2 * NC; ++k) {
-              o[n][k][e] *= f[e];
-              o[n][k][2 + e] *= f[e];
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int k = 0; k < G; ++k)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float w0 = w[u][k][2 * half], w1 = w[u][k][2 * half + 1];
-              const float zp = low_half(vp[u][half][k]) - C::centre;
-              z[n][k][0] = fmaf(w0, zp, z[n][k][0]);
-              z[n][k][1] = fmaf(w1, zp, z[n][k][1]);
-              const uint32_t hi = half2_of(w0, w1);
-              b[n][u][k][half][0] = transpose8(hi);
-              if constexpr (F32)
-                b[n][u][k][half][C::P - 1] = transpose8(half2_of(w0 - low_half(hi), w1 - low_half(hi >> 16)));
-            }
-      }
-      uint32_t vw[2][2][NC];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (lim[u] > k0 + 16 * u) {
-            load_words<NC>(vw[u][half], reinterpret_cast<const uint32_t *>(src[u] + 256 * NC) + (32 * half + lane) * NC);
-          } else {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) vw[u][half][c] = 0u;
-          }
-        }
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float acc[NQ][2][4];
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[n][e >> 2][e & 3] = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t lo[4], hi[4];
-          operands<F32>(vw[u][0][c], lo);
-          operands<F32>(vw[u][1][c], hi);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int part = 0; part < C::P; ++part) {
-              const uint32_t b0 = b[n][u][c / CPG][0][part], b1 = b[n][u][c / CPG][1][part];
-              mma(acc[n][0], lo[0], lo[1], hi[0], hi[1], b0, b1);
-              mma(acc[n][1], lo[2], lo[3], hi[2], hi[3], b0, b1);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[n][2 * c + (e >> 2)][e & 3] += acc[n][e >> 2][e & 3];
-      }
-    }
+      if (!ok) break;
 
-    // the warps' results meet in shared memory
+      // This warp's result to shared memory, once its last one there has been joined
+      // to the others' (sure, if the ring of units has gone round since); one that is
+      // the whole unit's goes out from here.
+      const bool only = parts == 1;
+      if (!only) {
+        if (last_un > 0 && un + 1 - last_un < kUnits &&
+            !(ok = wait_warp(joined(last_un - 1), ((last_un - 1) / kUnits) & 1u)))
+          break;
+        last_un = un + 1;
+      }
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+      for (int n_ = 0; n_ < NQ; ++n_)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 8 * n + 2 * t4 + e;
-        const float sum = column_sum(l[n][e]), inv = 1.0f / cw[n][e];
-        if (g8 == 0) reinterpret_cast<float2 *>(smem + C::ml_off)[warp * C::R + row] = make_float2(m[n][e], sum);
-        float *const out = reinterpret_cast<float *>(smem + C::o_off) + (warp * C::R + row) * C::HD;
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * n_ + 2 * t4 + e;
+          const float sum = column_sum(l[n_][e]);
+          float inv = 1.0f / cw[n_][e];
+          if (only && u.whole) inv *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+          if (g8 == 0) {
+            if (!only)
+              reinterpret_cast<float2 *>(smem + C::ml_off)[warp * C::R + row] = make_float2(m[n_][e], sum);
+            else if (!u.whole && row < u.rows)
+              p.parts.ml[static_cast<int64_t>(u.slot) * p.parts.rows + row] = make_float2(m[n_][e], sum);
+          }
+          float *const out = reinterpret_cast<float *>(smem + C::o_off) + (warp * C::R + row) * C::OS;
 #pragma unroll
-        for (int k = 0; k < G; ++k) z[n][k][e] = column_sum(z[n][k][e]);
-        auto put = [&](float v, float zz) { return fmaf(v, C::unit, -zz) * inv; };
+          for (int k = 0; k < G; ++k) z[n_][k][e] = column_sum(z[n_][k][e]);
+          auto put = [&](float v, float zz) { return fmaf(v, C::unit, -zz) * inv; };
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float zz = z[n][c / CPG][e];
-          // dimensions 4 g8 .. + 3 of the chunk: rows g8 and g8 + 8 of two products
-          *reinterpret_cast<float4 *>(out + 32 * c + 4 * g8) =
-              make_float4(put(o[n][2 * c][e], zz), put(o[n][2 * c][2 + e], zz),
-                          put(o[n][2 * c + 1][e], zz), put(o[n][2 * c + 1][2 + e], zz));
+          for (int c = 0; c < NC; ++c) {
+            const float zz = z[n_][c / CPG][e];
+            // dimensions 4 g8 .. + 3 of the chunk: rows g8 and g8 + 8 of two products
+            const float4 v = make_float4(put(o[n_][2 * c][e], zz), put(o[n_][2 * c][2 + e], zz),
+                                         put(o[n_][2 * c + 1][e], zz), put(o[n_][2 * c + 1][2 + e], zz));
+            const int d = 32 * c + 4 * g8;
+            if (!only)
+              *reinterpret_cast<float4 *>(out + d) = v;
+            else if (row < u.rows && d < hd)
+              store_row4(p, u, row, d, v);
+          }
         }
-      }
-    __syncthreads();
-    const bool whole = tile == 0 && stop == ntile;
-    const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);
-    for (int e = tid; e < rows * (C::HD / 4); e += kThreads) {
-      const int row = e / (C::HD / 4), d = 4 * (e - row * (C::HD / 4));
-      if (d >= hd) continue;
-      const float2 *const ml = reinterpret_cast<const float2 *>(smem + C::ml_off) + row;
-      float M = -INFINITY, L = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * C::R].x);
-      const float ref = M == -INFINITY ? 0.0f : M;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        // (zeros of a warp that saw no key count nothing; a NaN makes the row NaN,
-        // however small its warp's factor is)
-        const float f = ex2(ml[w * C::R].x - ref);
-        const float4 t = *reinterpret_cast<const float4 *>(smem + C::o_off + ((w * C::R + row) * C::HD + d) * 4);
-        L = fmaf(f, ml[w * C::R].y, L);
-        acc.x = fmaf(f, t.x, acc.x);
-        acc.y = fmaf(f, t.y, acc.y);
-        acc.z = fmaf(f, t.z, acc.z);
-        acc.w = fmaf(f, t.w, acc.w);
-      }
-      if (whole) {
-        const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
-        const int t = row / g, hq = row - t * g;
-        store_y4(p.a.y, (static_cast<int64_t>(q.q0 + t0 + t) * p.a.n_head + head0 + hq) * hd + d,
-                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.a.y_bf16);
-      } else {
-        const int64_t base = static_cast<int64_t>(slot) * p.parts.rows + row;
-        if (d == 0) p.parts.ml[base] = make_float2(M, L);
-        *reinterpret_cast<float4 *>(p.parts.o + base * hd + d) = acc;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wrote(un));
+    }
+    // copies still landing (after an abort; otherwise all have been used)
+    for (; ahead > 0; --ahead) {
+      mbar_wait_bounded(full(warp * D + stage), parity, p.status);
+      if (++stage == D) {
+        stage = 0;
+        parity ^= 1u;
       }
     }
-    __syncthreads();
-    if (tid == 0 && tile == 0 && !whole)
-      p.parts.open[blockIdx.x] = AttnOpen{q.q0 + t0, nt, v, sched_last(p.sc, run, x0, ntile)};
+    zero_loose_rows(p.a, p.sc, blockIdx.x, gridDim.x, 32 * NW);
   }
-  zero_loose_rows(p.a, p.sc, blockIdx.x, gridDim.x, kThreads);
 }
 
 template <int NC, int CPG, int NQ, bool F32>
 cudaError_t run_form(const Attn4 &p, int workers, cudaStream_t s) {
   auto kern = attn4_rows_kernel<NC, CPG, NQ, F32>;
   constexpr int smem = Form<NC, CPG, NQ, F32>::bytes;
-  static_assert(smem <= 227 * 1024, "shared memory");
   const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(workers), dim3(kThreads), smem, s, p);
+  return launch_pdl(kern, dim3(workers), dim3(Form<NC, CPG, NQ, F32>::threads), smem, s, p);
 }
 
 template <int NC, int CPG, int NQ>
@@ -592,7 +910,7 @@ AttnPlan attn4_rows_plan(const Kv4 &c, int64_t T, int n_head, int R) {
   p.U = p.rows / p.gsub;
   p.KT = kKT;
   p.fixed = 4 * kKT;
-  p.min_run = kWarps * kKT;
+  p.min_run = 4 * kKT;
   p.whole = kWholeKeys;
   p.workers = sm_count();
   return p;

@@ -16,7 +16,7 @@ and zero points apart, so the errors go by s (code + |zp|), named size:
   weight   relative e = expm1(es) + 2^-21 (the exponential's own error)
   weight times scale, to 16 bits: 2^-11 with bf16 queries, two parts (2^-22)
            with fp32 ones; below fp16's normal range half a step of 2^-24,
-           where the largest product of the row is at least 2^7: 2^-32 of it
+           where the largest product of the row is at least 2^4: 2^-29 of it
   result   sum_j p_j |v_j| (e_j + sum_i p_i e_i) for the weights above and below
            the line, sum_j p_j size_j 2 (L + 64) u for the sums, sum_j p_j s_j
            code_j (rounding) for the products.
@@ -167,7 +167,7 @@ def attend(q, keys, vals, group, visible, scale, q32):
         p /= p.sum(axis=1, keepdims=True)
         e = np.expm1(es) + 2.0 ** -21
         mean_e = (p * e).sum(axis=1, keepdims=True)
-        small = 2.0 ** -32 * (p[:, :, None] * spread(vals[2])[None, :, g]).max(axis=1) * 15 * len(k)
+        small = 2.0 ** -29 * (p[:, :, None] * spread(vals[2])[None, :, g]).max(axis=1) * 15 * len(k)
         y[rows, h] = p @ v[:, g]
         b[rows, h] = ((p * (e + mean_e)) @ np.abs(v[:, g]) + p @ vsize[:, g] * (2 * (L + 64) * U)
                       + p @ vcode[:, g] * low + small + 1e-30)

@@ -343,10 +343,10 @@ def test_attend_unseen_nans_do_not_matter(dev, dtype, nh, nkv, n):
     # The power of two that holds a row's weights in 16 bits goes by the largest
     # weight times scale of all groups, so without a group's it may be another one:
     # parts below fp16's normal range are then rounded elsewhere, each by at most
-    # 2^-32 of the largest, times a code of at most 15; and the sums of fp32 (2 u a
+    # 2^-29 of the largest, times a code of at most 15; and the sums of fp32 (2 u a
     # term) round those other parts.
     codes, zp, sc = ref.unpack(data, hd, 32, S)[1]
-    near = L * 2.0 ** -32 * 15 * sc.max() + 2 * (L + 64) * 2 * ref.U * ((15 + np.abs(zp)) * sc).max()
+    near = L * 2.0 ** -29 * 15 * sc.max() + 2 * (L + 64) * 2 * ref.U * ((15 + np.abs(zp)) * sc).max()
     for j in (0, 100, L - n, L - 1):
         first = max(0, j - (L - n))  # the first query that sees row j
         for part in range(2):
