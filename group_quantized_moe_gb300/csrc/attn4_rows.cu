@@ -7,23 +7,26 @@
 //   S[key, q] = sum_g s_g (sum_d code q' - zp_g sum_d q'),   q' = q 2^E
 //   O[dim, q] = sum_key (p s_g) code,   Z[g, q] = sum_key (p s_g) zp_g
 //   y = (O - Z) / l
-// A masked word of the cache is an operand register: a code in bits 4 to 7 of
-// an fp16 is the number code 2^-20, so that eight codes cost seven instructions
-// (three shifts, four masks) and no conversion.  (In bits 0 to 3 two of the
-// shifts could go, but the tensor cores line products up by the operands'
-// exponents, without the leading zeros of a subnormal: sums are then cut off at
-// 2^-19 of them, with the codes four bits higher at 2^-27.)  Keys and
-// dimensions go to the operands' rows (16), query rows to their columns (8):
-// few query rows waste little, and the scores of one product are, transposed by
-// movmatrix, the weights' operand of the next.
+// A masked word of the cache is an operand register: a code in the low four
+// bits of an fp16 is the number code 2^-24, and one four bits higher 16 times
+// that, so that eight codes cost five instructions and no conversion.  What is
+// odd about the factors is put right once: queries of odd places are divided by
+// 16 where they are made, odd rows of O when a unit ends.  (The tensor cores line
+// products up by the operands' exponents, without the leading zeros of a
+// subnormal, so sums with codes in the lowest bits are cut off at about 2^-19 of
+// the sum of their magnitudes: far below the weights' rounding, but not for fp32
+// queries, which take the codes as whole numbers.)  Keys and dimensions go to
+// the operands' rows (16), query rows to their columns (8): few query rows waste
+// little, and the scores of one product are, transposed by movmatrix, the
+// weights' operand of the next.
 //
 // Roundings: q' is fp16 with E such that the row's largest |q'| lies in
-// [2^14, 2^15): bf16 queries are exact down to 2^-29 of the largest; fp32 ones
+// [2^14, 2^15): bf16 queries are exact down to 2^-25 of the largest; fp32 ones
 // are split into two fp16.  The weights p s_g c are rounded to fp16 (2^-11;
 // fp32 queries: split in two as well), c a power of two per query row that
 // keeps them below 2^15 and moves when the maximum moves or the scale of a
-// value is so large that a product could leave the range.  The tensor cores cut their sums off instead of rounding,
-// so they run over 32 keys only and are added up in fp32.
+// value is so large that a product could leave the range.  The tensor cores'
+// sums of weights run over 32 keys and are added up in fp32.
 #include <cuda_fp16.h>
 
 #include <cstdint>
@@ -145,8 +148,8 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
 }
 
 // The four operand registers of a word of codes: its nibbles (0, 4), (1, 5),
-// (2, 6), (3, 7), each as code 2^-20, or with fp32 queries as code - 8: sums of
-// codes that are never negative grow, and what the tensor cores cut off them is
+// (2, 6), (3, 7), each as code 2^-24 (odd ones 16 times that), or with fp32
+// queries as code - 8: sums of codes that are never negative grow, and what the tensor cores cut off them is
 // then no longer small against a result in which most of them cancel (1.7e-6 of
 // its norm for 300 tokens of 2500 keys; centred 2.6e-7).
 template <bool F32>
@@ -161,9 +164,9 @@ __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) {
     return;
   }
   const uint32_t x = w >> 8;
-  a[0] = (w << 4) & 0x00F000F0u;
+  a[0] = w & 0x000F000Fu;
   a[1] = w & 0x00F000F0u;
-  a[2] = (x << 4) & 0x00F000F0u;
+  a[2] = x & 0x000F000Fu;
   a[3] = x & 0x00F000F0u;
 }
 
@@ -172,8 +175,8 @@ __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) {
 template <int NC, int CPG, int NQ, bool F32>
 struct Form {
   static constexpr int G = (NC + CPG - 1) / CPG, R = 8 * NQ, P = F32 ? 2 : 1, HD = 32 * NC;
-  // an operand of code c is (c - centre) / unit
-  static constexpr float unit = F32 ? 1.0f : 0x1p20f, centre = F32 ? 8.0f : 0.0f;
+  // an operand of code c is (c - centre) / unit, at odd places odd times that
+  static constexpr float unit = F32 ? 1.0f : 0x1p24f, centre = F32 ? 8.0f : 0.0f, odd = F32 ? 1.0f : 16.0f;
   // warps that multiply, and one that loads: three to a scheduler leave a thread
   // 168 registers, two 255
   static constexpr int warps = NQ == 1 && NC <= 4 && !(F32 && NC == 4 && CPG == 1) ? 11 : 7, threads = 32 * (warps + 1);
@@ -255,7 +258,8 @@ __device__ __forceinline__ void make_queries(const Attn4 &p, const Unit4 &u, int
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      op[0][c][j] = half2_of(x[c][j], x[c][j + 4]);
+      const float part = j & 1 ? 1.0f / C::odd : 1.0f;
+      op[0][c][j] = half2_of(x[c][j] * part, x[c][j + 4] * part);
       if constexpr (F32)
         op[C::P - 1][c][j] = half2_of(x[c][j] - low_half(op[0][c][j]), x[c][j + 4] - low_half(op[0][c][j] >> 16));
     }
@@ -840,13 +844,13 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
           float *const out = reinterpret_cast<float *>(smem + C::o_off) + (warp * C::R + row) * C::OS;
 #pragma unroll
           for (int k = 0; k < G; ++k) z[n_][k][e] = column_sum(z[n_][k][e]);
-          auto put = [&](float v, float zz) { return fmaf(v, C::unit, -zz) * inv; };
+          auto put = [&](float v, float zz, float odd) { return fmaf(v, C::unit / odd, -zz) * inv; };
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float zz = z[n_][c / CPG][e];
             // dimensions 4 g8 .. + 3 of the chunk: rows g8 and g8 + 8 of two products
-            const float4 v = make_float4(put(o[n_][2 * c][e], zz), put(o[n_][2 * c][2 + e], zz),
-                                         put(o[n_][2 * c + 1][e], zz), put(o[n_][2 * c + 1][2 + e], zz));
+            const float4 v = make_float4(put(o[n_][2 * c][e], zz, 1.0f), put(o[n_][2 * c][2 + e], zz, C::odd),
+                                         put(o[n_][2 * c + 1][e], zz, 1.0f), put(o[n_][2 * c + 1][2 + e], zz, C::odd));
             const int d = 32 * c + 4 * g8;
             if (!only)
               *reinterpret_cast<float4 *>(out + d) = v;

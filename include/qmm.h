@@ -492,7 +492,7 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
  * Arithmetic: the products multiply codes, which fp16 holds exactly, on the
  * tensor cores, and scales and zero points are applied in fp32; scores, maxima,
  * sums and results are fp32.  A query row is scaled by a power of two to fp16
- * (bf16 rows: exact for elements down to 2^-29 of the row's largest; fp32 rows:
+ * (bf16 rows: exact for elements down to 2^-25 of the row's largest; fp32 rows:
  * in two parts, 2^-22; an element of 2^114 or more counts as infinite).  With
  * bf16 queries each weight times its value's scale is rounded to 16 bits
  * (2^-11 in fp16; not in the sum it is divided by), whatever y_dtype is; with
