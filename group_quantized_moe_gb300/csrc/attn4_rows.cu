@@ -43,8 +43,9 @@ namespace qmm {
 namespace {
 
 constexpr int kKT = 32;           // keys of a step: two strips
-constexpr int kUnits = 16;          // units in the ring between the loading warp and the others
-constexpr int kAlone = 6;            // tiles of a unit that one warp takes alone
+constexpr int kUnits = 32;           // units in the ring between the loading warp and the others
+constexpr int kAlone = 12;           // tiles of a unit that one warp takes alone (750 requests of
+                                    // 200 keys 87 us; 181 where eleven warps share seven tiles)
 constexpr float kRescale = 8.0f;  // log2 of the growth of the maximum that is let pass
 constexpr float kTop = 32768.0f;  // of a weight
 
@@ -170,19 +171,21 @@ __device__ __forceinline__ void operands(uint32_t w, uint32_t (&a)[4]) {
   a[3] = x & 0x00F000F0u;
 }
 
-// NC: chunks of 32 dimensions; CPG: chunks of a group; NQ: tiles of eight query
-// rows; F32: the queries' type (else bf16).
-template <int NC, int CPG, int NQ, bool F32>
+// NC: chunks of 32 dimensions; CPG: chunks of a group; F32: the queries' type
+// (else bf16).  A unit has up to eight query rows: one tile of columns.  (Two tiles
+// share the codes' unpacking but leave a thread registers for seven warps instead
+// of eleven: 32 drafted tokens a head 82 us either way.)
+template <int NC, int CPG, bool F32>
 struct Form {
-  static constexpr int G = (NC + CPG - 1) / CPG, R = 8 * NQ, P = F32 ? 2 : 1, HD = 32 * NC;
+  static constexpr int G = (NC + CPG - 1) / CPG, R = 8, P = F32 ? 2 : 1, HD = 32 * NC;
   // an operand of code c is (c - centre) / unit, at odd places odd times that
   static constexpr float unit = F32 ? 1.0f : 0x1p24f, centre = F32 ? 8.0f : 0.0f, odd = F32 ? 1.0f : 16.0f;
   // warps that multiply, and one that loads: three to a scheduler leave a thread
   // 168 registers, two 255
-  static constexpr int warps = NQ == 1 && NC <= 4 && !(F32 && NC == 4 && CPG == 1) ? 11 : 7, threads = 32 * (warps + 1);
+  static constexpr int warps = NC <= 4 && !(F32 && NC == 4 && CPG == 1) ? 11 : 7, threads = 32 * (warps + 1);
   static constexpr int stage = 2 * (512 * NC + 128 * G);  // a tile of the cache
-  static constexpr bool qreg = NQ * P == 1 && NC <= 4;    // queries in registers, else in shared memory
-  static constexpr int q_warp = qreg ? 0 : P * NQ * NC * 512, q_bytes = warps * q_warp;
+  static constexpr bool qreg = !F32 && NC <= 4;    // queries in registers, else in shared memory
+  static constexpr int q_warp = qreg ? 0 : P * NC * 512, q_bytes = warps * q_warp;
   static constexpr int OS = HD + 4;  // floats between rows of results (four lanes store one each)
   static constexpr int o_bytes = warps * R * OS * 4, ml_bytes = warps * R * 8;
   static constexpr int fixed = q_bytes + o_bytes + ml_bytes + kUnits * 64 + 2048;
@@ -206,13 +209,13 @@ struct __align__(16) Unit4 {
 };
 
 // A query row's elements as operands: lane 4 col + t holds dimensions
-// 32 c + 8 t + j of row `col` of tile n, in pairs (0, 4), (1, 5), (2, 6), (3, 7).
+// 32 c + 8 t + j of row `col`, in pairs (0, 4), (1, 5), (2, 6), (3, 7).
 // ke: unit / 2^E scale log2 e, sum: by group, both of that row.
-template <int NC, int CPG, int NQ, bool F32>
-__device__ __forceinline__ void make_queries(const Attn4 &p, const Unit4 &u, int n, uint32_t (&op)[F32 ? 2 : 1][NC][4],
-                                             float (&sum)[Form<NC, CPG, NQ, F32>::G], float &ke) {
-  using C = Form<NC, CPG, NQ, F32>;
-  const int lane = threadIdx.x & 31, row = 8 * n + (lane >> 2), t4 = lane & 3, hd = p.a.head_dim;
+template <int NC, int CPG, bool F32>
+__device__ __forceinline__ void make_queries(const Attn4 &p, const Unit4 &u, uint32_t (&op)[F32 ? 2 : 1][NC][4],
+                                             float (&sum)[Form<NC, CPG, F32>::G], float &ke) {
+  using C = Form<NC, CPG, F32>;
+  const int lane = threadIdx.x & 31, row = lane >> 2, t4 = lane & 3, hd = p.a.head_dim;
   const int t = row / u.g;
   const int64_t i = static_cast<int64_t>(u.q_row + t) * p.a.q_stride + static_cast<int64_t>(u.head0 + row - t * u.g) * hd;
   float x[NC][8], top = 0.0f;
@@ -281,10 +284,10 @@ __device__ __forceinline__ void store_row4(const Attn4 &p, const Unit4 &u, int r
     *reinterpret_cast<float4 *>(p.parts.o + (static_cast<int64_t>(u.slot) * p.parts.rows + row) * hd + d) = v;
 }
 
-template <int NC, int CPG, int NQ, bool F32>
-__global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
+template <int NC, int CPG, bool F32>
+__global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
     attn4_rows_kernel(const __grid_constant__ Attn4 p) {
-  using C = Form<NC, CPG, NQ, F32>;
+  using C = Form<NC, CPG, F32>;
   constexpr int G = C::G, NW = C::warps, NS = C::stages, D = C::depth, P = C::P;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t scratch[NW + 1 + 4];
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
     uint32_t n = 0;  // the warps' turns so far
     // Short units of a long run go to one warp each: nothing to join, and others
     // run beside it.
-    const bool many = run.last - run.first >= 4 * NW * kAlone * kKT;
+    const bool many = run.last - run.first >= 2 * NW * kAlone * kKT;
     // the next unit of the run with tiles of it
     auto next_unit = [&]() {
       Unit4 u{};
@@ -519,52 +522,46 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
         continue;
       }
       const Unit4 u = us;
-      // this thread's columns of query tile n: rows 8 n + 2 t4 and the next
+      // this thread's columns: query rows 2 t4 and the next
       uint32_t qop[P][C::qreg ? NC : 1][4];
-      float o[NQ][2 * NC][4], z[NQ][G][2], qs[NQ][G][2], m[NQ][2], l[NQ][2], cw[NQ][2], lim_s[NQ][2], top_w[NQ][2], ke[NQ][2];
-      int vis[NQ][2];
+      float o[2 * NC][4], z[G][2], qs[G][2], m[2], l[2], cw[2], lim_s[2], top_w[2], ke[2];
+      int vis[2];
       uint8_t *const qmem = smem + C::q_off + warp * C::q_warp;
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
         float sum[G], k;
         if constexpr (C::qreg) {
-          make_queries<NC, CPG, NQ, F32>(p, u, n, qop, sum, k);
+          make_queries<NC, CPG, F32>(p, u, qop, sum, k);
         } else {
           uint32_t op[P][NC][4];
-          make_queries<NC, CPG, NQ, F32>(p, u, n, op, sum, k);
+          make_queries<NC, CPG, F32>(p, u, op, sum, k);
 #pragma unroll
           for (int part = 0; part < P; ++part)
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              *reinterpret_cast<uint4 *>(qmem + (((part * NQ + n) * NC + c) * 32 + lane) * 16) =
+              *reinterpret_cast<uint4 *>(qmem + ((part * NC + c) * 32 + lane) * 16) =
                   make_uint4(op[part][c][0], op[part][c][1], op[part][c][2], op[part][c][3]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int from = 4 * (2 * t4 + e);
-          ke[n][e] = __shfl_sync(0xFFFFFFFFu, k, from);
+          ke[e] = __shfl_sync(0xFFFFFFFFu, k, from);
 #pragma unroll
-          for (int j = 0; j < G; ++j) qs[n][j][e] = __shfl_sync(0xFFFFFFFFu, sum[j], from);
+          for (int j = 0; j < G; ++j) qs[j][e] = __shfl_sync(0xFFFFFFFFu, sum[j], from);
         }
-      }
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
 #pragma unroll
         for (int k = 0; k < 2 * NC; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][k][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) o[k][e] = 0.0f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = 8 * n + 2 * t4 + e;
-          m[n][e] = -INFINITY;
-          l[n][e] = top_w[n][e] = 0.0f;
-          cw[n][e] = 1.0f;
-          lim_s[n][e] = kTop / 256.0f;
-          vis[n][e] = row < u.rows ? min(u.all + row / u.g, u.end) : 0;
+          const int row = 2 * t4 + e;
+          m[e] = -INFINITY;
+          l[e] = top_w[e] = 0.0f;
+          cw[e] = 1.0f;
+          lim_s[e] = kTop / 256.0f;
+          vis[e] = row < u.rows ? min(u.all + row / u.g, u.end) : 0;
 #pragma unroll
-          for (int k = 0; k < G; ++k) z[n][k][e] = 0.0f;
+          for (int k = 0; k < G; ++k) z[k][e] = 0.0f;
         }
-      }
 #pragma unroll 1
       for (int kt = u.tile + rank; kt < u.stop; kt += step) {
         const int s = warp * D + stage;
@@ -574,7 +571,7 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
         const uint32_t have = here >> (2 * stage) & 3u;
         // some row misses some key of the tile
         const bool guard = k0 + kKT > u.all || have != 3u;
-        float sc[NQ][2][4];
+        float sc[2][4];
         uint32_t vp[2][2][G];  // value parameters of rows g8 and g8 + 8 of the strips
 #pragma unroll
         for (int w2 = 0; w2 < 2; ++w2) {
@@ -608,14 +605,12 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
           }
 #pragma unroll
           for (int k = 0; k < G; ++k) {
-            float acc[NQ][4];
+            float acc[4];
 #pragma unroll
             for (int c = k * CPG; c < (k + 1) * CPG && c < NC; ++c) {
               uint32_t lo[4], hi[4];
               operands<F32>(kw[0][c], lo);
               operands<F32>(kw[1][c], hi);
-#pragma unroll
-              for (int n_ = 0; n_ < NQ; ++n_)
 #pragma unroll
                 for (int part = 0; part < P; ++part) {
                   uint32_t b[4];
@@ -623,10 +618,10 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) b[j] = qop[part][c][j];
                   } else {
-                    load_words<4>(b, qmem + (((part * NQ + n_) * NC + c) * 32 + lane) * 16);
+                    load_words<4>(b, qmem + ((part * NC + c) * 32 + lane) * 16);
                   }
-                  mma(c == k * CPG && part == 0, acc[n_], lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
-                  mma(false, acc[n_], lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
+                  mma(c == k * CPG && part == 0, acc, lo[0], hi[0], lo[1], hi[1], b[0], b[1]);
+                  mma(false, acc, lo[2], hi[2], lo[3], hi[3], b[2], b[3]);
                 }
             }
 #pragma unroll
@@ -635,11 +630,9 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
               if constexpr (F32) zp -= C::centre;
               const float ks = __uint_as_float(kp[w][k] & 0xFFFF0000u);
 #pragma unroll
-              for (int n_ = 0; n_ < NQ; ++n_)
-#pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const float t = fmaf(-zp, qs[n_][k][e], acc[n_][2 * w + e]);
-                  float &y = sc[n_][w2][2 * w + e];
+                  const float t = fmaf(-zp, qs[k][e], acc[2 * w + e]);
+                  float &y = sc[w2][2 * w + e];
                   y = k == 0 ? ks * t : fmaf(ks, t, y);
                 }
             }
@@ -653,9 +646,7 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int k = 0; k < G; ++k) most_s = fmaxf(most_s, __uint_as_float(vp[w2][half][k]));
-        uint32_t b[NQ][2][G][2][P];
-#pragma unroll
-        for (int n_ = 0; n_ < NQ; ++n_) {
+        uint32_t b[2][G][2][P];
           uint32_t gone = 0;  // keys that the rows do not see
           if (guard) {
             branch();
@@ -664,8 +655,8 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int key = k0 + 16 * w2 + 8 * (e >> 1) + g8;
-                if (key >= vis[n_][e & 1] || !(have >> w2 & 1u)) {
-                  sc[n_][w2][e] = -INFINITY;
+                if (key >= vis[e & 1] || !(have >> w2 & 1u)) {
+                  sc[w2][e] = -INFINITY;
                   gone |= 1u << (4 * w2 + e);
                 }
               }
@@ -673,22 +664,22 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
           float top[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            top[e] = fmaxf(fmaxf(sc[n_][0][e], sc[n_][0][2 + e]), fmaxf(sc[n_][1][e], sc[n_][1][2 + e])) * ke[n_][e];
+            top[e] = fmaxf(fmaxf(sc[0][e], sc[0][2 + e]), fmaxf(sc[1][e], sc[1][2 + e])) * ke[e];
           // A row's maximum moves on by more than kRescale, or the scale of some
           // value is so large that a weight could leave fp16's range.
-          const bool move = __any_sync(0xFFFFFFFFu, top[0] > m[n_][0] + kRescale || top[1] > m[n_][1] + kRescale ||
-                                                        most_s > lim_s[n_][0] || most_s > lim_s[n_][1]);
+          const bool move = __any_sync(0xFFFFFFFFu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale ||
+                                                        most_s > lim_s[0] || most_s > lim_s[1]);
           float f[2] = {1.0f, 1.0f};
           if (move) {
             branch();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float t = column_max(top[e]);
-              if (t > m[n_][e] + kRescale) {
-                f[e] = ex2(m[n_][e] - t);
-                m[n_][e] = t;
-                l[n_][e] *= f[e];
-                top_w[n_][e] *= f[e];
+              if (t > m[e] + kRescale) {
+                f[e] = ex2(m[e] - t);
+                m[e] = t;
+                l[e] *= f[e];
+                top_w[e] *= f[e];
               }
             }
           }
@@ -697,9 +688,9 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
           for (int w2 = 0; w2 < 2; ++w2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float mm = m[n_][e & 1] == -INFINITY ? 0.0f : m[n_][e & 1];
-              w[w2][e] = ex2(fmaf(sc[n_][w2][e], ke[n_][e & 1], -mm));
-              l[n_][e & 1] += w[w2][e];
+              const float mm = m[e & 1] == -INFINITY ? 0.0f : m[e & 1];
+              w[w2][e] = ex2(fmaf(sc[w2][e], ke[e & 1], -mm));
+              l[e & 1] += w[w2][e];
             }
           if (move) {
             branch();
@@ -715,30 +706,30 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
                     most[e & 1] = fmaxf(most[e & 1], w[w2][e] * 0x1p-10f * __uint_as_float(vp[w2][e >> 1][k] & 0xFFFF0000u));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float t = fmaxf(column_max(most[e]), top_w[n_][e]);
-              top_w[n_][e] = t;
+              const float t = fmaxf(column_max(most[e]), top_w[e]);
+              top_w[e] = t;
               int turn = 0;  // log2 of what c moves by
               if (t > 0.0f) {
-                const int old = static_cast<int>(__float_as_uint(cw[n_][e]) >> 23);  // biased exponents
+                const int old = static_cast<int>(__float_as_uint(cw[e]) >> 23);  // biased exponents
                 const int now = max(5, min(248 - static_cast<int>(__float_as_uint(t) >> 23), 249));
                 turn = now - old;
-                cw[n_][e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
-                lim_s[n_][e] = __uint_as_float(static_cast<uint32_t>(min(261 - now, 254)) << 23);  // kTop / 2^8 / c
+                cw[e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+                lim_s[e] = __uint_as_float(static_cast<uint32_t>(min(261 - now, 254)) << 23);  // kTop / 2^8 / c
               }
               const float f0 = f[e] * pow2i(turn / 2), f1 = pow2i(turn - turn / 2);
 #pragma unroll
-              for (int k = 0; k < G; ++k) z[n_][k][e] = z[n_][k][e] * f0 * f1;
+              for (int k = 0; k < G; ++k) z[k][e] = z[k][e] * f0 * f1;
 #pragma unroll
               for (int k = 0; k < 2 * NC; ++k) {
-                o[n_][k][e] = o[n_][k][e] * f0 * f1;
-                o[n_][k][2 + e] = o[n_][k][2 + e] * f0 * f1;
+                o[k][e] = o[k][e] * f0 * f1;
+                o[k][2 + e] = o[k][2 + e] * f0 * f1;
               }
             }
           }
 #pragma unroll
           for (int w2 = 0; w2 < 2; ++w2)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[w2][e] *= cw[n_][e & 1];
+            for (int e = 0; e < 4; ++e) w[w2][e] *= cw[e & 1];
           float ws[2][G][4];
 #pragma unroll
           for (int w2 = 0; w2 < 2; ++w2)
@@ -767,14 +758,13 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
                 const float w0 = ws[w2][k][2 * half], w1 = ws[w2][k][2 * half + 1];
                 float zp = low_half(vp[w2][half][k]);
                 if constexpr (F32) zp -= C::centre;
-                z[n_][k][0] = fmaf(w0, zp, z[n_][k][0]);
-                z[n_][k][1] = fmaf(w1, zp, z[n_][k][1]);
+                z[k][0] = fmaf(w0, zp, z[k][0]);
+                z[k][1] = fmaf(w1, zp, z[k][1]);
                 const uint32_t hi = half2_of(w0, w1);
-                b[n_][w2][k][half][0] = transpose8(hi);
+                b[w2][k][half][0] = transpose8(hi);
                 if constexpr (F32)
-                  b[n_][w2][k][half][P - 1] = transpose8(half2_of(w0 - low_half(hi), w1 - low_half(hi >> 16)));
+                  b[w2][k][half][P - 1] = transpose8(half2_of(w0 - low_half(hi), w1 - low_half(hi >> 16)));
               }
-        }
         uint32_t vw[2][2][NC];
 #pragma unroll
         for (int w2 = 0; w2 < 2; ++w2)
@@ -790,29 +780,25 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
         fetch(un + kUnits);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          float acc[NQ][2][4];
+          float acc[2][4];
 #pragma unroll
           for (int w2 = 0; w2 < 2; ++w2) {
             uint32_t lo[4], hi[4];
             operands<F32>(vw[w2][0][c], lo);
             operands<F32>(vw[w2][1][c], hi);
 #pragma unroll
-            for (int n_ = 0; n_ < NQ; ++n_)
-#pragma unroll
               for (int part = 0; part < P; ++part) {
-                const uint32_t b0 = b[n_][w2][c / CPG][0][part], b1 = b[n_][w2][c / CPG][1][part];
-                mma(w2 == 0 && part == 0, acc[n_][0], lo[0], lo[1], hi[0], hi[1], b0, b1);
-                mma(w2 == 0 && part == 0, acc[n_][1], lo[2], lo[3], hi[2], hi[3], b0, b1);
+                const uint32_t b0 = b[w2][c / CPG][0][part], b1 = b[w2][c / CPG][1][part];
+                mma(w2 == 0 && part == 0, acc[0], lo[0], lo[1], hi[0], hi[1], b0, b1);
+                mma(w2 == 0 && part == 0, acc[1], lo[2], lo[3], hi[2], hi[3], b0, b1);
               }
           }
-#pragma unroll
-          for (int n_ = 0; n_ < NQ; ++n_)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
               for (int e = 0; e < 4; e += 2)
-                unpack2(add2(pack2(o[n_][2 * c + k][e], o[n_][2 * c + k][e + 1]), pack2(acc[n_][k][e], acc[n_][k][e + 1])),
-                        o[n_][2 * c + k][e], o[n_][2 * c + k][e + 1]);
+                unpack2(add2(pack2(o[2 * c + k][e], o[2 * c + k][e + 1]), pack2(acc[k][e], acc[k][e + 1])),
+                        o[2 * c + k][e], o[2 * c + k][e + 1]);
         }
       }
       if (!ok) break;
@@ -828,29 +814,27 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
         last_un = un + 1;
       }
 #pragma unroll
-      for (int n_ = 0; n_ < NQ; ++n_)
-#pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = 8 * n_ + 2 * t4 + e;
-          const float sum = column_sum(l[n_][e]);
-          float inv = 1.0f / cw[n_][e];
+          const int row = 2 * t4 + e;
+          const float sum = column_sum(l[e]);
+          float inv = 1.0f / cw[e];
           if (only && u.whole) inv *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
           if (g8 == 0) {
             if (!only)
-              reinterpret_cast<float2 *>(smem + C::ml_off)[warp * C::R + row] = make_float2(m[n_][e], sum);
+              reinterpret_cast<float2 *>(smem + C::ml_off)[warp * C::R + row] = make_float2(m[e], sum);
             else if (!u.whole && row < u.rows)
-              p.parts.ml[static_cast<int64_t>(u.slot) * p.parts.rows + row] = make_float2(m[n_][e], sum);
+              p.parts.ml[static_cast<int64_t>(u.slot) * p.parts.rows + row] = make_float2(m[e], sum);
           }
           float *const out = reinterpret_cast<float *>(smem + C::o_off) + (warp * C::R + row) * C::OS;
 #pragma unroll
-          for (int k = 0; k < G; ++k) z[n_][k][e] = column_sum(z[n_][k][e]);
+          for (int k = 0; k < G; ++k) z[k][e] = column_sum(z[k][e]);
           auto put = [&](float v, float zz, float odd) { return fmaf(v, C::unit / odd, -zz) * inv; };
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const float zz = z[n_][c / CPG][e];
+            const float zz = z[c / CPG][e];
             // dimensions 4 g8 .. + 3 of the chunk: rows g8 and g8 + 8 of two products
-            const float4 v = make_float4(put(o[n_][2 * c][e], zz, 1.0f), put(o[n_][2 * c][2 + e], zz, C::odd),
-                                         put(o[n_][2 * c + 1][e], zz, 1.0f), put(o[n_][2 * c + 1][2 + e], zz, C::odd));
+            const float4 v = make_float4(put(o[2 * c][e], zz, 1.0f), put(o[2 * c][2 + e], zz, C::odd),
+                                         put(o[2 * c + 1][e], zz, 1.0f), put(o[2 * c + 1][2 + e], zz, C::odd));
             const int d = 32 * c + 4 * g8;
             if (!only)
               *reinterpret_cast<float4 *>(out + d) = v;
@@ -873,47 +857,40 @@ __global__ void __launch_bounds__(Form<NC, CPG, NQ, F32>::threads, 1)
   }
 }
 
-template <int NC, int CPG, int NQ, bool F32>
+template <int NC, int CPG, bool F32>
 cudaError_t run_form(const Attn4 &p, int workers, cudaStream_t s) {
-  auto kern = attn4_rows_kernel<NC, CPG, NQ, F32>;
-  constexpr int smem = Form<NC, CPG, NQ, F32>::bytes;
+  auto kern = attn4_rows_kernel<NC, CPG, F32>;
+  constexpr int smem = Form<NC, CPG, F32>::bytes;
   const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(workers), dim3(Form<NC, CPG, NQ, F32>::threads), smem, s, p);
+  return launch_pdl(kern, dim3(workers), dim3(Form<NC, CPG, F32>::threads), smem, s, p);
 }
 
-template <int NC, int CPG, int NQ>
+template <int NC, int CPG>
 cudaError_t run_type(const Attn4 &p, int workers, cudaStream_t s) {
-  return p.a.bf16 ? run_form<NC, CPG, NQ, false>(p, workers, s) : run_form<NC, CPG, NQ, true>(p, workers, s);
+  return p.a.bf16 ? run_form<NC, CPG, false>(p, workers, s) : run_form<NC, CPG, true>(p, workers, s);
 }
 
 template <int NC>
-cudaError_t run_nc(const Attn4 &p, int rows, int workers, cudaStream_t s) {
-  if constexpr (NC > 1) {
-    if (p.c.cpg == 2) {
-      if constexpr (NC <= 4)
-        if (rows > 8) return run_type<NC, 2, 2>(p, workers, s);
-      return run_type<NC, 2, 1>(p, workers, s);
-    }
-  }
-  if constexpr (NC <= 4)
-    if (rows > 8) return run_type<NC, 1, 2>(p, workers, s);
-  return run_type<NC, 1, 1>(p, workers, s);
+cudaError_t run_nc(const Attn4 &p, int workers, cudaStream_t s) {
+  if constexpr (NC > 1)
+    if (p.c.cpg == 2) return run_type<NC, 2>(p, workers, s);
+  return run_type<NC, 1>(p, workers, s);
 }
 
 }  // namespace
 
-AttnPlan attn4_rows_plan(const Kv4 &c, int64_t T, int n_head, int R) {
+AttnPlan attn4_rows_plan(const Kv4 &c, int n_head) {
   const int grp = n_head / c.n_kv;
-  // rows that a request has for a key/value head, on average
-  const int64_t usual = R > 0 ? (T + R - 1) / R * grp : grp;
   AttnPlan p;
-  p.rows = usual > 8 && c.nc <= 4 ? 16 : 8;
+  p.rows = 8;
   p.gsub = grp < p.rows ? grp : p.rows;
   p.nsub = (grp + p.gsub - 1) / p.gsub;
   p.U = p.rows / p.gsub;
   p.KT = kKT;
-  p.fixed = 4 * kKT;
+  // A unit costs 2 to 4 us besides its keys, of which a CTA does 170 a us (64 requests
+  // of 100 to 16384 keys: 108 us; 132 with 128 keys, where workers of short ones lag).
+  p.fixed = 640;
   p.min_run = 4 * kKT;
   p.whole = kWholeKeys;
   p.workers = sm_count();
@@ -925,12 +902,12 @@ cudaError_t launch_attn4_rows(const AttnBatch &a, const Kv4 &c, const AttnPlan &
   Attn4 p{a, c, sc, parts, pl.gsub, pl.nsub, a.scale * 1.4426950408889634f, device_status()};
   if (!p.status) return cudaErrorInvalidDevice;
   switch (c.nc) {
-    case 1: return run_nc<1>(p, pl.rows, pl.workers, s);
-    case 2: return run_nc<2>(p, pl.rows, pl.workers, s);
-    case 3: return run_nc<3>(p, pl.rows, pl.workers, s);
-    case 4: return run_nc<4>(p, pl.rows, pl.workers, s);
-    case 6: return run_nc<6>(p, pl.rows, pl.workers, s);
-    default: return run_nc<8>(p, pl.rows, pl.workers, s);
+    case 1: return run_nc<1>(p, pl.workers, s);
+    case 2: return run_nc<2>(p, pl.workers, s);
+    case 3: return run_nc<3>(p, pl.workers, s);
+    case 4: return run_nc<4>(p, pl.workers, s);
+    case 6: return run_nc<6>(p, pl.workers, s);
+    default: return run_nc<8>(p, pl.workers, s);
   }
 }
 

@@ -63,7 +63,7 @@ size_t attn4_workspace_bytes(const Kv4 &c, bool q_bf16, int64_t T, int n_head, i
 cudaError_t launch_attn4(const AttnBatch &a, const Kv4 &c, void *workspace, cudaStream_t s);
 
 // The form for few rows.
-AttnPlan attn4_rows_plan(const Kv4 &c, int64_t T, int n_head, int R);
+AttnPlan attn4_rows_plan(const Kv4 &c, int n_head);
 cudaError_t launch_attn4_rows(const AttnBatch &a, const Kv4 &c, const AttnPlan &p, const AttnSched &sc,
                               const AttnParts &parts, cudaStream_t s);
 

@@ -54,12 +54,12 @@ int check_kv4(const char *who, const qmm_kv4_cache *c, Kv4 *out) {
 
 }  // namespace
 
-size_t attn4_workspace_bytes(const Kv4 &c, bool, int64_t T, int n_head, int R) {
-  return parts_layout(attn4_rows_plan(c, T, n_head, R), c.head_dim).total;
+size_t attn4_workspace_bytes(const Kv4 &c, bool, int64_t, int n_head, int) {
+  return parts_layout(attn4_rows_plan(c, n_head), c.head_dim).total;
 }
 
 cudaError_t launch_attn4(const AttnBatch &a, const Kv4 &c, void *workspace, cudaStream_t s) {
-  const AttnPlan p = attn4_rows_plan(c, a.T, a.n_head, a.R);
+  const AttnPlan p = attn4_rows_plan(c, a.n_head);
   return run_attn_plan(a, p, workspace, s, [&](const AttnSched &sc, const AttnParts &parts) {
     return launch_attn4_rows(a, c, p, sc, parts, s);
   });
