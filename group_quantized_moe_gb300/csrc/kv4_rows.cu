@@ -15,7 +15,7 @@
 //
 // Four lanes hold a row of a head, each eight dimensions of every chunk of 32:
 // a lane's codes of a key are consecutive words of the cache, and a group's
-// extremes meet in two shuffles.  A warp takes a token, eight heads at a time.
+// extremes meet in two shuffles.  A warp takes four heads of two tokens at a time.
 // Bound by HBM: qkv is read once, q and the codes written once.
 #include <cuda_fp16.h>
 
@@ -137,31 +137,60 @@ __device__ __forceinline__ void store_words(uint32_t *p, const uint32_t *w) {
   }
 }
 
+template <int NC>
+__device__ __forceinline__ void load_words(uint32_t *w, const uint32_t *p) {
+  if constexpr (NC % 4 == 0) {
+#pragma unroll
+    for (int c = 0; c < NC; c += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + c));
+      w[c] = v.x, w[c + 1] = v.y, w[c + 2] = v.z, w[c + 3] = v.w;
+    }
+  } else if constexpr (NC % 2 == 0) {
+#pragma unroll
+    for (int c = 0; c < NC; c += 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p + c));
+      w[c] = v.x, w[c + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) w[c] = __ldg(p + c);
+  }
+}
+
 // CPG: chunks of a group.
 template <int NC, int CPG, bool BF16>
-__global__ void __launch_bounds__(kThreads) rope_append_kv4_kernel(RopeAppend a, Kv4 cache, uint32_t *status) {
+__global__ void __launch_bounds__(kThreads, NC <= 4 ? 4 : 2) rope_append_kv4_kernel(RopeAppend a, Kv4 cache, uint32_t *status) {
   constexpr int G = (NC + CPG - 1) / CPG;
   pdl_enter();
   const int lane = threadIdx.x & 31, t4 = lane & 3, team = lane >> 2;
   const int heads = a.n_head + 2 * a.n_kv, turned = a.n_head + a.n_kv, hd = a.head_dim;
   const int64_t rows = cache.num_blocks << cache.block_shift;
   const int strip = kv4_strip(cache);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < a.T;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t p = a.positions[t], slot = a.slots ? a.slots[t] : -1;
+  // (two tokens, four heads) by turns: a few tokens still spread over many warps
+  const int quads = (heads + 3) / 4, odd = team & 1;
+  const int64_t pairs = (a.T + 1) / 2, step = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t dt = step / quads;
+  const int dp = static_cast<int>(step - dt * quads);
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  int64_t pair = item / quads;
+  int part = static_cast<int>(item - pair * quads);
+  for (; pair < pairs; pair += dt, part += dp) {
+    if (part >= quads) {
+      part -= quads;
+      if (++pair >= pairs) break;
+    }
+    const int64_t t = 2 * pair + odd;
+    const int64_t p = t < a.T ? a.positions[t] : -1, slot = t < a.T ? a.slots[t] : -1;
     // a padding row (position below 0) or one the table does not reach: zeros, no cache row
     const bool live = p >= 0 && p < a.max_seq;
-    const bool put = live && a.cached && slot >= 0 && slot < rows;
-    if (lane == 0) {
+    const bool put = live && slot >= 0 && slot < rows;
+    if (lane - 4 * odd == 0 && part == 0) {
       if (p >= a.max_seq) atomicOr(status, kDevBadPosition);
-      if (a.cached && live && slot >= rows) atomicOr(status, kDevBadBlock);
+      if (live && slot >= rows) atomicOr(status, kDevBadBlock);
     }
-    const int row = static_cast<int>(slot & ((1 << cache.block_shift) - 1)), r = row & 15;
-    uint8_t *block = cache.data + (put ? (slot >> cache.block_shift) * cache.block_stride : 0) +
-                     (put ? (row >> 4) * strip : 0);
-    for (int h0 = 0; h0 < heads; h0 += 8) {
-      const int h = h0 + team;
-      const bool on = h < heads;
+    {
+      const int h = 4 * part + (team >> 1);
+      const bool on = h < heads && t < a.T;
       Raw8<BF16> raw[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -173,6 +202,39 @@ __global__ void __launch_bounds__(kThreads) rope_append_kv4_kernel(RopeAppend a,
       }
       const bool query = h < a.n_head, key = !query && h < turned;
       const int hk = h - a.n_head - (key ? 0 : a.n_kv);
+      void *const packed = query ? a.q : key ? a.k : a.v;
+      const int64_t base = query ? (t * a.n_head + h) * hd : (t * a.n_kv + hk) * hd;
+      // eight dimensions of chunk c, turned, and stored where they go out as numbers
+      auto turn = [&](int c, float *y) {
+        const int d = 32 * c + 8 * t4;
+        raw[c].get(y);
+        if (!on || d >= hd) return false;
+        if (!live) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+        } else if (h < turned) {
+          const int64_t at = p * (hd / 2) + d / 2;
+          const float4 cs = __ldg(reinterpret_cast<const float4 *>(a.cos_t + at));
+          const float4 sn = __ldg(reinterpret_cast<const float4 *>(a.sin_t + at));
+          const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = y[2 * i], o = y[2 * i + 1];
+            y[2 * i] = fmaf(e, cc[i], -__fmul_rn(o, ss[i]));
+            y[2 * i + 1] = fmaf(e, ss[i], __fmul_rn(o, cc[i]));
+          }
+        }
+        if (packed) store8(packed, base + d, y, a.y_bf16);
+        return true;
+      };
+      if (4 * part + 4 <= a.n_head || !__any_sync(0xFFFFFFFFu, put)) {  // nothing here is quantised
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float y[8];
+          turn(c, y);
+        }
+        continue;
+      }
       uint32_t words[G * CPG], params[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -180,49 +242,42 @@ __global__ void __launch_bounds__(kThreads) rope_append_kv4_kernel(RopeAppend a,
         int n = 0;
 #pragma unroll
         for (int k = 0; k < CPG; ++k) {
-          const int c = g * CPG + k, d = 32 * c + 8 * t4;
-          if (c >= NC) {
+          const int c = g * CPG + k;
+          if (c < NC) {
+            if (turn(c < NC ? c : 0, x + 8 * k)) n = 8 * k + 8;
+          } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[8 * k + i] = 0.0f;
-            continue;
-          }
-          float *const y = x + 8 * k;
-          raw[c < NC ? c : 0].get(y);
-          if (on && d < hd) n = 8 * k + 8;
-          if (h < turned && d < hd && live) {
-            const int64_t at = p * (hd / 2) + d / 2;
-            const float4 cs = __ldg(reinterpret_cast<const float4 *>(a.cos_t + at));
-            const float4 sn = __ldg(reinterpret_cast<const float4 *>(a.sin_t + at));
-            const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float e = y[2 * i], o = y[2 * i + 1];
-              y[2 * i] = fmaf(e, cc[i], -__fmul_rn(o, ss[i]));
-              y[2 * i + 1] = fmaf(e, ss[i], __fmul_rn(o, cc[i]));
-            }
-          }
-          if (!live)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-          if (on && d < hd) {
-            void *const packed = query ? a.q : key ? a.k : a.v;
-            const int64_t base = query ? (t * a.n_head + h) * hd : (t * a.n_kv + hk) * hd;
-            if (packed) store8(packed, base + d, y, a.y_bf16);
           }
         }
         params[g] = quantise<8 * CPG>(x, n, words + g * CPG);
       }
-      if (put && on && !query) {
-        uint8_t *const s = block + static_cast<int64_t>(hk) * kv4_head_bytes(cache);
+      // Rows 2 j and 2 j + 1 share the words of values: where the pair's tokens go
+      // there, each lane stores whole words of both.
+      const int64_t other = __shfl_xor_sync(0xFFFFFFFFu, slot, 4);
+      const bool both = __shfl_xor_sync(0xFFFFFFFFu, put, 4) && put && (slot ^ other) == 1;
+      uint32_t theirs[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) theirs[c] = __shfl_xor_sync(0xFFFFFFFFu, words[c], 4);
+      if (on && put && !query) {
+        const int row = static_cast<int>(slot & ((1 << cache.block_shift) - 1)), r = row & 15;
+        uint8_t *const s = cache.data + (slot >> cache.block_shift) * cache.block_stride + (row >> 4) * strip +
+                           static_cast<int64_t>(hk) * kv4_head_bytes(cache);
+        uint32_t *const v = reinterpret_cast<uint32_t *>(s + 256 * NC) +
+                            (((r >> 3) * 8 + 2 * t4) * 4 + ((r & 7) >> 1)) * NC;
         if (key) {
           store_words<NC>(reinterpret_cast<uint32_t *>(s) + (r * 4 + t4) * NC, words);
+        } else if (both) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            words[c] = r & 1 ? __byte_perm(theirs[c], words[c], 0x7632u) : __byte_perm(words[c], theirs[c], 0x5410u);
+          store_words<NC>(v + (r & 1) * 4 * NC, words);
         } else {
-          uint16_t *const v = reinterpret_cast<uint16_t *>(s + 256 * NC) +
-                              2 * (((r >> 3) * 8 + 2 * t4) * 4 + ((r & 7) >> 1)) * NC + (r & 1);
+          uint16_t *const v16 = reinterpret_cast<uint16_t *>(v) + (r & 1);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            v[2 * c] = static_cast<uint16_t>(words[c]);
-            v[2 * (4 * NC + c)] = static_cast<uint16_t>(words[c] >> 16);
+            v16[2 * c] = static_cast<uint16_t>(words[c]);
+            v16[2 * (4 * NC + c)] = static_cast<uint16_t>(words[c] >> 16);
           }
         }
         uint32_t *const q = reinterpret_cast<uint32_t *>(s + 512 * NC) + (key ? 0 : 16 * cache.ng) + r * cache.ng;
@@ -256,40 +311,53 @@ __global__ void __launch_bounds__(kThreads)
       void *const out = key ? k : v;
       if (!out) continue;
       const uint8_t *const s = block + static_cast<int64_t>(hk) * kv4_head_bytes(cache);
-      const uint32_t *const kw = reinterpret_cast<const uint32_t *>(s) + (r * 4 + t4) * NC;
-      const uint16_t *const vw = reinterpret_cast<const uint16_t *>(s + 256 * NC) +
-                                 2 * (((r >> 3) * 8 + 2 * t4) * 4 + ((r & 7) >> 1)) * NC + (r & 1);
       const uint32_t *const q =
           reinterpret_cast<const uint32_t *>(s + 512 * NC) + (key ? 0 : 16 * cache.ng) + r * cache.ng;
+      uint32_t w[NC], par[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) w[c] = par[c] = 0u;
+      if (live) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          par[c] = __ldg(q + min(c / cache.cpg, cache.ng - 1));
+        if (key) {
+          load_words<NC>(w, reinterpret_cast<const uint32_t *>(s) + (r * 4 + t4) * NC);
+        } else {
+          // words of two rows, of which this one has one half
+          const uint32_t *const vw = reinterpret_cast<const uint32_t *>(s + 256 * NC) +
+                                     (((r >> 3) * 8 + 2 * t4) * 4 + ((r & 7) >> 1)) * NC;
+          uint32_t lo[NC], hi[NC];
+          load_words<NC>(lo, vw);
+          load_words<NC>(hi, vw + 4 * NC);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) w[c] = __byte_perm(lo[c], hi[c], r & 1 ? 0x7632u : 0x5410u);
+        }
+      }
+      const int64_t base = (i * cache.n_kv + hk) * hd;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int d = 32 * c + 8 * t4;
         if (d >= hd) continue;
+        const float scale = __uint_as_float(par[c] & 0xFFFF0000u);
+        const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(par[c])));
         float y[8];
-        uint32_t w = 0, par = 0;
-        if (live) {
-          w = key ? kw[c] : vw[2 * c] | static_cast<uint32_t>(vw[2 * (4 * NC + c)]) << 16;
-          par = q[c / cache.cpg];
-        }
-        const float scale = __uint_as_float(par & 0xFFFF0000u);
-        const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(par)));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = (static_cast<float>(w >> (4 * j) & 15u) - zp) * scale;
-        store8(out, (i * cache.n_kv + hk) * hd + d, y, bf16);
+        for (int j = 0; j < 8; ++j) y[j] = (static_cast<float>(w[c] >> (4 * j) & 15u) - zp) * scale;
+        store8(out, base + d, y, bf16);
       }
     }
   }
 }
 
-unsigned grid_of(int64_t rows) {
-  const int64_t most = static_cast<int64_t>(sm_count()) * 4, want = (rows + kWarps - 1) / kWarps;
+unsigned grid_of(int64_t rows, int per_sm) {
+  const int64_t most = static_cast<int64_t>(sm_count()) * per_sm, want = (rows + kWarps - 1) / kWarps;
   return static_cast<unsigned>(want < most ? want : most);
 }
 
 template <int NC, int CPG>
 cudaError_t run_append(const RopeAppend &a, const Kv4 &c, uint32_t *status, cudaStream_t s) {
   auto kern = a.x_bf16 ? rope_append_kv4_kernel<NC, CPG, true> : rope_append_kv4_kernel<NC, CPG, false>;
-  return launch_pdl(kern, dim3(grid_of(a.T)), dim3(kThreads), 0, s, a, c, status);
+  return launch_pdl(kern, dim3(grid_of((a.T + 1) / 2 * ((a.n_head + 2 * a.n_kv + 3) / 4), 4)), dim3(kThreads), 0, s, a, c, status);
 }
 
 template <int NC>
@@ -324,7 +392,7 @@ cudaError_t launch_kv4_read(const Kv4 &c, const int64_t *slots, int64_t n, void 
               : c.nc == 4 ? kv4_read_kernel<4>
               : c.nc == 6 ? kv4_read_kernel<6>
                           : kv4_read_kernel<8>;
-  return launch_pdl(kern, dim3(grid_of(n)), dim3(kThreads), 0, s, c, slots, n, k, v, bf16, status);
+  return launch_pdl(kern, dim3(grid_of(n, 8)), dim3(kThreads), 0, s, c, slots, n, k, v, bf16, status);
 }
 
 }  // namespace qmm
