@@ -66,5 +66,9 @@ cudaError_t launch_attn4(const AttnBatch &a, const Kv4 &c, void *workspace, cuda
 AttnPlan attn4_rows_plan(const Kv4 &c, int n_head);
 cudaError_t launch_attn4_rows(const AttnBatch &a, const Kv4 &c, const AttnPlan &p, const AttnSched &sc,
                               const AttnParts &parts, cudaStream_t s);
+// The form for many (its plan is attn_tc_plan's): whether it takes a call.
+bool attn4_tc_takes(const AttnBatch &a);
+cudaError_t launch_attn4_tc(const AttnBatch &a, const Kv4 &c, const AttnPlan &p, const AttnSched &sc,
+                            const AttnParts &parts, cudaStream_t s);
 
 }  // namespace qmm

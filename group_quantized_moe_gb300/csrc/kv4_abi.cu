@@ -1,5 +1,6 @@
 // kv4_abi.cu -- extern "C" entry points of the paged cache held in 4 bits:
 // argument validation and kernel selection.  Declared in include/qmm.h.
+#include <cstdlib>
 #include "attn_entry.h"
 #include "kv4.h"
 
@@ -54,14 +55,26 @@ int check_kv4(const char *who, const qmm_kv4_cache *c, Kv4 *out) {
 
 }  // namespace
 
-size_t attn4_workspace_bytes(const Kv4 &c, bool, int64_t, int n_head, int) {
-  return parts_layout(attn4_rows_plan(c, n_head), c.head_dim).total;
+// Query rows that a request has for a key/value head, on average, above which
+// the form for many rows is the faster one.
+static bool many_rows(const Kv4 &c, int64_t T, int n_head, int R) {
+  static const char *e = getenv("TCR");
+  return T * (n_head / c.n_kv) > static_cast<int64_t>(e ? atoi(e) : 24) * R;
+}
+
+size_t attn4_workspace_bytes(const Kv4 &c, bool q_bf16, int64_t T, int n_head, int R) {
+  // whether a call of many rows takes the form for them also depends on its stride
+  const size_t few = parts_layout(attn4_rows_plan(c, n_head), c.head_dim).total;
+  if (!q_bf16 || c.head_dim > 128 || !many_rows(c, T, n_head, R)) return few;
+  const size_t many = parts_layout(attn_tc_plan(true, T, n_head, c.n_kv, R), c.head_dim).total;
+  return many > few ? many : few;
 }
 
 cudaError_t launch_attn4(const AttnBatch &a, const Kv4 &c, void *workspace, cudaStream_t s) {
-  const AttnPlan p = attn4_rows_plan(c, a.n_head);
+  const bool tc = many_rows(c, a.T, a.n_head, a.R) && attn4_tc_takes(a);
+  const AttnPlan p = tc ? attn_tc_plan(true, a.T, a.n_head, a.n_kv, a.R) : attn4_rows_plan(c, a.n_head);
   return run_attn_plan(a, p, workspace, s, [&](const AttnSched &sc, const AttnParts &parts) {
-    return launch_attn4_rows(a, c, p, sc, parts, s);
+    return tc ? launch_attn4_tc(a, c, p, sc, parts, s) : launch_attn4_rows(a, c, p, sc, parts, s);
   });
 }
 

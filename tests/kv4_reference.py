@@ -17,6 +17,9 @@ and zero points apart, so the errors go by s (code + |zp|), named size:
   weight times scale, to 16 bits: 2^-11 with bf16 queries, two parts (2^-22)
            with fp32 ones; below fp16's normal range half a step of 2^-24,
            where the largest product of the row is at least 2^4: 2^-29 of it
+  tiles    (bf16 queries, head sizes up to 128, many rows a request): keys, values
+           and weights are rounded to bf16 instead, half a step each, 2^-8: of
+           every q k in a score, of every p v twice in the result
   result   sum_j p_j |v_j| (e_j + sum_i p_i e_i) for the weights above and below
            the line, sum_j p_j size_j 2 (L + 64) u for the sums, sum_j p_j s_j
            code_j (rounding) for the products.
@@ -138,7 +141,7 @@ def rope32(x, pos, cos, sin, n_rot):
     return y
 
 
-def attend(q, keys, vals, group, visible, scale, q32):
+def attend(q, keys, vals, group, visible, scale, q32, tiles=False):
     """q [n, nh, hd]; keys, vals: codes [L, nkv, hd], zps, scales [L, nkv, G];
     visible bool [n, L] -> y, bound [n, nh, hd]."""
     n, nh, hd = q.shape
@@ -162,6 +165,8 @@ def attend(q, keys, vals, group, visible, scale, q32):
         s = np.where(vis, scale * (q[:, h] @ k[:, g].T), -np.inf)
         top = np.where(vis, np.abs(s), 0).max(axis=1, keepdims=True)
         es = scale * (2 * U * (hd + 16) + (2.0 ** -22 if q32 else 0)) * (qh @ ksize[:, g].T) + 4 * U * top
+        if tiles:
+            es += scale * 2.0 ** -8 * (qh @ np.abs(k[:, g]).T)
         es += scale * 2.0 ** -34 * qh.max(axis=1, keepdims=True) * ksize[:, g].sum(-1)
         p = np.where(vis, np.exp(s - s.max(axis=1, keepdims=True)), 0)
         p /= p.sum(axis=1, keepdims=True)
@@ -169,14 +174,16 @@ def attend(q, keys, vals, group, visible, scale, q32):
         mean_e = (p * e).sum(axis=1, keepdims=True)
         small = 2.0 ** -29 * (p[:, :, None] * spread(vals[2])[None, :, g]).max(axis=1) * 15 * len(k)
         y[rows, h] = p @ v[:, g]
-        b[rows, h] = ((p * (e + mean_e)) @ np.abs(v[:, g]) + p @ vsize[:, g] * (2 * (L + 64) * U)
-                      + p @ vcode[:, g] * low + small + 1e-30)
+        rounded = p @ np.abs(v[:, g]) * (2 * 2.0 ** -8 + 2.0 ** -16) if tiles else p @ vcode[:, g] * low + small
+        b[rows, h] = ((p * (e + mean_e)) @ np.abs(v[:, g]) + p @ vsize[:, g] * (2 * (L + 64) * U) + rounded + 1e-30)
     return y, b
 
 
 def paged(q, data, group, S, table, lens, scale, q32):
-    """lens: (cache rows, new tokens) of each request."""
+    """lens: (cache rows, new tokens) of each request.  More than 24 query rows to a
+    key/value head and request, on average: tiles."""
     nb, hd = data.shape[0], q.shape[2]
+    tiles = not q32 and hd <= 128 and len(q) * (q.shape[1] // data.shape[1]) > 24 * len(lens)
     kk, vv = unpack(data, hd, group, S)
     parts, t = [], 0
     for r, (L, n) in enumerate(lens):
@@ -186,7 +193,7 @@ def paged(q, data, group, S, table, lens, scale, q32):
         ids = np.where(ok, ids, 0)
         rows = [[t_[ids, :, j % S] for t_ in part] for part in (kk, vv)]
         vis = (j[None, :] <= (L - n + np.arange(n))[:, None]) & ok[None, :]
-        parts.append(attend(q[t:t + n], *rows, group, vis, scale, q32))
+        parts.append(attend(q[t:t + n], *rows, group, vis, scale, q32, tiles))
         t += n
     pad = (len(q) - t,) + q.shape[1:]
     return (np.concatenate([y for y, _ in parts] + [np.zeros(pad)]),
