@@ -13,21 +13,25 @@
 namespace qmm {
 namespace {
 
-template <int NCH>
-__global__ void __launch_bounds__(Tc<NCH, false, true>::threads, 1)
+// NC: chunks of 32 dimensions.
+template <int NC>
+using Tc4 = Tc<(NC + 1) / 2, false, true>;
+
+template <int NC>
+__global__ void __launch_bounds__(Tc4<NC>::threads, 1)
     attn4_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ TcAttn p,
                     const __grid_constant__ Kv4 c) {
-  attn_tc_body<NCH, true, false, true>(tm_q, tm_q, tm_q, p, c);
+  attn_tc_body<(NC + 1) / 2, true, false, NC>(tm_q, tm_q, tm_q, p, c);
 }
 
-template <int NCH>
+template <int NC>
 cudaError_t run_tc(const CUtensorMap &q, const TcAttn &p, const Kv4 &c, int workers, cudaStream_t s) {
-  auto kern = attn4_tc_kernel<NCH>;
-  constexpr uint32_t smem = Tc<NCH, false, true>::bytes;
+  auto kern = attn4_tc_kernel<NC>;
+  constexpr uint32_t smem = Tc4<NC>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory");
   const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(workers), dim3(Tc<NCH, false, true>::threads), smem, s, q, p, c);
+  return launch_pdl(kern, dim3(workers), dim3(Tc4<NC>::threads), smem, s, q, p, c);
 }
 
 }  // namespace
@@ -52,7 +56,12 @@ cudaError_t launch_attn4_tc(const AttnBatch &a, const Kv4 &c, const AttnPlan &pl
   if (!p.status) return cudaErrorInvalidDevice;
   CUtensorMap q;
   if (!map_rows(&q, a.q, a.T, a.q_stride, a.n_head, a.head_dim, p.gsub, p.tpt)) return cudaErrorInvalidValue;
-  return a.head_dim <= 64 ? run_tc<1>(q, p, c, pl.workers, s) : run_tc<2>(q, p, c, pl.workers, s);
+  switch (c.nc) {
+    case 1: return run_tc<1>(q, p, c, pl.workers, s);
+    case 2: return run_tc<2>(q, p, c, pl.workers, s);
+    case 3: return run_tc<3>(q, p, c, pl.workers, s);
+    default: return run_tc<4>(q, p, c, pl.workers, s);
+  }
 }
 
 }  // namespace qmm

@@ -192,35 +192,81 @@ __device__ __noinline__ void add_marked4(const TcAttn &p, const Kv4 &c, const Un
   }
 }
 
-// Eight codes (code - zp) s in bf16, each rounded once: codes and zero points up
-// to 120 are whole numbers that bf16 has, others go through fp32.
-__device__ __forceinline__ uint4 codes_bf16(uint32_t w, uint32_t par) {
-  const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(par)));
-  uint32_t r[4];
-  if (fabsf(zp) <= 120.0f) {
-    const uint32_t x = w & 0x0F0F0F0Fu, y = w >> 4 & 0x0F0F0F0Fu;
-    const __nv_bfloat162 z2 = __float2bfloat162_rn(128.0f + zp);
-    const uint32_t sb = __byte_perm(par, 0u, 0x3232u);
-    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162 *>(&sb);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // 0x4300 + code: 128 + code
-      const uint32_t t = (__byte_perm(x, y, 0x0400u + 0x0101u * i) & 0x00FF00FFu) | 0x43004300u;
-      const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&t), z2), s2);
-      r[i] = *reinterpret_cast<const uint32_t *>(&v);
-    }
-  } else {
-    const float s = __uint_as_float(par & 0xFFFF0000u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = bf16x2((static_cast<float>(w >> (8 * i) & 15u) - zp) * s, (static_cast<float>(w >> (8 * i + 4) & 15u) - zp) * s);
+// (code - zp) s of eight codes in bf16, each rounded once.  Codes and zero points
+// of up to 120 are whole numbers that bf16 has (0x4300 + code is 128 + code), and
+// so are their differences; WIDE ones go through fp32.
+__device__ __forceinline__ bool wide_zp(uint32_t par) {
+  // (of an fp16's bits: its magnitude is above 120's, or it is not a number)
+  return (par & 0x7FFFu) > 0x5780u;
+}
+template <bool WIDE>
+struct Dequant {
+  __nv_bfloat162 zp, s;  // 128 + zp, s
+  float zf, sf;
+  __device__ __forceinline__ void set(uint32_t par) {
+    zf = __half2float(__ushort_as_half(static_cast<unsigned short>(par)));
+    sf = __uint_as_float(par & 0xFFFF0000u);
+    zp = __float2bfloat162_rn(128.0f + zf);
+    const uint32_t b = __byte_perm(par, 0u, 0x3232u);
+    s = *reinterpret_cast<const __nv_bfloat162 *>(&b);
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  __device__ __forceinline__ uint4 of(uint32_t w) const {
+    uint32_t r[4];
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = bf16x2((static_cast<float>(w >> (8 * i) & 15u) - zf) * sf,
+                      (static_cast<float>(w >> (8 * i + 4) & 15u) - zf) * sf);
+    } else {
+      const uint32_t x = w & 0x0F0F0F0Fu, y = w >> 4 & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t t = (__byte_perm(x, y, 0x0400u + 0x0101u * i) & 0x00FF00FFu) | 0x43004300u;
+        const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&t), zp), s);
+        r[i] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  }
+};
+
+// Eight dimensions of every chunk of a row (unit: which eight), from their words
+// and the parameters of the chunks, to row `key` of a tile.
+template <bool WIDE, int NC>
+__device__ __forceinline__ void put_row(uint8_t *tile, int key, int unit, const uint32_t (&w)[NC],
+                                        const uint32_t (&par)[NC], uint32_t keep) {
+  uint8_t *const row = tile + key * 128;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    Dequant<WIDE> q;
+    q.set(par[c]);
+    uint4 v = q.of(w[c]);
+    if (!(keep >> c & 1u)) v = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4 *>(row + (c >> 1) * kChunk + ((((c & 1) * 4 + unit) ^ (key & 7)) << 4)) = v;
+  }
 }
 
-// Q4: keys and values from the 4-bit cache c (tm_k, tm_v not used).
-template <int NCH, bool PAGED, bool STAGED, bool Q4>
+// N words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint32_t *p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) w[c] = p[c];
+  }
+}
+
+// Q4: keys and values from the 4-bit cache c4, of NC4 chunks of 32 dimensions (tm_k,
+// tm_v not used); 0: bf16.
+template <int NCH, bool PAGED, bool STAGED, int NC4>
 __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                              const TcAttn &p, const Kv4 &c4) {
+  constexpr bool Q4 = NC4 > 0;
   static_assert(!Q4 || (PAGED && !STAGED), "a 4-bit cache is paged, and leaves no room to stage rows");
   using C = Tc<NCH, STAGED, Q4>;
   constexpr int kThreads = C::threads;
@@ -314,7 +360,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
       // ------------------------------------- codes to bf16 tiles of keys and values
       // A word of a key's codes is eight dimensions, 16 bytes of its row in the
       // tile; two words of values are eight dimensions of two rows.
-      const int tid = threadIdx.x - 32 * kWarpCodes, strip = kv4_strip(c4), nc = c4.nc, ng = c4.ng, gsh = c4.cpg - 1;
+      const int tid = threadIdx.x - 32 * kWarpCodes, strip = kv4_strip(c4), ng = c4.ng, gsh = c4.cpg - 1;
       int s = 0, rs = 0;
       uint32_t phase = 1, raw_phase = 0;
       bool ok = true;
@@ -327,10 +373,6 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           // (stages are even in number: K and V have the same phase)
           if (!(ok = wait_warp(freed(s), phase) && wait_warp(freed(s + 1), phase))) break;
           uint8_t *const kd = gbase + C::kv_off + s * C::tile, *const vd = kd + C::tile;
-          auto place = [&](uint8_t *t, int key, int c, int unit, uint4 v) {
-            *reinterpret_cast<uint4 *>(t + (c >> 1) * kChunk + key * 128 +
-                                       ((((c & 1) * 4 + unit) ^ (key & 7)) << 4)) = v;
-          };
           bool found = false;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
@@ -339,38 +381,62 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
             if (some && !(ok = wait_warp(raw_full(rs), raw_phase))) break;
             const uint32_t have = some ? raw_strips[rs] : 0u;
             const uint8_t *const raw = gbase + C::raw_off + rs * C::raw;
-#pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-              const int st = 2 * i + (tid >> 6), r = tid >> 2 & 15, t = tid & 3, key = 64 * half + 16 * st + r;
-              const bool in = (have >> st & 1u) && kt * kKT + key < end;
-              const uint32_t *const words = reinterpret_cast<const uint32_t *>(raw + st * strip) + (r * 4 + t) * nc;
-              const uint32_t *const par = reinterpret_cast<const uint32_t *>(raw + st * strip + 512 * nc) + r * ng;
+            // this thread's part: eight dimensions a chunk of two keys (rows kr of strips
+            // ks, ks + 2) and of two rows of values
+            const int ks = tid >> 6, kr = tid >> 2 & 15, ku = tid & 3, vs = tid >> 5, vr = lane >> 2;
+            uint32_t kw[2][NC4], kp[2][NC4], vw[2][NC4], vp[2][NC4], kk[2], vk[2], wide = 0;
 #pragma unroll
-              for (int c = 0; c < 2 * NCH; ++c)
-                if (c < nc) place(kd, key, c, t, in ? codes_bf16(words[c], par[c >> gsh]) : make_uint4(0, 0, 0, 0));
+            for (int i = 0; i < 2; ++i) {
+              const int st = ks + 2 * i, key = 64 * half + 16 * st + kr;
+              kk[i] = (have >> st & 1u) && kt * kKT + key < end ? 0xFFu : 0u;
+              lds_words<NC4>(kw[i], reinterpret_cast<const uint32_t *>(raw + st * strip) + (kr * 4 + ku) * NC4);
+              const uint32_t *const par = reinterpret_cast<const uint32_t *>(raw + st * strip + 512 * NC4) + kr * ng;
+#pragma unroll
+              for (int c = 0; c < NC4; ++c) {
+                kp[i][c] = par[c >> gsh];
+                wide |= wide_zp(kp[i][c]);
+              }
             }
             {
-              const int st = tid >> 5, pair = lane >> 2, g2 = lane & 3, r = 2 * pair;
-              const uint32_t *const words = reinterpret_cast<const uint32_t *>(raw + st * strip + 256 * nc) +
-                                            (((pair >> 2) * 8 + 2 * g2) * 4 + (pair & 3)) * nc;
-              const uint32_t *const par = reinterpret_cast<const uint32_t *>(raw + st * strip + 512 * nc + 64 * ng) + r * ng;
+              uint32_t lo[NC4], hi[NC4];
+              const uint32_t *const words = reinterpret_cast<const uint32_t *>(raw + vs * strip + 256 * NC4) +
+                                            (((vr >> 2) * 8 + 2 * ku) * 4 + (vr & 3)) * NC4;
+              lds_words<NC4>(lo, words);
+              lds_words<NC4>(hi, words + 4 * NC4);
+              const uint32_t *const par =
+                  reinterpret_cast<const uint32_t *>(raw + vs * strip + 512 * NC4 + 64 * ng) + 2 * vr * ng;
 #pragma unroll
-              for (int c = 0; c < 2 * NCH; ++c) {
-                if (c >= nc) continue;
-                const uint32_t lo = words[c], hi = words[4 * nc + c];
+              for (int b = 0; b < 2; ++b) {
+                const int j = kt * kKT + 64 * half + 16 * vs + 2 * vr + b;
+                vk[b] = (have >> vs & 1u) && j < end ? 0xFFu : 0u;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const int key = 64 * half + 16 * st + r + b, j = kt * kKT + key;
-                  const uint32_t q = par[b * ng + (c >> gsh)];
-                  bool in = (have >> st & 1u) && j < end;
-                  // a value that is not finite stays out of a tile that some row sees only in part
-                  if (in && j >= all && !(fabsf(__uint_as_float(q & 0xFFFF0000u)) <= 3.0e38f)) {
-                    found = true;
-                    in = false;
-                  }
-                  place(vd, key, c, g2, in ? codes_bf16(__byte_perm(lo, hi, b ? 0x7632u : 0x5410u), q)
-                                           : make_uint4(0, 0, 0, 0));
+                for (int c = 0; c < NC4; ++c) {
+                  vw[b][c] = __byte_perm(lo[c], hi[c], b ? 0x7632u : 0x5410u);
+                  vp[b][c] = par[b * ng + (c >> gsh)];
+                  wide |= wide_zp(vp[b][c]);
                 }
+                // a value that is not finite stays out of a tile that some row sees only in part
+                if (vk[b] && j >= all) {
+#pragma unroll
+                  for (int c = 0; c < NC4; ++c)
+                    if ((vp[b][c] & 0x7F800000u) == 0x7F800000u) {
+                      vk[b] &= ~(1u << c);
+                      found = true;
+                    }
+                }
+              }
+            }
+            if (!__any_sync(0xFFFFFFFFu, wide)) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                put_row<false, NC4>(kd, 64 * half + 16 * (ks + 2 * i) + kr, ku, kw[i], kp[i], kk[i]);
+                put_row<false, NC4>(vd, 64 * half + 16 * vs + 2 * vr + i, ku, vw[i], vp[i], vk[i]);
+              }
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < 2; ++i) {
+                put_row<true, NC4>(kd, 64 * half + 16 * (ks + 2 * i) + kr, ku, kw[i], kp[i], kk[i]);
+                put_row<true, NC4>(vd, 64 * half + 16 * vs + 2 * vr + i, ku, vw[i], vp[i], vk[i]);
               }
             }
             __syncwarp();
