@@ -4,29 +4,28 @@
 // The tensor-core kernel of attn_tc.cu (tcgen05, scores and results in tensor
 // memory), whose tiles of 128 keys and values are made here from the codes: warp
 // 8 fetches the strips of 64 keys by bulk copies, three such halves in flight,
-// and four more warps turn them into bf16 tiles in shared memory, (code - zp) s
-// rounded once (2^-9 of a value).  The warpgroups that compute the weights have
-// 200 registers a thread, the others 56.
+// and two more warpgroups turn the codes of keys and of values into bf16 tiles in
+// shared memory, (code - zp) s rounded once (2^-8 of a value).
 #include "attn_tc_body.cuh"
 #include "kv4.h"
 
 namespace qmm {
 namespace {
 
-// NC: chunks of 32 dimensions.
+// NC: chunks of 32 dimensions; CPG: chunks of a group.
 template <int NC>
 using Tc4 = Tc<(NC + 1) / 2, false, true>;
 
-template <int NC>
+template <int NC, int CPG>
 __global__ void __launch_bounds__(Tc4<NC>::threads, 1)
     attn4_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ TcAttn p,
                     const __grid_constant__ Kv4 c) {
-  attn_tc_body<(NC + 1) / 2, true, false, NC>(tm_q, tm_q, tm_q, p, c);
+  attn_tc_body<(NC + 1) / 2, true, false, NC, CPG>(tm_q, tm_q, tm_q, p, c);
 }
 
-template <int NC>
+template <int NC, int CPG>
 cudaError_t run_tc(const CUtensorMap &q, const TcAttn &p, const Kv4 &c, int workers, cudaStream_t s) {
-  auto kern = attn4_tc_kernel<NC>;
+  auto kern = attn4_tc_kernel<NC, CPG>;
   constexpr uint32_t smem = Tc4<NC>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory");
   const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
@@ -56,11 +55,12 @@ cudaError_t launch_attn4_tc(const AttnBatch &a, const Kv4 &c, const AttnPlan &pl
   if (!p.status) return cudaErrorInvalidDevice;
   CUtensorMap q;
   if (!map_rows(&q, a.q, a.T, a.q_stride, a.n_head, a.head_dim, p.gsub, p.tpt)) return cudaErrorInvalidValue;
+  const bool two = c.cpg == 2;
   switch (c.nc) {
-    case 1: return run_tc<1>(q, p, c, pl.workers, s);
-    case 2: return run_tc<2>(q, p, c, pl.workers, s);
-    case 3: return run_tc<3>(q, p, c, pl.workers, s);
-    default: return run_tc<4>(q, p, c, pl.workers, s);
+    case 1: return run_tc<1, 1>(q, p, c, pl.workers, s);
+    case 2: return two ? run_tc<2, 2>(q, p, c, pl.workers, s) : run_tc<2, 1>(q, p, c, pl.workers, s);
+    case 3: return two ? run_tc<3, 2>(q, p, c, pl.workers, s) : run_tc<3, 1>(q, p, c, pl.workers, s);
+    default: return two ? run_tc<4, 2>(q, p, c, pl.workers, s) : run_tc<4, 1>(q, p, c, pl.workers, s);
   }
 }
 

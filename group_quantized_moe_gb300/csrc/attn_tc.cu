@@ -54,7 +54,7 @@ template <int NCH, bool PAGED, bool STAGED>
 __global__ void __launch_bounds__(Tc<NCH, STAGED, false>::threads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcAttn p) {
-  attn_tc_body<NCH, PAGED, STAGED, 0>(tm_q, tm_k, tm_v, p, Kv4{});
+  attn_tc_body<NCH, PAGED, STAGED, 0, 1>(tm_q, tm_k, tm_v, p, Kv4{});
 }
 
 // bf16 [block][n_kv][block_size][head_dim] as a 4-D map, box [64 columns,

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kKT = 128;              // keys per tile
 constexpr int kWarpKv = 8, kWarpMma = 9, kWarpClean = 10, kWarpQ = 11;
-constexpr int kWarpCodes = 12, kCodeWarps = 4;  // 4-bit cache: codes to bf16
+constexpr int kWarpCodes = 12;        // 4-bit cache: four warps for keys, four for values, to bf16
 constexpr int kRaw = 3;               // half tiles of codes in flight
 constexpr uint32_t kChunk = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
 constexpr int kUnits = 4;             // units in the ring between warp 11 and the others
@@ -31,7 +31,7 @@ constexpr float kRescale = 8.0f;      // log2 of the growth of the maximum that 
 // rows to store).
 template <int NCH, bool STAGED, bool Q4>
 struct Tc {
-  static constexpr int threads = Q4 ? 512 : 384;
+  static constexpr int threads = Q4 ? 640 : 384;
   static constexpr uint32_t tile = NCH * kChunk;            // one Q, K or V tile
   static constexpr int stages = NCH == 1 ? (STAGED || Q4 ? 8 : 10) : (STAGED || Q4 ? 4 : 5);  // K, V in turn
   static constexpr uint32_t q_off = 0, kv_off = 2 * tile;
@@ -231,17 +231,18 @@ struct Dequant {
 };
 
 // Eight dimensions of every chunk of a row (unit: which eight), from their words
-// and the parameters of the chunks, to row `key` of a tile.
-template <bool WIDE, int NC>
+// and the groups' parameters, to row `key` of a tile; zeros for a group that is
+// not to be kept.
+template <bool WIDE, int NC, int CPG>
 __device__ __forceinline__ void put_row(uint8_t *tile, int key, int unit, const uint32_t (&w)[NC],
-                                        const uint32_t (&par)[NC], uint32_t keep) {
+                                        const uint32_t (&par)[(NC + CPG - 1) / CPG], uint32_t keep) {
   uint8_t *const row = tile + key * 128;
+  Dequant<WIDE> q;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    Dequant<WIDE> q;
-    q.set(par[c]);
+    if (c % CPG == 0) q.set(par[c / CPG]);
     uint4 v = q.of(w[c]);
-    if (!(keep >> c & 1u)) v = make_uint4(0, 0, 0, 0);
+    if (!(keep >> (c / CPG) & 1u)) v = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4 *>(row + (c >> 1) * kChunk + ((((c & 1) * 4 + unit) ^ (key & 7)) << 4)) = v;
   }
 }
@@ -261,12 +262,13 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint32_t *p) {
   }
 }
 
-// Q4: keys and values from the 4-bit cache c4, of NC4 chunks of 32 dimensions (tm_k,
-// tm_v not used); 0: bf16.
-template <int NCH, bool PAGED, bool STAGED, int NC4>
+// Q4: keys and values from the 4-bit cache c4, of NC4 chunks of 32 dimensions, CPG4
+// to a group (tm_k, tm_v not used); 0: bf16.
+template <int NCH, bool PAGED, bool STAGED, int NC4, int CPG4>
 __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                              const TcAttn &p, const Kv4 &c4) {
   constexpr bool Q4 = NC4 > 0;
+  constexpr int G4 = Q4 ? (NC4 + CPG4 - 1) / CPG4 : 1;
   static_assert(!Q4 || (PAGED && !STAGED), "a 4-bit cache is paged, and leaves no room to stage rows");
   using C = Tc<NCH, STAGED, Q4>;
   constexpr int kThreads = C::threads;
@@ -313,17 +315,17 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
     }
     for (int k = 0; k < kUnits; ++k) {
       mbar_init(u_full(k), 1);
-      mbar_init(u_free(k), Q4 ? 10 + kCodeWarps : 11);  // warps 0-7, 8, 9, 10 (Q4: 12 to 15)
+      mbar_init(u_free(k), Q4 ? 18 : 11);  // warps 0-7, 8, 9, 10 (Q4: 12 to 19)
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
       mbar_init(freed(s), Q4 ? 1 : 2);  // the tensor core's and warp 10's
-      mbar_init(clean(s), Q4 ? kCodeWarps : 1);
+      mbar_init(clean(s), Q4 ? 4 : 1);
     }
     if constexpr (Q4)
       for (int s = 0; s < kRaw; ++s) {
         mbar_init(raw_full(s), 1);
-        mbar_init(raw_free(s), kCodeWarps);
+        mbar_init(raw_free(s), 8);
       }
     mbar_fence_init();
     *abort_flag = 0;
@@ -352,16 +354,21 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
     return __all_sync(0xFFFFFFFFu, wait_ok(bar, parity, p.status, abort_flag)) != 0;
   };
 
-  // 384 threads launched with 168 registers: 2 x 208 + 88 = 3 x 168; 512 with 128:
-  // 2 x 200 + 2 x 56 = 4 x 128
+  // 384 threads launched with 168 registers: 2 x 208 + 88 = 3 x 168; 640 with 96:
+  // 2 x 176 + 48 + 2 x 40 = 5 x 96
   if (Q4 && warp >= kWarpCodes) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if constexpr (Q4) {
       // ------------------------------------- codes to bf16 tiles of keys and values
       // A word of a key's codes is eight dimensions, 16 bytes of its row in the
       // tile; two words of values are eight dimensions of two rows.
-      const int tid = threadIdx.x - 32 * kWarpCodes, strip = kv4_strip(c4), ng = c4.ng, gsh = c4.cpg - 1;
-      int s = 0, rs = 0;
+      const int tid = threadIdx.x & 127, strip = kv4_strip(c4), ng = c4.ng;
+      const bool values = warp >= kWarpCodes + 4;
+      // This thread's part of 64 keys: eight dimensions (which: part) of every chunk of
+      // two rows.  Keys: rows kr of strips ks and ks + 2; values: rows 2 vr and the next
+      // of strip vs, which share their words.
+      const int part = tid & 3, ks = tid >> 6, kr = tid >> 2 & 15, vs = tid >> 5, vr = lane >> 2;
+      int s = values ? 1 : 0, rs = 0;
       uint32_t phase = 1, raw_phase = 0;
       bool ok = true;
       for (uint32_t un = 0; ok; ++un) {
@@ -369,75 +376,64 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         const Unit &ur = units[un % kUnits];
         if (!ur.valid) break;
         const int tile = ur.tile, stop = ur.stop, all = ur.all, end = ur.end;
-        for (int kt = tile; kt < stop && ok; ++kt) {
-          // (stages are even in number: K and V have the same phase)
-          if (!(ok = wait_warp(freed(s), phase) && wait_warp(freed(s + 1), phase))) break;
-          uint8_t *const kd = gbase + C::kv_off + s * C::tile, *const vd = kd + C::tile;
+        for (int kt = tile; kt < stop; ++kt) {
+          if (!(ok = wait_warp(freed(s), phase))) break;
+          uint8_t *const dst = gbase + C::kv_off + s * C::tile;
           bool found = false;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            const int k0 = kt * kKT + 64 * half;
-            const bool some = k0 < end;
+            const bool some = kt * kKT + 64 * half < end;
             if (some && !(ok = wait_warp(raw_full(rs), raw_phase))) break;
             const uint32_t have = some ? raw_strips[rs] : 0u;
             const uint8_t *const raw = gbase + C::raw_off + rs * C::raw;
-            // this thread's part: eight dimensions a chunk of two keys (rows kr of strips
-            // ks, ks + 2) and of two rows of values
-            const int ks = tid >> 6, kr = tid >> 2 & 15, ku = tid & 3, vs = tid >> 5, vr = lane >> 2;
-            uint32_t kw[2][NC4], kp[2][NC4], vw[2][NC4], vp[2][NC4], kk[2], vk[2], wide = 0;
+            uint32_t w[2][NC4], par[2][G4], keep[2], wide = 0;
+            int key[2];  // rows in the tile
+            if (!values) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int st = ks + 2 * i, key = 64 * half + 16 * st + kr;
-              kk[i] = (have >> st & 1u) && kt * kKT + key < end ? 0xFFu : 0u;
-              lds_words<NC4>(kw[i], reinterpret_cast<const uint32_t *>(raw + st * strip) + (kr * 4 + ku) * NC4);
-              const uint32_t *const par = reinterpret_cast<const uint32_t *>(raw + st * strip + 512 * NC4) + kr * ng;
+              for (int i = 0; i < 2; ++i) {
+                const int st = ks + 2 * i;
+                key[i] = 64 * half + 16 * st + kr;
+                keep[i] = (have >> st & 1u) && kt * kKT + key[i] < end ? 0xFFu : 0u;
+                lds_words<NC4>(w[i], reinterpret_cast<const uint32_t *>(raw + st * strip) + (kr * 4 + part) * NC4);
+                lds_words<G4>(par[i], reinterpret_cast<const uint32_t *>(raw + st * strip + 512 * NC4) + kr * ng);
+              }
+            } else {
+              const uint32_t *const words = reinterpret_cast<const uint32_t *>(raw + vs * strip + 256 * NC4) +
+                                            (((vr >> 2) * 8 + 2 * part) * 4 + (vr & 3)) * NC4;
+              lds_words<NC4>(w[0], words);
+              lds_words<NC4>(w[1], words + 4 * NC4);
 #pragma unroll
               for (int c = 0; c < NC4; ++c) {
-                kp[i][c] = par[c >> gsh];
-                wide |= wide_zp(kp[i][c]);
+                const uint32_t lo = w[0][c], hi = w[1][c];
+                w[0][c] = __byte_perm(lo, hi, 0x5410u);
+                w[1][c] = __byte_perm(lo, hi, 0x7632u);
               }
-            }
-            {
-              uint32_t lo[NC4], hi[NC4];
-              const uint32_t *const words = reinterpret_cast<const uint32_t *>(raw + vs * strip + 256 * NC4) +
-                                            (((vr >> 2) * 8 + 2 * ku) * 4 + (vr & 3)) * NC4;
-              lds_words<NC4>(lo, words);
-              lds_words<NC4>(hi, words + 4 * NC4);
-              const uint32_t *const par =
-                  reinterpret_cast<const uint32_t *>(raw + vs * strip + 512 * NC4 + 64 * ng) + 2 * vr * ng;
 #pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const int j = kt * kKT + 64 * half + 16 * vs + 2 * vr + b;
-                vk[b] = (have >> vs & 1u) && j < end ? 0xFFu : 0u;
-#pragma unroll
-                for (int c = 0; c < NC4; ++c) {
-                  vw[b][c] = __byte_perm(lo[c], hi[c], b ? 0x7632u : 0x5410u);
-                  vp[b][c] = par[b * ng + (c >> gsh)];
-                  wide |= wide_zp(vp[b][c]);
-                }
+              for (int i = 0; i < 2; ++i) {
+                key[i] = 64 * half + 16 * vs + 2 * vr + i;
+                const int j = kt * kKT + key[i];
+                keep[i] = (have >> vs & 1u) && j < end ? 0xFFu : 0u;
+                lds_words<G4>(par[i], reinterpret_cast<const uint32_t *>(raw + vs * strip + 512 * NC4 + 64 * ng) +
+                                          (2 * vr + i) * ng);
                 // a value that is not finite stays out of a tile that some row sees only in part
-                if (vk[b] && j >= all) {
+                if (keep[i] && j >= all) {
 #pragma unroll
-                  for (int c = 0; c < NC4; ++c)
-                    if ((vp[b][c] & 0x7F800000u) == 0x7F800000u) {
-                      vk[b] &= ~(1u << c);
+                  for (int g = 0; g < G4; ++g)
+                    if ((par[i][g] & 0x7F800000u) == 0x7F800000u) {
+                      keep[i] &= ~(1u << g);
                       found = true;
                     }
                 }
               }
             }
+#pragma unroll
+            for (int g = 0; g < G4; ++g) wide |= wide_zp(par[0][g]) | wide_zp(par[1][g]);
             if (!__any_sync(0xFFFFFFFFu, wide)) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                put_row<false, NC4>(kd, 64 * half + 16 * (ks + 2 * i) + kr, ku, kw[i], kp[i], kk[i]);
-                put_row<false, NC4>(vd, 64 * half + 16 * vs + 2 * vr + i, ku, vw[i], vp[i], vk[i]);
-              }
+              for (int i = 0; i < 2; ++i) put_row<false, NC4, CPG4>(dst, key[i], part, w[i], par[i], keep[i]);
             } else {
-#pragma unroll 1
-              for (int i = 0; i < 2; ++i) {
-                put_row<true, NC4>(kd, 64 * half + 16 * (ks + 2 * i) + kr, ku, kw[i], kp[i], kk[i]);
-                put_row<true, NC4>(vd, 64 * half + 16 * vs + 2 * vr + i, ku, vw[i], vp[i], vk[i]);
-              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) put_row<true, NC4, CPG4>(dst, key[i], part, w[i], par[i], keep[i]);
             }
             __syncwarp();
             if (some) {
@@ -452,13 +448,10 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           if (found) marked[un & 15u] = static_cast<int>(un + 1);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(clean(s));
-            mbar_arrive(clean(s + 1));
-          }
+          if (lane == 0) mbar_arrive(clean(s));
           s += 2;
-          if (s == NS) {
-            s = 0;
+          if (s >= NS) {  // (the stages are even in number)
+            s -= NS;
             phase ^= 1u;
           }
         }
@@ -467,7 +460,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
     }
   } else if (warp >= 8) {
     if constexpr (Q4)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpQ) {
@@ -836,7 +829,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
     __syncwarp();
   } else {
     if constexpr (Q4)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------- warpgroups
