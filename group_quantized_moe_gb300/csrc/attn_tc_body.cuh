@@ -231,19 +231,16 @@ struct Dequant {
 };
 
 // Eight dimensions of every chunk of a row (unit: which eight), from their words
-// and the groups' parameters, to row `key` of a tile; zeros for a group that is
-// not to be kept.
+// and the groups' parameters (0 gives zeros), to row `key` of a tile.
 template <bool WIDE, int NC, int CPG>
 __device__ __forceinline__ void put_row(uint8_t *tile, int key, int unit, const uint32_t (&w)[NC],
-                                        const uint32_t (&par)[(NC + CPG - 1) / CPG], uint32_t keep) {
+                                        const uint32_t (&par)[(NC + CPG - 1) / CPG]) {
   uint8_t *const row = tile + key * 128;
   Dequant<WIDE> q;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     if (c % CPG == 0) q.set(par[c / CPG]);
-    uint4 v = q.of(w[c]);
-    if (!(keep >> (c / CPG) & 1u)) v = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4 *>(row + (c >> 1) * kChunk + ((((c & 1) * 4 + unit) ^ (key & 7)) << 4)) = v;
+    *reinterpret_cast<uint4 *>(row + (c >> 1) * kChunk + ((((c & 1) * 4 + unit) ^ (key & 7)) << 4)) = q.of(w[c]);
   }
 }
 
@@ -386,16 +383,18 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
             if (some && !(ok = wait_warp(raw_full(rs), raw_phase))) break;
             const uint32_t have = some ? raw_strips[rs] : 0u;
             const uint8_t *const raw = gbase + C::raw_off + rs * C::raw;
-            uint32_t w[2][NC4], par[2][G4], keep[2], wide = 0;
+            uint32_t w[2][NC4], par[2][G4], wide = 0;
             int key[2];  // rows in the tile
             if (!values) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int st = ks + 2 * i;
                 key[i] = 64 * half + 16 * st + kr;
-                keep[i] = (have >> st & 1u) && kt * kKT + key[i] < end ? 0xFFu : 0u;
+                const bool in = (have >> st & 1u) && kt * kKT + key[i] < end;
                 lds_words<NC4>(w[i], reinterpret_cast<const uint32_t *>(raw + st * strip) + (kr * 4 + part) * NC4);
                 lds_words<G4>(par[i], reinterpret_cast<const uint32_t *>(raw + st * strip + 512 * NC4) + kr * ng);
+#pragma unroll
+                for (int g = 0; g < G4; ++g) par[i][g] = in ? par[i][g] : 0u;
               }
             } else {
               const uint32_t *const words = reinterpret_cast<const uint32_t *>(raw + vs * strip + 256 * NC4) +
@@ -412,17 +411,15 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               for (int i = 0; i < 2; ++i) {
                 key[i] = 64 * half + 16 * vs + 2 * vr + i;
                 const int j = kt * kKT + key[i];
-                keep[i] = (have >> vs & 1u) && j < end ? 0xFFu : 0u;
+                const bool in = (have >> vs & 1u) && j < end;
                 lds_words<G4>(par[i], reinterpret_cast<const uint32_t *>(raw + vs * strip + 512 * NC4 + 64 * ng) +
                                           (2 * vr + i) * ng);
-                // a value that is not finite stays out of a tile that some row sees only in part
-                if (keep[i] && j >= all) {
 #pragma unroll
-                  for (int g = 0; g < G4; ++g)
-                    if ((par[i][g] & 0x7F800000u) == 0x7F800000u) {
-                      keep[i] &= ~(1u << g);
-                      found = true;
-                    }
+                for (int g = 0; g < G4; ++g) {
+                  // a value that is not finite stays out of a tile that some row sees only in part
+                  const bool out = j >= all && (par[i][g] & 0x7F800000u) == 0x7F800000u;
+                  found |= in && out;
+                  par[i][g] = in && !out ? par[i][g] : 0u;
                 }
               }
             }
@@ -430,10 +427,10 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
             for (int g = 0; g < G4; ++g) wide |= wide_zp(par[0][g]) | wide_zp(par[1][g]);
             if (!__any_sync(0xFFFFFFFFu, wide)) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) put_row<false, NC4, CPG4>(dst, key[i], part, w[i], par[i], keep[i]);
+              for (int i = 0; i < 2; ++i) put_row<false, NC4, CPG4>(dst, key[i], part, w[i], par[i]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) put_row<true, NC4, CPG4>(dst, key[i], part, w[i], par[i], keep[i]);
+              for (int i = 0; i < 2; ++i) put_row<true, NC4, CPG4>(dst, key[i], part, w[i], par[i]);
             }
             __syncwarp();
             if (some) {
