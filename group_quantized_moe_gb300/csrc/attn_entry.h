@@ -109,10 +109,11 @@ inline PartsLayout parts_layout(const AttnPlan &p, int head_dim) {
 }
 
 // Runs a planned call: carves the workspace, cuts the call up, launches the
-// kernel and, where units may be divided, the one that joins their parts.
+// kernel and, where units may be divided, the one that joins their parts.  For
+// the requests of lo + 1 to hi tokens.
 template <typename Launch>
 cudaError_t run_attn_plan(const AttnBatch &a, const AttnPlan &p, void *workspace, cudaStream_t s,
-                          Launch launch) {
+                          Launch launch, int lo = 0, int hi = 0x7FFFFFFF) {
   const PartsLayout l = parts_layout(p, a.head_dim);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   AttnParts parts{reinterpret_cast<AttnOpen *>(base + l.open),
@@ -125,7 +126,7 @@ cudaError_t run_attn_plan(const AttnBatch &a, const AttnPlan &p, void *workspace
   const bool whole = cap <= kWholeKeys && usual <= p.whole;
   AttnSched sc{a.cu, a.kvl, a.R, a.n_kv * p.nsub, p.U, log2i(p.KT), p.fixed, p.min_run,
                ~uint64_t(0) / static_cast<uint64_t>(p.workers) + 1, whole, a.T,
-               static_cast<int>(cap)};
+               static_cast<int>(cap), lo, hi};
   const cudaError_t e = launch(sc, parts);
   if (e != cudaSuccess || whole) return e;
   return launch_attn_join(a, p, parts, s);

@@ -45,6 +45,7 @@ struct AttnSched {
   bool whole;          // units are not divided: each goes to the run that holds its start
   int64_t T;           // query rows in the buffers
   int cap;             // keys the block table can hold (below 2^29)
+  int lo = 0, hi = 0x7FFFFFFF;  // requests of lo + 1 .. hi tokens have units here
 };
 
 struct AttnReq {
@@ -60,6 +61,7 @@ __device__ __forceinline__ AttnReq sched_req(const AttnSched &s, int r) {
   const int64_t hi = b < lo ? lo : (b > s.T ? s.T : b);
   q.q0 = static_cast<int>(lo);
   q.n = static_cast<int>(hi - lo);
+  if (q.n <= s.lo || q.n > s.hi) q.n = 0;  // another kernel's
   // tokens of the request, those behind the buffers' end included: the rows
   // that there are keep their keys.  2^30 rows: more than any table holds, for
   // each of its tokens

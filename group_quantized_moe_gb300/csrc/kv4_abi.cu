@@ -1,6 +1,5 @@
 // kv4_abi.cu -- extern "C" entry points of the paged cache held in 4 bits:
 // argument validation and kernel selection.  Declared in include/qmm.h.
-#include <cstdlib>
 #include "attn_entry.h"
 #include "kv4.h"
 
@@ -55,27 +54,56 @@ int check_kv4(const char *who, const qmm_kv4_cache *c, Kv4 *out) {
 
 }  // namespace
 
-// Query rows that a request has for a key/value head, on average, above which
-// the form for many rows is the faster one.
-static bool many_rows(const Kv4 &c, int64_t T, int n_head, int R) {
-  static const char *e = getenv("TCR");
-  return T * (n_head / c.n_kv) > static_cast<int64_t>(e ? atoi(e) : 24) * R;
+namespace {
+
+// The forms for few and for many query rows of a key/value head cost the same at
+// about 24 rows a request (40 requests of 2000 keys, 32 heads over 8: 16 rows 73
+// and 88 us, 24 rows 100 and 89 us, 48 rows 178 and 93 us).  Where a call has long
+// chunks and may have single tokens beside them, each takes its own: 20 requests,
+// four of them chunks, 0.87 ms instead of 1.00 in the form for many alone.  How
+// long a request is stands on the device only, so both are launched, and find their
+// requests there; an empty one costs 4 us, which 1024 rows beyond one token a
+// request outweigh.
+struct Split {
+  bool few, many;
+  int tokens;  // of a request, up to which it goes to the form for few
+};
+
+Split split_rows(const Kv4 &c, int64_t T, int n_head, int R) {
+  constexpr int kRows = 24, kLong = 1024;
+  const int64_t grp = n_head / c.n_kv;
+  if (R > 1 && (T - R) * grp >= kLong) return {true, true, static_cast<int>(kRows / grp)};
+  const bool many = T * grp > static_cast<int64_t>(kRows) * R;
+  return {!many, many, 0};
 }
 
+}  // namespace
+
 size_t attn4_workspace_bytes(const Kv4 &c, bool q_bf16, int64_t T, int n_head, int R) {
-  // whether a call of many rows takes the form for them also depends on its stride
+  // whether a call takes the form for many rows also depends on its stride
   const size_t few = parts_layout(attn4_rows_plan(c, n_head), c.head_dim).total;
-  if (!q_bf16 || c.head_dim > 128 || !many_rows(c, T, n_head, R)) return few;
-  const size_t many = parts_layout(attn_tc_plan(true, T, n_head, c.n_kv, R), c.head_dim).total;
-  return many > few ? many : few;
+  if (!q_bf16 || c.head_dim > 128) return few;
+  const Split f = split_rows(c, T, n_head, R);
+  const size_t many = f.many ? parts_layout(attn_tc_plan(true, T, n_head, c.n_kv, R), c.head_dim).total : 0;
+  return f.few ? few + many : many > few ? many : few;
 }
 
 cudaError_t launch_attn4(const AttnBatch &a, const Kv4 &c, void *workspace, cudaStream_t s) {
-  const bool tc = many_rows(c, a.T, a.n_head, a.R) && attn4_tc_takes(a);
-  const AttnPlan p = tc ? attn_tc_plan(true, a.T, a.n_head, a.n_kv, a.R) : attn4_rows_plan(c, a.n_head);
-  return run_attn_plan(a, p, workspace, s, [&](const AttnSched &sc, const AttnParts &parts) {
-    return tc ? launch_attn4_tc(a, c, p, sc, parts, s) : launch_attn4_rows(a, c, p, sc, parts, s);
-  });
+  const AttnPlan few = attn4_rows_plan(c, a.n_head);
+  const auto run_few = [&](const AttnSched &sc, const AttnParts &parts) {
+    return launch_attn4_rows(a, c, few, sc, parts, s);
+  };
+  const Split f = split_rows(c, a.T, a.n_head, a.R);
+  if (!f.many || !attn4_tc_takes(a)) return run_attn_plan(a, few, workspace, s, run_few);
+  const AttnPlan many = attn_tc_plan(true, a.T, a.n_head, a.n_kv, a.R);
+  const auto run_many = [&](const AttnSched &sc, const AttnParts &parts) {
+    return launch_attn4_tc(a, c, many, sc, parts, s);
+  };
+  if (!f.few) return run_attn_plan(a, many, workspace, s, run_many);
+  const cudaError_t e = run_attn_plan(a, few, workspace, s, run_few, 0, f.tokens);
+  if (e != cudaSuccess) return e;
+  return run_attn_plan(a, many, static_cast<uint8_t *>(workspace) + parts_layout(few, c.head_dim).total, s, run_many,
+                       f.tokens);
 }
 
 }  // namespace qmm

@@ -180,10 +180,14 @@ def attend(q, keys, vals, group, visible, scale, q32, tiles=False):
 
 
 def paged(q, data, group, S, table, lens, scale, q32):
-    """lens: (cache rows, new tokens) of each request.  More than 24 query rows to a
-    key/value head and request, on average: tiles."""
+    """lens: (cache rows, new tokens) of each request.  Tiles: requests with more
+    than 24 query rows to a key/value head in a call of 1024 such rows beyond a
+    token a request, all requests of other calls with more than 24 on average."""
     nb, hd = data.shape[0], q.shape[2]
-    tiles = not q32 and hd <= 128 and len(q) * (q.shape[1] // data.shape[1]) > 24 * len(lens)
+    grp, R = q.shape[1] // data.shape[1], len(lens)
+    tc = not q32 and hd <= 128
+    both = R > 1 and (len(q) - R) * grp >= 1024
+    tiles = [tc and (n * grp > 24 if both else len(q) * grp > 24 * R) for _, n in lens]
     kk, vv = unpack(data, hd, group, S)
     parts, t = [], 0
     for r, (L, n) in enumerate(lens):
@@ -193,7 +197,7 @@ def paged(q, data, group, S, table, lens, scale, q32):
         ids = np.where(ok, ids, 0)
         rows = [[t_[ids, :, j % S] for t_ in part] for part in (kk, vv)]
         vis = (j[None, :] <= (L - n + np.arange(n))[:, None]) & ok[None, :]
-        parts.append(attend(q[t:t + n], *rows, group, vis, scale, q32, tiles))
+        parts.append(attend(q[t:t + n], *rows, group, vis, scale, q32, tiles[r]))
         t += n
     pad = (len(q) - t,) + q.shape[1:]
     return (np.concatenate([y for y, _ in parts] + [np.zeros(pad)]),

@@ -257,6 +257,14 @@ def test_attend_few_tokens_each(dev, n, dtype):
     run_attend([(900, n), (n, n), (40, n), (2, n)], 8, 2, 128, 64, 16, dtype, bad=[(0, 50)])
 
 
+@pytest.mark.parametrize("nh,nkv,hd,group", [(8, 2, 128, 64), (28, 4, 80, 32), (32, 1, 64, 32), (4, 4, 32, 32)])
+def test_attend_chunks_beside_single_tokens(dev, nh, nkv, hd, group):
+    """Long chunks and short requests in one call: each goes to its own kernel."""
+    run_attend([(1, 1), (700, 600), (33, 1), (900, 1), (300, 300), (0, 1), (64, 3), (12, 40), (0, 0), (512, 200)],
+               nh, nkv, hd, group, 16, BF16, BF16, pad=3, bad=[(1, 9), (3, 20)])
+    run_attend([(1500, 1200), (40, 1)], nh, nkv, hd, group, 64, BF16)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attend_rows_that_see_no_key(dev, dtype):
     run_attend([(3, 10), (0, 4), (130, 140), (1, 300), (-5, 2)], 4, 2, 64, 32, 16, dtype)
