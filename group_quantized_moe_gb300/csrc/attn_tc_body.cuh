@@ -3,6 +3,8 @@
 // 4 bits).  What they compute and how their warps share it stands there.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <cstdint>
 
 #include "attn_batch.h"
@@ -41,11 +43,13 @@ struct Tc {
   static constexpr uint32_t bar_off = out_off + (STAGED ? 8 * 4096 : 0);
   // q_full[2], q_free[2], x_full, drain, s_full[2], p_full[2][2], o_full[2],
   // u_full[kUnits], u_free[kUnits], then full, freed, clean [stages], and raw_full,
-  // raw_free [kRaw]
-  static constexpr int nbar = 14 + 2 * kUnits + 3 * stages + 2 * kRaw;
+  // raw_free [kRaw], q_ready [kUnits + 1]
+  static constexpr int nbar = 14 + 2 * kUnits + 3 * stages + 2 * kRaw + kUnits + 1;
   static constexpr uint32_t unit_off = (bar_off + nbar * 8 + 15) & ~15u;
   static constexpr uint32_t misc_off = unit_off + kUnits * 64;  // tmem, abort, bad, -, marked[16], strips[kRaw + 1]
-  static constexpr uint32_t bytes = misc_off + 96 + 2 * 128 * 4 + 1024;
+  // 4-bit keys: by tile, whether a warp scaled rows of it [4], what they are to be multiplied by [128]
+  static constexpr uint32_t key_off = misc_off + 96 + 2 * 128 * 4;
+  static constexpr uint32_t bytes = key_off + (Q4 ? stages / 2 * 528 : 0) + 1024;
   static constexpr uint32_t o_col = 256, o_step = NCH * 64;  // tensor memory columns of O
 };
 
@@ -115,9 +119,9 @@ __device__ __forceinline__ uint64_t desc_values(uint32_t addr) {
          (static_cast<uint64_t>(2) << 61);
 }
 
-// bf16 x bf16 -> fp32, M = 128; values: B with N contiguous.
-__device__ __forceinline__ uint32_t idesc_bf16(int n, bool values) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (values ? 1u << 16 : 0u) |
+// bf16 x bf16 (f16: fp16 x fp16) -> fp32, M = 128; values: B with N contiguous.
+__device__ __forceinline__ uint32_t idesc_bf16(int n, bool values, bool f16 = false) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (values ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
@@ -244,6 +248,95 @@ __device__ __forceinline__ void put_row(uint8_t *tile, int key, int unit, const 
   }
 }
 
+// A key row's like it in fp16, which holds (code - zp) s to 2^-11 of it where bf16
+// holds 2^-8 (with bf16 keys a chunk's result is off by 0.0028 of its norm, with
+// fp16 ones 0.0020): scores magnify what is lost.  s: scales that have been
+// brought into fp16's range.
+__device__ __forceinline__ bool wide_zp16(uint32_t par) { return (par & 0x7FFFu) > 0x63D0u; }  // above 1000
+template <bool WIDE, int NC, int CPG>
+__device__ __forceinline__ void put_key(uint8_t *tile, int key, int unit, const uint32_t (&w)[NC],
+                                        const uint32_t (&par)[(NC + CPG - 1) / CPG], float scale) {
+  uint8_t *const row = tile + key * 128;
+  __half2 z2, s2;
+  float zf = 0.0f, sf = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (c % CPG == 0) {
+      zf = __half2float(__ushort_as_half(static_cast<unsigned short>(par[c / CPG])));
+      sf = __uint_as_float(par[c / CPG] & 0xFFFF0000u) * scale;
+      z2 = __float2half2_rn(1024.0f + zf);
+      s2 = __float2half2_rn(sf);
+    }
+    uint32_t r[4];
+    const uint32_t x = w[c] & 0x0F0F0F0Fu, y = w[c] >> 4 & 0x0F0F0F0Fu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (WIDE) {
+        const __half2 v = __floats2half2_rn((static_cast<float>(x >> (8 * i) & 15u) - zf) * sf,
+                                            (static_cast<float>(y >> (8 * i) & 15u) - zf) * sf);
+        r[i] = *reinterpret_cast<const uint32_t *>(&v);
+      } else {  // 0x6400 + code: 1024 + code
+        const uint32_t t = (__byte_perm(x, y, 0x0400u + 0x0101u * i) & 0x00FF00FFu) | 0x64006400u;
+        const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&t), z2), s2);
+        r[i] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+    }
+    *reinterpret_cast<uint4 *>(row + (c >> 1) * kChunk + ((((c & 1) * 4 + unit) ^ (key & 7)) << 4)) =
+        make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
+
+__device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }
+
+// Power of two by which a key row is divided for fp16: none where its largest
+// value lies in [2^-10, 2^15), or where it is all zeros.
+template <int G>
+__device__ __forceinline__ int key_exponent(const uint32_t (&par)[G]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const float zf = __half2float(__ushort_as_half(static_cast<unsigned short>(par[g])));
+    top = fmaxf(top, __uint_as_float(par[g] & 0xFFFF0000u) * fmaxf(fabsf(zf), fabsf(15.0f - zf)));
+  }
+  if ((top >= 0x1p-10f && top < 0x1p15f) || top < 0x1p-96f) return 0;
+  return static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13;
+}
+
+// A query row of a tile from bf16 to fp16, times 2^E with its largest element in
+// [2^14, 2^15); returns E.  (An element of 2^114 or more becomes infinite.)
+template <int NCH>
+__device__ __forceinline__ int scale_query(uint8_t *tile, int row, int nch) {
+  uint4 v[NCH * 8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[8 * c + j] = c < nch ? *reinterpret_cast<const uint4 *>(tile + c * kChunk + row * 128 + ((j ^ (row & 7)) << 4))
+                             : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {v[8 * c + j].x, v[8 * c + j].y, v[8 * c + j].z, v[8 * c + j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7FFFu, x[i] >> 16 & 0x7FFFu));
+    }
+  // of bf16 bits; not finite: as it is
+  const int E = top == 0 || top >= 0x7F80u ? 0 : max(-100, min(14 - (static_cast<int>(top >> 7) - 127), 100));
+  const float up = pow2_of(E);
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t x[4] = {v[8 * c + j].x, v[8 * c + j].y, v[8 * c + j].z, v[8 * c + j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
+        x[i] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+      if (c < nch)
+        *reinterpret_cast<uint4 *>(tile + c * kChunk + row * 128 + ((j ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+  return E;
+}
+
 // N words of shared memory.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint32_t *p) {
@@ -289,6 +382,9 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
   auto clean = [&](int s) { return bars + kStageBars + 8 * (2 * NS + s); };
   auto raw_full = [&](int s) { return bars + kStageBars + 8 * (3 * NS + s); };
   auto raw_free = [&](int s) { return bars + kStageBars + 8 * (3 * NS + kRaw + s); };
+  // queries in fp16: tile A by unit (not every warp waits for every unit's), tile B
+  auto q_ready = [&](uint32_t n) { return bars + kStageBars + 8 * (3 * NS + 2 * kRaw + n % kUnits); };
+  const uint32_t q_ready_b = bars + kStageBars + 8 * (3 * NS + 2 * kRaw + kUnits);
   Unit *units = reinterpret_cast<Unit *>(gbase + C::unit_off);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + C::misc_off);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + C::misc_off + 4);
@@ -296,6 +392,9 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
   volatile int *marked = reinterpret_cast<volatile int *>(gbase + C::misc_off + 16);  // [16]
   volatile uint32_t *raw_strips = reinterpret_cast<volatile uint32_t *>(gbase + C::misc_off + 80);  // [kRaw]
   float *xm = reinterpret_cast<float *>(gbase + C::misc_off + 96), *xl = xm + 128;
+  // of tile s / 2: its warps' marks, its rows' factors
+  auto key_marks = [&](int s) { return reinterpret_cast<volatile uint32_t *>(gbase + C::key_off + s / 2 * 528); };
+  auto key_factors = [&](int s) { return reinterpret_cast<float *>(gbase + C::key_off + s / 2 * 528 + 16); };
   __shared__ int64_t scratch[kThreads / 32 + 4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,6 +423,8 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         mbar_init(raw_full(s), 1);
         mbar_init(raw_free(s), 8);
       }
+    if constexpr (Q4)
+      for (int k = 0; k <= kUnits; ++k) mbar_init(k < kUnits ? q_ready(k) : q_ready_b, 4);
     mbar_fence_init();
     *abort_flag = 0;
     *bad_seen = 0;
@@ -376,7 +477,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         for (int kt = tile; kt < stop; ++kt) {
           if (!(ok = wait_warp(freed(s), phase))) break;
           uint8_t *const dst = gbase + C::kv_off + s * C::tile;
-          bool found = false;
+          bool found = false, scaled = false;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             const bool some = kt * kKT + 64 * half < end;
@@ -423,14 +524,33 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
                 }
               }
             }
+            if (!values) {
+              int e[2];
 #pragma unroll
-            for (int g = 0; g < G4; ++g) wide |= wide_zp(par[0][g]) | wide_zp(par[1][g]);
-            if (!__any_sync(0xFFFFFFFFu, wide)) {
+              for (int i = 0; i < 2; ++i) {
+                e[i] = key_exponent<G4>(par[i]);
+                scaled |= e[i] != 0;
+                if (part == 0) key_factors(s)[key[i]] = pow2_of(e[i]);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) put_row<false, NC4, CPG4>(dst, key[i], part, w[i], par[i]);
+                for (int g = 0; g < G4; ++g) wide |= wide_zp16(par[i][g]);
+              }
+              if (!__any_sync(0xFFFFFFFFu, wide)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) put_key<false, NC4, CPG4>(dst, key[i], part, w[i], par[i], pow2_of(-e[i]));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) put_key<true, NC4, CPG4>(dst, key[i], part, w[i], par[i], pow2_of(-e[i]));
+              }
             } else {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) put_row<true, NC4, CPG4>(dst, key[i], part, w[i], par[i]);
+              for (int g = 0; g < G4; ++g) wide |= wide_zp(par[0][g]) | wide_zp(par[1][g]);
+              if (!__any_sync(0xFFFFFFFFu, wide)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) put_row<false, NC4, CPG4>(dst, key[i], part, w[i], par[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) put_row<true, NC4, CPG4>(dst, key[i], part, w[i], par[i]);
+              }
             }
             __syncwarp();
             if (some) {
@@ -443,6 +563,8 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           }
           if (!ok) break;
           if (found) marked[un & 15u] = static_cast<int>(un + 1);
+          scaled = __any_sync(0xFFFFFFFFu, scaled);
+          if (!values && lane == 0) key_marks(s)[warp & 3] = scaled;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(clean(s));
@@ -720,11 +842,12 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
       // thread, so a turn waits as little as it can: warp 10 passes the loads
       // in order, so that one look at the latest of them covers the others.
       const int ksteps = (hd + 15) / 16;
-      const uint32_t id_s = idesc_bf16(kKT, false), id_o = idesc_bf16(ksteps * 16, true);
+      const uint32_t id_s = idesc_bf16(kKT, false, Q4), id_o = idesc_bf16(ksteps * 16, true);
       const uint64_t kd0 = smem_desc_sw128(base + C::kv_off), vd0 = desc_values(base + C::kv_off);
       const uint64_t qd0 = smem_desc_sw128(base + C::q_off);
       uint32_t n0 = 0;                    // loads before the unit
       uint32_t ready = 0;                 // loads known to have passed warp 10
+      uint32_t ready_v = 0;               // values known to be there
       uint32_t np = 0, np_other = 0;      // P tiles taken from this / the other warpgroup
       uint32_t pairs = 0;                 // units with two query tiles so far
       bool ok = true;
@@ -748,7 +871,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         // Warpgroup 1 is the last user of every tile of a pair.
         bool held = false, held_other = false, first = true, first_other = true;
         int w = 0;
-        if (!(ok = wait(q_full(0), un & 1u))) break;
+        if (!(ok = wait(Q4 ? q_ready(un) : q_full(0), (Q4 ? un / kUnits : un) & 1u))) break;
         for (; held || held_other || cur < last || cur_other < last_other; w ^= 1) {
           const bool more = cur < last, frees = !pair || w;
           const uint32_t nk = n0 + 2 * cur, nv = n0 + 2 * (cur - step) + 1;
@@ -758,6 +881,11 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           if ((held || more) && static_cast<int>(need - ready) >= 0) {
             if (!(ok = wait(clean(need % NS), (need / NS) & 1u))) break;
             ready = need + 1;
+          }
+          // (4-bit values are made by other warps than keys, and may be behind them)
+          if (Q4 && held && static_cast<int>(nv - ready_v) >= 0) {
+            if (!(ok = wait(clean(nv % NS), (nv / NS) & 1u))) break;
+            ready_v = nv + 1;
           }
           if (held) {
             const int s = nv % NS;
@@ -782,7 +910,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               if (!(ok = wait(clean(nk % NS), (nk / NS) & 1u))) break;
               ready = nk + 1;
             }
-            if (pair && w && cur == 0 && !(ok = wait(q_full(1), pairs & 1u))) break;
+            if (pair && w && cur == 0 && !(ok = wait(Q4 ? q_ready_b : q_full(1), pairs & 1u))) break;
             const int s = nk % NS;
             const uint64_t qd = qd0 + ((pair && w) ? C::tile >> 4 : 0u);
             const uint64_t kd = kd0 + s * (C::tile >> 4);
@@ -837,6 +965,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
     // rows of a tile are (token, head) with gsub heads a token, of which g count
     const int tok = row / p.gsub, hq = row - tok * p.gsub;
     uint32_t nt = 0, no = 0, nx = 0;
+    uint32_t loaded = 0, two = 0;  // (4-bit keys) key and value tiles of earlier units; units with two query tiles
     bool ok = true;
     for (uint32_t un = 0; ok; ++un) {
       if (!(ok = wait_warp(u_full(un), (un / kUnits) & 1u))) break;
@@ -850,7 +979,23 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
       const bool busy = __any_sync(0xFFFFFFFFu, live);
       const int all = min(u.all + tw, u.end);  // keys every row of the tile sees
       const int vis = min(all + tok, u.end);   // keys this row sees
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f, sl2 = p.sl2;
+      if constexpr (Q4) {
+        // the tile's queries to fp16, each row times a power of two that its scores lose again
+        if (w == 0 || pair) {
+          if (!(ok = wait_warp(q_full(w), (w ? two : un) & 1u))) break;
+          const int E = scale_query<NCH>(gbase + C::q_off + w * C::tile, row, nch);
+          sl2 *= pow2_of(-E);
+          if (!pair) xl[row] = sl2;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(w ? q_ready_b : q_ready(un));
+        } else if (first < last) {
+          if (!(ok = wait_warp(q_ready(un), (un / kUnits) & 1u))) break;
+          sl2 = xl[row];
+        }
+        two += pair ? 1u : 0u;
+      }
 #pragma unroll 1
       for (int kt = first; kt < last; kt += step, ++nt) {
         if (!(ok = wait_warp(s_full(w), nt & 1u))) break;
@@ -868,6 +1013,22 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               bad = id < 0 || id >= p.a.num_blocks;
             }
             gone = __ballot_sync(0xFFFFFFFFu, bad);
+          }
+          if constexpr (Q4) {
+            const int s = (loaded + 2 * (kt - u.tile)) % NS;
+            volatile uint32_t *const marks = key_marks(s);
+            if (marks[0] | marks[1] | marks[2] | marks[3]) {
+              const float *const by = key_factors(s);
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld32(ts + 32 * c, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * by[32 * c + j]);
+                tmem_st32(ts + 32 * c, v);
+              }
+              tmem_wait_st();
+            }
           }
           if (k0 + kKT > all || gone) {
             const int lim = vis - k0;
@@ -897,10 +1058,10 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
             for (int k = 0; k < 4; ++k)
               mx[k] = max3(mx[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool grow = (top - m) * p.sl2 > kRescale;  // -inf - -inf: NaN, no
+          const bool grow = (top - m) * sl2 > kRescale;  // -inf - -inf: NaN, no
           if (__any_sync(0xFFFFFFFFu, grow)) {
             const float mn = grow ? top : m;
-            const float f = mn == m ? 1.0f : ex2((m - mn) * p.sl2);
+            const float f = mn == m ? 1.0f : ex2((m - mn) * sl2);
             l *= f;
             m = mn;
             if (kt != first) {
@@ -914,8 +1075,8 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               }
             }
           }
-          const float ref = m == -INFINITY ? 0.0f : m * p.sl2;
-          const f32x2 a2 = pack2(p.sl2, p.sl2), b2 = pack2(-ref, -ref);
+          const float ref = m == -INFINITY ? 0.0f : m * sl2;
+          const f32x2 a2 = pack2(sl2, sl2), b2 = pack2(-ref, -ref);
           f32x2 sum[2] = {0ull, 0ull};
           // P overwrites the first columns of S, and goes out in two halves:
           // the tensor core starts on the first while the second is computed
@@ -951,6 +1112,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         }
       }
       if (!ok) break;
+      loaded += 2 * (u.stop - u.tile);
       const bool have = first < last;
       if (have) {
         if (!(ok = wait_warp(o_full(w), no++ & 1u))) break;
@@ -994,8 +1156,8 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           if (live) {
             const float m1 = xm[row], mn = fmaxf(m, m1);
             const float r = mn == -INFINITY ? 0.0f : mn;
-            f0 = ex2((m - r) * p.sl2);
-            f1 = ex2((m1 - r) * p.sl2);
+            f0 = ex2((m - r) * sl2);
+            f1 = ex2((m1 - r) * sl2);
             l = l * f0 + xl[row] * f1;
             m = mn;
           }
@@ -1016,7 +1178,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
                     : reinterpret_cast<uint8_t *>(p.parts.o + slot * hd);
           uint8_t *out = out0 + static_cast<int64_t>(line) * bytes;
           if (!whole && live)
-            p.parts.ml[slot + line] = make_float2(m == -INFINITY ? m : m * p.sl2, l);
+            p.parts.ml[slot + line] = make_float2(m == -INFINITY ? m : m * sl2, l);
           const float k0 = f0 * inv, k1 = f1 * inv;
           // STAGED: a thread holds a row, and rows lie far apart: stored from
           // here, one instruction would touch 32 lines.  128 bytes of each row

@@ -70,7 +70,7 @@ struct Split {
 };
 
 Split split_rows(const Kv4 &c, int64_t T, int n_head, int R) {
-  constexpr int kRows = 24, kLong = 1024;
+  constexpr int kRows = 40, kLong = 1024;
   const int64_t grp = n_head / c.n_kv;
   if (R > 1 && (T - R) * grp >= kLong) return {true, true, static_cast<int>(kRows / grp)};
   const bool many = T * grp > static_cast<int64_t>(kRows) * R;

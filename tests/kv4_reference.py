@@ -17,9 +17,10 @@ and zero points apart, so the errors go by s (code + |zp|), named size:
   weight times scale, to 16 bits: 2^-11 with bf16 queries, two parts (2^-22)
            with fp32 ones; below fp16's normal range half a step of 2^-24,
            where the largest product of the row is at least 2^4: 2^-29 of it
-  tiles    (bf16 queries, head sizes up to 128, many rows a request): keys, values
-           and weights are rounded to bf16 instead, half a step each, 2^-8: of
-           every q k in a score, of every p v twice in the result
+  tiles    (bf16 queries, head sizes up to 128, many rows a request): keys are
+           rounded to fp16, half a step, 2^-11 of every q k in a score (2^-25 of q
+           below fp16's normal range), values and weights to bf16, 2^-8 of every
+           p v twice in the result
   result   sum_j p_j |v_j| (e_j + sum_i p_i e_i) for the weights above and below
            the line, sum_j p_j size_j 2 (L + 64) u for the sums, sum_j p_j s_j
            code_j (rounding) for the products.
@@ -166,7 +167,7 @@ def attend(q, keys, vals, group, visible, scale, q32, tiles=False):
         top = np.where(vis, np.abs(s), 0).max(axis=1, keepdims=True)
         es = scale * (2 * U * (hd + 16) + (2.0 ** -22 if q32 else 0)) * (qh @ ksize[:, g].T) + 4 * U * top
         if tiles:
-            es += scale * 2.0 ** -8 * (qh @ np.abs(k[:, g]).T)
+            es += scale * (2.0 ** -11 * (qh @ np.abs(k[:, g]).T) + 2.0 ** -25 * qh.sum(axis=1, keepdims=True))
         es += scale * 2.0 ** -34 * qh.max(axis=1, keepdims=True) * ksize[:, g].sum(-1)
         p = np.where(vis, np.exp(s - s.max(axis=1, keepdims=True)), 0)
         p /= p.sum(axis=1, keepdims=True)
@@ -181,13 +182,13 @@ def attend(q, keys, vals, group, visible, scale, q32, tiles=False):
 
 def paged(q, data, group, S, table, lens, scale, q32):
     """lens: (cache rows, new tokens) of each request.  Tiles: requests with more
-    than 24 query rows to a key/value head in a call of 1024 such rows beyond a
-    token a request, all requests of other calls with more than 24 on average."""
+    than 40 query rows to a key/value head in a call of 1024 such rows beyond a
+    token a request, all requests of other calls with more than 40 on average."""
     nb, hd = data.shape[0], q.shape[2]
     grp, R = q.shape[1] // data.shape[1], len(lens)
     tc = not q32 and hd <= 128
     both = R > 1 and (len(q) - R) * grp >= 1024
-    tiles = [tc and (n * grp > 24 if both else len(q) * grp > 24 * R) for _, n in lens]
+    tiles = [tc and (n * grp > 40 if both else len(q) * grp > 40 * R) for _, n in lens]
     kk, vv = unpack(data, hd, group, S)
     parts, t = [], 0
     for r, (L, n) in enumerate(lens):

@@ -262,6 +262,8 @@ def test_attend_chunks_beside_single_tokens(dev, nh, nkv, hd, group):
     """Long chunks and short requests in one call: each goes to its own kernel."""
     run_attend([(1, 1), (700, 600), (33, 1), (900, 1), (300, 300), (0, 1), (64, 3), (12, 40), (0, 0), (512, 200)],
                nh, nkv, hd, group, 16, BF16, BF16, pad=3, bad=[(1, 9), (3, 20)])
+    if hd == 128:  # several units to a worker, of two query tiles and of one, some divided
+        run_attend([(700, 200)] * 24, nh, nkv, hd, group, 16, BF16, BF16)
     run_attend([(1500, 1200), (40, 1)], nh, nkv, hd, group, 64, BF16)
 
 
