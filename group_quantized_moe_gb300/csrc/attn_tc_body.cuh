@@ -288,51 +288,52 @@ __device__ __forceinline__ void put_key(uint8_t *tile, int key, int unit, const 
 
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }
 
-// Power of two by which a key row is divided for fp16: none where its largest
-// value lies in [2^-10, 2^15), or where it is all zeros.
+// A bound of a key row's values: |code - zp| s <= (|zp| + 16) s.
 template <int G>
-__device__ __forceinline__ int key_exponent(const uint32_t (&par)[G]) {
+__device__ __forceinline__ float key_bound(const uint32_t (&par)[G]) {
   float top = 0.0f;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const float zf = __half2float(__ushort_as_half(static_cast<unsigned short>(par[g])));
-    top = fmaxf(top, __uint_as_float(par[g] & 0xFFFF0000u) * fmaxf(fabsf(zf), fabsf(15.0f - zf)));
-  }
-  if ((top >= 0x1p-10f && top < 0x1p15f) || top < 0x1p-96f) return 0;
-  return static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13;
+  for (int g = 0; g < G; ++g)
+    top = fmaxf(top, __uint_as_float(par[g] & 0xFFFF0000u) *
+                         (fabsf(__half2float(__ushort_as_half(static_cast<unsigned short>(par[g])))) + 16.0f));
+  return top;
+}
+// Whether the row goes into fp16 as it is: bound in [2^-9, 2^15), or all zeros.
+__device__ __forceinline__ bool key_fits(float top) { return (top >= 0x1p-9f && top < 0x1p15f) || top < 0x1p-94f; }
+// Else the power of two that it is divided by.
+__device__ __forceinline__ int key_exponent(float top) {
+  return key_fits(top) ? 0 : static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13;
 }
 
 // A query row of a tile from bf16 to fp16, times 2^E with its largest element in
 // [2^14, 2^15); returns E.  (An element of 2^114 or more becomes infinite.)
-template <int NCH>
 __device__ __forceinline__ int scale_query(uint8_t *tile, int row, int nch) {
-  uint4 v[NCH * 8];
+  auto at = [&](int c, int j) { return reinterpret_cast<uint4 *>(tile + c * kChunk + row * 128 + ((j ^ (row & 7)) << 4)); };
   uint32_t top = 0;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c)
+#pragma unroll 1
+  for (int c = 0; c < nch; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[8 * c + j] = c < nch ? *reinterpret_cast<const uint4 *>(tile + c * kChunk + row * 128 + ((j ^ (row & 7)) << 4))
-                             : make_uint4(0, 0, 0, 0);
-      const uint32_t x[4] = {v[8 * c + j].x, v[8 * c + j].y, v[8 * c + j].z, v[8 * c + j].w};
+      const uint4 v = *at(c, j);
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7FFFu, x[i] >> 16 & 0x7FFFu));
     }
   // of bf16 bits; not finite: as it is
   const int E = top == 0 || top >= 0x7F80u ? 0 : max(-100, min(14 - (static_cast<int>(top >> 7) - 127), 100));
   const float up = pow2_of(E);
-#pragma unroll
-  for (int c = 0; c < NCH; ++c)
-#pragma unroll
+#pragma unroll 1
+  for (int c = 0; c < nch; ++c)
+#pragma unroll 4
     for (int j = 0; j < 8; ++j) {
-      uint32_t x[4] = {v[8 * c + j].x, v[8 * c + j].y, v[8 * c + j].z, v[8 * c + j].w};
+      const uint4 v = *at(c, j);
+      uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __half2 h = __floats2half2_rn(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
         x[i] = *reinterpret_cast<const uint32_t *>(&h);
       }
-      if (c < nch)
-        *reinterpret_cast<uint4 *>(tile + c * kChunk + row * 128 + ((j ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+      *at(c, j) = make_uint4(x[0], x[1], x[2], x[3]);
     }
   return E;
 }
@@ -393,7 +394,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
   volatile uint32_t *raw_strips = reinterpret_cast<volatile uint32_t *>(gbase + C::misc_off + 80);  // [kRaw]
   float *xm = reinterpret_cast<float *>(gbase + C::misc_off + 96), *xl = xm + 128;
   // of tile s / 2: its warps' marks, its rows' factors
-  auto key_marks = [&](int s) { return reinterpret_cast<volatile uint32_t *>(gbase + C::key_off + s / 2 * 528); };
+  auto key_marks = [&](int s) { return reinterpret_cast<uint4 *>(gbase + C::key_off + s / 2 * 528); };
   auto key_factors = [&](int s) { return reinterpret_cast<float *>(gbase + C::key_off + s / 2 * 528 + 16); };
   __shared__ int64_t scratch[kThreads / 32 + 4];
 
@@ -477,7 +478,8 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         for (int kt = tile; kt < stop; ++kt) {
           if (!(ok = wait_warp(freed(s), phase))) break;
           uint8_t *const dst = gbase + C::kv_off + s * C::tile;
-          bool found = false, scaled = false;
+          bool found = false;
+          uint32_t scaled = 0;  // halves of which this warp has written factors
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             const bool some = kt * kKT + 64 * half < end;
@@ -525,21 +527,25 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               }
             }
             if (!values) {
-              int e[2];
+              float top[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                e[i] = key_exponent<G4>(par[i]);
-                scaled |= e[i] != 0;
-                if (part == 0) key_factors(s)[key[i]] = pow2_of(e[i]);
+                top[i] = key_bound<G4>(par[i]);
+                wide |= !key_fits(top[i]);
 #pragma unroll
                 for (int g = 0; g < G4; ++g) wide |= wide_zp16(par[i][g]);
               }
               if (!__any_sync(0xFFFFFFFFu, wide)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) put_key<false, NC4, CPG4>(dst, key[i], part, w[i], par[i], pow2_of(-e[i]));
+                for (int i = 0; i < 2; ++i) put_key<false, NC4, CPG4>(dst, key[i], part, w[i], par[i], 1.0f);
               } else {
+                scaled |= 1u << half;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) put_key<true, NC4, CPG4>(dst, key[i], part, w[i], par[i], pow2_of(-e[i]));
+                for (int i = 0; i < 2; ++i) {
+                  const int e = key_exponent(top[i]);
+                  if (part == 0) key_factors(s)[key[i]] = pow2_of(e);
+                  put_key<true, NC4, CPG4>(dst, key[i], part, w[i], par[i], pow2_of(-e));
+                }
               }
             } else {
 #pragma unroll
@@ -563,8 +569,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           }
           if (!ok) break;
           if (found) marked[un & 15u] = static_cast<int>(un + 1);
-          scaled = __any_sync(0xFFFFFFFFu, scaled);
-          if (!values && lane == 0) key_marks(s)[warp & 3] = scaled;
+          if (!values && lane == 0) reinterpret_cast<uint32_t *>(key_marks(s))[warp & 3] = scaled;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(clean(s));
@@ -984,7 +989,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         // the tile's queries to fp16, each row times a power of two that its scores lose again
         if (w == 0 || pair) {
           if (!(ok = wait_warp(q_full(w), (w ? two : un) & 1u))) break;
-          const int E = scale_query<NCH>(gbase + C::q_off + w * C::tile, row, nch);
+          const int E = scale_query(gbase + C::q_off + w * C::tile, row, nch);
           sl2 *= pow2_of(-E);
           if (!pair) xl[row] = sl2;
           fence_proxy_async_smem();
@@ -1016,15 +1021,18 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           }
           if constexpr (Q4) {
             const int s = (loaded + 2 * (kt - u.tile)) % NS;
-            volatile uint32_t *const marks = key_marks(s);
-            if (marks[0] | marks[1] | marks[2] | marks[3]) {
+            const uint4 marks = *key_marks(s);
+            if (marks.x | marks.y | marks.z | marks.w) {
+              // row j of the tile was made by warp 2 (strip % 2) + (row of the strip) / 8
               const float *const by = key_factors(s);
+              const uint32_t mark[4] = {marks.x, marks.y, marks.z, marks.w};
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 uint32_t v[32];
                 tmem_ld32(ts + 32 * c, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * by[32 * c + j]);
+                for (int j = 0; j < 32; ++j)
+                  if (mark[j >> 3] >> (c >> 1) & 1u) v[j] = __float_as_uint(__uint_as_float(v[j]) * by[32 * c + j]);
                 tmem_st32(ts + 32 * c, v);
               }
               tmem_wait_st();
