@@ -454,9 +454,9 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
   };
 
   // 384 threads launched with 168 registers: 2 x 208 + 88 = 3 x 168; 640 with 96:
-  // 2 x 176 + 48 + 2 x 40 = 5 x 96
+  // 2 x 176 + 32 + 2 x 48 = 5 x 96
   if (Q4 && warp >= kWarpCodes) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if constexpr (Q4) {
       // ------------------------------------- codes to bf16 tiles of keys and values
       // A word of a key's codes is eight dimensions, 16 bytes of its row in the
@@ -584,7 +584,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
     }
   } else if (warp >= 8) {
     if constexpr (Q4)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpQ) {

@@ -487,16 +487,27 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
 
 /*
  * qmm_attn_paged over a 4-bit cache; q_dtype: of q.  Masks, lengths, tables,
- * rows of no request, NaNs and status bits as there; a row of the cache that is
- * seen must have been written by qmm_rope_append_kv4.
- * Arithmetic: the products multiply codes, which fp16 holds exactly, on the
- * tensor cores, and scales and zero points are applied in fp32; scores, maxima,
- * sums and results are fp32.  A query row is scaled by a power of two to fp16
- * (bf16 rows: exact for elements down to 2^-25 of the row's largest; fp32 rows:
- * in two parts, 2^-22; an element of 2^114 or more counts as infinite).  With
- * bf16 queries each weight times its value's scale is rounded to 16 bits
- * (2^-11 in fp16; not in the sum it is divided by), whatever y_dtype is; with
- * fp32 queries it has two parts, 2^-22.
+ * rows of no request, NaNs and status bits as there (a value's group that reads
+ * as NaN makes its dimensions NaN); a row of the cache that is seen must have been
+ * written by qmm_rope_append_kv4.
+ * Arithmetic: scores, maxima, sums and results are fp32, the products run on
+ * the tensor cores.  Few query rows a request: the products multiply codes,
+ * which fp16 holds exactly, and scales and zero points are applied in fp32.  A
+ * query row is scaled by a power of two to fp16 (bf16 rows: exact for elements
+ * down to 2^-25 of the row's largest; fp32 rows: in two parts, 2^-22; an element
+ * of 2^114 or more counts as infinite).  With bf16 queries each weight times its
+ * value's scale is rounded to 16 bits (2^-11; not in the sum it is divided by),
+ * whatever y_dtype is; with fp32 queries it has two parts, 2^-22.
+ * Many (bf16 queries, head_dim up to 128, q's rows a multiple of 16 bytes apart):
+ * keys are rounded to fp16 (2^-11), values and weights to bf16 (2^-8 each).  With
+ * n_head / n_kv query rows a token, that is so for all requests of a call with
+ * more than 40 rows a request on average; and where a call of several requests
+ * has 1024 rows or more beyond one token a request, for those requests of it that
+ * have more than 40.
+ * Two kernel launches, four in such a mixed call, half of them where no request
+ * can have more than 512 keys; results are reproducible bit for bit.  workspace:
+ * 256-byte aligned, contents on entry do not matter; calls that may run at the
+ * same time need one each.
  */
 size_t qmm_attn_paged_kv4_workspace_bytes(const qmm_kv4_cache *cache, int32_t q_dtype, int64_t T, int32_t n_head,
                                           int32_t R);
