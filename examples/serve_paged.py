@@ -2,13 +2,15 @@
 cache: prompts admitted together, then decoding one token per request and step,
 with one request joining while the others decode.
 
-    python examples/serve_paged.py [--width 4096] [--heads 32] [--kv-heads 8]
+    python examples/serve_paged.py [--width 4096] [--heads 32] [--kv-heads 8] [--four-bit]
 
 Weights are random, INT8 in groups of 64; the "tokens" are random activations.
 Every step runs kv_plan (block tables and slots on the GPU from the lengths),
 and attn_layer_paged: the quantised projections, rope_append and attn_prompt or
 attn_paged.  Prints what each step did, and checks the decoded rows against one
-attn_prompt over each request's whole sequence.
+attn_prompt over each request's whole sequence.  --four-bit holds the cache in 4
+bits (groups of 64), a little over a quarter of the memory: the difference is
+then what that costs.
 """
 from __future__ import annotations
 
@@ -27,7 +29,8 @@ class Server:
     """One layer, its cache and block tables, and the requests' lengths."""
 
     def __init__(self, width, heads, kv_heads, head_dim, blocks=512, block_size=16, columns=64,
-                 requests=8, max_seq=1024, dtype=torch.bfloat16, seed=0):
+                 requests=8, max_seq=1024, dtype=torch.bfloat16, seed=0,
+                 four_bit=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
         rows = (heads + 2 * kv_heads) * head_dim
         w = torch.randn(rows, width, device="cuda", generator=g) * width ** -0.5
@@ -36,7 +39,9 @@ class Server:
         self.wo = lib.qmm_quantize_groupwise(wo, 8, 64)
         self.heads, self.kv_heads, self.block_size = heads, kv_heads, block_size
         self.cos, self.sin = lib.rope_table(max_seq, head_dim)
-        self.cache = lib.paged_kv(blocks, kv_heads, block_size, head_dim, dtype)
+        self.dtype = dtype
+        self.cache = (lib.paged_kv4(blocks, kv_heads, block_size, head_dim) if four_bit else
+                      lib.paged_kv(blocks, kv_heads, block_size, head_dim, dtype))
         self.free = torch.arange(blocks, dtype=torch.int32, device="cuda")
         self.table = torch.full((requests, columns), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros(requests, dtype=torch.int32, device="cuda")
@@ -58,7 +63,7 @@ class Server:
         n = x.shape[0]
         q, k, v = lib.rope_append(qkv, self.heads, torch.arange(n, dtype=torch.int32, device="cuda"),
                                   None, self.cos, self.sin, None, keep_kv=True, n_kv=self.kv_heads,
-                                  y_dtype=self.cache.k.dtype)
+                                  y_dtype=self.dtype)
         cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
         a = lib.attn_prompt(q, k, v, cu, y_dtype=x.dtype)
         return lib.qmm_linear_batched(a.view(n, -1), self.wo)
@@ -71,10 +76,11 @@ def main(argv=None) -> float:
     ap.add_argument("--kv-heads", type=int, default=8)
     ap.add_argument("--head-dim", type=int, default=128)
     ap.add_argument("--steps", type=int, default=12)
+    ap.add_argument("--four-bit", action="store_true")
     ap.add_argument("--quiet", action="store_true")
     a = ap.parse_args(argv)
     say = (lambda *s: None) if a.quiet else print
-    s = Server(a.width, a.heads, a.kv_heads, a.head_dim, requests=4)
+    s = Server(a.width, a.heads, a.kv_heads, a.head_dim, requests=4, four_bit=a.four_bit)
     g = torch.Generator(device="cuda").manual_seed(1)
     tokens = lambda n: torch.randn(n, a.width, device="cuda", generator=g).bfloat16()
     seen = [[] for _ in range(4)]  # every request's inputs

@@ -538,3 +538,54 @@ def test_layer(dev, dtype, prompts):
     c2 = q.paged_kv(20, nkv, S, hd, F32)
     z = q.attn_layer_paged(x.float(), wqkv, wo, nh, cos, sin, c2, p0, t0, prompts=prompts)
     assert (y.float() - z).norm() < 0.2 * z.norm()
+
+
+def test_example_serves_from_a_4_bit_cache(dev):
+    """examples/serve_paged.py --four-bit runs, and its rows are those of the whole
+    sequences but for four bits of keys and values: a step is a fifteenth of a
+    group's range, some five deviations, so a value is off by a tenth of one."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_paged.py")
+    spec = importlib.util.spec_from_file_location("serve_paged", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    worst = m.main(["--quiet", "--four-bit", "--width", "1024", "--heads", "8", "--kv-heads", "2"])
+    assert 1e-3 < worst < 0.5
+
+
+def test_two_streams_at_once(dev):
+    """Two calls on two streams, each with its own workspace, give what they give alone."""
+    data = torch.from_numpy(filled(60, 2, 128, 64, 32, 3)).cuda()
+    cache, table = q.PagedKV4(data, 128, 64, 32), torch.arange(60, dtype=torch.int32, device="cuda").view(3, 20)
+    sides = []
+    for n, dtype in ((1, BF16), (90, BF16), (2, F32)):
+        qq = rnd(n, (3 * n, 8, 128), dtype).cuda()
+        args = (qq, cache, table, i32([0, n, 2 * n, 3 * n]), i32([600, 333, 640]))
+        ws = torch.empty(q.qmm_attn_paged_workspace_bytes(qq, cache, 3), dtype=torch.uint8, device="cuda")
+        sides.append((args, ws, q.attn_paged(*args, workspace=ws).clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        out = [q.attn_paged(*a, workspace=ws, stream=s) for a, ws, _, s in sides]
+        torch.cuda.synchronize()
+        for y, (_, _, want, _) in zip(out, sides):
+            assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype,n", [(BF16, 1), (F32, 1), (BF16, 64)])
+def test_repeated_calls_agree(dev, dtype, n):
+    """Many units to a worker, whole and divided, the same bits every time."""
+    rng = np.random.default_rng(2)
+    lens = [int(v) for v in rng.integers(1, 1500, 64)]
+    need = [-(-v // 16) for v in lens]
+    data = torch.from_numpy(filled(sum(need), 2, 64, 32, 16, 3)).cuda()
+    table, used = np.full((64, max(need)), -1, dtype=np.int32), 0
+    for r, k in enumerate(need):
+        table[r, :k] = np.arange(used, used + k)
+        used += k
+    qq = rnd(1, (64 * n, 8, 64), dtype, 2.0).cuda()
+    args = (qq, q.PagedKV4(data, 64, 32, 16), torch.from_numpy(table).cuda(), cu_of([n] * 64), i32(lens))
+    first = q.attn_paged(*args)
+    for _ in range(30):
+        assert torch.equal(q.attn_paged(*args), first)
+    assert q.qmm_device_status(clear=True) == 0
