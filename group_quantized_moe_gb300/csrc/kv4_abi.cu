@@ -56,24 +56,37 @@ int check_kv4(const char *who, const qmm_kv4_cache *c, Kv4 *out) {
 
 namespace {
 
-// The forms for few and for many query rows of a key/value head cost the same at
-// about 24 rows a request (40 requests of 2000 keys, 32 heads over 8: 16 rows 73
-// and 88 us, 24 rows 100 and 89 us, 48 rows 178 and 93 us).  Where a call has long
-// chunks and may have single tokens beside them, each takes its own: 20 requests,
-// four of them chunks, 0.87 ms instead of 1.00 in the form for many alone.  How
-// long a request is stands on the device only, so both are launched, and find their
-// requests there; an empty one costs 4 us, which 1024 rows beyond one token a
-// request outweigh.
+// Which form a call takes.  The form for few query rows reads a cache faster and
+// begins sooner, the one for many costs hardly more with each row.  Rows per
+// request and key/value head, few / many in us (32 heads of 128 over 8, groups
+// of 64):
+//   40 requests of 2000 keys    24: 98 / 118    32: 124 / 121   40: 153 / 124
+//    8 requests of 16000 keys   24: 109 / 142   32: 138 / 143   40: 167 / 145
+//  300 requests of 400 keys     16: 242 / 272   24: 352 / 280   32: 460 / 281
+//    4 requests of 6000 keys    32: 45 / 51     40: 51 / 52     48: 58 / 52
+// so kRows = 32.
+// Where a call has chunks and may have single tokens beside them, each takes its
+// own.  How long a request is stands on the device only, so both forms are launched
+// and find their requests there, which costs 7 to 15 us where one has none.  One
+// chunk and single tokens, 3000 keys each, few / many / both:
+//   chunk of 64     20 requests  65 / 101 / 80    64 requests   98 / 260 / 130
+//   chunk of 256     2 requests 124 / 60 / 74     20 requests  136 / 123 / 92
+//                   64 requests 171 / 281 / 135
+//   chunk of 1024    2 requests 382 / 96 / 109    64 requests  437 / 344 / 170
+// so both from kMixed = 6 requests on (a single token costs the form for many about
+// 3.5 us), and from kLong = 512 rows beyond a token a request; twice that where the
+// average is for the form for few, as then the rows may be drafts of all requests
+// (30 of up to 5 tokens, 28 heads over 4: 52 us, both 68).
 struct Split {
   bool few, many;
   int tokens;  // of a request, up to which it goes to the form for few
 };
 
 Split split_rows(const Kv4 &c, int64_t T, int n_head, int R) {
-  constexpr int kRows = 40, kLong = 1024;
+  constexpr int kRows = 32, kLong = 512, kMixed = 6;
   const int64_t grp = n_head / c.n_kv;
-  if (R > 1 && (T - R) * grp >= kLong) return {true, true, static_cast<int>(kRows / grp)};
   const bool many = T * grp > static_cast<int64_t>(kRows) * R;
+  if (R >= kMixed && (T - R) * grp >= (many ? kLong : 2 * kLong)) return {true, true, static_cast<int>(kRows / grp)};
   return {!many, many, 0};
 }
 

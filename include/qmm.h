@@ -501,9 +501,9 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
  * Many (bf16 queries, head_dim up to 128, q's rows a multiple of 16 bytes apart):
  * keys are rounded to fp16 (2^-11), values and weights to bf16 (2^-8 each).  With
  * n_head / n_kv query rows a token, that is so for all requests of a call with
- * more than 40 rows a request on average; and where a call of several requests
- * has 1024 rows or more beyond one token a request, for those requests of it that
- * have more than 40.
+ * more than 32 rows a request on average; but where a call of six requests or
+ * more has 512 rows or more beyond one token a request (1024 where the average is
+ * at most 32), for those requests of it that have more than 32.
  * Two kernel launches, four in such a mixed call, half of them where no request
  * can have more than 512 keys; results are reproducible bit for bit.  workspace:
  * 256-byte aligned, contents on entry do not matter; calls that may run at the

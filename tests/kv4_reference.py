@@ -182,13 +182,14 @@ def attend(q, keys, vals, group, visible, scale, q32, tiles=False):
 
 def paged(q, data, group, S, table, lens, scale, q32):
     """lens: (cache rows, new tokens) of each request.  Tiles: requests with more
-    than 40 query rows to a key/value head in a call of 1024 such rows beyond a
-    token a request, all requests of other calls with more than 40 on average."""
+    than 32 query rows to a key/value head in a call of six or more that has 512
+    such rows beyond a token a request (1024 where the average is at most 32), all
+    requests of other calls with more than 32 on average."""
     nb, hd = data.shape[0], q.shape[2]
     grp, R = q.shape[1] // data.shape[1], len(lens)
     tc = not q32 and hd <= 128
-    both = R > 1 and (len(q) - R) * grp >= 1024
-    tiles = [tc and (n * grp > 40 if both else len(q) * grp > 40 * R) for _, n in lens]
+    both = R >= 6 and (len(q) - R) * grp >= (512 if len(q) * grp > 32 * R else 1024)
+    tiles = [tc and (n * grp > 32 if both else len(q) * grp > 32 * R) for _, n in lens]
     kk, vv = unpack(data, hd, group, S)
     parts, t = [], 0
     for r, (L, n) in enumerate(lens):
