@@ -15,8 +15,20 @@
 //
 // Four lanes hold a row of a head, each eight dimensions of every chunk of 32:
 // a lane's codes of a key are consecutive words of the cache, and a group's
-// extremes meet in two shuffles.  A warp takes four heads of two tokens at a time.
-// Bound by HBM: qkv is read once, q and the codes written once.
+// extremes meet in two shuffles.  A warp takes four heads of two tokens at a time;
+// where they are neighbours in the cache (prompts), each lane stores or loads
+// whole words of both, which share the words of values.
+//
+// Measured, 32 heads of 128 over 8, groups of 64:
+//   append  16384 tokens in bf16, 354 MB in and out: 87 us, 4.1 TB/s.  One token and
+//           eight heads a warp took 230 us: half words of values were stored one by
+//           one.  What bounds it now is the arithmetic of the codes.
+//   read    100000 rows to bf16, 525 MB in and out: 102 us, 5.1 TB/s (a copy 6.8).
+//           160 us where a warp took a row of eight heads after the other; 108 with
+//           a 64-bit division a step and codes shifted and converted one by one
+//           (issue slots 67 % busy, DRAM 52 %); 119 where 40 registers left six
+//           blocks of the eight of a grid resident.
+// A few rows are launch-bound: 3 us (300 rows to fp32), 4 us (7 tokens).
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -290,61 +302,83 @@ __global__ void __launch_bounds__(kThreads, NC <= 4 ? 4 : 2) rope_append_kv4_ker
 }
 
 template <int NC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, NC <= 4 ? 8 : 4)
     kv4_read_kernel(Kv4 cache, const int64_t *slots, int64_t n, void *k, void *v, bool bf16, uint32_t *status) {
   pdl_enter();
-  const int lane = threadIdx.x & 31, t4 = lane & 3, team = lane >> 2, hd = cache.head_dim;
+  const int lane = threadIdx.x & 31, t4 = lane & 3, team = lane >> 2, hd = cache.head_dim, odd = team & 1;
   const int64_t rows = cache.num_blocks << cache.block_shift;
   const int strip = kv4_strip(cache);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < n;
-       i += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t slot = slots[i];
+  // A warp takes two rows of four heads, its CTA sixteen: neighbours share sectors.
+  const unsigned quads = (2 * cache.n_kv + 3) / 4;
+  const int64_t pairs = (n + 1) / 2;
+  const unsigned di = gridDim.x / quads, dp = gridDim.x - di * quads;
+  int64_t pair = static_cast<int64_t>(blockIdx.x / quads) * kWarps + (threadIdx.x >> 5);
+  unsigned part = blockIdx.x % quads;
+  for (; pair < pairs; pair += static_cast<int64_t>(di) * kWarps, part += dp) {
+    if (part >= quads) {
+      part -= quads;
+      pair += kWarps;
+      if (pair >= pairs) break;
+    }
+    const int64_t i = 2 * pair + odd;
+    const int64_t slot = i < n ? slots[i] : -1;
     const bool live = slot >= 0 && slot < rows;
-    if (lane == 0 && slot >= rows) atomicOr(status, kDevBadBlock);
+    if (lane - 4 * odd == 0 && part == 0 && slot >= rows) atomicOr(status, kDevBadBlock);
+    const int64_t other = __shfl_xor_sync(0xFFFFFFFFu, slot, 4);
+    const bool both = live && other < rows && (slot ^ other) == 1;
+    const int h = 4 * part + (team >> 1);
+    const bool key = h < cache.n_kv;
+    const int hk = key ? h : h - cache.n_kv;
+    void *const out = key ? k : v;
+    const bool on = h < 2 * cache.n_kv && i < n && out;
     const int row = static_cast<int>(slot & ((1 << cache.block_shift) - 1)), r = row & 15;
-    const uint8_t *block = cache.data + (live ? (slot >> cache.block_shift) * cache.block_stride + (row >> 4) * strip : 0);
-    for (int h0 = 0; h0 < 2 * cache.n_kv; h0 += 8) {
-      const int h = h0 + team;
-      if (h >= 2 * cache.n_kv) break;
-      const bool key = h < cache.n_kv;
-      const int hk = key ? h : h - cache.n_kv;
-      void *const out = key ? k : v;
-      if (!out) continue;
-      const uint8_t *const s = block + static_cast<int64_t>(hk) * kv4_head_bytes(cache);
+    const uint8_t *const s = cache.data + (slot >> cache.block_shift) * cache.block_stride + (row >> 4) * strip +
+                             static_cast<int64_t>(hk) * kv4_head_bytes(cache);
+    uint32_t w[NC], par[NC], hi[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) w[c] = par[c] = hi[c] = 0u;
+    if (live && on) {
       const uint32_t *const q =
           reinterpret_cast<const uint32_t *>(s + 512 * NC) + (key ? 0 : 16 * cache.ng) + r * cache.ng;
-      uint32_t w[NC], par[NC];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) w[c] = par[c] = 0u;
-      if (live) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-          par[c] = __ldg(q + min(c / cache.cpg, cache.ng - 1));
-        if (key) {
-          load_words<NC>(w, reinterpret_cast<const uint32_t *>(s) + (r * 4 + t4) * NC);
-        } else {
-          // words of two rows, of which this one has one half
-          const uint32_t *const vw = reinterpret_cast<const uint32_t *>(s + 256 * NC) +
-                                     (((r >> 3) * 8 + 2 * t4) * 4 + ((r & 7) >> 1)) * NC;
-          uint32_t lo[NC], hi[NC];
-          load_words<NC>(lo, vw);
-          load_words<NC>(hi, vw + 4 * NC);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) w[c] = __byte_perm(lo[c], hi[c], r & 1 ? 0x7632u : 0x5410u);
-        }
+      for (int c = 0; c < NC; ++c)
+        par[c] = c % 2 && cache.cpg == 2 ? par[c - c % 2] : __ldg(q + min(c / cache.cpg, cache.ng - 1));
+      if (key) {
+        load_words<NC>(w, reinterpret_cast<const uint32_t *>(s) + (r * 4 + t4) * NC);
+      } else {
+        // words of two rows, of which this one has one half
+        const uint32_t *const vw =
+            reinterpret_cast<const uint32_t *>(s + 256 * NC) + (((r >> 3) * 8 + 2 * t4) * 4 + ((r & 7) >> 1)) * NC;
+        load_words<NC>(w, vw + (both ? (r & 1) * 4 * NC : 0));
+        if (!both) load_words<NC>(hi, vw + 4 * NC);
       }
-      const int64_t base = (i * cache.n_kv + hk) * hd;
+    }
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int d = 32 * c + 8 * t4;
-        if (d >= hd) continue;
-        const float scale = __uint_as_float(par[c] & 0xFFFF0000u);
-        const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(par[c])));
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = (static_cast<float>(w[c] >> (4 * j) & 15u) - zp) * scale;
-        store8(out, base + d, y, bf16);
+    for (int c = 0; c < NC; ++c) {
+      const uint32_t theirs = __shfl_xor_sync(0xFFFFFFFFu, w[c], 4);
+      if (!key) {
+        const uint32_t lo = both && (r & 1) ? theirs : w[c], up = !both ? hi[c] : r & 1 ? w[c] : theirs;
+        w[c] = __byte_perm(lo, up, r & 1 ? 0x7632u : 0x5410u);
       }
+    }
+    if (!on) continue;
+    const int64_t base = (i * cache.n_kv + hk) * hd;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int d = 32 * c + 8 * t4;
+      if (d >= hd) continue;
+      const float scale = __uint_as_float(par[c] & 0xFFFF0000u);
+      const float zp = __half2float(__ushort_as_half(static_cast<unsigned short>(par[c])));
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // the code where it is, as low bits of 2^23: code 16^(j % 4), exact, and with
+        // the zero point taken off rounded once
+        const uint32_t half = j < 4 ? w[c] : w[c] >> 16;
+        const float at = __uint_as_float((half & 15u << 4 * (j % 4)) | 0x4B000000u) - 8388608.0f;
+        y[j] = fmaf(at, 1.0f / (1 << 4 * (j % 4)), -zp) * scale;
+      }
+      store8(out, base + d, y, bf16);
     }
   }
 }
@@ -392,7 +426,8 @@ cudaError_t launch_kv4_read(const Kv4 &c, const int64_t *slots, int64_t n, void 
               : c.nc == 4 ? kv4_read_kernel<4>
               : c.nc == 6 ? kv4_read_kernel<6>
                           : kv4_read_kernel<8>;
-  return launch_pdl(kern, dim3(grid_of(n, 8)), dim3(kThreads), 0, s, c, slots, n, k, v, bf16, status);
+  return launch_pdl(kern, dim3(grid_of((n + 15) / 16 * kWarps * ((2 * c.n_kv + 3) / 4), c.nc <= 4 ? 8 : 4)), dim3(kThreads), 0, s, c, slots, n, k, v, bf16,
+                    status);
 }
 
 }  // namespace qmm
