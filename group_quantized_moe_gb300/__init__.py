@@ -1060,7 +1060,7 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
             raise ValueError(f"the cache has {desc.n_kv} heads of {desc.head_dim}, the call "
                              f"{n_kv} of {hd}")
         n_kv = desc.n_kv
-        if cache.__class__ is not PagedKV4:
+        if not isinstance(cache, PagedKV4):
             y_dtype = cache.k.dtype
         else:
             if y_dtype is None:
@@ -1100,7 +1100,7 @@ def rope_append(qkv: torch.Tensor, n_head: int, positions: torch.Tensor, slots: 
         k = _new((T, n_kv, hd), y_dtype, qkv.device, stream)
     if keep_kv and v is None:
         v = _new((T, n_kv, hd), y_dtype, qkv.device, stream)
-    if cache.__class__ is PagedKV4:
+    if isinstance(cache, PagedKV4):
         rc = lib().qmm_rope_append_kv4(qkv.data_ptr(), _dtype_code(qkv), T,
                                        qkv.stride(0) if T > 1 else width, n_head, positions.data_ptr(),
                                        slots.data_ptr(), rope_cos.data_ptr(), rope_sin.data_ptr(),
@@ -1199,7 +1199,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
 
 def qmm_attn_paged_workspace_bytes(q: torch.Tensor, cache: PagedKV | PagedKV4,
                                    n_requests: int) -> int:
-    if cache.__class__ is PagedKV4:
+    if isinstance(cache, PagedKV4):
         return int(lib().qmm_attn_paged_kv4_workspace_bytes(ctypes.byref(cache._desc()), _dtype_code(q),
                                                             q.shape[0], q.shape[1], n_requests))
     return int(lib().qmm_attn_paged_workspace_bytes(ctypes.byref(cache._desc()), q.shape[0],
@@ -1218,7 +1218,7 @@ def attn_paged(q: torch.Tensor, cache: PagedKV | PagedKV4, block_table: torch.Te
     sq = _heads(q, "q")
     T, nh, hd = q.shape
     desc = cache._desc()
-    kv4 = cache.__class__ is PagedKV4
+    kv4 = isinstance(cache, PagedKV4)
     if kv4:
         if hd != desc.head_dim:
             raise ValueError(f"q has head_dim {hd}, the cache {desc.head_dim}")

@@ -13,7 +13,7 @@
 // warpgroups multiply its column of scores (a mark per tile says so).
 //
 // What bounds it: making the tiles.  Without that the same call takes 0.64 ms
-// instead of 1.07 (20 requests, 3500 tokens in four chunks over up to 21000 keys,
+// instead of 1.07 (20 requests, 4076 tokens in four chunks over up to 21000 keys,
 // 32 heads over 8 of 128); one warpgroup for both kinds of codes took 1.56 ms with
 // bf16 keys, two 1.01 (fp16 costs the rest); conversions with a branch a word 2.4.
 // Registers: 176 a thread for the warpgroups that compute the weights, 48 for

@@ -21,14 +21,15 @@
 //
 // Measured, 32 heads of 128 over 8, groups of 64:
 //   append  16384 tokens in bf16, 354 MB in and out: 87 us, 4.1 TB/s.  One token and
-//           eight heads a warp took 230 us: half words of values were stored one by
-//           one.  What bounds it now is the arithmetic of the codes.
+//           eight heads a warp took 195 us: half words of values were stored one by
+//           one.  Four blocks an SM: 3, 5 and 6 took 122, 102 and 126.  What bounds it
+//           now is the arithmetic of the codes.
 //   read    100000 rows to bf16, 525 MB in and out: 102 us, 5.1 TB/s (a copy 6.8).
-//           160 us where a warp took a row of eight heads after the other; 108 with
+//           111 us where a warp took a row of eight heads after the other; 108 with
 //           a 64-bit division a step and codes shifted and converted one by one
 //           (issue slots 67 % busy, DRAM 52 %); 119 where 40 registers left six
 //           blocks of the eight of a grid resident.
-// A few rows are launch-bound: 3 us (300 rows to fp32), 4 us (7 tokens).
+// A few rows are launch-bound: 3 us (300 rows to fp32).
 #include <cuda_fp16.h>
 
 #include <cfloat>
