@@ -198,10 +198,16 @@ __device__ __noinline__ void add_marked4(const TcAttn &p, const Kv4 &c, const Un
 
 // (code - zp) s of eight codes in bf16, each rounded once.  Codes and zero points
 // of up to 120 are whole numbers that bf16 has (0x4300 + code is 128 + code), and
-// so are their differences; WIDE ones go through fp32.
+// so are their differences; WIDE ones go through fp32.  Dimensions j and j + 4
+// become neighbours, as a mask leaves them: where results leave tensor memory,
+// dim_at finds dimension j of 32.
 __device__ __forceinline__ bool wide_zp(uint32_t par) {
   // (of an fp16's bits: its magnitude is above 120's, or it is not a number)
   return (par & 0x7FFFu) > 0x5780u;
+}
+template <bool Q4>
+__device__ __forceinline__ constexpr int dim_at(int j) {
+  return Q4 ? (j & ~7) + (j % 8 < 4 ? 2 * (j % 8) : 2 * (j % 8) - 7) : j;
 }
 template <bool WIDE>
 struct Dequant {
@@ -216,16 +222,13 @@ struct Dequant {
   }
   __device__ __forceinline__ uint4 of(uint32_t w) const {
     uint32_t r[4];
-    if constexpr (WIDE) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r[i] = bf16x2((static_cast<float>(w >> (8 * i) & 15u) - zf) * sf,
-                      (static_cast<float>(w >> (8 * i + 4) & 15u) - zf) * sf);
-    } else {
-      const uint32_t x = w & 0x0F0F0F0Fu, y = w >> 4 & 0x0F0F0F0Fu;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t t = (__byte_perm(x, y, 0x0400u + 0x0101u * i) & 0x00FF00FFu) | 0x43004300u;
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (WIDE) {
+        r[i] = bf16x2((static_cast<float>(w >> (4 * i) & 15u) - zf) * sf,
+                      (static_cast<float>(w >> (4 * i + 16) & 15u) - zf) * sf);
+      } else {
+        const uint32_t t = (w >> (4 * i) & 0x000F000Fu) | 0x43004300u;
         const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&t), zp), s);
         r[i] = *reinterpret_cast<const uint32_t *>(&v);
       }
@@ -1155,7 +1158,8 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                   *reinterpret_cast<uint4 *>(xat(8 * c + j)) =
-                      make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                      make_uint4(o[dim_at<Q4>(4 * j)], o[dim_at<Q4>(4 * j + 1)], o[dim_at<Q4>(4 * j + 2)],
+                                 o[dim_at<Q4>(4 * j + 3)]);
             }
             if (live) {
               xm[row] = m;
@@ -1208,7 +1212,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               uint32_t o[32];
               tmem_ld32(to + 32 * c, o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = have ? __uint_as_float(o[j]) * k0 : 0.0f;
+              for (int j = 0; j < 32; ++j) v[j] = have ? __uint_as_float(o[dim_at<Q4>(j)]) * k0 : 0.0f;
             }
             if (join) {
 #pragma unroll
