@@ -12,12 +12,16 @@
 // its scores lose again; a key row out of fp16's range is divided by one, and the
 // warpgroups multiply its column of scores (a mark per tile says so).
 //
-// What bounds it: making the tiles.  Without that the same call takes 0.64 ms
-// instead of 1.07 (20 requests, 4076 tokens in four chunks over up to 21000 keys,
-// 32 heads over 8 of 128); one warpgroup for both kinds of codes took 1.56 ms with
-// bf16 keys, two 1.01 (fp16 costs the rest); conversions with a branch a word 2.4.
-// Registers: 176 a thread for the warpgroups that compute the weights, 48 for
-// those of the codes, 32 for the others (168, 48 and 48: 1.13 ms).
+// What bounds it: making the tiles, beside the exponentials, for every query tile
+// pair again: issue slots are 53 % busy, the tensor cores 42 % of the time.  20
+// requests, 4076 tokens in four chunks over up to 21000 keys, 32 heads over 8 of
+// 128: 0.99 ms, 0.6 without conversions.  One warpgroup for both kinds of codes took
+// 1.56 ms with bf16 keys, two 1.01 (fp16 keys 0.06 more); conversions with a branch
+// a word 2.4; codes put back into the dimensions' order 1.07; words read only after
+// their parameters 1.04.
+// Registers: 176 a thread for the warpgroups that compute the weights, 48 for those
+// of the codes, 32 for the others (168, 32 and 56: the same; 160, 32 and 64: 1.53 ms;
+// 168, 48 and 48, before the dimensions' order: 1.13 against 1.07).
 #include "attn_tc_body.cuh"
 #include "kv4.h"
 
