@@ -589,3 +589,52 @@ def test_repeated_calls_agree(dev, dtype, n):
     for _ in range(30):
         assert torch.equal(q.attn_paged(*args), first)
     assert q.qmm_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("lens", [
+    [(300, 8)] * 3, [(300, 9)] * 3,                                    # 32 rows a request, 36
+    [(200, 1)] * 4 + [(500, 140)], [(200, 1)] * 5 + [(500, 140)],      # five requests, six
+    [(90, 1)] * 30 + [(400, 128)], [(90, 1)] * 30 + [(400, 129)],      # 508 rows beyond a token each, 512
+    [(90, 1)] * 40 + [(400, 256)], [(90, 1)] * 40 + [(400, 257)],      # ... 1020, 1024, at most 32 on average
+    [(60, 8), (60, 9)] * 16 + [(700, 300)], [(40, 40)] * 8,
+])
+def test_attend_around_the_rules_that_choose(dev, lens):
+    run_attend(lens, 8, 2, 128, 64, 32, BF16, pad=1)
+
+
+def test_a_captured_call_whose_requests_change_kernels(dev):
+    """One captured call of 400 tokens in eight requests, replayed with the tokens
+    spread anew, and two such graphs that share a workspace of any contents."""
+    nh, nkv, hd, S, R, T = 8, 2, 128, 32, 8, 400
+    data = filled(R * 20, nkv, hd, 64, S, 11)
+    cache = q.PagedKV4(torch.from_numpy(data).cuda(), hd, 64, S)
+    table = torch.arange(R * 20, dtype=torch.int32, device="cuda").view(R, 20)
+    ws = torch.full((q.qmm_attn_paged_workspace_bytes(torch.empty((T, nh, hd), dtype=BF16, device="cuda"), cache, R),),
+                    0xFF, dtype=torch.uint8, device="cuda")
+    sides = []
+    for seed in (1, 2):
+        qq = rnd(seed, (T, nh, hd), BF16, 2.0).cuda()
+        cu, kv, y = cu_of([50] * R), i32([100] * R), torch.empty((T, nh, hd), device="cuda")
+        call = lambda qq=qq, cu=cu, kv=kv, y=y: q.attn_paged(qq, cache, table, cu, kv, y=y, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        sides.append((qq, cu, kv, y, g))
+    spreads = [[1, 1, 1, 393, 1, 1, 1, 1], [50] * R, [0, 0, 400, 0, 0, 0, 0, 0], [1, 8, 9, 300, 1, 1, 70, 0], [1] * R]
+    for i, new in enumerate(spreads):
+        have = [[0, 600, 17, 640, 333, 1, 128, 64], [640] * R][i % 2]
+        lens = [(min(640, max(h, n)), n) for h, n in zip(have, new)]
+        for qq, cu, kv, y, g in sides:
+            cu.copy_(cu_of(new))
+            kv.copy_(i32(L for L, _ in lens))
+            y.fill_(9)
+        ws.fill_(0xFF)
+        for side in sides:
+            side[4].replay()
+        torch.cuda.synchronize()
+        for qq, cu, kv, y, g in sides:
+            want, b = ref.paged(num(qq), data, 64, S, table.cpu().numpy(), lens, hd ** -0.5, False)
+            assert_within(num(y), want, round_bound(want, b, F32), str(new))
+    assert q.qmm_device_status(clear=True) == 0
