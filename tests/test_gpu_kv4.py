@@ -638,3 +638,29 @@ def test_a_captured_call_whose_requests_change_kernels(dev):
             want, b = ref.paged(num(qq), data, 64, S, table.cpu().numpy(), lens, hd ** -0.5, False)
             assert_within(num(y), want, round_bound(want, b, F32), str(new))
     assert q.qmm_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("order", ["up", "down", "from 1", "swapped", "twice"])
+@pytest.mark.parametrize("hd,group,n_kv", [(128, 64, 2), (96, 32, 1), (200, 64, 3)])
+def test_rows_in_any_order(dev, order, hd, group, n_kv):
+    """Neighbours in the cache share words of values: pairs of rows the right way
+    round, the other way round, and rows that only look like pairs."""
+    S, n = 16, 64
+    at = np.arange(n)
+    slots = {"up": at, "down": at[::-1], "from 1": (at + 1) % n, "swapped": at ^ 1, "twice": at // 2}[order]
+    data = filled(n // S, n_kv, hd, group, S, 13)
+    cache = q.PagedKV4(torch.from_numpy(data).cuda(), hd, group, S)
+    where = torch.from_numpy(np.ascontiguousarray(slots)).cuda()
+    for got, part in zip(q.kv4_read(cache, where), ref.unpack(data, hd, group, S)):
+        want = ref.values([t.astype(np.float32) for t in part], group)[slots // S, :, slots % S]
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+    if order == "twice":
+        return  # (tokens do not share a slot)
+    x = rnd(4, (n, 4 * n_kv * hd), F32)
+    cos, sin = q.rope_table(8, hd, device="cuda")
+    q.rope_append(x.cuda(), 2 * n_kv, i32([0] * n), where, cos, sin, cache)
+    want = data.copy()
+    rows = x.numpy().reshape(n, -1, hd)  # position 0 turns nothing
+    for t in range(n):
+        ref.put(want, hd, group, S, int(slots[t]), rows[t, 2 * n_kv:3 * n_kv], rows[t, 3 * n_kv:])
+    np.testing.assert_array_equal(cache.data.cpu().numpy(), want)
