@@ -20,11 +20,12 @@
 // whole words of both, which share the words of values.
 //
 // Measured, 32 heads of 128 over 8, groups of 64:
-//   append  16384 tokens in bf16, 354 MB in and out: 87 us, 4.1 TB/s.  One token and
+//   append  16384 tokens in bf16, 354 MB in and out: 81 us, 4.4 TB/s.  One token and
 //           eight heads a warp took 195 us: half words of values were stored one by
-//           one.  Four blocks an SM: 3, 5 and 6 took 122, 102 and 126.  What bounds it
-//           now is the arithmetic of the codes (integer pipe 60 %, issue slots 58 %,
-//           DRAM 52 %); positions and slots fetched a turn ahead change nothing.
+//           one.  Four blocks an SM: 3, 5 and 6 took 122, 102 and 126 (four: 87).  What
+//           bounds it is the arithmetic of the codes (integer pipe 60 %, issue slots
+//           58 %, DRAM 52 %): 87 -> 81 by a look for infinities on the FMA pipe and
+//           no clamp at 0; positions and slots fetched a turn ahead change nothing.
 //   read    100000 rows to bf16, 525 MB in and out: 102 us, 5.1 TB/s (a copy 6.8).
 //           111 us where a warp took a row of eight heads after the other; 108 with
 //           a 64-bit division a step and codes shifted and converted one by one
@@ -33,7 +34,6 @@
 // A few rows are launch-bound: 3 us (300 rows to fp32).
 #include <cuda_fp16.h>
 
-#include <cfloat>
 #include <cstdint>
 
 #include "attn_batch.h"
@@ -101,15 +101,16 @@ __device__ __forceinline__ void store8(void *p, int64_t i, const float *x, bool 
 template <int N>
 __device__ __forceinline__ uint32_t quantise(const float *x, int n, uint32_t *words) {
   float lo = INFINITY, hi = -INFINITY;
-  bool bad = false;
+  float zero = 0.0f;  // until something is not finite
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (i < n) {
       lo = fminf(lo, x[i]);
       hi = fmaxf(hi, x[i]);
-      bad |= !(fabsf(x[i]) <= FLT_MAX);
+      zero = fmaf(x[i], 0.0f, zero);
     }
   }
+  bool bad = zero != 0.0f;
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
@@ -121,7 +122,8 @@ __device__ __forceinline__ uint32_t quantise(const float *x, int n, uint32_t *wo
   s = fmaxf(fmaxf(s, __fmul_rn(top, 0x1p-11f)), 0x1p-100f);
   const uint32_t sb = (__float_as_uint(s) + 0xFFFFu) & 0xFFFF0000u;
   const float inv = __frcp_rn(__uint_as_float(sb));
-  // rint(v / s) as an integer: the sum's bits less the magic number's
+  // rint(v / s) as an integer: the sum's bits less the magic number's.  No code of a
+  // finite group is below 0: every step grows with v, and lo gives 0.
   const int z = __float_as_int(kMagic) - __float_as_int(__fadd_rn(__fmul_rn(lo, inv), kMagic));
 #pragma unroll
   for (int w = 0; w < N / 8; ++w) {
@@ -129,7 +131,7 @@ __device__ __forceinline__ uint32_t quantise(const float *x, int n, uint32_t *wo
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = __float_as_int(__fadd_rn(__fmul_rn(x[8 * w + j], inv), kMagic)) + (z - __float_as_int(kMagic));
-      v |= static_cast<uint32_t>(min(max(c, 0), 15)) << (4 * j);
+      v += static_cast<uint32_t>(min(c, 15)) << (4 * j);
     }
     words[w] = bad || 8 * w >= n ? 0u : v;
   }
