@@ -47,9 +47,14 @@ struct Tc {
   static constexpr int nbar = 14 + 2 * kUnits + 3 * stages + 2 * kRaw + kUnits + 1;
   static constexpr uint32_t unit_off = (bar_off + nbar * 8 + 15) & ~15u;
   static constexpr uint32_t misc_off = unit_off + kUnits * 64;  // tmem, abort, bad, -, marked[16], strips[kRaw + 1]
-  // 4-bit keys: by tile, whether a warp scaled rows of it [4], what they are to be multiplied by [128]
+  // 4-bit keys: by tile, whether a warp scaled rows of it [4], what their scores are to be
+  // multiplied by [128].  A ring twice as deep as that of the key tiles: the commit behind
+  // Q K^T that frees a key tile says nothing of the warpgroups, which read marks and
+  // factors after it.  Tile t + key_slots is made once Q K^T of tile t + key_slots / 2 is
+  // done, which is issued after the weights of tile t have been handed over.
+  static constexpr int key_slots = Q4 ? stages : 0;
   static constexpr uint32_t key_off = misc_off + 96 + 2 * 128 * 4;
-  static constexpr uint32_t bytes = key_off + (Q4 ? stages / 2 * 528 : 0) + 1024;
+  static constexpr uint32_t bytes = key_off + key_slots * 528 + 1024;
   static constexpr uint32_t o_col = 256, o_step = NCH * 64;  // tensor memory columns of O
 };
 
@@ -404,9 +409,9 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
   volatile int *marked = reinterpret_cast<volatile int *>(gbase + C::misc_off + 16);  // [16]
   volatile uint32_t *raw_strips = reinterpret_cast<volatile uint32_t *>(gbase + C::misc_off + 80);  // [kRaw]
   float *xm = reinterpret_cast<float *>(gbase + C::misc_off + 96), *xl = xm + 128;
-  // of tile s / 2: its warps' marks, its rows' factors
-  auto key_marks = [&](int s) { return reinterpret_cast<uint4 *>(gbase + C::key_off + s / 2 * 528); };
-  auto key_factors = [&](int s) { return reinterpret_cast<float *>(gbase + C::key_off + s / 2 * 528 + 16); };
+  // of tile t of this worker, slot t % key_slots: its warps' marks, its rows' factors
+  auto key_marks = [&](int slot) { return reinterpret_cast<uint4 *>(gbase + C::key_off + slot * 528); };
+  auto key_factors = [&](int slot) { return reinterpret_cast<float *>(gbase + C::key_off + slot * 528 + 16); };
   __shared__ int64_t scratch[kThreads / 32 + 4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -489,6 +494,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         for (int kt = tile; kt < stop; ++kt) {
           if (!(ok = wait_warp(freed(s), phase))) break;
           uint8_t *const dst = gbase + C::kv_off + s * C::tile;
+          const int slot = s / 2 + (phase ? 0 : C::key_slots / 2);  // (keys: s is even)
           bool found = false;
           uint32_t scaled = 0;  // halves of which this warp has written factors
 #pragma unroll 1
@@ -554,7 +560,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                   const int e = key_exponent(top[i]);
-                  if (part == 0) key_factors(s)[key[i]] = pow2_of(e);
+                  if (part == 0) key_factors(slot)[key[i]] = pow2_of(e);
                   put_key<true, NC4, CPG4>(dst, key[i], part, w[i], par[i], pow2_of(-e));
                 }
               }
@@ -580,7 +586,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
           }
           if (!ok) break;
           if (found) marked[un & 15u] = static_cast<int>(un + 1);
-          if (!values && lane == 0) reinterpret_cast<uint32_t *>(key_marks(s))[warp & 3] = scaled;
+          if (!values && lane == 0) reinterpret_cast<uint32_t *>(key_marks(slot))[warp & 3] = scaled;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(clean(s));
@@ -981,7 +987,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
     // rows of a tile are (token, head) with gsub heads a token, of which g count
     const int tok = row / p.gsub, hq = row - tok * p.gsub;
     uint32_t nt = 0, no = 0, nx = 0;
-    uint32_t loaded = 0, two = 0;  // (4-bit keys) key and value tiles of earlier units; units with two query tiles
+    uint32_t loaded = 0, two = 0;  // (4-bit keys) key tiles of earlier units; units with two query tiles
     bool ok = true;
     for (uint32_t un = 0; ok; ++un) {
       if (!(ok = wait_warp(u_full(un), (un / kUnits) & 1u))) break;
@@ -1031,11 +1037,11 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
             gone = __ballot_sync(0xFFFFFFFFu, bad);
           }
           if constexpr (Q4) {
-            const int s = (loaded + 2 * (kt - u.tile)) % NS;
-            const uint4 marks = *key_marks(s);
+            const int slot = (loaded + (kt - u.tile)) % C::key_slots;
+            const uint4 marks = *key_marks(slot);
             if (marks.x | marks.y | marks.z | marks.w) {
               // row j of the tile was made by warp 2 (strip % 2) + (row of the strip) / 8
-              const float *const by = key_factors(s);
+              const float *const by = key_factors(slot);
               const uint32_t mark[4] = {marks.x, marks.y, marks.z, marks.w};
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
@@ -1131,7 +1137,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         }
       }
       if (!ok) break;
-      loaded += 2 * (u.stop - u.tile);
+      loaded += u.stop - u.tile;
       const bool have = first < last;
       if (have) {
         if (!(ok = wait_warp(o_full(w), no++ & 1u))) break;
