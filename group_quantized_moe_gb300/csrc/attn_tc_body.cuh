@@ -301,21 +301,29 @@ __device__ __forceinline__ void put_key(uint8_t *tile, int key, int unit, const 
 
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }
 
-// A bound of a key row's values: |code - zp| s <= (|zp| + 16) s.
+// Parameters of a group of zeros (or of values up to 2^-96, which count as zeros), and
+// those of key rows that are not there: the smallest scale, 2^-100, and no zero point.
+constexpr uint32_t kZeros = 0x0D800000u;
+// Whether a group of keys goes into fp16 as it is: a scale in [2^-14, 2^5), which fp16
+// has exactly (rounded below that, all of the group's values would be off alike, by up
+// to 2^-6), and a zero point of up to 1000.
+__device__ __forceinline__ bool plain_keys(uint32_t par) {
+  return (par - 0x38800000u < 0x42000000u - 0x38800000u || par == kZeros) && !wide_zp16(par);
+}
+// The power of two that a row with other groups is divided by: none where its scales
+// and values lie in fp16's range all the same, else what brings its bound
+// (|zp| + 16) s >= |code - zp| s to [2^13, 2^14).
 template <int G>
-__device__ __forceinline__ float key_bound(const uint32_t (&par)[G]) {
+__device__ __forceinline__ int key_exponent(const uint32_t (&par)[G]) {
   float top = 0.0f;
+  bool low = false;
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+  for (int g = 0; g < G; ++g) {
     top = fmaxf(top, __uint_as_float(par[g] & 0xFFFF0000u) *
                          (fabsf(__half2float(__ushort_as_half(static_cast<unsigned short>(par[g])))) + 16.0f));
-  return top;
-}
-// Whether the row goes into fp16 as it is: bound in [2^-9, 2^15), or all zeros.
-__device__ __forceinline__ bool key_fits(float top) { return (top >= 0x1p-9f && top < 0x1p15f) || top < 0x1p-94f; }
-// Else the power of two that it is divided by.
-__device__ __forceinline__ int key_exponent(float top) {
-  return key_fits(top) ? 0 : static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13;
+    low |= par[g] < 0x38800000u && par[g] != kZeros;
+  }
+  return low || top >= 0x1p15f ? static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13 : 0;
 }
 
 // A query row of a tile from bf16 to fp16, times 2^E with its largest element in
@@ -514,7 +522,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
                 lds_words<NC4>(w[i], reinterpret_cast<const uint32_t *>(raw + st * strip) + (kr * 4 + part) * NC4);
                 lds_words<G4>(par[i], reinterpret_cast<const uint32_t *>(raw + st * strip + 512 * NC4) + kr * ng);
 #pragma unroll
-                for (int g = 0; g < G4; ++g) par[i][g] = in ? par[i][g] : 0u;
+                for (int g = 0; g < G4; ++g) par[i][g] = in ? par[i][g] : kZeros;
               }
             } else {
               const uint32_t *const words = reinterpret_cast<const uint32_t *>(raw + vs * strip + 256 * NC4) +
@@ -544,14 +552,8 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               }
             }
             if (!values) {
-              float top[2];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                top[i] = key_bound<G4>(par[i]);
-                wide |= !key_fits(top[i]);
-#pragma unroll
-                for (int g = 0; g < G4; ++g) wide |= wide_zp16(par[i][g]);
-              }
+              for (int g = 0; g < G4; ++g) wide |= !plain_keys(par[0][g]) | !plain_keys(par[1][g]);
               if (!__any_sync(0xFFFFFFFFu, wide)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) put_key<false, NC4, CPG4>(dst, key[i], part, w[i], par[i], 1.0f);
@@ -559,7 +561,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
                 scaled |= 1u << half;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const int e = key_exponent(top[i]);
+                  const int e = key_exponent<G4>(par[i]);
                   if (part == 0) key_factors(slot)[key[i]] = pow2_of(e);
                   put_key<true, NC4, CPG4>(dst, key[i], part, w[i], par[i], pow2_of(-e));
                 }

@@ -499,7 +499,9 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
  * value's scale is rounded to 16 bits (2^-11; not in the sum it is divided by),
  * whatever y_dtype is; with fp32 queries it has two parts, 2^-22.
  * Many (bf16 queries, head_dim up to 128, q's rows a multiple of 16 bytes apart):
- * keys are rounded to fp16 (2^-11), values and weights to bf16 (2^-8 each).  With
+ * keys are rounded to fp16 (2^-11; in a row whose scales leave fp16's range also
+ * 2^-38 of its largest (|zp| + 16) s, and where all of a row's scales are 2^-100
+ * without zero points it counts as zeros), values and weights to bf16 (2^-8 each).  With
  * n_head / n_kv query rows a token, that is so for all requests of a call with
  * more than 32 rows a request on average; but where a call of six requests or
  * more has 512 rows or more beyond one token a request (1024 where the average is

@@ -145,3 +145,27 @@ def test_value_zero_points_out_of_range(dev, nh, nkv, hd, group, lens):
 
 def test_values_of_any_scale(dev):
     run_chunks(LENS["pairs"], 8, 2, 128, 64, 16, normal, scaled(np.arange(-40, 41, 8)), 0)
+
+
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("nh,nkv,hd,group", [(8, 2, 128, 64), (16, 4, 64, 32), (4, 1, 96, 32)])
+def test_narrow_key_groups(dev, nh, nkv, hd, group, lens):
+    """Groups of keys far from zero beside their range, whose scales are below fp16's
+    normal numbers although their values are not.  Scales rounded to fp16 would be off
+    by as much for every value of a row: values have the sign of that error."""
+    row = {}
+
+    def keys(rng, shape):
+        g = shape[:3] + (-(-hd // group), 1)
+        row["s"] = s = rng.choice(np.arange(129, 160, 2), shape[:3] + (1, 1)) * 2.0 ** -25
+        z = rng.choice([-1, 1], g) * np.rint(0.0037 / s)
+        codes = rng.integers(0, 16, g[:4] + (group,))
+        codes[..., 0], codes[..., 1] = 0, 15
+        return ((z + codes) * s).reshape(shape[:3] + (-1,))[..., :hd]
+
+    def values(rng, shape):
+        s = row["s"][..., 0]
+        return np.where(s.astype(np.float16) > s, 1.0, -1.0) * (1 + 0.1 * rng.standard_normal(shape))
+
+    (_, zp, s), _ = run_chunks(LENS[lens], nh, nkv, hd, group, 16, keys, values, 12, positive=True)
+    assert (s < 2.0 ** -14).all() and ((np.abs(zp) + 16) * s >= 2.0 ** -9).all() and (np.abs(zp) <= 1000).all()
