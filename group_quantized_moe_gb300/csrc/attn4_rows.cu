@@ -23,10 +23,12 @@
 // Roundings: q' is fp16 with E such that the row's largest |q'| lies in
 // [2^14, 2^15): bf16 queries are exact down to 2^-25 of the largest; fp32 ones
 // are split into two fp16.  The weights p s_g c are rounded to fp16 (2^-11;
-// fp32 queries: split in two as well), c a power of two per query row that
-// keeps them below 2^15 and moves when the maximum moves or the scale of a
-// value is so large that a product could leave the range.  The tensor cores'
-// sums of weights run over 32 keys and are added up in fp32.
+// fp32 queries: split in two as well), c a power of two per query row and group
+// that keeps them below 2^15 and moves when the maximum moves or the scale of a
+// value is so large that a product could leave the range: each group's own, as the
+// others' scales may lie any number of powers of two away.  Z takes them before the
+// rounding, which then costs 15 steps of a scale at most, not |zp| of them.  The
+// tensor cores' sums of weights run over 32 keys and are added up in fp32.
 //
 // Measured, 32 heads of 128 over 8, groups of 64, bf16: one token of 64 requests of
 // 5400 keys (400 MB of cache) 105 us, 3.8 TB/s, 55 % of a copy; with direct loads
@@ -58,6 +60,7 @@ constexpr int kAlone = 12;           // tiles of a unit that one warp takes alon
                                     // 200 keys 87 us; 181 where eleven warps share seven tiles)
 constexpr float kRescale = 8.0f;  // log2 of the growth of the maximum that is let pass
 constexpr float kTop = 32768.0f;  // of a weight
+constexpr float kMost = 0x1p120f;  // of a power of two that it is multiplied by, and that to begin with
 
 struct Attn4 {
   AttnBatch a;
@@ -115,6 +118,12 @@ __device__ __forceinline__ float column_sum(float v) {
 __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
       const Unit4 u = us;
       // this thread's columns: query rows 2 t4 and the next
       uint32_t qop[P][C::qreg ? NC : 1][4];
-      float o[2 * NC][4], z[G][2], qs[G][2], m[2], l[2], cw[2], lim_s[2], top_w[2], ke[2];
+      float o[2 * NC][4], z[G][2], qs[G][2], m[2], l[2], cw[G][2], ke[2];
       int vis[2];
       uint8_t *const qmem = smem + C::q_off + warp * C::q_warp;
         float sum[G], k;
@@ -565,12 +574,13 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
         for (int e = 0; e < 2; ++e) {
           const int row = 2 * t4 + e;
           m[e] = -INFINITY;
-          l[e] = top_w[e] = 0.0f;
-          cw[e] = 1.0f;
-          lim_s[e] = kTop / 256.0f;
+          l[e] = 0.0f;
           vis[e] = row < u.rows ? min(u.all + row / u.g, u.end) : 0;
 #pragma unroll
-          for (int k = 0; k < G; ++k) z[k][e] = 0.0f;
+          for (int k = 0; k < G; ++k) {
+            z[k][e] = 0.0f;
+            cw[k][e] = kMost;
+          }
         }
 #pragma unroll 1
       for (int kt = u.tile + rank; kt < u.stop; kt += step) {
@@ -649,13 +659,14 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
           }
         }
         // weights
-        float most_s = 0.0f;  // largest scale of a value
+        // The scale of some value is so large that a weight could leave fp16's range.
+        bool large = false;
 #pragma unroll
-        for (int w2 = 0; w2 < 2; ++w2)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int k = 0; k < G; ++k) most_s = fmaxf(most_s, __uint_as_float(vp[w2][half][k]));
+        for (int k = 0; k < G; ++k) {
+          const float most = fmaxf(fmaxf(__uint_as_float(vp[0][0][k]), __uint_as_float(vp[0][1][k])),
+                                   fmaxf(__uint_as_float(vp[1][0][k]), __uint_as_float(vp[1][1][k])));
+          large |= most * fmaxf(cw[k][0], cw[k][1]) > kTop / 256.0f;
+        }
         uint32_t b[2][G][2][P];
           uint32_t gone = 0;  // keys that the rows do not see
           if (guard) {
@@ -675,10 +686,9 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             top[e] = fmaxf(fmaxf(sc[0][e], sc[0][2 + e]), fmaxf(sc[1][e], sc[1][2 + e])) * ke[e];
-          // A row's maximum moves on by more than kRescale, or the scale of some
-          // value is so large that a weight could leave fp16's range.
-          const bool move = __any_sync(0xFFFFFFFFu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale ||
-                                                        most_s > lim_s[0] || most_s > lim_s[1]);
+          // or a row's maximum moves on by more than kRescale
+          const bool move =
+              __any_sync(0xFFFFFFFFu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale || large);
           float f[2] = {1.0f, 1.0f};
           if (move) {
             branch();
@@ -689,7 +699,6 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
                 f[e] = ex2(m[e] - t);
                 m[e] = t;
                 l[e] *= f[e];
-                top_w[e] *= f[e];
               }
             }
           }
@@ -704,77 +713,79 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
             }
           if (move) {
             branch();
-            // c anew: the largest product so far to [2^4, 2^5)
-            float most[2] = {0.0f, 0.0f};
+            // c of each group anew: the largest product to [2^4, 2^5), of this tile or, at
+            // least 2^4 / c, of those before
 #pragma unroll
-            for (int w2 = 0; w2 < 2; ++w2)
+            for (int k = 0; k < G; ++k) {
+              float most[2] = {0.0f, 0.0f};
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
+              for (int w2 = 0; w2 < 2; ++w2)
 #pragma unroll
-                for (int k = 0; k < G; ++k)
+                for (int e = 0; e < 4; ++e)
                   if (!(gone >> (4 * w2 + e) & 1u))  // (2^-10: scales up to 2^125)
                     most[e & 1] = fmaxf(most[e & 1], w[w2][e] * 0x1p-10f * __uint_as_float(vp[w2][e >> 1][k] & 0xFFFF0000u));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float t = fmaxf(column_max(most[e]), top_w[e]);
-              top_w[e] = t;
-              int turn = 0;  // log2 of what c moves by
-              if (t > 0.0f) {
-                const int old = static_cast<int>(__float_as_uint(cw[e]) >> 23);  // biased exponents
-                const int now = max(5, min(248 - static_cast<int>(__float_as_uint(t) >> 23), 249));
-                turn = now - old;
-                cw[e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
-                lim_s[e] = __uint_as_float(static_cast<uint32_t>(min(261 - now, 254)) << 23);  // kTop / 2^8 / c
-              }
-              const float f0 = f[e] * pow2i(turn / 2), f1 = pow2i(turn - turn / 2);
+              for (int e = 0; e < 2; ++e) {
+                const int old = static_cast<int>(__float_as_uint(cw[k][e]) >> 23);  // biased exponents
+                const float before = f[e] * __uint_as_float(static_cast<uint32_t>(248 - old) << 23);
+                const float t = fmaxf(column_max(most[e]), before);
+                const int now = max(5, min(248 - static_cast<int>(__float_as_uint(t) >> 23), 247));
+                cw[k][e] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+                const int turn = now - old;
+                const float f0 = f[e] * pow2i(turn / 2), f1 = pow2i(turn - turn / 2);
+                z[k][e] = z[k][e] * f0 * f1;
 #pragma unroll
-              for (int k = 0; k < G; ++k) z[k][e] = z[k][e] * f0 * f1;
-#pragma unroll
-              for (int k = 0; k < 2 * NC; ++k) {
-                o[k][e] = o[k][e] * f0 * f1;
-                o[k][2 + e] = o[k][2 + e] * f0 * f1;
+                for (int c = 2 * CPG * k; c < 2 * CPG * (k + 1) && c < 2 * NC; ++c) {
+                  o[c][e] = o[c][e] * f0 * f1;
+                  o[c][2 + e] = o[c][2 + e] * f0 * f1;
+                }
               }
             }
           }
+          constexpr int KB = G < 4 ? G : 4;  // groups at a time (registers)
 #pragma unroll
-          for (int w2 = 0; w2 < 2; ++w2)
+          for (int kb = 0; kb < G; kb += KB) {
+            float ws[2][KB][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[w2][e] *= cw[e & 1];
-          float ws[2][G][4];
+            for (int k = kb; k < kb + KB && k < G; ++k) {
+              const f32x2 c2 = pack2(cw[k][0], cw[k][1]);
 #pragma unroll
-          for (int w2 = 0; w2 < 2; ++w2)
+              for (int w2 = 0; w2 < 2; ++w2)
 #pragma unroll
-            for (int k = 0; k < G; ++k)
+                for (int half = 0; half < 2; ++half) {
+                  const float s = __uint_as_float(vp[w2][half][k] & 0xFFFF0000u);
+                  unpack2(mul2(mul2(pack2(w[w2][2 * half], w[w2][2 * half + 1]), c2), pack2(s, s)),
+                          ws[w2][k - kb][2 * half], ws[w2][k - kb][2 * half + 1]);
+                }
+            }
+            if (guard) {
+              branch();
+              // not even 0 * NaN of a key that is not seen
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                ws[w2][k][e] = w[w2][e] * __uint_as_float(vp[w2][e >> 1][k] & 0xFFFF0000u);
-          if (guard) {
-            branch();
-            // not even 0 * NaN of a key that is not seen
+              for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (gone >> (4 * w2 + e) & 1u)
+#pragma unroll
+                    for (int k = 0; k < KB; ++k) ws[w2][k][e] = 0.0f;
+            }
 #pragma unroll
             for (int w2 = 0; w2 < 2; ++w2)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (gone >> (4 * w2 + e) & 1u)
+              for (int k = kb; k < kb + KB && k < G; ++k)
 #pragma unroll
-                  for (int k = 0; k < G; ++k) ws[w2][k][e] = 0.0f;
+                for (int half = 0; half < 2; ++half) {
+                  const float w0 = ws[w2][k - kb][2 * half], w1 = ws[w2][k - kb][2 * half + 1];
+                  float zp = low_half(vp[w2][half][k]);
+                  if constexpr (F32) zp -= C::centre;
+                  z[k][0] = fmaf(w0, zp, z[k][0]);
+                  z[k][1] = fmaf(w1, zp, z[k][1]);
+                  const uint32_t hi = half2_of(w0, w1);
+                  b[w2][k][half][0] = transpose8(hi);
+                  if constexpr (F32)
+                    b[w2][k][half][P - 1] = transpose8(half2_of(w0 - low_half(hi), w1 - low_half(hi >> 16)));
+                }
           }
-#pragma unroll
-          for (int w2 = 0; w2 < 2; ++w2)
-#pragma unroll
-            for (int k = 0; k < G; ++k)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const float w0 = ws[w2][k][2 * half], w1 = ws[w2][k][2 * half + 1];
-                float zp = low_half(vp[w2][half][k]);
-                if constexpr (F32) zp -= C::centre;
-                z[k][0] = fmaf(w0, zp, z[k][0]);
-                z[k][1] = fmaf(w1, zp, z[k][1]);
-                const uint32_t hi = half2_of(w0, w1);
-                b[w2][k][half][0] = transpose8(hi);
-                if constexpr (F32)
-                  b[w2][k][half][P - 1] = transpose8(half2_of(w0 - low_half(hi), w1 - low_half(hi >> 16)));
-              }
         uint32_t vw[2][2][NC];
 #pragma unroll
         for (int w2 = 0; w2 < 2; ++w2)
@@ -827,8 +838,7 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
         for (int e = 0; e < 2; ++e) {
           const int row = 2 * t4 + e;
           const float sum = column_sum(l[e]);
-          float inv = 1.0f / cw[e];
-          if (only && u.whole) inv *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+          const float inv = only && u.whole ? (sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f) : 1.0f;
           if (g8 == 0) {
             if (!only)
               reinterpret_cast<float2 *>(smem + C::ml_off)[warp * C::R + row] = make_float2(m[e], sum);
@@ -838,10 +848,11 @@ __global__ void __launch_bounds__(Form<NC, CPG, F32>::threads, 1)
           float *const out = reinterpret_cast<float *>(smem + C::o_off) + (warp * C::R + row) * C::OS;
 #pragma unroll
           for (int k = 0; k < G; ++k) z[k][e] = column_sum(z[k][e]);
-          auto put = [&](float v, float zz, float odd) { return fmaf(v, C::unit / odd, -zz) * inv; };
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float zz = z[c / CPG][e];
+            const float down = __uint_as_float((254u << 23) - __float_as_uint(cw[c / CPG][e]));  // 1 / c
+            auto put = [&](float v, float zz, float odd) { return fmaf(v, C::unit / odd, -zz) * down * inv; };
             // dimensions 4 g8 .. + 3 of the chunk: rows g8 and g8 + 8 of two products
             const float4 v = make_float4(put(o[2 * c][e], zz, 1.0f), put(o[2 * c][2 + e], zz, C::odd),
                                          put(o[2 * c + 1][e], zz, 1.0f), put(o[2 * c + 1][2 + e], zz, C::odd));

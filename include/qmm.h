@@ -497,7 +497,8 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
  * down to 2^-25 of the row's largest; fp32 rows: in two parts, 2^-22; an element
  * of 2^114 or more counts as infinite).  With bf16 queries each weight times its
  * value's scale is rounded to 16 bits (2^-11; not in the sum it is divided by),
- * whatever y_dtype is; with fp32 queries it has two parts, 2^-22.
+ * whatever y_dtype is; with fp32 queries it has two parts, 2^-22.  Either way a
+ * product is off by up to 2^-29 of the row's largest of the same group, too.
  * Many (bf16 queries, head_dim up to 128, q's rows a multiple of 16 bytes apart):
  * keys are rounded to fp16 (2^-11; in a row whose scales leave fp16's range also
  * 2^-38 of its largest (|zp| + 16) s, and where all of a row's scales are 2^-100
