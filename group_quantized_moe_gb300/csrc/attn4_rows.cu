@@ -68,7 +68,8 @@ struct Attn4 {
   AttnSched sc;
   AttnParts parts;
   int gsub, nsub;
-  float sl2;  // scale log2(e)
+  float sl2;   // scale log2(e)
+  int most_e;  // of the power of two that a query row is scaled by
   uint32_t *status;
 };
 
@@ -266,7 +267,7 @@ __device__ __forceinline__ void make_queries(const Attn4 &p, const Unit4 &u, uin
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   int E = 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-  E = top > 0.0f ? max(-100, min(E, 100)) : 0;
+  E = top > 0.0f ? max(-100, min(E, p.most_e)) : 0;
   const float up = pow2i(E);
   ke = p.sl2 * C::unit * pow2i(-E);
 #pragma unroll
@@ -920,7 +921,8 @@ AttnPlan attn4_rows_plan(const Kv4 &c, int n_head) {
 
 cudaError_t launch_attn4_rows(const AttnBatch &a, const Kv4 &c, const AttnPlan &pl, const AttnSched &sc,
                               const AttnParts &parts, cudaStream_t s) {
-  Attn4 p{a, c, sc, parts, pl.gsub, pl.nsub, a.scale * 1.4426950408889634f, device_status()};
+  const float sl2 = a.scale * 1.4426950408889634f;
+  Attn4 p{a, c, sc, parts, pl.gsub, pl.nsub, sl2, kv4_most_exponent(sl2), device_status()};
   if (!p.status) return cudaErrorInvalidDevice;
   switch (c.nc) {
     case 1: return run_nc<1>(p, pl.workers, s);

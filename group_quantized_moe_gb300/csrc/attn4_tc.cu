@@ -67,6 +67,7 @@ cudaError_t launch_attn4_tc(const AttnBatch &a, const Kv4 &c, const AttnPlan &pl
   p.tpt = pl.U / 2;
   p.block_shift = c.block_shift;
   p.sl2 = a.scale * 1.4426950408889634f;
+  p.most_e = kv4_most_exponent(p.sl2);
   p.status = device_status();
   if (!p.status) return cudaErrorInvalidDevice;
   CUtensorMap q;

@@ -66,6 +66,7 @@ struct TcAttn {
   int box_rows;         // rows per key box
   int block_shift;      // log2 of the cache's block size
   float sl2;            // scale log2(e)
+  int most_e;           // (4-bit keys) of the power of two that a query row is scaled by
   uint32_t *status;
 };
 
@@ -329,7 +330,7 @@ __device__ __forceinline__ int key_exponent(const uint32_t (&par)[G]) {
 // A query row of a tile from bf16 to fp16, times 2^E with its largest element in
 // [2^14, 2^15), dimensions in put_key's order; returns E.  (An element of 2^114 or
 // more becomes infinite.)
-__device__ __forceinline__ int scale_query(uint8_t *tile, int row, int nch) {
+__device__ __forceinline__ int scale_query(uint8_t *tile, int row, int nch, int most) {
   auto at = [&](int c, int j) { return reinterpret_cast<uint4 *>(tile + c * kChunk + row * 128 + ((j ^ (row & 7)) << 4)); };
   uint32_t top = 0;
 #pragma unroll 1
@@ -342,7 +343,7 @@ __device__ __forceinline__ int scale_query(uint8_t *tile, int row, int nch) {
       for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7FFFu, x[i] >> 16 & 0x7FFFu));
     }
   // of bf16 bits; not finite: as it is
-  const int E = top == 0 || top >= 0x7F80u ? 0 : max(-100, min(14 - (static_cast<int>(top >> 7) - 127), 100));
+  const int E = top == 0 || top >= 0x7F80u ? 0 : max(-100, min(14 - (static_cast<int>(top >> 7) - 127), most));
   const float up = pow2_of(E);
 #pragma unroll 1
   for (int c = 0; c < nch; ++c)
@@ -1008,7 +1009,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
         // the tile's queries to fp16, each row times a power of two that its scores lose again
         if (w == 0 || pair) {
           if (!(ok = wait_warp(q_full(w), (w ? two : un) & 1u))) break;
-          const int E = scale_query(gbase + C::q_off + w * C::tile, row, nch);
+          const int E = scale_query(gbase + C::q_off + w * C::tile, row, nch, p.most_e);
           sl2 *= pow2_of(-E);
           if (!pair) xl[row] = sl2;
           fence_proxy_async_smem();

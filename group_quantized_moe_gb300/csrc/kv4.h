@@ -21,6 +21,7 @@
 // tokens are stored without a look at their neighbours.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -47,6 +48,13 @@ __host__ __device__ inline int kv4_groups(int head_dim, int group) { return (hea
 // Bytes of a strip; where its parts begin.
 __host__ __device__ inline int kv4_strip(const Kv4 &c) { return 512 * c.nc + 128 * c.ng; }
 __host__ __device__ inline int kv4_head_bytes(const Kv4 &c) { return kv4_strip(c) << (c.block_shift - 4); }
+
+// The largest power of two by which query rows are scaled into fp16: scale log2(e)
+// divided by it stays a normal number of fp32 (as zero it would make NaNs of masked scores).
+inline int kv4_most_exponent(float sl2) {
+  const int e = std::ilogb(sl2) + 126;
+  return e < 100 ? e : 100;
+}
 
 // Rotary positions and the cache write (a.cached, a.k_cache, a.v_cache and the
 // block fields of `a` are not used: c says where rows go, c.data null: nowhere).

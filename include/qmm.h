@@ -495,7 +495,8 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
  * which fp16 holds exactly, and scales and zero points are applied in fp32.  A
  * query row is scaled by a power of two to fp16 (bf16 rows: exact for elements
  * down to 2^-25 of the row's largest; fp32 rows: in two parts, 2^-22; an element
- * of 2^114 or more counts as infinite).  With bf16 queries each weight times its
+ * of 2^114 or more counts as infinite, one below 2^-124 as zero, with a scale below
+ * 2^-26 one below 2^-150 / scale; keys of 2^100 or more may give infinite scores).  With bf16 queries each weight times its
  * value's scale is rounded to 16 bits (2^-11; not in the sum it is divided by),
  * whatever y_dtype is; with fp32 queries it has two parts, 2^-22.  Either way a
  * product is off by up to 2^-29 of the row's largest of the same group, too.
