@@ -169,3 +169,39 @@ def test_narrow_key_groups(dev, nh, nkv, hd, group, lens):
 
     (_, zp, s), _ = run_chunks(LENS[lens], nh, nkv, hd, group, 16, keys, values, 12, positive=True)
     assert (s < 2.0 ** -14).all() and ((np.abs(zp) + 16) * s >= 2.0 ** -9).all() and (np.abs(zp) <= 1000).all()
+
+
+@pytest.mark.parametrize("exponents", [(0,), (0, -24), (20, 24)])
+def test_key_groups_of_zeros(dev, exponents):
+    """Zeros in some groups and some rows, beside keys in fp16's range and out of it."""
+    def keys(rng, shape):
+        k = scaled(exponents)(rng, shape)
+        k[..., :64] *= rng.random(shape[:3] + (1,)) < 0.7
+        k[..., 64:] *= rng.random(shape[:3] + (1,)) < 0.7
+        return k
+
+    (_, zp, s), _ = run_chunks(LENS["pairs"], 8, 2, 128, 64, 16, keys, normal, -max(exponents))
+    assert ((s == 2.0 ** -100) & (zp == 0)).any() and (s == 2.0 ** -100).all(-1).any()
+
+
+@pytest.mark.parametrize("exponents", [(0,), (0, 24)])
+@pytest.mark.parametrize("n", [12, 200])
+def test_nan_keys_beside_rows_out_of_range(dev, n, exponents):
+    """A NaN in a group of a key reaches the queries that see it, and only them."""
+    nh, nkv, hd, group, S, L = 8, 2, 128, 64, 16, 600
+    rng = np.random.default_rng(6)
+    nb = -(-L // S)
+    k = scaled(exponents)(rng, (nb, nkv, S, hd)).astype(np.float32)
+    v = rng.standard_normal((nb, nkv, S, hd)).astype(np.float32)
+    qq = (rnd(3, (n, nh, hd), BF16).float() * 2.0 ** -max(exponents)).bfloat16().cuda()
+    call = lambda k: q.attn_paged(qq, q.PagedKV4(torch.from_numpy(pack(
+        ref.quantise(k, group), ref.quantise(v, group), hd, group, S)).cuda(), hd, group, S),
+        torch.arange(nb, dtype=torch.int32, device="cuda")[None], i32([0, n]), i32([L]))
+    clean = call(k)
+    assert clean.isfinite().all()
+    for j in (L - n // 2, L - 1):
+        bad = k.copy()
+        bad[j // S, :, j % S, 5] = np.nan
+        y = call(bad)
+        first = j - (L - n)
+        assert torch.equal(y[:first], clean[:first]) and y[first:].isnan().all()
