@@ -33,12 +33,14 @@
 // Measured, 32 heads of 128 over 8, groups of 64, bf16: one token of 64 requests of
 // 5400 keys (400 MB of cache) 105 us, 3.8 TB/s, 55 % of a copy; with direct loads
 // instead of bulk copies ahead of each warp 226, with conversions in place of masked
-// words 111.  DRAM reads are the cache's bytes and DRAM is half busy: what bounds it
-// is instructions, 324 of a warp to a strip (2.3 KB), which eleven warps of 168
-// registers issue in half of the cycles.  Fifteen warps of 128 registers spill.
-// fp32 queries, with two parts to each, 40 us for 12 requests, 32 heads over 32 (49
-// MB).  Each further eight query rows of a head cost a pass over the codes: 40
-// requests of 2000 keys 37 us with 4 rows, 72 with 16, 124 with 32.
+// words 111.  DRAM reads are the cache's bytes.  Nothing is full: DRAM 49 %, issue
+// slots 45 %, the integer pipe 47 %.  What bounds it is the chain within a warp
+// (products, maximum, exponentials, products; 322 instructions to a strip of 2.3 KB):
+// of three warps to a scheduler one can issue in 51 % of the cycles.  Fifteen warps of
+// 128 registers spill.  Half of each product's columns are empty with four heads to a
+// key/value head.  fp32 queries, with two parts to each, 42 us for 12 requests, 32
+// heads over 32 (49 MB).  Each further eight query rows of a head cost a pass over the
+// codes: 40 requests of 2000 keys 38 us with 4 rows, 74 with 16, 126 with 32.
 #include <cuda_fp16.h>
 
 #include <cstdint>

@@ -13,9 +13,9 @@
 // warpgroups multiply its column of scores (a mark per tile says so).
 //
 // What bounds it: making the tiles, beside the exponentials, for every query tile
-// pair again: issue slots are 53 % busy, the tensor cores 42 % of the time.  20
+// pair again: issue slots are 51 % busy, the tensor cores 41 % of the time.  20
 // requests, 4076 tokens in four chunks over up to 21000 keys, 32 heads over 8 of
-// 128: 0.99 ms, 0.6 without conversions.  One warpgroup for both kinds of codes took
+// 128: 1.02 ms, 0.6 without conversions.  One warpgroup for both kinds of codes took
 // 1.56 ms with bf16 keys, two 1.01 (fp16 keys 0.06 more); conversions with a branch
 // a word 2.4; codes put back into the dimensions' order 1.07; words read only after
 // their parameters 1.04.

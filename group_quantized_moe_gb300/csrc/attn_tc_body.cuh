@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kKT = 128;              // keys per tile
 constexpr int kWarpKv = 8, kWarpMma = 9, kWarpClean = 10, kWarpQ = 11;
-constexpr int kWarpCodes = 12;        // 4-bit cache: four warps for keys, four for values, to bf16
+constexpr int kWarpCodes = 12;        // 4-bit cache: four warps for keys (to fp16), four for values (to bf16)
 constexpr int kRaw = 3;               // half tiles of codes in flight
 constexpr uint32_t kChunk = 128 * 128;  // bytes of 128 rows x 64 bf16 columns
 constexpr int kUnits = 4;             // units in the ring between warp 11 and the others
@@ -483,7 +483,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
   if (Q4 && warp >= kWarpCodes) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if constexpr (Q4) {
-      // ------------------------------------- codes to bf16 tiles of keys and values
+      // ------------------------- codes to tiles of keys (fp16) and values (bf16)
       // A word of a key's codes is eight dimensions, 16 bytes of its row in the
       // tile; two words of values are eight dimensions of two rows.
       const int tid = threadIdx.x & 127, strip = kv4_strip(c4), ng = c4.ng;

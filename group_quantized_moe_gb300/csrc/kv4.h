@@ -57,7 +57,7 @@ inline int kv4_most_exponent(float sl2) {
 }
 
 // Rotary positions and the cache write (a.cached, a.k_cache, a.v_cache and the
-// block fields of `a` are not used: c says where rows go, c.data null: nowhere).
+// block fields of `a` are not used: c says where rows go).
 cudaError_t launch_rope_append_kv4(const RopeAppend &a, const Kv4 &c, cudaStream_t s);
 
 // Rows slots[i] of the cache as numbers: k, v [n, n_kv, head_dim] (either may be

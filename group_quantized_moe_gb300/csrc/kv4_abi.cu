@@ -60,23 +60,23 @@ namespace {
 // begins sooner, the one for many costs hardly more with each row.  Rows per
 // request and key/value head, few / many in us (32 heads of 128 over 8, groups
 // of 64):
-//   40 requests of 2000 keys    24: 98 / 118    32: 124 / 121   40: 153 / 124
-//    8 requests of 16000 keys   24: 109 / 142   32: 138 / 143   40: 167 / 145
-//  300 requests of 400 keys     16: 242 / 272   24: 352 / 280   32: 460 / 281
-//    4 requests of 6000 keys    32: 45 / 51     40: 51 / 52     48: 58 / 52
+//   40 requests of 2000 keys    24: 99 / 116    32: 126 / 117   40: 155 / 120
+//    8 requests of 16000 keys   24: 109 / 139   32: 138 / 139   40: 168 / 142
+//  300 requests of 400 keys     16: 244 / 262   24: 354 / 268   32: 463 / 273
+//    4 requests of 6000 keys    32: 45 / 47     40: 52 / 48     48: 59 / 49
 // so kRows = 32.
 // Where a call has chunks and may have single tokens beside them, each takes its
 // own.  How long a request is stands on the device only, so both forms are launched
 // and find their requests there, which costs 7 to 15 us where one has none.  One
 // chunk and single tokens, 3000 keys each, few / many / both:
-//   chunk of 64     20 requests  65 / 101 / 80    64 requests   98 / 260 / 130
-//   chunk of 256     2 requests 124 / 60 / 74     20 requests  136 / 123 / 92
-//                   64 requests 171 / 281 / 135
-//   chunk of 1024    2 requests 382 / 96 / 109    64 requests  437 / 344 / 170
+//   chunk of 64     20 requests  66 / 99 / 81     64 requests   99 / 257 / 131
+//   chunk of 256     2 requests 126 / 59 / 73     20 requests  140 / 119 / 92
+//                   64 requests 174 / 274 / 135
+//   chunk of 1024    2 requests 390 / 92 / 106    64 requests  445 / 326 / 168
 // so both from kMixed = 6 requests on (a single token costs the form for many about
 // 3.5 us), and from kLong = 512 rows beyond a token a request; twice that where the
 // average is for the form for few, as then the rows may be drafts of all requests
-// (30 of up to 5 tokens, 28 heads over 4: 52 us, both 68).
+// (30 of up to 5 tokens, 28 heads over 4: 53 us, both 70).
 struct Split {
   bool few, many;
   int tokens;  // of a request, up to which it goes to the form for few
@@ -172,7 +172,6 @@ int qmm_rope_append_kv4(const void *qkv, int32_t x_dtype, int64_t T, int64_t row
   a.k = k;
   a.v = v;
   a.y_bf16 = y_dtype == QMM_BF16;
-  a.cached = true;
   const cudaError_t e = launch_rope_append_kv4(a, c, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QMM_OK : cuda_refuse(e, who);
 }

@@ -22,14 +22,17 @@
 // Measured, 32 heads of 128 over 8, groups of 64:
 //   append  16384 tokens in bf16, 354 MB in and out: 81 us, 4.4 TB/s.  One token and
 //           eight heads a warp took 195 us: half words of values were stored one by
-//           one.  Four blocks an SM: 3, 5 and 6 took 122, 102 and 126 (four: 87).  What
-//           bounds it is the arithmetic of the codes (integer pipe 60 %, issue slots
-//           58 %, DRAM 52 %): 87 -> 81 by a look for infinities on the FMA pipe and
-//           no clamp at 0; positions and slots fetched a turn ahead change nothing.
-//   read    100000 rows to bf16, 525 MB in and out: 102 us, 5.1 TB/s (a copy 6.8).
-//           111 us where a warp took a row of eight heads after the other; 108 with
-//           a 64-bit division a step and codes shifted and converted one by one
-//           (issue slots 67 % busy, DRAM 52 %); 119 where 40 registers left six
+//           one.  Four blocks an SM: 3, 5 and 6 took 122, 102 and 126 (four: 87).
+//           Nothing is full (issue slots 54 %, DRAM 53 %, integer pipe 49 %): warps
+//           wait for their rows, 8 of the 13 cycles between two instructions, with
+//           nothing of the next pair in flight.  87 -> 81 by a look for infinities on
+//           the FMA pipe and no clamp at 0; positions and slots fetched a turn ahead
+//           change nothing.
+//   read    100000 rows to bf16, 525 MB in and out: 101 us, 5.2 TB/s (a copy 6.8).
+//           Issue slots 65 %, integer pipe 62 %, DRAM 56 %; half of a warp's time is
+//           waiting for words.  111 us where a warp took a row of eight heads after the
+//           other; 108 with a 64-bit division a step and codes shifted and converted
+//           one by one (issue slots 67 %, DRAM 52 %); 119 where 40 registers left six
 //           blocks of the eight of a grid resident.
 // A few rows are launch-bound: 3 us (300 rows to fp32).
 #include <cuda_fp16.h>

@@ -434,7 +434,10 @@ int qmm_attn_paged(const void *q, int64_t T, int64_t q_stride, int32_t n_head,
 /*
  * A layer's paged cache held in 4 bits: keys and values quantised per row, head
  * and group of 32 or 64 dimensions [P1 section 3.2's group-wise codes, for the
- * cache of section 3.4], a quarter to a third of the bytes of bf16.  Per group
+ * cache of section 3.4].  Rows are padded to whole chunks of 32 dimensions, beyond
+ * four chunks to an even number: for head sizes of 32, 64, 96, 128, 192 and 256 that
+ * is 0.28 to 0.31 of the bytes of bf16, for others more (0.34 to 0.36 for 160, 0.45
+ * to 0.5 for 40, 1.25 for 8).  Per group
  *   lo, hi = min, max;  top = max(|lo|, |hi|)
  *   s  = the next bf16 at or above max((hi - lo) / 15, top / 2048, 2^-100)
  *   zp = -rint(lo / s),  code = clamp(rint(v / s) + zp, 0, 15)
@@ -496,7 +499,8 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
  * query row is scaled by a power of two to fp16 (bf16 rows: exact for elements
  * down to 2^-25 of the row's largest; fp32 rows: in two parts, 2^-22; an element
  * of 2^114 or more counts as infinite, one below 2^-124 as zero, with a scale below
- * 2^-26 one below 2^-150 / scale; keys of 2^100 or more may give infinite scores).  With bf16 queries each weight times its
+ * 2^-26 one below 2^-150 / scale; keys of 2^100 or more may give infinite scores,
+ * values of 2^119 or more infinite results).  With bf16 queries each weight times its
  * value's scale is rounded to 16 bits (2^-11; not in the sum it is divided by),
  * whatever y_dtype is; with fp32 queries it has two parts, 2^-22.  Either way a
  * product is off by up to 2^-29 of the row's largest of the same group, too.
