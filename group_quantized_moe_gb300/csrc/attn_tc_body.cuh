@@ -97,6 +97,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The same, but numbers beyond bf16's largest become that one, not infinities.
+__device__ __forceinline__ uint32_t bf16x2_finite(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
 // Not zero when one of eight bf16 values is not finite (its exponent, all ones,
@@ -204,12 +210,13 @@ __device__ __noinline__ void add_marked4(const TcAttn &p, const Kv4 &c, const Un
 
 // (code - zp) s of eight codes in bf16, each rounded once.  Codes and zero points
 // of up to 120 are whole numbers that bf16 has (0x4300 + code is 128 + code), and
-// so are their differences; WIDE ones go through fp32.  Dimensions j and j + 4
-// become neighbours, as a mask leaves them: where results leave tensor memory,
-// dim_at finds dimension j of 32.
-__device__ __forceinline__ bool wide_zp(uint32_t par) {
+// so are their differences; WIDE ones go through fp32, as do scales of 2^121 or more:
+// their values may be beyond bf16's largest, and an infinity would make a NaN of the
+// weight 0 of a row that does not see it.  Dimensions j and j + 4 become neighbours, as
+// a mask leaves them: where results leave tensor memory, dim_at finds dimension j of 32.
+__device__ __forceinline__ bool wide_values(uint32_t par) {
   // (of an fp16's bits: its magnitude is above 120's, or it is not a number)
-  return (par & 0x7FFFu) > 0x5780u;
+  return (par & 0x7FFFu) > 0x5780u || par >= 0x7C000000u;
 }
 template <bool Q4>
 __device__ __forceinline__ constexpr int dim_at(int j) {
@@ -231,8 +238,8 @@ struct Dequant {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (WIDE) {
-        r[i] = bf16x2((static_cast<float>(w >> (4 * i) & 15u) - zf) * sf,
-                      (static_cast<float>(w >> (4 * i + 16) & 15u) - zf) * sf);
+        r[i] = bf16x2_finite((static_cast<float>(w >> (4 * i) & 15u) - zf) * sf,
+                             (static_cast<float>(w >> (4 * i + 16) & 15u) - zf) * sf);
       } else {
         const uint32_t t = (w >> (4 * i) & 0x000F000Fu) | 0x43004300u;
         const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&t), zp), s);
@@ -569,7 +576,7 @@ __device__ __forceinline__ void attn_tc_body(const CUtensorMap &tm_q, const CUte
               }
             } else {
 #pragma unroll
-              for (int g = 0; g < G4; ++g) wide |= wide_zp(par[0][g]) | wide_zp(par[1][g]);
+              for (int g = 0; g < G4; ++g) wide |= wide_values(par[0][g]) | wide_values(par[1][g]);
               if (!__any_sync(0xFFFFFFFFu, wide)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) put_row<false, NC4, CPG4>(dst, key[i], part, w[i], par[i]);

@@ -205,3 +205,23 @@ def test_nan_keys_beside_rows_out_of_range(dev, n, exponents):
         y = call(bad)
         first = j - (L - n)
         assert torch.equal(y[:first], clean[:first]) and y[first:].isnan().all()
+
+
+@pytest.mark.parametrize("n", [12, 200])
+def test_largest_values_unseen(dev, n):
+    """Values next to fp32's largest, which bf16 would round to infinity, reach no
+    query that does not see them."""
+    nh, nkv, hd, group, S, L = 8, 2, 128, 64, 16, 600
+    rng = np.random.default_rng(6)
+    nb = -(-L // S)
+    k, v = rng.standard_normal((2, nb, nkv, S, hd)).astype(np.float32)
+    qq = rnd(3, (n, nh, hd), BF16).cuda()
+    call = lambda v: q.attn_paged(qq, q.PagedKV4(torch.from_numpy(pack(
+        ref.quantise(k, group), ref.quantise(v, group), hd, group, S)).cuda(), hd, group, S),
+        torch.arange(nb, dtype=torch.int32, device="cuda")[None], i32([0, n]), i32([L]))
+    clean = call(v)
+    for j in (L - n // 2, L - 1):
+        large = v.copy()
+        large[j // S, :, j % S] = np.where(np.arange(hd) % 2, np.float32(3.4e38), np.float32(0))
+        first = j - (L - n)
+        assert torch.equal(call(large)[:first], clean[:first])
