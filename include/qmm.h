@@ -503,7 +503,9 @@ int qmm_kv4_read(const qmm_kv4_cache *cache, const int64_t *slots, int64_t n, vo
  * values of 2^119 or more infinite results).  With bf16 queries each weight times its
  * value's scale is rounded to 16 bits (2^-11; not in the sum it is divided by),
  * whatever y_dtype is; with fp32 queries it has two parts, 2^-22.  Either way a
- * product is off by up to 2^-29 of the row's largest of the same group, too.
+ * product is off by up to 2^-29 of the row's largest of the same group, too.  What is
+ * rounded away counts once for every step of the code above 0 (fp32 queries: for
+ * every step that it lies from 8, so that a value of 0 may be off by 8).
  * Many (bf16 queries, head_dim up to 128, q's rows a multiple of 16 bytes apart):
  * keys are rounded to fp16 (2^-11; in a row whose scales leave fp16's range also
  * 2^-38 of its largest (|zp| + 16) s, and where all of a row's scales are 2^-100
